@@ -416,6 +416,261 @@ mj_status mj_quantize_pack_q(const void* q_vllm, void* q_packed, float* q_descal
 mj_status mj_unpack_o(const void* o_packed, void* o_vllm, int32_t num_seqs, int32_t q_len,
                       int32_t h_k, int32_t h_r, int32_t head_dim, mj_stream_t stream);
 
+/* ------------------------------------------------- the cache's own operators
+ *
+ * Around the decode step: new tokens' rotary positions and their rows in the
+ * cache (mj_rope_append), attention whose scores are modified before the
+ * softmax (mj_decode_attn_mod), the attention weight each cached key receives
+ * (mj_key_weights) and the eviction of the keys with little of it
+ * (mj_evict).  The pages have no counterpart of these; the formulas below are
+ * their definition.  The conventions above hold. */
+
+/* Shape of an mj_rope_append call.
+ *   num_seqs     sequences (>= 1)
+ *   q_len        new tokens of every sequence when cu_tokens is NULL
+ *   h_k, h_r     kv heads, query heads per kv head
+ *   head_dim     must be 128
+ *   page_size    16, 32, 64 or 128
+ *   max_blocks, num_pages   as in mj_decode_params
+ *   rot_dim      leading elements of a head that are rotated: a multiple of
+ *                16 up to 128; the others pass unchanged
+ *   n_axes       position axes, 1..4 (1: text; 3: time, height, width)
+ *   interleaved  0: pair i is elements (i, i + rot_dim/2); 1: (2i, 2i + 1)
+ *   max_pos      rows of the table */
+typedef struct {
+  int32_t num_seqs, q_len, h_k, h_r, head_dim, page_size, max_blocks, num_pages;
+  int32_t rot_dim, n_axes, interleaved, max_pos;
+} mj_rope_params;
+
+/* Arguments of mj_rope_append.  Pointers are device memory except freq_axis.
+ *   q, k, v      bf16 rows of 128: token t, head h at x + t*x_tok + h*x_head
+ *                (strides in elements, multiples of 8; 16-byte aligned; the
+ *                three may be slices of one projection's output)
+ *   num_tokens   tokens in q, k, v
+ *   positions    int32, axis a of token t at a*pos_axis + t
+ *   cos_sin      fp32 [max_pos][rot_dim], 16-byte aligned: row p holds
+ *                cos(p w_i) for i < rot_dim/2, then sin(p w_i)
+ *   freq_axis    HOST uint8[rot_dim/2]: the axis whose position turns
+ *                frequency i; NULL: axis 0 for all.  (Sections of
+ *                frequencies, or axes that alternate, are both such a map.)
+ *   cu_tokens    int32[num_seqs + 1], non-decreasing: tokens cu_tokens[b] ..
+ *                cu_tokens[b+1] - 1 are sequence b's; NULL: q_len tokens each
+ *                (num_tokens == num_seqs*q_len).  Tokens at or past
+ *                cu_tokens[num_seqs] are padding: their outputs are left as
+ *                they were.
+ *   q_out        bf16; q_packed = 1: (num_seqs, h_k, q_len*h_r, 128) as
+ *                mj_decode_attn reads it, sequences q_out_stride elements
+ *                apart (at least h_k*q_len*h_r*128; cu_tokens NULL);
+ *                q_packed = 0: (num_tokens, h_k*h_r, 128), tokens
+ *                q_out_stride apart (at least h_k*h_r*128); it may then be q
+ *                itself (same base, q_head 128, q_tok == q_out_stride), else
+ *                no output overlaps an input
+ *   k_cache, v_cache, k_page .. v_head   e4m3 pools as in mj_decode_args,
+ *                strides in bytes, multiples of 16
+ *   block_table, seq_lens, k_descale, v_descale and their strides   as in
+ *                mj_decode_args; seq_lens counts the new tokens: token i of
+ *                the n new ones of sequence b goes to slot seq_lens[b] - n + i.
+ *                A token whose slot is negative has its Q written and no
+ *                K / V.  Tokens of one call must have slots of their own
+ *                (pages that sequences share are not written).
+ *   key_pos      optional int32: slot j of (b, g) at b*kp_seq + g*kp_head + j
+ *                receives the token's position on axis 0 (see mj_evict)
+ *   status       optional int32, caller-zeroed: MJ_ERR_INVALID_ARG when a
+ *                position is outside [0, max_pos) (that token is left out
+ *                whole), or a slot past max_blocks*page_size or its page
+ *                outside [0, num_pages) (no K / V is written) */
+typedef struct {
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t q_tok, q_head, k_tok, k_head_in, v_tok, v_head_in;
+  int32_t num_tokens;
+  const int32_t* positions;
+  int64_t pos_axis;
+  const float* cos_sin;
+  const uint8_t* freq_axis;
+  const int32_t* cu_tokens;
+  void* q_out;
+  int32_t q_packed;
+  int64_t q_out_stride;
+  uint8_t* k_cache;
+  uint8_t* v_cache;
+  int64_t k_page, k_row, k_head, v_page, v_row, v_head;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const float* k_descale;
+  const float* v_descale;
+  int64_t kd_seq, kd_head, vd_seq, vd_head;
+  int32_t* key_pos;
+  int64_t kp_seq, kp_head;
+  int32_t* status;
+} mj_rope_args;
+
+/* Rotary positions with one to four axes, and the new tokens' rows:
+ *   p = positions[freq_axis[i]][t], c = cos_sin[p][i], s = cos_sin[p][rot_dim/2 + i]
+ *   (x_a, x_b) of pair i -> (x_a c - x_b s, x_b c + x_a s)      in fp32
+ *   Q: bf16 of it;  K: e4m3 of it / k_descale[b,g];  V: e4m3(v / v_descale[b,g])
+ * (IEEE fp32 division; e4m3 to nearest even, saturating at +-448; NaN gives
+ * a NaN code).  The rotated K is not rounded to bf16 in between.  One kernel
+ * launch on `stream`; deterministic.
+ * Errors: MJ_ERR_INVALID_ARG, MJ_ERR_UNSUPPORTED (head_dim, page_size,
+ * rot_dim, n_axes, over 2^30 rows of slots, over 4096 heads), MJ_ERR_CUDA. */
+mj_status mj_rope_append(const mj_rope_params* params, const mj_rope_args* args, mj_stream_t stream);
+
+/* Modifiers of the attention scores.  For query token i (0 .. q_len-1) of
+ * sequence b at position pos = L_b - q_len + i, head h and key j:
+ *   z = z_j of the decode operation above
+ *   softcap > 0:        z <- softcap * tanh(z / softcap)
+ *   alibi_slopes:       z <- z - alibi_slopes[h] * |pos - j|
+ *   row i sees key j if j < L_b and
+ *       j < prefix[b], or
+ *       begin <= j <= end,  begin = max(0, key_begin[b*q_len + i] if given,
+ *                                       pos - window + 1 if window > 0)
+ *                           end = pos (causal) or L_b - 1,
+ *                                 and at most key_end[b*q_len + i] - 1 if given
+ * (key_begin / key_end: the token's document in a sequence that holds
+ * several; prefix: keys every token sees, also ahead of its own position, or
+ * the first keys kept in view of a window).  Other keys weigh nothing
+ * whatever their K holds.  V must be finite for every key below L_b that lies
+ * in the sequence's span (mj_score_spans; without spans: every key below
+ * L_b), also where some rows do not see it; outside the span V may hold
+ * anything.  A row that sees no key gets O = 0 and LSE = -inf.
+ *   softcap       0 = off; finite, >= 0
+ *   window        0 = off; > 0 needs params.causal
+ *   alibi_slopes  device fp32[h_k*h_r], finite, or NULL
+ *   key_begin, key_end   device int32[num_seqs*q_len] or NULL
+ *   prefix        device int32[num_seqs] or NULL
+ * Positions are slots of the cache: after mj_evict has moved rows only
+ * softcap still means what it says. */
+typedef struct {
+  float softcap;
+  int32_t window;
+  const float* alibi_slopes;
+  const int32_t* key_begin;
+  const int32_t* key_end;
+  const int32_t* prefix;
+} mj_score_mod;
+
+/* Which keys of each sequence any of its rows sees, so that a plan and the
+ * decode skip the others: spans[4 b] = (n_prefix, first, end, 0): no row sees
+ * key j unless j < n_prefix or first <= j < end (n_prefix <= first <= end <=
+ * L_b).  plan_lens[b] is the length to plan with (mj_decode_plan,
+ * mj_decode_plan_device): its tiles are the ceil(n_prefix/128) first ones of
+ * the sequence, then those from tile first/128 on.
+ *   mod          pointers are HOST memory in mj_score_spans and device memory
+ *                in mj_score_spans_device
+ *   seq_lens     int32[num_seqs], host / device; 0 <= L_b <=
+ *                max_blocks*page_size (device: clamped to that range)
+ *   spans        int32[num_seqs][4], host / device (16-byte aligned)
+ *   plan_lens    int32[num_seqs], host / device
+ * The device form is one small kernel and may be captured in a graph.
+ * Errors: MJ_ERR_INVALID_ARG, MJ_ERR_UNSUPPORTED (params), MJ_ERR_CUDA. */
+mj_status mj_score_spans(const mj_decode_params* params, const mj_score_mod* mod, const int32_t* seq_lens_host,
+                         int32_t* spans_host, int32_t* plan_lens_host);
+mj_status mj_score_spans_device(const mj_decode_params* params, const mj_score_mod* mod, const int32_t* seq_lens,
+                                int32_t* spans, int32_t* plan_lens, mj_stream_t stream);
+
+/* mj_decode_attn with modified scores.  The same arguments and results;
+ * besides:
+ *   params        kernel must be MJ_KERNEL_TENSOR_CORE_QROWS (plan with the
+ *                 same params); kv_format any but MJ_KV_NVFP4
+ *   mod           modifiers (device pointers)
+ *   spans         device int32[num_seqs][4] of mj_score_spans or
+ *                 mj_score_spans_device, with args->work planned from its
+ *                 plan_lens; keys outside a
+ *                 sequence's span weigh nothing (and V there may hold
+ *                 anything).  NULL: all keys, planned from seq_lens.
+ * Errors: as mj_decode_attn; MJ_ERR_UNSUPPORTED for another kernel or nvfp4;
+ * MJ_ERR_INVALID_ARG for a modifier out of range. */
+mj_status mj_decode_attn_mod(const mj_decode_params* params, const mj_score_mod* mod, const int32_t* spans,
+                             const mj_decode_args* args, mj_stream_t stream);
+
+/* The attention weight every cached key receives, added up:
+ *   w_j = sum over the rows n of (b, g) that see j of exp(z_nj - lse[b,g,n])
+ *   acc[b,g,j] <- (j >= L_b - fresh ? 0 : decay * acc[b,g,j]) + w_j,  j < L_b
+ * with the (modified) logits z of the decode step whose lse is given; acc of
+ * slots at or past L_b is left as it was.
+ *   params        as for the decode step; kv_format any but MJ_KV_NVFP4; the
+ *                 kernel field is not looked at
+ *   mod           the step's modifiers (device pointers) or NULL
+ *   args          read: q, q_seq_stride, k and its strides, block_table,
+ *                 seq_lens, work, num_work (a plan made from seq_lens
+ *                 themselves, so that every tile of every sequence is in it
+ *                 once), q_descale, k_descale and their strides,
+ *                 softmax_scale, lse, status; the rest is ignored
+ *   acc           device fp32, slot j of (b, g) at b*acc_seq + g*acc_head + j
+ *                 (elements; room for the longest sequence)
+ *   decay         0 <= decay <= 1; with 0 (and for fresh keys) acc is not read
+ *   fresh         >= 0: the newest keys, whose accumulators start from zero
+ *                 (q_len after a decode step that appended q_len tokens)
+ * A row with lse = -inf adds nothing.  One launch per 256 packed rows; every
+ * sum in a fixed order.
+ * Errors: MJ_ERR_INVALID_ARG, MJ_ERR_UNSUPPORTED, MJ_ERR_CUDA. */
+mj_status mj_key_weights(const mj_decode_params* params, const mj_score_mod* mod, const mj_decode_args* args,
+                         float* acc, int64_t acc_seq, int64_t acc_head, float decay, int32_t fresh,
+                         mj_stream_t stream);
+
+/* Device-side arguments of mj_evict.
+ *   k, v, strides, k_scales, v_scales and their strides   the pools, as in
+ *                mj_decode_args, of any kv_format; written
+ *   block_table, seq_lens   as in mj_decode_args
+ *   acc          fp32 weights, slot j of (b, g) at b*acc_seq + g*acc_head + j
+ *                (strides as in mj_key_weights)
+ *   acc_out      the kept slots' weights, same strides; acc itself or a
+ *                buffer apart from it (so key_pos_out)
+ *   key_pos      optional int32, same strides: the position of the token each
+ *                slot holds; NULL: position = slot.  With it key_pos_out (may
+ *                be key_pos) and next_pos are required
+ *   next_pos     int32[num_seqs]: the next token's position; with key_pos
+ *                NULL it is seq_lens[b] and this is ignored
+ *   new_lens     out int32[num_seqs]: min(L_b, budget); not seq_lens itself
+ *   budget       keys kept per head, >= 1
+ *   keep_first, keep_last   >= 0, together at most budget: slots with position
+ *                < keep_first or >= next_pos - keep_last rank above all others
+ *   workspace    >= mj_evict_workspace_bytes, 16-byte aligned; need not be
+ *                initialised
+ *   status       optional int32, caller-zeroed: MJ_ERR_INVALID_ARG when a
+ *                length is out of range or a page of a row to move is outside
+ *                [0, num_pages) (that row is not moved) */
+typedef struct {
+  uint8_t* k;
+  uint8_t* v;
+  int64_t k_page, k_row, k_head, v_page, v_row, v_head;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const float* acc;
+  float* acc_out;
+  int64_t acc_seq, acc_head;
+  const int32_t* key_pos;
+  int32_t* key_pos_out;
+  const int32_t* next_pos;
+  int32_t* new_lens;
+  int32_t budget, keep_first, keep_last;
+  void* workspace;
+  size_t workspace_bytes;
+  int32_t* status;
+  uint8_t* k_scales;
+  uint8_t* v_scales;
+  int64_t ks_page, ks_head, vs_page, vs_head;
+} mj_evict_args;
+
+size_t mj_evict_workspace_bytes(const mj_decode_params* params, int32_t budget);
+
+/* Cuts every (sequence, kv head) to `budget` keys: the ones that rank first by
+ * (protected, weight descending, slot ascending); a NaN weight ranks below
+ * every other, -0 equals 0.  With new = min(L_b, budget), the kept rows at or
+ * past slot `new` move, in order, into the slots below it that are not kept,
+ * also in order (K, V, scales, weight, position); rows kept below `new` stay.
+ * Slots at or past new keep what they held; acc_out and key_pos_out are
+ * written below new only.  Heads keep different tokens; a sequence's pages
+ * past ceil(new / page_size) are free afterwards.  Pages must not be shared
+ * between sequences.  Deterministic; two launches on `stream`.
+ *   params        num_seqs, h_k, head_dim, page_size, max_blocks, num_pages
+ *                 and kv_format are used
+ * Errors: MJ_ERR_INVALID_ARG, MJ_ERR_UNSUPPORTED, MJ_ERR_CAPACITY
+ * (workspace), MJ_ERR_CUDA. */
+mj_status mj_evict(const mj_decode_params* params, const mj_evict_args* args, mj_stream_t stream);
+
 /* Static text for a status code. */
 const char* mj_status_string(mj_status status);
 

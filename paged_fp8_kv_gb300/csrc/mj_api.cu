@@ -53,8 +53,11 @@ int device_sm_count() {
   return n;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+
+}  // namespace
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // nvfp4 scale planes: present, 16-byte aligned, page and head strides
 // 16-byte multiples (a page's rows of one head are 8 bytes apart).
@@ -67,6 +70,8 @@ bool scales_ok(const mj_decode_params& p, const mj_decode_args& a) {
   return true;
 }
 
+namespace {
+
 const char* kv_format_name(int f) {
   switch (f) {
     case MJ_KV_E3M2: return "e3m2";
@@ -76,6 +81,8 @@ const char* kv_format_name(int f) {
     default: return "e4m3";
   }
 }
+
+}  // namespace
 
 // K/V pool pointers and byte strides: 16-byte aligned (the page gathers'
 // TMA boxes), 32-byte aligned for the packed narrow formats (their TMA
@@ -91,6 +98,8 @@ bool kv_layout_ok(const mj_decode_params& p, const void* k, const void* v, const
     if (s <= 0 || (s & mask) != 0 || s >= (int64_t{1} << 40)) return false;
   return true;
 }
+
+namespace {
 
 constexpr int kDefaultL2Prefetch = 0;  // tiles; measured choice
 constexpr int kDefaultKvEvictFirst = 1;  // measured choice (faster on every workload)
@@ -111,6 +120,10 @@ constexpr int kOneHeadUnitsPerSm = 2;
 constexpr int kQRowsFrom = 16;
 
 }  // namespace
+
+int kv_evict_first(const mj_decode_params& p) {
+  return p.kv_evict_first == 0 ? kDefaultKvEvictFirst : (p.kv_evict_first > 0 ? 1 : 0);
+}
 
 KernelChoice choose_kernel(const mj_decode_params& p) {
   const int n_q = p.q_len * p.h_r;
@@ -202,13 +215,12 @@ extern "C" mj_status mj_kernel_name(const mj_decode_params* params, char* buf, i
   return MJ_OK;
 }
 
-extern "C" mj_status mj_decode_attn(const mj_decode_params* params, const mj_decode_args* args,
-                                    mj_stream_t stream_) {
-  mj_status st = check_params(params);
-  if (st != MJ_OK) return st;
-  if (!args) return MJ_ERR_INVALID_ARG;
-  const mj_decode_params& p = *params;
-  const mj_decode_args& a = *args;
+namespace {
+
+// One decode step for checked params; with `mod` non-null on modified scores
+// (the query-rows kernel's instances for them).
+mj_status decode_step(const mj_decode_params& p, const mj_decode_args& a, const ScoreModDev* mod,
+                      mj_stream_t stream_) {
   if (!a.q || !a.k || !a.v || !a.block_table || !a.seq_lens || !a.work || !a.n_splits || !a.q_descale ||
       !a.k_descale || !a.v_descale || !a.o || !a.lse)
     return MJ_ERR_INVALID_ARG;
@@ -235,7 +247,8 @@ extern "C" mj_status mj_decode_attn(const mj_decode_params* params, const mj_dec
     if ((reinterpret_cast<uintptr_t>(a.workspace) & (kAlign - 1)) != 0) return MJ_ERR_INVALID_ARG;
   }
 
-  DecodeDev d{};
+  DecodeModDev d{};
+  if (mod) d.mod = *mod;
   d.q = a.q;
   d.q_seq = a.q_seq_stride;
   d.k = a.k;
@@ -283,7 +296,7 @@ extern "C" mj_status mj_decode_attn(const mj_decode_params* params, const mj_dec
   d.num_work = a.num_work;
   d.num_pages = p.num_pages;
   d.l2_prefetch = p.l2_prefetch == 0 ? kDefaultL2Prefetch : (p.l2_prefetch < 0 ? 0 : p.l2_prefetch);
-  d.kv_evict_first = p.kv_evict_first == 0 ? kDefaultKvEvictFirst : (p.kv_evict_first > 0 ? 1 : 0);
+  d.kv_evict_first = kv_evict_first(p);
   d.kv_format = p.kv_format;
   d.ks = a.k_scales;
   d.vs = a.v_scales;
@@ -302,20 +315,23 @@ extern "C" mj_status mj_decode_attn(const mj_decode_params* params, const mj_dec
   const bool merge = p.max_splits > 1 && merge_splits > 1;
   if (verbose())
     std::fprintf(stderr,
-                 "mj_decode_attn: kernel=%s num_seqs=%d h_k=%d n_q=%d (q_len %d x h_r %d) page_size=%d %s "
+                 "%s: kernel=%s num_seqs=%d h_k=%d n_q=%d (q_len %d x h_r %d) page_size=%d %s "
                  "q=%s kv=%s work_items=%d merge=%s (max_n_splits %d of max_splits %d) kv_evict_first=%d\n",
-                 kc.name, p.num_seqs, p.h_k, p.q_len * p.h_r, p.q_len, p.h_r, p.page_size,
+                 mod ? "mj_decode_attn_mod" : "mj_decode_attn", kc.name, p.num_seqs, p.h_k, p.q_len * p.h_r, p.q_len,
+                 p.h_r, p.page_size,
                  p.causal ? "causal" : "non-causal", p.q_dtype == MJ_E4M3 ? "e4m3" : "bf16",
                  kv_format_name(p.kv_format), a.num_work, merge ? "yes" : "no", merge_splits, p.max_splits,
                  d.kv_evict_first);
   // an NVTX range around the launches, so a profiler's timeline names them
-  nvtxRangePushA("mj_decode_attn");
+  nvtxRangePushA(mod ? "mj_decode_attn_mod" : "mj_decode_attn");
   struct RangeEnd {
     ~RangeEnd() { nvtxRangePop(); }
   } range_end;
   cudaError_t e = cudaSuccess;
   if (ev[0] && (e = cudaEventRecord(ev[0], stream)) != cudaSuccess) return MJ_ERR_CUDA;
-  if (kc.kind == KernelKind::kTensorCoreQRows) {
+  if (mod) {
+    e = launch_decode_qm_mod(d, kc.rows_per_cta, kc.n_q_tiles, p.q_dtype == MJ_E4M3, stream);
+  } else if (kc.kind == KernelKind::kTensorCoreQRows) {
     e = launch_decode_qm(d, kc.rows_per_cta, kc.n_q_tiles, p.q_dtype == MJ_E4M3, stream);
   } else if (kc.kind == KernelKind::kTensorCoreGrouped) {
     const int sms = device_sm_count();
@@ -336,6 +352,28 @@ extern "C" mj_status mj_decode_attn(const mj_decode_params* params, const mj_dec
   }
   if (ev[2] && cudaEventRecord(ev[2], stream) != cudaSuccess) return MJ_ERR_CUDA;
   return MJ_OK;
+}
+
+}  // namespace
+
+extern "C" mj_status mj_decode_attn(const mj_decode_params* params, const mj_decode_args* args,
+                                    mj_stream_t stream) {
+  const mj_status st = check_params(params);
+  if (st != MJ_OK) return st;
+  if (!args) return MJ_ERR_INVALID_ARG;
+  return decode_step(*params, *args, nullptr, stream);
+}
+
+extern "C" mj_status mj_decode_attn_mod(const mj_decode_params* params, const mj_score_mod* mod, const int32_t* spans,
+                                        const mj_decode_args* args, mj_stream_t stream) {
+  mj_status st = check_params(params);
+  if (st != MJ_OK) return st;
+  if (!args || !mod) return MJ_ERR_INVALID_ARG;
+  if (params->kernel != MJ_KERNEL_TENSOR_CORE_QROWS) return MJ_ERR_UNSUPPORTED;
+  ScoreModDev m{};
+  st = score_mod_dev(*params, *mod, spans, &m);
+  if (st != MJ_OK) return st;
+  return decode_step(*params, *args, &m, stream);
 }
 
 namespace {

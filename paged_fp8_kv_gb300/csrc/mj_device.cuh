@@ -41,6 +41,76 @@ struct DecodeDev {
   int64_t ks_page, ks_head, vs_page, vs_head;
 };
 
+// Modifiers of the scores (mj_score_mod), with the device arrays they read.
+struct ScoreModDev {
+  float softcap;               // 0 = off
+  int32_t window;              // 0 = off
+  const float* slopes;         // [h_k * h_r] or null
+  const int32_t* key_begin;    // [num_seqs * q_len] or null
+  const int32_t* key_end;
+  const int32_t* prefix;       // [num_seqs] or null
+  const int4* spans;           // (n_prefix, first, end, 0) per sequence or null: all keys
+};
+
+struct DecodeModDev : DecodeDev {
+  ScoreModDev mod;
+};
+
+// mj_rope_append (mj_rope_params, mj_rope_args).
+struct RopeDev {
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  int64_t q_tok, q_head, k_tok, k_head_in, v_tok, v_head_in;
+  const int32_t* positions;
+  int64_t pos_axis;
+  const float* cos_sin;
+  const int32_t* cu_tokens;
+  __nv_bfloat16* q_out;
+  int64_t q_out_stride;
+  uint8_t* k_cache;
+  uint8_t* v_cache;
+  int64_t k_page, k_row, k_head, v_page, v_row, v_head;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const float* kd;
+  const float* vd;
+  int64_t kd_seq, kd_head, vd_seq, vd_head;
+  int32_t* key_pos;
+  int64_t kp_seq, kp_head;
+  int32_t* status;
+  int32_t num_tokens, num_seqs, q_len, h_k, h_r, page_size, max_blocks, num_pages;
+  int32_t rot_dim, max_pos, q_packed, interleaved;
+  uint8_t axis_of[64];  // the axis of each frequency
+};
+
+// mj_evict: counts[bg] moves of (b, g), destination slots at
+// moves[bg * 2 * moves_cap], source slots moves_cap further.
+struct EvictDev {
+  uint8_t* k;
+  uint8_t* v;
+  int64_t k_page, k_row, k_head, v_page, v_row, v_head;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const float* acc;
+  float* acc_out;
+  int64_t acc_seq, acc_head;
+  const int32_t* key_pos;
+  int32_t* key_pos_out;
+  const int32_t* next_pos;
+  int32_t* new_lens;
+  int32_t* counts;
+  int32_t* moves;
+  int32_t moves_cap;
+  int32_t budget, keep_first, keep_last;
+  int32_t num_seqs, h_k, page_size, max_blocks, num_pages;
+  int32_t row_bytes;  // of one K / V row: 128, 96 or 64
+  int32_t* status;
+  uint8_t* ks;  // nvfp4 scale planes or null
+  uint8_t* vs;
+  int64_t ks_page, ks_head, vs_page, vs_head;
+};
+
 // Bits per K/V code of a pool format (mj_kv_format: e4m3, e3m2, e2m3, e2m1,
 // nvfp4).
 __host__ __device__ constexpr int kv_bits(int kv_format) {

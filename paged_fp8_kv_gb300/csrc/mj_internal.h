@@ -33,6 +33,18 @@ bool tcg_supported(int h_k, int n_q, int* heads_per_cta, int* rows_per_head);
 // Validates the shape fields every entry point shares.
 mj_status check_params(const mj_decode_params* p);
 
+// Alignment, and the K/V pool and nvfp4 scale-plane layout rules.
+bool aligned16(const void* p);
+bool kv_layout_ok(const mj_decode_params& p, const void* k, const void* v, const int64_t (&strides)[6]);
+bool scales_ok(const mj_decode_params& p, const mj_decode_args& a);
+
+// The K/V loads' L2 policy: params' choice or the library's.
+int kv_evict_first(const mj_decode_params& p);
+
+// Checked score modifiers as the kernels take them.
+struct ScoreModDev;
+mj_status score_mod_dev(const mj_decode_params& p, const mj_score_mod& mod, const int32_t* spans, ScoreModDev* out);
+
 // Kernel choice for valid params.
 KernelChoice choose_kernel(const mj_decode_params& p);
 

@@ -64,6 +64,23 @@ cudaError_t launch_decode_qm(const DecodeDev& a, int rows_per_cta, int n_q_tiles
                              cudaStream_t stream);
 int qm_smem_bytes(bool q_e4m3);
 
+// The same with modified scores (decode_qm.cuh instances of their own).
+cudaError_t launch_decode_qm_mod(const DecodeModDev& a, int rows_per_cta, int n_q_tiles, bool q_e4m3,
+                                 cudaStream_t stream);
+
+// Spans of the keys any row sees and the lengths to plan with.
+cudaError_t launch_score_spans(const ScoreModDev& m, const int32_t* seq_lens, int num_seqs, int q_len, int causal,
+                               int64_t max_len, int4* spans, int32_t* plan_lens, cudaStream_t stream);
+
+// Accumulated attention weights of packed rows n0 .. n0 + n_rows - 1 (at
+// most 256): acc[b][g][j] of a.work's tiles.
+cudaError_t launch_key_weights(const DecodeModDev& a, bool q_e4m3, bool has_mod, int n0, int n_rows, const float* lse,
+                               float* acc, int64_t acc_seq, int64_t acc_head, float decay, int fresh,
+                               cudaStream_t stream);
+
+cudaError_t launch_rope_append(const RopeDev& a, cudaStream_t stream);
+cudaError_t launch_evict(const EvictDev& a, cudaStream_t stream);
+
 // TMA descriptor of a paged e4m3 pool seen as (d bytes, rows in page, kv
 // heads, pages); one box is box_rows rows of box_heads heads (head-major in
 // shared memory), 128-byte swizzle.

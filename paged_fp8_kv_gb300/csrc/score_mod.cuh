@@ -1,0 +1,128 @@
+// Modified attention scores: which keys a row sees, the soft cap and the
+// distance bias, shared by the decode and key-weight kernels.
+#pragma once
+
+#include <vector_types.h>
+#include <vector_functions.h>
+
+#include <cstdint>
+
+#include "mj_device.cuh"
+
+namespace mj {
+
+// Keys a query token sees: j < pfx or lo <= j <= hi.
+struct RowRange {
+  int lo, hi, pfx;
+};
+
+// Query token qi of sequence b (L keys in the cache).  Host and device: the
+// host form of the spans follows the same rule.
+__host__ __device__ __forceinline__ RowRange row_range(const ScoreModDev& m, int causal, int q_len, int b, int L,
+                                                       int qi) {
+  const int pos = L - q_len + qi;
+  RowRange r;
+  r.hi = causal && pos < L - 1 ? pos : L - 1;
+  r.lo = 0;
+  if (m.window > 0) {
+    const int w = pos - m.window + 1;  // window <= 2^30: no overflow
+    r.lo = w > 0 ? w : 0;
+  }
+  if (m.key_begin) {
+    const int k = m.key_begin[static_cast<int64_t>(b) * q_len + qi];
+    r.lo = k > r.lo ? k : r.lo;
+  }
+  if (m.key_end) {
+    const int k = m.key_end[static_cast<int64_t>(b) * q_len + qi];
+    const int last = (k > 0 ? k : 0) - 1;
+    r.hi = last < r.hi ? last : r.hi;
+  }
+  r.pfx = 0;
+  if (m.prefix) {
+    const int p = m.prefix[b];
+    r.pfx = p < 0 ? 0 : (p > L ? L : p);
+  }
+  return r;
+}
+
+// The span of a sequence whose rows see keys [first, last] between them
+// (last < first: none) and [0, pfx), and the length to plan with: its tiles
+// are the prefix's, then those from first / 128 to the end.
+__host__ __device__ __forceinline__ int4 make_span(int first, int last, int pfx, int32_t* plan_len) {
+  int begin = pfx, end = pfx;
+  if (first <= last) {
+    begin = first > pfx ? first : pfx;
+    end = last + 1 > pfx ? last + 1 : pfx;
+    begin = begin < end ? begin : end;
+  }
+  const int jump = begin / 128 - (pfx + 127) / 128;  // tiles between them
+  *plan_len = jump > 0 ? end - 128 * jump : end;
+  return make_int4(pfx, begin, end, 0);
+}
+
+// tanh(t) to about fp32 precision.  Below 0.6 an odd polynomial (degree 11,
+// relative error 1e-7 after rounding; coefficients fitted for this file by
+// minimax over [0, 0.6]); above, (1 - e) / (1 + e) with e = exp(-2|t|) <= 0.31,
+// whose subtraction no longer cancels.  (tanh.approx is good to 2^-11 only: a
+// cap of 50 would make that 0.02 in a logit.)
+__device__ __forceinline__ float tanh_small(float t) {
+  const float u = t * t;
+  float p = -5.852168662e-03f;
+  p = fmaf(p, u, 2.075362916e-02f);
+  p = fmaf(p, u, -5.376870490e-02f);
+  p = fmaf(p, u, 1.333168896e-01f);
+  p = fmaf(p, u, -3.333328326e-01f);
+  p = fmaf(p, u, 9.999999975e-01f);
+  return t * p;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kTanhSmall = 0.6f;
+__device__ __forceinline__ float tanh_any(float t) {
+  const float at = fabsf(t);
+  const float e = fast_exp2(at * (-2.f * kLog2e));
+  const float big = copysignf((1.f - e) * rcp_approx(1.f + e), t);
+  return at < kTanhSmall ? tanh_small(t) : big;
+}
+
+// Raw scores r[0..N) (fp32 bits) of one row at keys j0 .. j0 + N - 1 -> logits
+// in log2 units, in place.
+//   c1: raw score -> t = z / softcap, or (no cap) -> log2 units
+//   cap2: softcap in log2 units (0: no cap)
+//   slope2, pos: distance bias in log2 units (0: none)
+template <int N>
+__device__ __forceinline__ void modify_scores(uint32_t* r, float c1, float cap2, float slope2, float pos_minus_j0) {
+  float s[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) s[e] = __uint_as_float(r[e]);
+  if (cap2 > 0.f) {
+    float top = 0.f;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      s[e] *= c1;
+      top = fmaxf(top, fabsf(s[e]));
+    }
+    // scores small against the cap (most, in practice) need no exponential
+    if (__all_sync(0xffffffffu, top < kTanhSmall)) {
+#pragma unroll
+      for (int e = 0; e < N; ++e) s[e] = cap2 * tanh_small(s[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; ++e) s[e] = cap2 * tanh_any(s[e]);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e) s[e] *= c1;
+  }
+  if (slope2 != 0.f) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) s[e] = fmaf(-slope2, fabsf(pos_minus_j0 - static_cast<float>(e)), s[e]);
+  }
+#pragma unroll
+  for (int e = 0; e < N; ++e) r[e] = __float_as_uint(s[e]);
+}
+
+}  // namespace mj

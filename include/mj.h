@@ -572,7 +572,8 @@ mj_status mj_score_spans_device(const mj_decode_params* params, const mj_score_m
 
 /* mj_decode_attn with modified scores.  The same arguments and results;
  * besides:
- *   params        kernel must be MJ_KERNEL_TENSOR_CORE_QROWS (plan with the
+ *   params        kernel MJ_KERNEL_AUTO, MJ_KERNEL_TENSOR_CORE_QROWS, or
+ *                 MJ_KERNEL_TENSOR_CORE up to 16 packed rows (plan with the
  *                 same params); kv_format any but MJ_KV_NVFP4
  *   mod           modifiers (device pointers)
  *   spans         device int32[num_seqs][4] of mj_score_spans or

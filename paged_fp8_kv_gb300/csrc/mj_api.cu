@@ -330,7 +330,9 @@ mj_status decode_step(const mj_decode_params& p, const mj_decode_args& a, const 
   cudaError_t e = cudaSuccess;
   if (ev[0] && (e = cudaEventRecord(ev[0], stream)) != cudaSuccess) return MJ_ERR_CUDA;
   if (mod) {
-    e = launch_decode_qm_mod(d, kc.rows_per_cta, kc.n_q_tiles, p.q_dtype == MJ_E4M3, stream);
+    e = kc.kind == KernelKind::kTensorCore
+            ? launch_decode_tc_mod(d, kc.rows_per_cta, kc.n_q_tiles, p.q_dtype == MJ_E4M3, stream)
+            : launch_decode_qm_mod(d, kc.rows_per_cta, kc.n_q_tiles, p.q_dtype == MJ_E4M3, stream);
   } else if (kc.kind == KernelKind::kTensorCoreQRows) {
     e = launch_decode_qm(d, kc.rows_per_cta, kc.n_q_tiles, p.q_dtype == MJ_E4M3, stream);
   } else if (kc.kind == KernelKind::kTensorCoreGrouped) {
@@ -369,7 +371,11 @@ extern "C" mj_status mj_decode_attn_mod(const mj_decode_params* params, const mj
   mj_status st = check_params(params);
   if (st != MJ_OK) return st;
   if (!args || !mod) return MJ_ERR_INVALID_ARG;
-  if (params->kernel != MJ_KERNEL_TENSOR_CORE_QROWS) return MJ_ERR_UNSUPPORTED;
+  // the families with instances for modified scores
+  const KernelChoice kc = choose_kernel(*params);
+  if (params->kv_format == MJ_KV_NVFP4 ||
+      !(kc.kind == KernelKind::kTensorCoreQRows || (kc.kind == KernelKind::kTensorCore && kc.rows_per_cta <= 16)))
+    return MJ_ERR_UNSUPPORTED;
   ScoreModDev m{};
   st = score_mod_dev(*params, *mod, spans, &m);
   if (st != MJ_OK) return st;

@@ -64,7 +64,9 @@ cudaError_t launch_decode_qm(const DecodeDev& a, int rows_per_cta, int n_q_tiles
                              cudaStream_t stream);
 int qm_smem_bytes(bool q_e4m3);
 
-// The same with modified scores (decode_qm.cuh instances of their own).
+// Both on modified scores (instances of their own; decode_tc up to 16 rows).
+cudaError_t launch_decode_tc_mod(const DecodeModDev& a, int rows_per_cta, int n_q_tiles, bool q_e4m3,
+                                 cudaStream_t stream);
 cudaError_t launch_decode_qm_mod(const DecodeModDev& a, int rows_per_cta, int n_q_tiles, bool q_e4m3,
                                  cudaStream_t stream);
 
@@ -90,6 +92,10 @@ cudaError_t launch_evict(const EvictDev& a, cudaStream_t stream);
 // kind::f8f6f4 MMA.
 bool make_kv_map(CUtensorMap* m, const uint8_t* base, int page_size, int h_k, int num_pages, int64_t s_row,
                  int64_t s_head, int64_t s_page, int box_rows, int box_heads, int kv_format);
+
+// The same of an nvfp4 pool's codes, or of its scale plane.
+bool make_nv_map(CUtensorMap* m, const uint8_t* base, bool scales, int page_size, int h_k, int num_pages,
+                 int64_t s_row, int64_t s_head, int64_t s_page);
 
 // Merge of split sequences' partials into O / LSE; max_n_splits (> 1) sizes
 // the number of warps that share one row.

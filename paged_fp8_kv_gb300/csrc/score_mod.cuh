@@ -125,4 +125,29 @@ __device__ __forceinline__ void modify_scores(uint32_t* r, float c1, float cap2,
   for (int e = 0; e < N; ++e) r[e] = __float_as_uint(s[e]);
 }
 
+// The same for one key and N rows: s[c] is row c's score of the key at
+// position `key`, the rows' slopes (log2 units) and positions in shared memory.
+template <int N>
+__device__ __forceinline__ void modify_columns(float* s, float c1, float cap2, bool bias, const float* slope2,
+                                               const float* pos, float key) {
+#pragma unroll
+  for (int c = 0; c < N; ++c) s[c] *= c1;
+  if (cap2 > 0.f) {
+    float top = 0.f;
+#pragma unroll
+    for (int c = 0; c < N; ++c) top = fmaxf(top, fabsf(s[c]));
+    if (__all_sync(0xffffffffu, top < kTanhSmall)) {
+#pragma unroll
+      for (int c = 0; c < N; ++c) s[c] = cap2 * tanh_small(s[c]);
+    } else {
+#pragma unroll
+      for (int c = 0; c < N; ++c) s[c] = cap2 * tanh_any(s[c]);
+    }
+  }
+  if (bias) {
+#pragma unroll
+    for (int c = 0; c < N; ++c) s[c] = fmaf(-slope2[c], fabsf(pos[c] - key), s[c]);
+  }
+}
+
 }  // namespace mj

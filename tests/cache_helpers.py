@@ -121,8 +121,8 @@ class Reference:
 class ModStep:
     """A workload's modified decode on the device: spans, plan and the call."""
 
-    def __init__(self, w, mod, spans=True, force_splits=0, kv_layout="nhd", fill=float("nan")):
-        self.s = s = DecodeSession(w, kernel=QROWS, kv_layout=kv_layout)
+    def __init__(self, w, mod, spans=True, force_splits=0, kv_layout="nhd", fill=float("nan"), kernel=QROWS):
+        self.s = s = DecodeSession(w, kernel=kernel, kv_layout=kv_layout)
         self.w, self.mod = w, mod
         if w.q_len > 1:
             mj.pack_q(s.q_vllm, s.q_packed, w.num_seqs, w.q_len, w.h_k, w.h_r)

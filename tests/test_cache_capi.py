@@ -129,9 +129,13 @@ def test_decode_attn_mod_refused():
     assert _mod_status(p, _set(mj.ScoreModArgs(), window=5), a) == BAD
     p, a = _attn()
     assert _mod_status(p, mj.ScoreModArgs(), a, spans=_ptr() + 4) == BAD  # spans are 16-byte rows
-    for kernel in (mj.MJ_KERNEL_AUTO, mj.MJ_KERNEL_CUDA_CORE, mj.MJ_KERNEL_TENSOR_CORE):
-        p, a = _attn(kernel=kernel)
-        assert _mod_status(p, mj.ScoreModArgs(), a) == UNSUP
+    p, a = _attn(kernel=mj.MJ_KERNEL_CUDA_CORE)
+    assert _mod_status(p, mj.ScoreModArgs(), a) == UNSUP
+    p, a = _attn(kernel=mj.MJ_KERNEL_TENSOR_CORE_GROUPED)
+    assert _mod_status(p, mj.ScoreModArgs(), a) == UNSUP
+    p, a = _attn(kernel=mj.MJ_KERNEL_TENSOR_CORE)
+    p.h_r = 17  # past the swap-AB instances
+    assert _mod_status(p, mj.ScoreModArgs(), a) == UNSUP
     p, a = _attn(kernel=mj.MJ_KERNEL_AUTO, kv_format=mj.MJ_KV_NVFP4, q_dtype=mj.MJ_E4M3)
     assert _mod_status(p, mj.ScoreModArgs(), a) == UNSUP
     p, a = _attn()

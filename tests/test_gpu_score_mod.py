@@ -5,6 +5,7 @@ sizes, pool formats and layouts; empty and short sequences; splits; NaN codes
 outside the span; the device spans; determinism, graphs and streams."""
 
 import copy
+import itertools
 
 import numpy as np
 import pytest
@@ -40,11 +41,15 @@ MODS = {
 
 
 def check(w, kw, seed=0, **step):
+    """Every kernel family that takes the shape."""
     mod, host = make_mod(w, np.random.default_rng(seed), **kw)
-    st = ModStep(w, mod, **step)
     ref = Reference(w, host)
-    ref.check(*st.run())
-    return st, ref
+    for kernel in families(w):
+        ref.check(*ModStep(w, mod, kernel=kernel, **step).run())
+
+
+def families(w):
+    return (mj.MJ_KERNEL_TENSOR_CORE_QROWS,) + ((mj.MJ_KERNEL_AUTO,) if w.q_len * w.h_r <= 16 else ())
 
 
 @pytest.mark.parametrize("kw", MODS.values(), ids=MODS.keys())
@@ -90,9 +95,9 @@ def test_rows_that_see_nothing():
     end = np.array([[0, 500, 60], [950, 950, 950]], dtype=np.int32)
     host = dict(softcap=0.0, window=0, slopes=None, begin=begin, end=end, prefix=None)
     mod = mj.ScoreMod(key_begin=torch.from_numpy(begin).cuda(), key_end=torch.from_numpy(end).cuda())
-    for spans in (True, False):
-        st = ModStep(w, mod, spans=spans)
-        ref = Reference(w, host)
+    ref = Reference(w, host)
+    for spans, kernel in itertools.product((True, False), families(w)):
+        st = ModStep(w, mod, spans=spans, kernel=kernel)
         o, lse = st.run()
         assert np.isneginf(lse[1]).all() and np.isneginf(lse[0, 0, :8]).all()
         ref.check(o, lse)
@@ -123,8 +128,9 @@ def test_nan_outside_the_span_and_in_masked_keys():
         # blocks wholly between prefix and window: entries that name no page
         for blk in range(-(-int(spans[b][0]) // 16), int(spans[b][1]) // 16):
             w.block_table[b, blk] = (-1, 2**31 - 1)[blk % 2]
-    ref.check(*ModStep(w, mod).run())
-    ref.check(*ModStep(w, mod, force_splits=4).run())
+    for kernel in families(w):
+        ref.check(*ModStep(w, mod, kernel=kernel).run())
+        ref.check(*ModStep(w, mod, force_splits=4, kernel=kernel).run())
 
 
 def test_wide_window_matches_plain_decode_bits():
@@ -132,7 +138,7 @@ def test_wide_window_matches_plain_decode_bits():
     rounding and its O to the bf16 step."""
     w = syn.make_workload("mod", [700, 90], 1, 2, 8, 16, seed=2, max_splits=1)
     mod, _ = make_mod(w, np.random.default_rng(0), window=10000)
-    st = ModStep(w, mod)
+    st = ModStep(w, mod, kernel=mj.MJ_KERNEL_AUTO)
     o, lse = st.run()
     st.s.decode()
     torch.cuda.synchronize()
@@ -155,11 +161,12 @@ def test_device_spans_match_host(q_len):
         assert np.array_equal(spans.cpu().numpy(), want[0]) and np.array_equal(lens.cpu().numpy(), want[1])
 
 
-def test_graph_of_spans_plan_and_decode_follows_the_lengths():
+@pytest.mark.parametrize("kernel", [mj.MJ_KERNEL_AUTO, mj.MJ_KERNEL_TENSOR_CORE_QROWS])
+def test_graph_of_spans_plan_and_decode_follows_the_lengths(kernel):
     """One captured step, replayed while the lengths change."""
     w = syn.make_workload("mod", [900, 700, 64], 2, 2, 4, 16, seed=31, max_splits=8)
     mod, host = make_mod(w, np.random.default_rng(0), softcap=12.0, window=260)
-    st = ModStep(w, mod)
+    st = ModStep(w, mod, kernel=kernel)
     s = st.s
     pad = mj.decode_plan_max_items(s.params)
     work = torch.zeros(pad, 4, dtype=torch.int32, device="cuda")

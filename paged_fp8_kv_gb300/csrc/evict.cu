@@ -12,18 +12,23 @@
 //
 // Ranks are 32-bit keys: protected slots the largest, then the weights in
 // order (sign-folded bits, -0 as 0), NaN the smallest.  The threshold comes
-// from three histogram passes over the key's digits (11, 11 and 10 bits, most
-// significant first); slots equal to the threshold are kept in slot order
-// until `new` is reached, by counting.
+// from histogram passes of 11 bits, most significant first, over the keys'
+// offsets from the smallest one: weights lie within a few binades, so without
+// the offset the first pass would count nearly all of them in a few dozen
+// bins, whose shared-memory atomics then wait on one another.  Slots equal to
+// the threshold are kept in slot order until `new` is reached, by counting.
 //
-// One cluster of 1 to 16 CTAs serves a (b, g), its slots cut into that many
-// runs: a CTA reads its run once, keeps the keys in shared memory for the
-// later passes, and the cluster's histograms and counts are summed over
-// distributed shared memory.  The move lists meet in the workspace (L2) and
-// the cluster's CTAs then copy the rows between them: eight lanes a row of 128
-// bytes, K and V, two moves in flight a lane.  One launch; long caches of few
+// Kernel 1: one cluster of 1 to 8 CTAs serves a (b, g), its slots cut into that
+// many runs.  A CTA reads its run's weights and positions once, keeps the keys
+// in shared memory for the later passes, and the cluster's histograms and
+// counts are summed over distributed shared memory.  It writes the kept slots'
+// weights, and the move lists with their pages looked up.  Long caches of few
 // heads get their CTAs from the cluster, short ones of many heads from the
-// grid, four 512-thread CTAs an SM.
+// grid, four CTAs an SM.
+// Kernel 2 moves the rows: the moves of all groups are one list, cut evenly
+// over the CTAs (a group's share differs by its length and its luck), sixteen
+// lanes a move, four moves in flight a thread.  Bound: the round trip of
+// dependent loads (list, then rows at random places), so bytes in flight.
 
 #include <cuda_runtime.h>
 
@@ -33,10 +38,11 @@
 namespace mj {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kMaxCluster = 16;
+constexpr int kMaxCluster = 8;
+constexpr int kMaxKeys = 49152;  // keys of a run in shared memory
 constexpr int kStatusInvalidArg = 1;  // MJ_ERR_INVALID_ARG
 
 __device__ __forceinline__ uint32_t rank_key(float w, bool held) {
@@ -85,12 +91,13 @@ struct Shared {
   int hist[2][kBins];
   int warp_sums[kWarps];
   int totals[4];  // holes, movers of this CTA
+  uint32_t range[2];  // smallest key, largest unprotected key of this CTA
   uint32_t bin;
   int need;
   int bin_count;
 };
 
-__global__ void __launch_bounds__(kThreads) evict_kernel(const EvictDev a, int cluster, int key_cap) {
+__global__ void __launch_bounds__(kThreads, 4) evict_select_kernel(const EvictDev a, int cluster, int key_cap) {
   // a programmatic dependent: no global access before the grid ahead is done
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
@@ -117,6 +124,7 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictDev a, int c
   const int n = L - begin < per_cta ? L - begin : per_cta;
 
   if (L <= a.budget) {  // nothing leaves (uniform over the cluster)
+    if (rank == 0 && tid == 0) a.counts[bg] = 0;
     for (int i = tid; i < n; i += kThreads) {
       const int j = begin + i;
       if (copy_acc) a.acc_out[off + j] = acc[j];
@@ -131,69 +139,175 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictDev a, int c
     return rank_key(acc[j], p < a.keep_first || p >= end);
   };
   const bool cached = n <= key_cap;
+  // 16-byte accesses where the planes allow them (runs start at multiples of 32)
+  const bool wide =
+      ((reinterpret_cast<uintptr_t>(acc) | reinterpret_cast<uintptr_t>(a.acc_out + off) |
+        (pos ? reinterpret_cast<uintptr_t>(pos) | reinterpret_cast<uintptr_t>(a.key_pos_out + off) : 0u)) & 15u) == 0;
   auto key_of = [&](int i) { return cached ? keys[i] : make_key(begin + i); };
 
-  // ---- the threshold: the fresh-th largest key.  need: how many keys of the
+  // ---- the one read of the weights (and positions): keys and their range,
+  // and the copy of every slot below the new length (the holes among them are
+  // written again by the moves)
+  uint32_t k_min = 0xFFFFFFFFu, k_max = 0u;
+  {
+    auto take = [&](int i, float w, int p) {
+      const uint32_t k = rank_key(w, p < a.keep_first || p >= end);
+      if (cached) keys[i] = k;
+      k_min = k < k_min ? k : k_min;
+      k_max = k > k_max && k != 0xFFFFFFFFu ? k : k_max;
+    };
+    const int quads = wide ? n / 4 : 0;
+    constexpr int kBatch = 4;  // loads in flight a thread, before any of their stores
+    for (int v0 = tid; v0 < quads; v0 += kBatch * kThreads) {
+      float4 w[kBatch];
+      int4 p[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int v = v0 + u * kThreads, j = begin + 4 * v;
+        if (v < quads) w[u] = *reinterpret_cast<const float4*>(acc + j);
+        p[u] = pos && v < quads ? *reinterpret_cast<const int4*>(pos + j) : make_int4(j, j + 1, j + 2, j + 3);
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int v = v0 + u * kThreads, j = begin + 4 * v;
+        if (v >= quads) break;
+        take(4 * v, w[u].x, p[u].x);
+        take(4 * v + 1, w[u].y, p[u].y);
+        take(4 * v + 2, w[u].z, p[u].z);
+        take(4 * v + 3, w[u].w, p[u].w);
+        if (j + 3 < fresh) {
+          if (copy_acc) *reinterpret_cast<float4*>(a.acc_out + off + j) = w[u];
+          if (copy_pos) *reinterpret_cast<int4*>(a.key_pos_out + off + j) = p[u];
+        } else {
+          const float ws[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+          const int ps[4] = {p[u].x, p[u].y, p[u].z, p[u].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (j + e >= fresh) break;
+            if (copy_acc) a.acc_out[off + j + e] = ws[e];
+            if (copy_pos) a.key_pos_out[off + j + e] = ps[e];
+          }
+        }
+      }
+    }
+    for (int i = 4 * quads + tid; i < n; i += kThreads) {
+      const int j = begin + i;
+      const float w = acc[j];
+      const int p = pos ? pos[j] : j;
+      take(i, w, p);
+      if (j < fresh) {
+        if (copy_acc) a.acc_out[off + j] = w;
+        if (copy_pos) a.key_pos_out[off + j] = p;
+      }
+    }
+  }
+  for (int i = tid; i < 2 * kBins; i += kThreads) (&s.hist[0][0])[i] = 0;
+  if (tid < 2) s.range[tid] = tid == 0 ? 0xFFFFFFFFu : 0u;
+  __syncthreads();
+  k_min = __reduce_min_sync(0xffffffffu, k_min);
+  k_max = __reduce_max_sync(0xffffffffu, k_max);
+  if (lane == 0) {
+    atomicMin(&s.range[0], k_min);
+    atomicMax(&s.range[1], k_max);
+  }
+  if (cluster > 1) {
+    cluster_sync();
+    const uint32_t r = lane < cluster ? lane : rank;
+    k_min = __reduce_min_sync(0xffffffffu, static_cast<uint32_t>(ld_cluster(map_rank(ptx::smem_u32(&s.range[0]), r))));
+    k_max = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(ld_cluster(map_rank(ptx::smem_u32(&s.range[1]), r))));
+  } else {
+    __syncthreads();
+    k_min = s.range[0];
+    k_max = s.range[1];
+  }
+  // protected slots rank just above the largest other key; all as offsets
+  // (all protected: one value)
+  const uint32_t k_top = k_max >= k_min ? k_max + 1 : k_min;
+  auto digits_of = [&](uint32_t k) { return (k < k_top ? k : k_top) - k_min; };
+  const int bits = 32 - __clz(k_top - k_min);  // 0: all keys equal
+  const int passes = bits <= 11 ? 1 : (bits <= 22 ? 2 : 3);
+
+  // ---- the threshold: the fresh-th largest.  need: how many keys of the
   // prefix found so far are kept
   uint32_t prefix = 0;
   int need = fresh;
-  for (int i = tid; i < 2 * kBins; i += kThreads) (&s.hist[0][0])[i] = 0;
-  __syncthreads();
-#pragma unroll
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
-    const uint32_t digits = pass == 2 ? 1023u : 2047u;
+  int left_bits = bits;
+  for (int pass = 0; pass < passes; ++pass) {
+    const int width = left_bits < 11 ? left_bits : 11, above = left_bits;
+    left_bits -= width;
+    const int shift = left_bits;
     int* const hist = s.hist[pass & 1];
     if (pass == 2) {  // every CTA has read pass 0's counts (it passed pass 1's barrier)
       for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
       __syncthreads();
     }
-    if (pass == 0) {
-#pragma unroll 4
-      for (int i = tid; i < n; i += kThreads) {
-        const uint32_t k = make_key(begin + i);
-        if (cached) keys[i] = k;
-        atomicAdd(&hist[k >> 21], 1);
-      }
-    } else {
-      const int above = pass == 1 ? 21 : 10;
-      for (int i = tid; i < n; i += kThreads) {
-        const uint32_t k = key_of(i);
-        if ((k >> above) == (prefix >> above)) atomicAdd(&hist[(k >> shift) & digits], 1);
-      }
+    const uint32_t mask = (1u << width) - 1u;
+    // (above = 32 only when every bit is left: then all keys match)
+#pragma unroll 8
+    for (int i = tid; i < n; i += kThreads) {
+      const uint32_t k = digits_of(key_of(i));
+      if (pass == 0 || (k >> above) == (prefix >> above)) atomicAdd(&hist[(k >> shift) & mask], 1);
     }
-    cluster_sync();
-    // every CTA sums the cluster's counts: thread t bins 4 t' .. 4 t' + 3 from
-    // the top, so that a prefix sum over the threads counts the larger keys
+    if (cluster > 1)
+      cluster_sync();
+    else
+      __syncthreads();
+    // every CTA sums the cluster's counts: thread t eight bins, the highest
+    // first, so that a prefix sum over the threads counts the larger keys
     const int q = kThreads - 1 - tid;
-    int4 c = make_int4(0, 0, 0, 0);
-    const uint32_t mine = ptx::smem_u32(hist + 4 * q);
-    for (int r = 0; r < cluster; ++r) {
-      const int4 v = ld_cluster_v4(map_rank(mine, r));
-      c.x += v.x;
-      c.y += v.y;
-      c.z += v.z;
-      c.w += v.w;
+    int c[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    const uint32_t mine = ptx::smem_u32(hist + 8 * q);
+    // (four CTAs' counts in flight, each CTA starting with its own: all reading
+    // one at a time would queue on that one's SM)
+    for (int r0 = 0; r0 < cluster; r0 += 4) {
+      int4 lo[4], hi[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const uint32_t at = map_rank(mine, (rank + r0 + u) & (cluster - 1));
+        lo[u] = ld_cluster_v4(at);
+        hi[u] = ld_cluster_v4(at + 16);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (r0 + u >= cluster) break;
+        c[0] += hi[u].w;
+        c[1] += hi[u].z;
+        c[2] += hi[u].y;
+        c[3] += hi[u].x;
+        c[4] += lo[u].w;
+        c[5] += lo[u].z;
+        c[6] += lo[u].y;
+        c[7] += lo[u].x;
+      }
     }
-    const int sum = c.x + c.y + c.z + c.w;
+    int sum = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum += c[e];
     int total;
     int before = warp_sum_before(sum, lane, total);
     if (lane == 31) s.warp_sums[warp] = total;
     __syncthreads();
-    for (int w = 0; w < warp; ++w) before += s.warp_sums[w];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) before += w < warp ? s.warp_sums[w] : 0;
     if (before < need && need <= before + sum) {  // one thread: the threshold's digit is among its bins
-      const int cnt[4] = {c.w, c.z, c.y, c.x};
-      int left = need - before, e = 0;
-      while (e < 3 && cnt[e] < left) left -= cnt[e++];
-      s.bin = 4 * q + 3 - e;
-      s.need = left;
-      s.bin_count = cnt[e];
+      int left = need - before;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (left > 0 && left <= c[e]) {
+          s.bin = 8 * q + 7 - e;
+          s.need = left;
+          s.bin_count = c[e];
+        }
+        left -= c[e];
+      }
     }
     __syncthreads();
     prefix |= s.bin << shift;
     need = s.need;
   }
-  static_assert(kThreads * 4 == kBins, "four bins a thread");
+  static_assert(kThreads * 8 == kBins, "eight bins a thread");
+  const int* const last_hist = s.hist[(passes - 1) & 1];
+  const uint32_t last_bin = s.bin;
   // keys above the threshold are kept, and of the ties (equal to it) the
   // first `need`; those of lower runs are in the last histogram
   const bool all_ties = s.bin_count == need;
@@ -203,11 +317,14 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictDev a, int c
   const int row0 = warp * rows_per_warp < rows ? warp * rows_per_warp : rows;
   const int row1 = row0 + rows_per_warp < rows ? row0 + rows_per_warp : rows;
   if (!all_ties) {
-    for (int r = 0; r < rank; ++r) tie_rank += ld_cluster(map_rank(ptx::smem_u32(&s.hist[0][prefix & 1023u]), r));
+    const int theirs = ld_cluster(map_rank(ptx::smem_u32(last_hist + last_bin), lane < cluster ? lane : rank));
+    int all;
+    const int before = warp_sum_before(lane < cluster ? theirs : 0, lane, all);
+    tie_rank = __shfl_sync(0xffffffffu, before, rank);
     int mine = 0;
     for (int r = row0; r < row1; ++r) {
       const int i = r * 32 + lane;
-      mine += __popc(__ballot_sync(0xffffffffu, i < n && key_of(i) == prefix));
+      mine += __popc(__ballot_sync(0xffffffffu, i < n && digits_of(key_of(i)) == prefix));
     }
     __syncthreads();
     if (lane == 0) s.warp_sums[warp] = mine;
@@ -218,7 +335,7 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictDev a, int c
   auto flags = [&](int r, int& ties, uint32_t& holes, uint32_t& movers) {
     const int i = r * 32 + lane;
     const bool in = i < n;
-    const uint32_t k = in ? key_of(i) : 0u;
+    const uint32_t k = in ? digits_of(key_of(i)) : 0u;
     bool keep = in && k >= prefix;
     if (!all_ties) {
       const uint32_t tie = __ballot_sync(0xffffffffu, in && k == prefix);
@@ -230,11 +347,13 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictDev a, int c
     movers = __ballot_sync(0xffffffffu, keep && j >= fresh);
   };
   int n_holes = 0, n_movers = 0, ties = tie_rank;
+#pragma unroll 4
   for (int r = row0; r < row1; ++r) {
     uint32_t h, m;
     flags(r, ties, h, m);
     n_holes += __popc(h);
     n_movers += __popc(m);
+    if (cached && lane < 2) keys[r * 32 + lane] = lane == 0 ? h : m;  // over the row's keys, done with
   }
   __syncthreads();
   if (lane == 0) s.warp_sums[warp] = n_holes | (n_movers << 16);
@@ -255,110 +374,178 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictDev a, int c
   }
   cluster_sync();
   int moves_n = 0;
-  for (int r = 0; r < cluster; ++r) {
+  {  // lane r: CTA r's counts
+    const uint32_t r = lane < cluster ? lane : rank;
     const int h = ld_cluster(map_rank(ptx::smem_u32(&s.totals[0]), r));
     const int m = ld_cluster(map_rank(ptx::smem_u32(&s.totals[1]), r));
-    if (r < rank) {
-      hole_at += h;
-      mover_at += m;
-    }
-    moves_n += h;
+    int all;
+    int before = warp_sum_before(lane < cluster ? h : 0, lane, all);
+    hole_at += __shfl_sync(0xffffffffu, before, rank);
+    moves_n = all;
+    before = warp_sum_before(lane < cluster ? m : 0, lane, all);
+    mover_at += __shfl_sync(0xffffffffu, before, rank);
   }
-  int32_t* const moves = a.moves + static_cast<int64_t>(bg) * a.moves_cap * 2;  // [dst | src]
+  // (slot, page) of every destination, then of every source
+  int2* const to = reinterpret_cast<int2*>(a.moves) + static_cast<int64_t>(bg) * a.moves_cap * 2;
+  int2* const from = to + a.moves_cap;
+  const int32_t* const table = a.block_table + static_cast<int64_t>(b) * a.max_blocks;
+  const int page_shift = 31 - __clz(a.page_size);
   ties = tie_rank;
   const uint32_t below = (1u << lane) - 1u;
+#pragma unroll 4
   for (int r = row0; r < row1; ++r) {
     uint32_t h, m;
-    flags(r, ties, h, m);
+    if (cached) {
+      h = keys[r * 32];
+      m = keys[r * 32 + 1];
+    } else {
+      flags(r, ties, h, m);
+    }
     const int j = begin + r * 32 + lane;
-    if ((h >> lane) & 1u) moves[hole_at + __popc(h & below)] = j;
-    if ((m >> lane) & 1u) moves[a.moves_cap + mover_at + __popc(m & below)] = j;
+    const bool is_hole = (h >> lane) & 1u, is_mover = (m >> lane) & 1u;
+    if (is_hole || is_mover) {
+      const int2 e = make_int2(j, __ldg(table + (j >> page_shift)));
+      if (is_hole) to[hole_at + __popc(h & below)] = e;
+      if (is_mover) from[mover_at + __popc(m & below)] = e;
+    }
     hole_at += __popc(h);
     mover_at += __popc(m);
-    if (j < fresh && j < begin + n && !((h >> lane) & 1u)) {
-      if (copy_acc) a.acc_out[off + j] = acc[j];
-      if (copy_pos) a.key_pos_out[off + j] = pos[j];
-    }
   }
-  cluster_sync();  // the lists are whole (and no CTA's shared memory is read any more)
+  if (rank == 0 && tid == 0) a.counts[bg] = moves_n;
+  if (cluster > 1) cluster_sync();  // no CTA leaves while its shared memory may be read
+}
 
-  // ---- the moves: eight lanes one, CTAs of the cluster in turn
-  const int32_t* const table = a.block_table + static_cast<int64_t>(b) * a.max_blocks;
-  const int vecs = a.row_bytes / 16;  // 8, 6 or 4 of the eight lanes
-  const int lane8 = tid & 7;
-  constexpr int kUnroll = 2;
-  const int step = cluster * (kThreads / 8);
-  for (int i0 = rank * (kThreads / 8) + (tid >> 3); i0 < moves_n; i0 += step * kUnroll) {
-    int dst[kUnroll], src[kUnroll], dp[kUnroll], sp[kUnroll];
-    bool ok[kUnroll];
-    uint4 kv[kUnroll], vv[kUnroll];
+__global__ void __launch_bounds__(kThreads, 4) evict_move_kernel(const EvictDev a, int groups) {
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  __shared__ int64_t warp_sums[kWarps];
+  __shared__ int s_group;
+  __shared__ int64_t s_before;  // moves of the groups before s_group
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // all moves are one list, in group order; this CTA's share of it
+  const int per = (groups + kThreads - 1) / kThreads;
+  const int g0 = tid * per < groups ? tid * per : groups;
+  const int g1 = g0 + per < groups ? g0 + per : groups;
+  int64_t mine = 0;
+  for (int q = g0; q < g1; ++q) mine += a.counts[q];
+  int64_t x = mine;
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int i = i0 + u * step;
-      ok[u] = i < moves_n;
-      dst[u] = ok[u] ? moves[i] : 0;
-      src[u] = ok[u] ? moves[a.moves_cap + i] : 0;
-    }
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) warp_sums[warp] = x;
+  __syncthreads();
+  int64_t before = x - mine, total = 0;
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      dp[u] = table[dst[u] / a.page_size];
-      sp[u] = table[src[u] / a.page_size];
-      if (ok[u] && lane8 == 0) {
-        a.acc_out[off + dst[u]] = acc[src[u]];
-        if (pos) a.key_pos_out[off + dst[u]] = pos[src[u]];
-      }
-      if (ok[u] && (dp[u] < 0 || dp[u] >= a.num_pages || sp[u] < 0 || sp[u] >= a.num_pages)) {
-        if (lane8 == 0 && a.status) atomicExch(a.status, kStatusInvalidArg);
-        ok[u] = false;
-      }
-    }
+  for (int w = 0; w < kWarps; ++w) {
+    before += w < warp ? warp_sums[w] : 0;
+    total += warp_sums[w];
+  }
+  const int64_t first = total * blockIdx.x / gridDim.x, last = total * (blockIdx.x + 1) / gridDim.x;
+  if (first == last) return;  // uniform over the CTA
+  if (before <= first && first < before + mine) {  // one thread: the first move's group
+    int q = g0;
+    while (first >= before + a.counts[q]) before += a.counts[q++];
+    s_group = q;
+    s_before = before;
+  }
+  __syncthreads();
+
+  // sixteen lanes a move (eight vectors of its K row and eight of its V row;
+  // lane 0 its weight and lane 1 its position), kUnroll of them in flight,
+  // every load before any store
+  const int l16 = tid & 15, l8 = tid & 7;
+  const bool is_v = l16 >= 8;
+  const bool has_vec = l8 < a.row_bytes / 16;  // 8, 6 or 4 of the eight
+  const int page_mask = a.page_size - 1;       // 16, 32, 64 or 128 rows
+  const int64_t page_step = is_v ? a.v_page : a.k_page, row_step = is_v ? a.v_row : a.k_row;
+  const bool has_word = l16 == 0 || (l16 == 1 && a.key_pos);
+  constexpr int kUnroll = 4;
+  constexpr int step = kThreads / 16;
+  int64_t at = first, group_begin = s_before;
+  for (int bg = s_group; at < last; ++bg) {
+    const int count = a.counts[bg];
+    const int64_t group_end = group_begin + count;
+    const int stop = static_cast<int>((group_end < last ? group_end : last) - group_begin);  // moves of this group
+    const int b = bg / a.h_k, g = bg - b * a.h_k;
+    const int64_t off = b * a.acc_seq + g * a.acc_head;
+    const int2* const to = reinterpret_cast<const int2*>(a.moves) + static_cast<int64_t>(bg) * a.moves_cap * 2;
+    const int2* const from = to + a.moves_cap;
+    uint8_t* const pool = (is_v ? a.v + g * a.v_head : a.k + g * a.k_head) + l8 * 16;
+    const uint32_t* const word_in = l16 == 0 ? reinterpret_cast<const uint32_t*>(a.acc + off)
+                                             : reinterpret_cast<const uint32_t*>(a.key_pos + off);
+    uint32_t* const word_out = l16 == 0 ? reinterpret_cast<uint32_t*>(a.acc_out + off)
+                                        : reinterpret_cast<uint32_t*>(a.key_pos_out + off);
+    const int start = static_cast<int>(at - group_begin) + (tid >> 4);
+    int2 dst[kUnroll], src[kUnroll];
+    auto fetch = [&](int i0) {
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      if (ok[u] && lane8 < vecs) {
-        const int sr = src[u] % a.page_size;
-        kv[u] = *reinterpret_cast<const uint4*>(a.k + sp[u] * a.k_page + sr * a.k_row + g * a.k_head + lane8 * 16);
-        vv[u] = *reinterpret_cast<const uint4*>(a.v + sp[u] * a.v_page + sr * a.v_row + g * a.v_head + lane8 * 16);
+      for (int u = 0; u < kUnroll; ++u) {
+        const int i = i0 + u * step;
+        dst[u] = i < stop ? to[i] : make_int2(0, -2);  // page -2: no move
+        src[u] = i < stop ? from[i] : make_int2(0, -2);
       }
-    }
+    };
+    if (start < stop) fetch(start);
+    for (int i0 = start; i0 < stop; i0 += step * kUnroll) {
+      uint4 row[kUnroll];
+      uint32_t word[kUnroll];
+      int2 to_now[kUnroll];
+      int sp[kUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int dr = dst[u] % a.page_size;
-      if (ok[u] && lane8 < vecs) {
-        *reinterpret_cast<uint4*>(a.k + dp[u] * a.k_page + dr * a.k_row + g * a.k_head + lane8 * 16) = kv[u];
-        *reinterpret_cast<uint4*>(a.v + dp[u] * a.v_page + dr * a.v_row + g * a.v_head + lane8 * 16) = vv[u];
+      for (int u = 0; u < kUnroll; ++u) {
+        to_now[u] = dst[u];
+        sp[u] = src[u].y;
+        const bool ok = static_cast<uint32_t>(dst[u].y) < static_cast<uint32_t>(a.num_pages) &&
+                        static_cast<uint32_t>(sp[u]) < static_cast<uint32_t>(a.num_pages);
+        if (!ok && sp[u] != -2) sp[u] = -1;  // a page that is none
+        if (sp[u] >= 0 && has_vec)
+          row[u] = *reinterpret_cast<const uint4*>(pool + sp[u] * page_step + (src[u].x & page_mask) * row_step);
+        if (sp[u] != -2 && has_word) word[u] = word_in[src[u].x];
       }
-      if (a.ks && ok[u] && lane8 < 2) {  // nvfp4: the row's eight scales, K on lane 0, V on lane 1
-        const int sr = src[u] % a.page_size;
-        uint8_t* const base = lane8 == 0 ? a.ks : a.vs;
-        const int64_t page = lane8 == 0 ? a.ks_page : a.vs_page, head = lane8 == 0 ? a.ks_head : a.vs_head;
-        *reinterpret_cast<uint2*>(base + dp[u] * page + g * head + dr * 8) =
-            *reinterpret_cast<const uint2*>(base + sp[u] * page + g * head + sr * 8);
+      if (a.ks && l8 == 0) {  // nvfp4: the rows' eight scales, K's and V's
+        uint8_t* const plane = is_v ? a.vs + g * a.vs_head : a.ks + g * a.ks_head;
+        const int64_t step_s = is_v ? a.vs_page : a.ks_page;
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+          if (sp[u] >= 0)
+            *reinterpret_cast<uint2*>(plane + to_now[u].y * step_s + (to_now[u].x & page_mask) * 8) =
+                *reinterpret_cast<const uint2*>(plane + sp[u] * step_s + (src[u].x & page_mask) * 8);
+      }
+      if (i0 + step * kUnroll < stop) fetch(i0 + step * kUnroll);  // the next round's list entries
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        if (sp[u] >= 0 && has_vec)
+          *reinterpret_cast<uint4*>(pool + to_now[u].y * page_step + (to_now[u].x & page_mask) * row_step) = row[u];
+        if (sp[u] != -2 && has_word) word_out[to_now[u].x] = word[u];
+        if (sp[u] == -1 && l16 == 0 && a.status) atomicExch(a.status, kStatusInvalidArg);
       }
     }
+    group_begin = group_end;
+    at = group_end < last ? group_end : last;
   }
 }
 
 }  // namespace
 
-cudaError_t launch_evict(const EvictDev& a, cudaStream_t stream) {
+cudaError_t launch_evict(const EvictDev& a, int sm_count, cudaStream_t stream) {
   const int64_t groups = static_cast<int64_t>(a.num_seqs) * a.h_k;
   const int64_t max_len = static_cast<int64_t>(a.max_blocks) * a.page_size;
   // CTAs a group: enough to fill about one wave (four an SM), each with 2048
   // slots or more
   int cluster = 1;
-  while (cluster < kMaxCluster && groups * cluster * 2 <= 152 * 4 && max_len / (cluster * 2) >= 2048) cluster *= 2;
+  while (cluster < kMaxCluster && groups * cluster * 2 <= sm_count * 4 && max_len / (cluster * 2) >= 2048) cluster *= 2;
   // keys in shared memory when a run fits beside the histograms (else they
   // are made again from the weights, in L2, by every pass)
   const int64_t run = (max_len + cluster - 1) / cluster + 32;
-  const int key_cap = run <= 49152 ? static_cast<int>(run) : 0;
-  const size_t smem = static_cast<size_t>(key_cap) * 4;
-  cudaError_t e = cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 49152 * 4);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  const int key_cap = run <= kMaxKeys ? static_cast<int>(run) : 0;
+  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxKeys * 4);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(groups * cluster), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = static_cast<size_t>(key_cap) * 4;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -369,7 +556,12 @@ cudaError_t launch_evict(const EvictDev& a, cudaStream_t stream) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, evict_kernel, a, cluster, key_cap);
+  e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a, cluster, key_cap);
+  if (e != cudaSuccess || a.moves_cap == 0) return e;
+  const int64_t most = (groups * a.moves_cap + 15) / 16;  // CTAs with one move a half warp
+  const int64_t ctas = most < sm_count * 4 ? most : sm_count * 4;
+  return launch_pdl(evict_move_kernel, dim3(static_cast<unsigned>(ctas), 1, 1), dim3(kThreads, 1, 1), 0, stream, a,
+                    static_cast<int>(groups));
 }
 
 }  // namespace mj

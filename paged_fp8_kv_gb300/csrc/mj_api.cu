@@ -40,6 +40,10 @@ WorkspaceLayout workspace_layout(const mj_decode_params& p) {
   return w;
 }
 
+bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+
+}  // namespace
+
 // SMs of the current device (the persistent kernel's grid), cached per
 // device; 0 when it cannot be read.
 int device_sm_count() {
@@ -52,10 +56,6 @@ int device_sm_count() {
   if (dev < 64) cache[dev] = n;
   return n;
 }
-
-bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
-
-}  // namespace
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

@@ -287,7 +287,7 @@ namespace {
 
 struct EvictLayout {
   int64_t cap;  // moves of one (b, g) at most
-  size_t moves_off, total;
+  size_t counts_off, total;
 };
 
 EvictLayout evict_layout(const mj_decode_params& p, int32_t budget) {
@@ -295,8 +295,9 @@ EvictLayout evict_layout(const mj_decode_params& p, int32_t budget) {
   const int64_t max_len = static_cast<int64_t>(p.max_blocks) * p.page_size;
   w.cap = std::max<int64_t>(0, std::min<int64_t>(budget, max_len - budget));
   const size_t groups = static_cast<size_t>(p.num_seqs) * p.h_k;
-  w.moves_off = (groups * 4 + 15) / 16 * 16;
-  w.total = w.moves_off + groups * static_cast<size_t>(w.cap) * 8;
+  // (slot, page) of a destination and a source a move, and the moves' number
+  w.counts_off = groups * static_cast<size_t>(w.cap) * 16;
+  w.total = w.counts_off + groups * 4;
   return w;
 }
 
@@ -350,7 +351,7 @@ extern "C" mj_status mj_evict(const mj_decode_params* params, const mj_evict_arg
   const EvictLayout w = evict_layout(p, a.budget);
   if (!a.workspace || !aligned16(a.workspace)) return MJ_ERR_INVALID_ARG;
   if (a.workspace_bytes < w.total) return MJ_ERR_CAPACITY;
-  if (w.cap * p.num_seqs * p.h_k > (int64_t{1} << 36)) return MJ_ERR_UNSUPPORTED;  // the move grid's range
+  if (static_cast<int64_t>(p.num_seqs) * p.h_k > (int64_t{1} << 27)) return MJ_ERR_UNSUPPORTED;  // the grid's range
 
   EvictDev d{};
   d.k = a.k;
@@ -371,8 +372,8 @@ extern "C" mj_status mj_evict(const mj_decode_params* params, const mj_evict_arg
   d.key_pos_out = a.key_pos_out;
   d.next_pos = a.next_pos;
   d.new_lens = a.new_lens;
-  d.counts = static_cast<int32_t*>(a.workspace);
-  d.moves = reinterpret_cast<int32_t*>(static_cast<char*>(a.workspace) + w.moves_off);
+  d.moves = static_cast<int32_t*>(a.workspace);
+  d.counts = reinterpret_cast<int32_t*>(static_cast<char*>(a.workspace) + w.counts_off);
   d.moves_cap = static_cast<int32_t>(w.cap);
   d.budget = a.budget;
   d.keep_first = a.keep_first;
@@ -392,6 +393,8 @@ extern "C" mj_status mj_evict(const mj_decode_params* params, const mj_evict_arg
     d.vs_page = a.vs_page;
     d.vs_head = a.vs_head;
   }
+  const int sms = device_sm_count();
+  if (sms < 1) return MJ_ERR_CUDA;
   const NvtxRange range("mj_evict");
-  return launch_evict(d, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MJ_OK : MJ_ERR_CUDA;
+  return launch_evict(d, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MJ_OK : MJ_ERR_CUDA;
 }

@@ -84,8 +84,9 @@ struct RopeDev {
   uint8_t axis_of[64];  // the axis of each frequency
 };
 
-// mj_evict: counts[bg] moves of (b, g), destination slots at
-// moves[bg * 2 * moves_cap], source slots moves_cap further.
+// mj_evict: counts[bg] moves of (b, g); its lists are moves_cap (slot, page)
+// pairs of destinations at pair bg * 2 * moves_cap of `moves`, then as many of
+// sources.
 struct EvictDev {
   uint8_t* k;
   uint8_t* v;

@@ -38,6 +38,9 @@ bool aligned16(const void* p);
 bool kv_layout_ok(const mj_decode_params& p, const void* k, const void* v, const int64_t (&strides)[6]);
 bool scales_ok(const mj_decode_params& p, const mj_decode_args& a);
 
+// SMs of the current device, cached per device; 0 when it cannot be read.
+int device_sm_count();
+
 // The K/V loads' L2 policy: params' choice or the library's.
 int kv_evict_first(const mj_decode_params& p);
 

@@ -81,7 +81,7 @@ cudaError_t launch_key_weights(const DecodeModDev& a, bool q_e4m3, bool has_mod,
                                cudaStream_t stream);
 
 cudaError_t launch_rope_append(const RopeDev& a, cudaStream_t stream);
-cudaError_t launch_evict(const EvictDev& a, cudaStream_t stream);
+cudaError_t launch_evict(const EvictDev& a, int sm_count, cudaStream_t stream);
 
 // TMA descriptor of a paged e4m3 pool seen as (d bytes, rows in page, kv
 // heads, pages); one box is box_rows rows of box_heads heads (head-major in

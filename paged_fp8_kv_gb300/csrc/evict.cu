@@ -24,7 +24,7 @@
 // counts are summed over distributed shared memory.  It writes the kept slots'
 // weights, and the move lists with their pages looked up.  Long caches of few
 // heads get their CTAs from the cluster, short ones of many heads from the
-// grid, four CTAs an SM.
+// grid, two CTAs an SM.
 // Kernel 2 moves the rows: the moves of all groups are one list, cut evenly
 // over the CTAs (a group's share differs by its length and its luck), sixteen
 // lanes a move, four moves in flight a thread.  Bound: the round trip of
@@ -38,8 +38,10 @@
 namespace mj {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;     // of the move kernel
 constexpr int kWarps = kThreads / 32;
+constexpr int kSelThreads = 512;  // of the selection
+constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxKeys = 49152;  // keys of a run in shared memory
@@ -89,7 +91,7 @@ __device__ __forceinline__ int warp_sum_before(int v, int lane, int& total) {
 
 struct Shared {
   int hist[2][kBins];
-  int warp_sums[kWarps];
+  int warp_sums[kSelWarps];
   int totals[4];  // holes, movers of this CTA
   uint32_t range[2];  // smallest key, largest unprotected key of this CTA
   uint32_t bin;
@@ -97,7 +99,7 @@ struct Shared {
   int bin_count;
 };
 
-__global__ void __launch_bounds__(kThreads, 4) evict_select_kernel(const EvictDev a, int cluster, int key_cap) {
+__global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const EvictDev a, int cluster, int key_cap) {
   // a programmatic dependent: no global access before the grid ahead is done
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
@@ -125,7 +127,7 @@ __global__ void __launch_bounds__(kThreads, 4) evict_select_kernel(const EvictDe
 
   if (L <= a.budget) {  // nothing leaves (uniform over the cluster)
     if (rank == 0 && tid == 0) a.counts[bg] = 0;
-    for (int i = tid; i < n; i += kThreads) {
+    for (int i = tid; i < n; i += kSelThreads) {
       const int j = begin + i;
       if (copy_acc) a.acc_out[off + j] = acc[j];
       if (copy_pos) a.key_pos_out[off + j] = pos[j];
@@ -158,18 +160,18 @@ __global__ void __launch_bounds__(kThreads, 4) evict_select_kernel(const EvictDe
     };
     const int quads = wide ? n / 4 : 0;
     constexpr int kBatch = 4;  // loads in flight a thread, before any of their stores
-    for (int v0 = tid; v0 < quads; v0 += kBatch * kThreads) {
+    for (int v0 = tid; v0 < quads; v0 += kBatch * kSelThreads) {
       float4 w[kBatch];
       int4 p[kBatch];
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        const int v = v0 + u * kThreads, j = begin + 4 * v;
+        const int v = v0 + u * kSelThreads, j = begin + 4 * v;
         if (v < quads) w[u] = *reinterpret_cast<const float4*>(acc + j);
         p[u] = pos && v < quads ? *reinterpret_cast<const int4*>(pos + j) : make_int4(j, j + 1, j + 2, j + 3);
       }
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        const int v = v0 + u * kThreads, j = begin + 4 * v;
+        const int v = v0 + u * kSelThreads, j = begin + 4 * v;
         if (v >= quads) break;
         take(4 * v, w[u].x, p[u].x);
         take(4 * v + 1, w[u].y, p[u].y);
@@ -190,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 4) evict_select_kernel(const EvictDe
         }
       }
     }
-    for (int i = 4 * quads + tid; i < n; i += kThreads) {
+    for (int i = 4 * quads + tid; i < n; i += kSelThreads) {
       const int j = begin + i;
       const float w = acc[j];
       const int p = pos ? pos[j] : j;
@@ -201,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 4) evict_select_kernel(const EvictDe
       }
     }
   }
-  for (int i = tid; i < 2 * kBins; i += kThreads) (&s.hist[0][0])[i] = 0;
+  for (int i = tid; i < 2 * kBins; i += kSelThreads) (&s.hist[0][0])[i] = 0;
   if (tid < 2) s.range[tid] = tid == 0 ? 0xFFFFFFFFu : 0u;
   __syncthreads();
   k_min = __reduce_min_sync(0xffffffffu, k_min);
@@ -238,13 +240,13 @@ __global__ void __launch_bounds__(kThreads, 4) evict_select_kernel(const EvictDe
     const int shift = left_bits;
     int* const hist = s.hist[pass & 1];
     if (pass == 2) {  // every CTA has read pass 0's counts (it passed pass 1's barrier)
-      for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
+      for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
       __syncthreads();
     }
     const uint32_t mask = (1u << width) - 1u;
     // (above = 32 only when every bit is left: then all keys match)
 #pragma unroll 8
-    for (int i = tid; i < n; i += kThreads) {
+    for (int i = tid; i < n; i += kSelThreads) {
       const uint32_t k = digits_of(key_of(i));
       if (pass == 0 || (k >> above) == (prefix >> above)) atomicAdd(&hist[(k >> shift) & mask], 1);
     }
@@ -252,49 +254,43 @@ __global__ void __launch_bounds__(kThreads, 4) evict_select_kernel(const EvictDe
       cluster_sync();
     else
       __syncthreads();
-    // every CTA sums the cluster's counts: thread t eight bins, the highest
+    // every CTA sums the cluster's counts: thread t four bins, the highest
     // first, so that a prefix sum over the threads counts the larger keys
-    const int q = kThreads - 1 - tid;
-    int c[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    const uint32_t mine = ptx::smem_u32(hist + 8 * q);
-    // (four CTAs' counts in flight, each CTA starting with its own: all reading
-    // one at a time would queue on that one's SM)
-    for (int r0 = 0; r0 < cluster; r0 += 4) {
-      int4 lo[4], hi[4];
+    const int q = kSelThreads - 1 - tid;
+    int4 v = *reinterpret_cast<const int4*>(hist + 4 * q);
+    int c[4] = {v.w, v.z, v.y, v.x};
+    if (cluster > 1) {
+      // (three other CTAs' counts in flight, each CTA going round from its own
+      // neighbour: all reading one at a time would queue on that one's SM)
+      const uint32_t mine = ptx::smem_u32(hist + 4 * q);
+      for (int r0 = 1; r0 < cluster; r0 += 3) {
+        int4 o[3];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const uint32_t at = map_rank(mine, (rank + r0 + u) & (cluster - 1));
-        lo[u] = ld_cluster_v4(at);
-        hi[u] = ld_cluster_v4(at + 16);
-      }
+        for (int u = 0; u < 3; ++u)
+          if (r0 + u < cluster) o[u] = ld_cluster_v4(map_rank(mine, (rank + r0 + u) & (cluster - 1)));
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if (r0 + u >= cluster) break;
-        c[0] += hi[u].w;
-        c[1] += hi[u].z;
-        c[2] += hi[u].y;
-        c[3] += hi[u].x;
-        c[4] += lo[u].w;
-        c[5] += lo[u].z;
-        c[6] += lo[u].y;
-        c[7] += lo[u].x;
+        for (int u = 0; u < 3; ++u) {
+          if (r0 + u >= cluster) break;
+          c[0] += o[u].w;
+          c[1] += o[u].z;
+          c[2] += o[u].y;
+          c[3] += o[u].x;
+        }
       }
     }
-    int sum = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) sum += c[e];
+    const int sum = c[0] + c[1] + c[2] + c[3];
     int total;
     int before = warp_sum_before(sum, lane, total);
     if (lane == 31) s.warp_sums[warp] = total;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) before += w < warp ? s.warp_sums[w] : 0;
+    for (int w = 0; w < kSelWarps; ++w) before += w < warp ? s.warp_sums[w] : 0;
     if (before < need && need <= before + sum) {  // one thread: the threshold's digit is among its bins
       int left = need - before;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
+      for (int e = 0; e < 4; ++e) {
         if (left > 0 && left <= c[e]) {
-          s.bin = 8 * q + 7 - e;
+          s.bin = 4 * q + 3 - e;
           s.need = left;
           s.bin_count = c[e];
         }
@@ -305,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 4) evict_select_kernel(const EvictDe
     prefix |= s.bin << shift;
     need = s.need;
   }
-  static_assert(kThreads * 8 == kBins, "eight bins a thread");
+  static_assert(kSelThreads * 4 == kBins, "four bins a thread");
   const int* const last_hist = s.hist[(passes - 1) & 1];
   const uint32_t last_bin = s.bin;
   // keys above the threshold are kept, and of the ties (equal to it) the
@@ -313,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 4) evict_select_kernel(const EvictDe
   const bool all_ties = s.bin_count == need;
   int tie_rank = 0;  // ties before this warp's rows
   const int rows = (n + 31) / 32;
-  const int rows_per_warp = (rows + kWarps - 1) / kWarps;
+  const int rows_per_warp = (rows + kSelWarps - 1) / kSelWarps;
   const int row0 = warp * rows_per_warp < rows ? warp * rows_per_warp : rows;
   const int row1 = row0 + rows_per_warp < rows ? row0 + rows_per_warp : rows;
   if (!all_ties) {
@@ -359,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 4) evict_select_kernel(const EvictDe
   if (lane == 0) s.warp_sums[warp] = n_holes | (n_movers << 16);
   __syncthreads();
   int hole_at = 0, mover_at = 0, cta_holes = 0, cta_movers = 0;
-  for (int w = 0; w < kWarps; ++w) {
+  for (int w = 0; w < kSelWarps; ++w) {
     const int v = s.warp_sums[w], h = v & 0xFFFF, m = v >> 16;
     if (w < warp) {
       hole_at += h;
@@ -532,10 +528,10 @@ __global__ void __launch_bounds__(kThreads, 4) evict_move_kernel(const EvictDev 
 cudaError_t launch_evict(const EvictDev& a, int sm_count, cudaStream_t stream) {
   const int64_t groups = static_cast<int64_t>(a.num_seqs) * a.h_k;
   const int64_t max_len = static_cast<int64_t>(a.max_blocks) * a.page_size;
-  // CTAs a group: enough to fill about one wave (four an SM), each with 2048
+  // CTAs a group: enough to fill about one wave (two an SM), each with 2048
   // slots or more
   int cluster = 1;
-  while (cluster < kMaxCluster && groups * cluster * 2 <= sm_count * 4 && max_len / (cluster * 2) >= 2048) cluster *= 2;
+  while (cluster < kMaxCluster && groups * cluster * 2 <= sm_count * 2 && max_len / (cluster * 2) >= 2048) cluster *= 2;
   // keys in shared memory when a run fits beside the histograms (else they
   // are made again from the weights, in L2, by every pass)
   const int64_t run = (max_len + cluster - 1) / cluster + 32;
@@ -544,7 +540,7 @@ cudaError_t launch_evict(const EvictDev& a, int sm_count, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(groups * cluster), 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.blockDim = dim3(kSelThreads, 1, 1);
   cfg.dynamicSmemBytes = static_cast<size_t>(key_cap) * 4;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];

@@ -27,7 +27,8 @@
 // grid, two CTAs an SM.
 // Kernel 2 moves the rows: the moves of all groups are one list, cut evenly
 // over the CTAs (a group's share differs by its length and its luck), sixteen
-// lanes a move, four moves in flight a thread.  Bound: the round trip of
+// lanes a move, two in flight a thread (GB300: 86 us for the whole call on a
+// decode batch; one in flight 95, four 90, eight 87).  Bound: the round trip of
 // dependent loads (list, then rows at random places), so bytes in flight.
 
 #include <cuda_runtime.h>
@@ -457,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 4) evict_move_kernel(const EvictDev 
   const int page_mask = a.page_size - 1;       // 16, 32, 64 or 128 rows
   const int64_t page_step = is_v ? a.v_page : a.k_page, row_step = is_v ? a.v_row : a.k_row;
   const bool has_word = l16 == 0 || (l16 == 1 && a.key_pos);
-  constexpr int kUnroll = 4;
+  constexpr int kUnroll = 2;
   constexpr int step = kThreads / 16;
   int64_t at = first, group_begin = s_before;
   for (int bg = s_group; at < last; ++bg) {

@@ -8,19 +8,25 @@
 // thread-local, and one coalesced 4-byte store a key is all that leaves.  The
 // logits and the row sums are fp32; bf16 Q is split into hi + lo e4m3 parts
 // as in the decode kernels (exact down to 2^-10 of the scaled row maximum).
-// With lse known there is no running maximum and nothing to merge between the
-// plan's items.
+// With lse known there is no running maximum and nothing to merge, so the
+// plan's items are only a list of tiles: it is cut evenly, whatever the items'
+// lengths, into shares for which every kv head has a resident CTA, and a CTA
+// walks its share as segments of one item each, the K ring running on across
+// them.  The heads' CTAs of a share go over the same pages side by side: their
+// rows of a token are neighbours, and the loads' 256-byte L2 sectors serve two
+// of them (shares cut across the heads read a quarter more from HBM).
 //
 // Bound: 128 bytes of K a key and head against one exponential per row and
-// key: HBM up to about 80 rows, the exponential units above.  256 packed rows
-// a launch (TMEM holds two buffers of 256 columns); more rows are further
-// launches that add on, in order.
+// key: HBM up to about 64 rows, the exponential units and the MMA above.  256
+// packed rows a launch (TMEM holds two buffers of 256 columns); more rows are
+// further launches that add on, in order.
 //
 // Roles (320 threads): warp 0 issues the K tiles into a ring, warp 1 (TMEM
-// allocator) the MMAs, warps 2-5 and 6-9 take alternate tiles.  Up to 128
-// rows two CTAs fit an SM, one's start and end under the other's stream.
-// Tiles that no row sees (a window, documents) are neither loaded nor
-// multiplied; their weights only decay.
+// allocator) the MMAs, warps 2-5 and 6-9 take alternate tiles.  Up to 64 rows
+// two CTAs fit an SM, one's segment starts under the other's stream.  Q parts
+// and row constants are double-buffered over segments.  Tiles that no row sees
+// (a window, documents) are neither loaded nor multiplied; their weights only
+// decay.
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -37,9 +43,9 @@ constexpr int kTileBytes = kKeys * 128;      // 16 KB
 constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s: far above any legal wait
 constexpr int kStatusTimeout = 5;            // MJ_ERR_TIMEOUT
 constexpr int kThreads = 64 + 256;
-constexpr int kMaxRows = 256;
 constexpr int kMaxStages = 8;
 constexpr int kBarCons = 1;  // named barrier of the 256 consumer threads
+constexpr int kTwoCtaRows = 64;  // rows up to which two CTAs share an SM
 
 struct KwArgs {
   DecodeModDev d;
@@ -48,8 +54,8 @@ struct KwArgs {
   int64_t acc_seq, acc_head;
   float decay;
   int32_t fresh;
-  int32_t n0, n_rows;   // packed rows of this launch
-  int32_t n_mma;        // n_rows rounded up to 16: the MMA's N
+  int32_t n0, n_rows;  // packed rows of this launch
+  int32_t n_mma;       // n_rows rounded up to 16: the MMA's N
   int32_t stages;
   int32_t tmem_cols;
   int32_t off_q, off_row, off_bar;  // shared memory, from the 1 KB boundary
@@ -63,6 +69,87 @@ __device__ __forceinline__ void set_abort(volatile int* abort, int32_t* status) 
 // 128-byte-swizzled K-major row: 16-byte chunk cc of row r at cc ^ (r % 8)
 __device__ __forceinline__ uint8_t* swz(uint8_t* part, int r, int cc) { return part + r * 128 + ((cc ^ (r & 7)) << 4); }
 
+// The CTA's share as segments: tiles [t0, t1) of sequence b, of the CTA's head.
+struct Segment {
+  int t0, t1, b;
+};
+struct Walk {
+  const int4* work;
+  int num_work;
+  int w, t;      // where the next segment starts
+  int64_t left;  // tiles of the share still to come
+  __device__ __forceinline__ bool next(Segment& s) {
+    while (left > 0 && w < num_work) {
+      const int4 item = work[w];
+      const int tiles = item.z - item.y;
+      if (t >= tiles) {
+        t = 0;
+        ++w;
+        continue;
+      }
+      const int n = tiles - t < left ? tiles - t : static_cast<int>(left);
+      s = Segment{item.y + t, item.y + t + n, item.x};
+      t += n;
+      left -= n;
+      return true;
+    }
+    return false;
+  }
+};
+
+// Ranges of the launch's rows of one sequence, over a warp (identical in every
+// warp): the smallest and largest first and last keys, and the prefix.
+struct Limits {
+  int lo_min, lo_max, hi_min, hi_max, pfx;
+  // some row sees a key of the tile
+  __device__ __forceinline__ bool seen(int key0) const {
+    return key0 < pfx || (key0 <= hi_max && key0 + kKeys - 1 >= lo_min);
+  }
+  // one of the tiles [t0, t1) is seen
+  __device__ __forceinline__ bool any(int t0, int t1) const {
+    if (t0 * kKeys < pfx) return true;
+    if (hi_max < 0) return false;
+    const int from = lo_min / kKeys > t0 ? lo_min / kKeys : t0, to = hi_max / kKeys < t1 - 1 ? hi_max / kKeys : t1 - 1;
+    return from <= to;
+  }
+  // every row sees every key of the tile
+  __device__ __forceinline__ bool whole(int key0) const {
+    return key0 + kKeys <= pfx || (key0 >= lo_max && key0 + kKeys - 1 <= hi_min);
+  }
+};
+template <bool kMod>
+__device__ __forceinline__ Limits warp_limits(const KwArgs& p, int b, int L, int lane) {
+  const DecodeModDev& a = p.d;
+  const int q0 = p.n0 / a.h_r, q1 = (p.n0 + p.n_rows - 1) / a.h_r;
+  Limits m;
+  if constexpr (!kMod) {
+    const int first = L - a.q_len + q0, last = L - a.q_len + q1;
+    m.lo_min = m.lo_max = 0;
+    m.hi_min = a.causal && first < L - 1 ? first : L - 1;
+    m.hi_max = a.causal && last < L - 1 ? last : L - 1;
+    m.pfx = 0;
+  } else {
+    int lo_min = INT32_MAX, lo_max = -1, hi_min = INT32_MAX, hi_max = -1;
+    m.pfx = 0;
+    for (int qi = q0 + lane; qi <= q1; qi += 32) {
+      const RowRange r = row_range(a.mod, a.causal, a.q_len, b, L, qi);
+      m.pfx = r.pfx;
+      lo_max = r.lo > lo_max ? r.lo : lo_max;
+      hi_min = r.hi < hi_min ? r.hi : hi_min;
+      if (r.lo <= r.hi) {
+        lo_min = r.lo < lo_min ? r.lo : lo_min;
+        hi_max = r.hi > hi_max ? r.hi : hi_max;
+      }
+    }
+    m.lo_min = __reduce_min_sync(0xffffffffu, lo_min);
+    m.lo_max = __reduce_max_sync(0xffffffffu, lo_max);
+    m.hi_min = __reduce_min_sync(0xffffffffu, hi_min);
+    m.hi_max = __reduce_max_sync(0xffffffffu, hi_max);
+    m.pfx = __reduce_max_sync(0xffffffffu, m.pfx);
+  }
+  return m;
+}
+
 template <bool kQe4m3, bool kMod>
 __global__ void __launch_bounds__(kThreads, 2)
     key_weights_kernel(const __grid_constant__ KwArgs p, const __grid_constant__ CUtensorMap tmap_k) {
@@ -73,104 +160,99 @@ __global__ void __launch_bounds__(kThreads, 2)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = ptx::smem_u32(sm);
-  // per-row constants, [kMaxRows] each
-  float* const row_lse2 = reinterpret_cast<float*>(sm + p.off_row);
-  int* const row_hi = reinterpret_cast<int*>(row_lse2 + kMaxRows);
-  int* const row_lo = row_hi + kMaxRows;
-  float* const row_slope2 = reinterpret_cast<float*>(row_lo + kMaxRows);
-  float* const row_pos = row_slope2 + kMaxRows;
+  // per-row constants of a segment, two buffers of [5][n_mma]
+  float* const row_base = reinterpret_cast<float*>(sm + p.off_row);
   uint8_t* const misc = sm + p.off_bar + 8 * (2 * kMaxStages + 8);
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(misc);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(misc + 4);
-  int* const lim = reinterpret_cast<int*>(misc + 8);  // lo_min, lo_max, hi_min, hi_max over the rows
-  float* const amax_red = reinterpret_cast<float*>(misc + 32);  // [8]
+  float* const amax_red = reinterpret_cast<float*>(misc + 32);      // [8]
+  int64_t* const scan_red = reinterpret_cast<int64_t*>(misc + 64);  // [10]
+  int* const walk_s = reinterpret_cast<int*>(misc + 160);           // w, t of the share's first tile
 
   const uint32_t bar0 = sbase + p.off_bar;
   auto kfull = [&](int s) { return bar0 + 8u * s; };
   auto kempty = [&](int s) { return bar0 + 8u * (kMaxStages + s); };
   auto sfull = [&](int wg) { return bar0 + 8u * (2 * kMaxStages + wg); };
   auto sfree = [&](int wg) { return bar0 + 8u * (2 * kMaxStages + 2 + wg); };
-  const uint32_t qready = bar0 + 8u * (2 * kMaxStages + 4);
-  const uint32_t drain = qready + 8u;
+  auto qready = [&](int s) { return bar0 + 8u * (2 * kMaxStages + 4 + s); };
+  const uint32_t drain = bar0 + 8u * (2 * kMaxStages + 6);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int g = blockIdx.x % a.h_k;
-  const int4 item = reinterpret_cast<const int4*>(a.work)[blockIdx.x / a.h_k];
-  const int b = item.x, t_begin = item.y, t_end = item.z;
-  if (t_end <= t_begin) return;  // padding item
-  int L = a.seq_lens[b];
-  L = L < a.max_blocks * a.page_size ? L : a.max_blocks * a.page_size;  // acc has no more slots
-  const int T = t_end - t_begin;
   const int stages = p.stages;
+  const int4* const work = reinterpret_cast<const int4*>(a.work);
 
   if (tid == 0) {
     for (int s = 0; s < stages; ++s) {
       ptx::mbar_init(kfull(s), 1);
       ptx::mbar_init(kempty(s), 1);
     }
-    for (int wg = 0; wg < 2; ++wg) {
-      ptx::mbar_init(sfull(wg), 1);
-      ptx::mbar_init(sfree(wg), 4);
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(sfull(i), 1);
+      ptx::mbar_init(sfree(i), 4);
+      ptx::mbar_init(qready(i), 1);
     }
-    ptx::mbar_init(qready, 1);
     ptx::mbar_init(drain, 1);
     *abort_flag = 0;
-    lim[0] = INT32_MAX;
-    lim[1] = -1;
-    lim[2] = INT32_MAX;
-    lim[3] = -1;
     ptx::fence_mbar_init();
   }
-  __syncthreads();
+  // ---- this CTA's share: tiles [first, last) of the items' tiles in order,
+  // for one kv head; the CTAs of the other heads' shares run beside it
+  const int g = blockIdx.x % a.h_k;
+  int64_t first, last;
+  {
+    const int per = (a.num_work + kThreads - 1) / kThreads;
+    const int w0 = tid * per < a.num_work ? tid * per : a.num_work;
+    const int w1 = w0 + per < a.num_work ? w0 + per : a.num_work;
+    int64_t mine = 0;
+    for (int w = w0; w < w1; ++w) {
+      const int4 item = work[w];
+      mine += item.z > item.y ? item.z - item.y : 0;
+    }
+    int64_t x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) scan_red[warp] = x;
+    __syncthreads();
+    int64_t before = x - mine, total = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      before += w < warp ? scan_red[w] : 0;
+      total += scan_red[w];
+    }
+    const int shares = gridDim.x / a.h_k, share = blockIdx.x / a.h_k;
+    first = total * share / shares;
+    last = total * (share + 1) / shares;
+    if (before <= first && first < before + mine) {  // one thread: where the share starts
+      for (int w = w0;; ++w) {
+        const int4 item = work[w];
+        const int64_t tiles = item.z > item.y ? item.z - item.y : 0;
+        if (first < before + tiles) {
+          walk_s[0] = w;
+          walk_s[1] = static_cast<int>(first - before);
+          break;
+        }
+        before += tiles;
+      }
+    }
+  }
+  if (first == last) return;  // nothing to do (uniform over the CTA, before TMEM)
   if (warp == 1) {
     ptx::tmem_alloc(ptx::smem_u32(tmem_slot), p.tmem_cols);
     ptx::tmem_relinquish();
-  }
-  // the rows' ranges: thread r is row r
-  int pfx = 0;
-  if (kMod && a.mod.prefix) {
-    pfx = a.mod.prefix[b];
-    pfx = pfx < 0 ? 0 : (pfx > L ? L : pfx);
-  }
-  if (tid < kMaxRows) {
-    const int n = p.n0 + tid;
-    const bool live = tid < p.n_rows;
-    float lse2 = INFINITY, slope2 = 0.f;
-    int lo = 0, hi = -1, pos = 0;
-    if (live) {
-      const int qi = n / a.h_r;
-      pos = L - a.q_len + qi;
-      if constexpr (kMod) {
-        const RowRange r = row_range(a.mod, a.causal, a.q_len, b, L, qi);
-        lo = r.lo;
-        hi = r.hi;
-        if (a.mod.slopes) slope2 = a.mod.slopes[g * a.h_r + n % a.h_r] * kLog2e;
-      } else {
-        hi = a.causal && pos < L - 1 ? pos : L - 1;
-      }
-      const float lse = p.lse[(static_cast<int64_t>(b) * a.h_k + g) * a.n_q + n];
-      lse2 = lse == -INFINITY ? INFINITY : lse * kLog2e;  // a row without keys adds nothing
-      atomicMin(&lim[0], lo <= hi ? lo : INT32_MAX);
-      atomicMax(&lim[1], lo);
-      atomicMin(&lim[2], hi);
-      atomicMax(&lim[3], lo <= hi ? hi : -1);
-    }
-    row_lse2[tid] = lse2;
-    row_hi[tid] = hi;
-    row_lo[tid] = lo;
-    row_slope2[tid] = slope2;
-    row_pos[tid] = static_cast<float>(pos);
   }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int lo_min = lim[0], lo_max = lim[1], hi_min = lim[2], hi_max = lim[3];
-  auto key_of_tile = [&](int i) { return (t_begin + i) * kKeys; };
-  // a tile some row sees (every role walks the same list)
-  auto seen = [&](int i) {
-    const int k0 = key_of_tile(i);
-    return k0 < pfx || (k0 <= hi_max && k0 + kKeys - 1 >= lo_min);
+  Walk walk{work, a.num_work, walk_s[0], walk_s[1], last - first};
+  Segment sg;
+  const int max_len = a.max_blocks * a.page_size;  // acc has no more slots
+  auto length_of = [&](int b) {
+    const int L = a.seq_lens[b];
+    return L < max_len ? L : max_len;
   };
 
   if (warp == 0) {
@@ -179,47 +261,53 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int box_rows = PS < kKeys ? PS : kKeys;
     const int nbox = kKeys / box_rows;
     const bool active = lane < nbox;
-    const int64_t bt_row = static_cast<int64_t>(b) * a.max_blocks;
-    int valid_pages = (L + PS - 1) / PS;
-    valid_pages = valid_pages < a.max_blocks ? valid_pages : a.max_blocks;
     if (lane == 0) ptx::prefetch_tmap(&tmap_k);
     const bool evict_first = a.kv_evict_first != 0;
     const uint64_t policy = ptx::policy_evict_first();
     const uint32_t tile_tx = kv_box_bytes(a.kv_format, kKeys);
-    // block-table entries from a register window (lane l: block wbase + l),
-    // the next 32 one refill ahead
-    auto load_win = [&](int base) -> int {
-      const int blk = base + lane;
-      return blk < valid_pages ? a.block_table[bt_row + blk] : a.num_pages;
-    };
-    int wbase = key_of_tile(0) / PS;
-    int win = load_win(wbase), win_next = load_win(wbase + 32);
-    int u = 0;
-    for (int i = 0; i < T; ++i) {
-      const int key0 = key_of_tile(i);
-      if (key0 / PS >= wbase + 32) {
-        wbase += 32;
-        win = win_next;
-        win_next = load_win(wbase + 32);
-      }
-      if (!seen(i)) continue;
-      const int st = u % stages;
-      if (u >= stages) {
-        const bool freed = ptx::mbar_wait_bounded(kempty(st), ((u / stages) - 1) & 1, abort_flag, kWaitNs);
-        if (__any_sync(0xffffffffu, !freed)) {
-          if (lane == 0) set_abort(abort_flag, a.status);
-          break;
+    int u = 0;  // tiles issued
+    bool ok = true;
+    while (ok && walk.next(sg)) {
+      const int L = length_of(sg.b);
+      const Limits lim = warp_limits<kMod>(p, sg.b, L, lane);
+      const int64_t bt_row = static_cast<int64_t>(sg.b) * a.max_blocks;
+      int valid_pages = (L + PS - 1) / PS;
+      valid_pages = valid_pages < a.max_blocks ? valid_pages : a.max_blocks;
+      // block-table entries from a register window (lane l: block wbase + l),
+      // the next 32 one refill ahead
+      auto load_win = [&](int base) -> int {
+        const int blk = base + lane;
+        return blk < valid_pages ? a.block_table[bt_row + blk] : a.num_pages;
+      };
+      int wbase = sg.t0 * kKeys / PS;
+      int win = load_win(wbase), win_next = load_win(wbase + 32);
+      for (int t = sg.t0; t < sg.t1; ++t) {
+        const int key0 = t * kKeys;
+        if (key0 / PS >= wbase + 32) {
+          wbase += 32;
+          win = win_next;
+          win_next = load_win(wbase + 32);
         }
+        if (!lim.seen(key0)) continue;
+        const int st = u % stages;
+        if (u >= stages) {
+          const bool freed = ptx::mbar_wait_bounded(kempty(st), ((u / stages) - 1) & 1, abort_flag, kWaitNs);
+          if (__any_sync(0xffffffffu, !freed)) {
+            if (lane == 0) set_abort(abort_flag, a.status);
+            ok = false;
+            break;
+          }
+        }
+        const int key = key0 + lane * box_rows;
+        const int pg = __shfl_sync(0xffffffffu, win, (key / PS - wbase) & 31);
+        const int page = (active && key < L) ? pg : a.num_pages;  // out of bounds: zeros
+        if (lane == 0) ptx::mbar_arrive_expect_tx(kfull(st), tile_tx);
+        __syncwarp();
+        if (active)
+          ptx::tma_load_kv(sbase + st * kTileBytes + lane * box_rows * 128, &tmap_k, kfull(st), 0, key % PS, g, page,
+                           evict_first, policy);
+        ++u;
       }
-      const int key = key0 + lane * box_rows;
-      const int pg = __shfl_sync(0xffffffffu, win, (key / PS - wbase) & 31);
-      const int page = (active && key < L) ? pg : a.num_pages;  // out of bounds: zeros
-      if (lane == 0) ptx::mbar_arrive_expect_tx(kfull(st), tile_tx);
-      __syncwarp();
-      if (active)
-        ptx::tma_load_kv(sbase + st * kTileBytes + lane * box_rows * 128, &tmap_k, kfull(st), 0, key % PS, g, page,
-                         evict_first, policy);
-      ++u;
     }
     if (*abort_flag && lane == 0) {  // leave no copy in flight
       volatile int never = 0;
@@ -228,34 +316,45 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   } else if (warp == 1) {
     // --------------------------------------------------------------- MMA
-    if (lane == 0) {
-      bool ok = ptx::mbar_wait_bounded(qready, 0, abort_flag, kWaitNs);
-      const uint32_t idesc = ptx::idesc_f8f6f4(kKeys, p.n_mma, false, false, kv_mma_format(a.kv_format), 0);
-      const uint64_t kdesc0 = ptx::smem_desc(sbase, 16, 1024, ptx::kSwizzle128B);
-      const uint64_t qdesc = ptx::smem_desc(sbase + p.off_q, 16, 1024, ptx::kSwizzle128B);
-      const uint64_t part_step = static_cast<uint64_t>(p.n_mma * 128) >> 4;
-      int u = 0;
-      for (int i = 0; ok && i < T; ++i) {
-        if (!seen(i)) continue;
-        const int st = u % stages, wg = u & 1, t = u >> 1;
-        if (!ptx::mbar_wait_bounded(kfull(st), (u / stages) & 1, abort_flag, kWaitNs) ||
-            (t >= 1 && !ptx::mbar_wait_bounded(sfree(wg), (t - 1) & 1, abort_flag, kWaitNs))) {
-          ok = false;
-          break;
-        }
-        ptx::tc_fence_after();
-        const uint64_t kdesc = kdesc0 + static_cast<uint64_t>((st * kTileBytes) >> 4);
-        const uint32_t d = tmem + wg * (p.tmem_cols >> 1);
+    // (the whole warp walks and takes the limits; lane 0 waits and issues)
+    const uint32_t idesc = ptx::idesc_f8f6f4(kKeys, p.n_mma, false, false, kv_mma_format(a.kv_format), 0);
+    const uint64_t kdesc0 = ptx::smem_desc(sbase, 16, 1024, ptx::kSwizzle128B);
+    const uint64_t part_step = static_cast<uint64_t>(p.n_mma * 128) >> 4;
+    int u = 0, s = 0;  // tiles, segments with a seen tile (only those have a Q buffer)
+    bool ok = true;
+    while (ok && walk.next(sg)) {
+      const Limits lim = warp_limits<kMod>(p, sg.b, length_of(sg.b), lane);
+      if (!lim.any(sg.t0, sg.t1)) continue;
+      const uint64_t qdesc =
+          ptx::smem_desc(sbase + p.off_q + (s & 1) * p.n_mma * 128 * kParts, 16, 1024, ptx::kSwizzle128B);
+      if (lane == 0) {
+        ok = ptx::mbar_wait_bounded(qready(s & 1), (s >> 1) & 1, abort_flag, kWaitNs);
+        for (int t = sg.t0; ok && t < sg.t1; ++t) {
+          if (!lim.seen(t * kKeys)) continue;
+          const int st = u % stages, wg = u & 1, n = u >> 1;
+          if (!ptx::mbar_wait_bounded(kfull(st), (u / stages) & 1, abort_flag, kWaitNs) ||
+              (n >= 1 && !ptx::mbar_wait_bounded(sfree(wg), (n - 1) & 1, abort_flag, kWaitNs))) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+          const uint64_t kdesc = kdesc0 + static_cast<uint64_t>((st * kTileBytes) >> 4);
+          const uint32_t d = tmem + wg * (p.tmem_cols >> 1);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
+          for (int kk = 0; kk < 4; ++kk) {
 #pragma unroll
-          for (int part = 0; part < kParts; ++part)
-            ptx::mma_e4m3(d, kdesc + 2 * kk, qdesc + part * part_step + 2 * kk, idesc, (kk > 0 || part > 0) ? 1u : 0u);
+            for (int part = 0; part < kParts; ++part)
+              ptx::mma_e4m3(d, kdesc + 2 * kk, qdesc + part * part_step + 2 * kk, idesc, (kk > 0 || part > 0) ? 1u : 0u);
+          }
+          ptx::mma_commit(sfull(wg));
+          ptx::mma_commit(kempty(st));
+          ++u;
         }
-        ptx::mma_commit(sfull(wg));
-        ptx::mma_commit(kempty(st));
-        ++u;
       }
+      ++s;
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+    }
+    if (lane == 0) {
       if (!ok) set_abort(abort_flag, a.status);
       ptx::mma_commit(drain);
       volatile int never = 0;
@@ -263,146 +362,222 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   } else {
     // ----------------------------------------------------------- weights
-    const int ct = tid - 64;  // consumer thread = Q row to lay out
+    const int ct = tid - 64;  // consumer thread
     const int wg = ct >> 7, quarter = warp & 3;
     const int key_in_tile = quarter * 32 + lane;
-    const float kd = a.kd[b * a.kd_seq + g * a.kd_head];
-    const float qd = a.qd[b * a.qd_seq + g * a.qd_head];
-
-    // ---- Q row -> one (e4m3) or two (bf16: hi + lo) operand rows
-    uint8_t* const qbase = sm + p.off_q;
-    const bool live = ct < p.n_rows;
-    const int64_t qoff = b * a.q_seq + (static_cast<int64_t>(g) * a.n_q + p.n0 + (live ? ct : 0)) * kHeadDimDev;
-    int shift = 0;
-    if constexpr (kQe4m3) {
-      if (ct < p.n_mma) {
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.q) + qoff);
-#pragma unroll
-        for (int cc = 0; cc < 8; ++cc)
-          *reinterpret_cast<uint4*>(swz(qbase, ct, cc)) = live ? src[cc] : make_uint4(0u, 0u, 0u, 0u);
-      }
-    } else {
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + qoff);
-      uint4 raw[16];
-      uint32_t mbits = 0;
-#pragma unroll
-      for (int w = 0; w < 16; ++w) {
-        raw[w] = live ? src[w] : make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t v4[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) mbits = max(mbits, max(v4[e] & 0x7FFFu, (v4[e] >> 16) & 0x7FFFu));
-      }
-      float amax = __uint_as_float(mbits << 16);
-#pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      if (lane == 0) amax_red[warp - 2] = amax;
-      ptx::named_bar_sync(kBarCons, 256);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, amax_red[i]);
-      if (amax > 0.f) {
-        const int e = static_cast<int>((__float_as_uint(amax) >> 23) & 0xFF) - 127;
-        shift = 7 - e;  // max |q| 2^shift in [128, 256)
-        shift = shift > 126 ? 126 : (shift < -126 ? -126 : shift);
-      }
-      const float qscale = ldexpf(1.f, shift);
-      if (ct < p.n_mma) {
-#pragma unroll
-        for (int cc = 0; cc < 8; ++cc) {
-          uint32_t hw[4], lw[4];
-          const uint32_t w8[8] = {raw[2 * cc].x,     raw[2 * cc].y,     raw[2 * cc].z,     raw[2 * cc].w,
-                                  raw[2 * cc + 1].x, raw[2 * cc + 1].y, raw[2 * cc + 1].z, raw[2 * cc + 1].w};
-#pragma unroll
-          for (int wi = 0; wi < 4; ++wi) {
-            float x[4], hf[4];
-            x[0] = __uint_as_float(w8[2 * wi] << 16) * qscale;
-            x[1] = __uint_as_float(w8[2 * wi] & 0xFFFF0000u) * qscale;
-            x[2] = __uint_as_float(w8[2 * wi + 1] << 16) * qscale;
-            x[3] = __uint_as_float(w8[2 * wi + 1] & 0xFFFF0000u) * qscale;
-            const uint16_t h01 = ptx::f32x2_to_e4m3x2(x[0], x[1]);
-            const uint16_t h23 = ptx::f32x2_to_e4m3x2(x[2], x[3]);
-            hw[wi] = static_cast<uint32_t>(h01) | (static_cast<uint32_t>(h23) << 16);
-            e4m3x4_to_f32(hw[wi], hf);
-            const uint16_t l01 = ptx::f32x2_to_e4m3x2(x[0] - hf[0], x[1] - hf[1]);
-            const uint16_t l23 = ptx::f32x2_to_e4m3x2(x[2] - hf[2], x[3] - hf[3]);
-            lw[wi] = static_cast<uint32_t>(l01) | (static_cast<uint32_t>(l23) << 16);
-          }
-          *reinterpret_cast<uint4*>(swz(qbase, ct, cc)) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-          *reinterpret_cast<uint4*>(swz(qbase + p.n_mma * 128, ct, cc)) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
-        }
-      }
-    }
-    ptx::fence_proxy_async_smem();
-    ptx::named_bar_sync(kBarCons, 256);
-    if (ct == 0) ptx::mbar_arrive(qready);
-
-    const float to_logit = a.softmax_scale * qd * kd * ldexpf(1.f, -shift);
-    const float cap2 = kMod ? a.mod.softcap * kLog2e : 0.f;
-    const float c1 = kMod && a.mod.softcap > 0.f ? to_logit / a.mod.softcap : to_logit * kLog2e;
     const uint32_t tmem_s = tmem + wg * (p.tmem_cols >> 1) + (static_cast<uint32_t>(quarter * 32) << 16);
-    float* const acc = p.acc + b * p.acc_seq + g * p.acc_head;
-    int u = 0;
-    for (int i = 0; i < T; ++i) {
-      const int key0 = key_of_tile(i);
-      const int key = key0 + key_in_tile;
-      const bool is_seen = seen(i);
-      if (is_seen ? (u & 1) != wg : (i & 1) != wg) {  // the other group's tile
-        u += is_seen;
-        continue;
-      }
-      const bool reads = key < L - p.fresh && p.decay > 0.f;
-      float sum = 0.f;
-      const float old = reads ? acc[key] : 0.f;
-      if (is_seen) {
-        const int t = u >> 1;
-        ++u;
-        if (!ptx::mbar_wait_bounded(sfull(wg), t & 1, abort_flag, kWaitNs)) set_abort(abort_flag, a.status);
-        ptx::tc_fence_after();
-        const bool unmasked =
-            key0 + kKeys <= pfx || (key0 >= lo_max && key0 + kKeys - 1 <= hi_min);  // uniform over the CTA
-        const float fkey = static_cast<float>(key);
-        for (int c0 = 0; c0 < p.n_mma; c0 += 16) {
-          uint32_t r[16];
-          MJ_TMEM_LD16(tmem_s + c0, r);
-          ptx::tmem_ld_wait();
-          if (c0 + 16 >= p.n_mma) {  // read whole: the next MMA may overwrite it
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(sfree(wg));
-          }
-          float y[16];
+    const float cap2 = kMod ? a.mod.softcap * kLog2e : 0.f;
+    const float2 cap22 = make_float2(cap2, cap2);
+    int u = 0, s = 0;
+    while (walk.next(sg)) {
+      const int b = sg.b;
+      const int L = length_of(b);
+      const Limits lim = warp_limits<kMod>(p, b, L, lane);
+      const float kd = a.kd[b * a.kd_seq + g * a.kd_head];
+      const float qd = a.qd[b * a.qd_seq + g * a.qd_head];
+      float* const row_nlse2 = row_base + (s & 1) * 5 * p.n_mma;  // -lse in log2 units
+      float* const row_slope2 = row_nlse2 + p.n_mma;
+      float* const row_pos = row_slope2 + p.n_mma;
+      int* const row_lo = reinterpret_cast<int*>(row_pos + p.n_mma);
+      int* const row_hi = row_lo + p.n_mma;
+      uint8_t* const qbase = sm + p.off_q + (s & 1) * p.n_mma * 128 * kParts;
+
+      int shift = 0;
+      // ---- Q rows -> one (e4m3) or two (bf16: hi + lo) operand rows, a
+      // 16-element chunk a thread and round
+      if (lim.any(sg.t0, sg.t1)) {
+        const int64_t q_at = b * a.q_seq + (static_cast<int64_t>(g) * a.n_q + p.n0) * kHeadDimDev;
+        const int chunks = p.n_mma * 8;
+        if constexpr (!kQe4m3) {
+          uint32_t mbits = 0;  // bf16 |q| maximum: integer maximum of the magnitude bits
+          for (int id = ct; id < p.n_rows * 8; id += 256) {
+            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + q_at + id * 16);
+            const uint4 r0 = src[0], r1 = src[1];
+            const uint32_t v8[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
 #pragma unroll
-          for (int e = 0; e < 16; ++e) y[e] = __uint_as_float(r[e]) * c1;
-          if constexpr (kMod) {
-            if (cap2 > 0.f) {
+            for (int e = 0; e < 8; ++e) mbits = max(mbits, max(v8[e] & 0x7FFFu, (v8[e] >> 16) & 0x7FFFu));
+          }
+          mbits = __reduce_max_sync(0xffffffffu, mbits);
+          if (lane == 0) amax_red[warp - 2] = __uint_as_float(mbits << 16);
+        }
+        // (also: both groups are done with the segment before, so this one's
+        // buffers, used two segments ago, are free)
+        ptx::named_bar_sync(kBarCons, 256);
+        if constexpr (!kQe4m3) {
+          float amax = 0.f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) amax = fmaxf(amax, amax_red[i]);
+          if (amax > 0.f) {
+            const int e = static_cast<int>((__float_as_uint(amax) >> 23) & 0xFF) - 127;
+            shift = 7 - e;  // max |q| 2^shift in [128, 256)
+            shift = shift > 126 ? 126 : (shift < -126 ? -126 : shift);
+          }
+        }
+        const float qscale = ldexpf(1.f, shift);
+        for (int id = ct; id < chunks; id += 256) {
+          const int r = id >> 3, cc = id & 7;
+          const bool live = r < p.n_rows;
+          if constexpr (kQe4m3) {
+            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.q) + q_at + id * 16);
+            *reinterpret_cast<uint4*>(swz(qbase, r, cc)) = live ? *src : make_uint4(0u, 0u, 0u, 0u);
+          } else {
+            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + q_at + id * 16);
+            const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+            const uint4 r0 = live ? src[0] : z, r1 = live ? src[1] : z;
+            const uint32_t w8[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
+            uint32_t hw[4], lw[4];
+#pragma unroll
+            for (int wi = 0; wi < 4; ++wi) {
+              float x[4], hf[4];
+              x[0] = __uint_as_float(w8[2 * wi] << 16) * qscale;
+              x[1] = __uint_as_float(w8[2 * wi] & 0xFFFF0000u) * qscale;
+              x[2] = __uint_as_float(w8[2 * wi + 1] << 16) * qscale;
+              x[3] = __uint_as_float(w8[2 * wi + 1] & 0xFFFF0000u) * qscale;
+              const uint16_t h01 = ptx::f32x2_to_e4m3x2(x[0], x[1]);
+              const uint16_t h23 = ptx::f32x2_to_e4m3x2(x[2], x[3]);
+              hw[wi] = static_cast<uint32_t>(h01) | (static_cast<uint32_t>(h23) << 16);
+              e4m3x4_to_f32(hw[wi], hf);
+              const uint16_t l01 = ptx::f32x2_to_e4m3x2(x[0] - hf[0], x[1] - hf[1]);
+              const uint16_t l23 = ptx::f32x2_to_e4m3x2(x[2] - hf[2], x[3] - hf[3]);
+              lw[wi] = static_cast<uint32_t>(l01) | (static_cast<uint32_t>(l23) << 16);
+            }
+            *reinterpret_cast<uint4*>(swz(qbase, r, cc)) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+            *reinterpret_cast<uint4*>(swz(qbase + p.n_mma * 128, r, cc)) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+          }
+        }
+        // ---- the rows' constants; a row past n_rows or without keys adds
+        // 2^-inf (its scores are finite: Q's rows are zeros or data)
+        if (ct < p.n_mma) {
+          const int n = p.n0 + ct;
+          float nlse2 = -INFINITY, slope2 = 0.f;
+          int lo = 0, hi = -1, pos = 0;
+          if (ct < p.n_rows) {
+            const int qi = n / a.h_r;
+            pos = L - a.q_len + qi;
+            if constexpr (kMod) {
+              const RowRange r = row_range(a.mod, a.causal, a.q_len, b, L, qi);
+              lo = r.lo;
+              hi = r.hi;
+              if (a.mod.slopes) slope2 = a.mod.slopes[g * a.h_r + n % a.h_r] * kLog2e;
+            } else {
+              hi = a.causal && pos < L - 1 ? pos : L - 1;
+            }
+            const float lse = p.lse[(static_cast<int64_t>(b) * a.h_k + g) * a.n_q + n];
+            nlse2 = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
+          }
+          row_nlse2[ct] = nlse2;
+          row_slope2[ct] = slope2;
+          row_pos[ct] = static_cast<float>(pos);
+          row_lo[ct] = lo;
+          row_hi[ct] = hi;
+        }
+        ptx::fence_proxy_async_smem();
+        ptx::named_bar_sync(kBarCons, 256);
+        if (ct == 0) ptx::mbar_arrive(qready(s & 1));
+        ++s;
+      }
+
+      const float to_logit = a.softmax_scale * qd * kd * ldexpf(1.f, -shift);
+      const float c1 = cap2 > 0.f ? to_logit / a.mod.softcap : to_logit * kLog2e;
+      const float2 c12 = make_float2(c1, c1);
+      const int pos_min = L - a.q_len + p.n0 / a.h_r;  // of the launch's rows
+      float* const acc = p.acc + b * p.acc_seq + g * p.acc_head;
+      // this group's tiles: every second one that is seen (the MMA's order),
+      // and every second of the others; the accumulators of its next tile are
+      // on their way while it works on one
+      auto reads = [&](int key) { return key < L - p.fresh && p.decay > 0.f; };
+      auto own = [&](int t) {  // its first tile from t on, counting the other group's in u
+        for (; t < sg.t1; ++t) {
+          if (lim.seen(t * kKeys)) {
+            if ((u & 1) == wg) break;
+            ++u;
+          } else if ((t & 1) == wg) {
+            break;
+          }
+        }
+        return t;
+      };
+      int t = own(sg.t0);
+      float old = t < sg.t1 && reads(t * kKeys + key_in_tile) ? acc[t * kKeys + key_in_tile] : 0.f;
+      while (t < sg.t1) {
+        const int key0 = t * kKeys;
+        const int key = key0 + key_in_tile;
+        const bool is_seen = lim.seen(key0);
+        const int n = u >> 1;  // its place among the group's seen tiles
+        u += is_seen;
+        const int t_next = own(t + 1);
+        const float old_next =
+            t_next < sg.t1 && reads(t_next * kKeys + key_in_tile) ? acc[t_next * kKeys + key_in_tile] : 0.f;
+        float2 sum2 = make_float2(0.f, 0.f);
+        if (is_seen) {
+          if (!ptx::mbar_wait_bounded(sfull(wg), n & 1, abort_flag, kWaitNs)) set_abort(abort_flag, a.status);
+          ptx::tc_fence_after();
+          const bool whole = lim.whole(key0);  // uniform
+          const float fkey = static_cast<float>(key);
+          const float2 nkey2 = make_float2(-fkey, -fkey);
+          const bool ahead = key0 + kKeys - 1 > pos_min;  // some distance may be negative
+          for (int c0 = 0; c0 < p.n_mma; c0 += 16) {
+            uint32_t r[16];
+            MJ_TMEM_LD16(tmem_s + c0, r);
+            ptx::tmem_ld_wait();
+            if (c0 + 16 >= p.n_mma) {  // read whole: the next MMA may overwrite it
+              ptx::tc_fence_before();
+              __syncwarp();
+              if (lane == 0) ptx::mbar_arrive(sfree(wg));
+            }
+            float2 y[8];
+            if (kMod && cap2 > 0.f) {
               float top = 0.f;
 #pragma unroll
-              for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(y[e]));
+              for (int e = 0; e < 8; ++e) {
+                y[e] = mul2(make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])), c12);
+                top = fmax3(top, fabsf(y[e].x), fabsf(y[e].y));
+              }
+              // scores small against the cap (most, in practice) need no exponential
               if (__all_sync(0xffffffffu, top < kTanhSmall)) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) y[e] = cap2 * tanh_small(y[e]);
+                for (int e = 0; e < 8; ++e) y[e] = tanh_small2(y[e]);
               } else {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) y[e] = cap2 * tanh_any(y[e]);
+                for (int e = 0; e < 8; ++e) y[e] = make_float2(tanh_any(y[e].x), tanh_any(y[e].y));
+              }
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                y[e] = fma2(y[e], cap22, *reinterpret_cast<const float2*>(row_nlse2 + c0 + 2 * e));
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                y[e] = fma2(make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])), c12,
+                            *reinterpret_cast<const float2*>(row_nlse2 + c0 + 2 * e));
+            }
+            if (kMod && a.mod.slopes) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float2 sl = *reinterpret_cast<const float2*>(row_slope2 + c0 + 2 * e);
+                float2 d = add2(*reinterpret_cast<const float2*>(row_pos + c0 + 2 * e), nkey2);
+                if (ahead) d = make_float2(fabsf(d.x), fabsf(d.y));
+                y[e] = fma2(make_float2(-sl.x, -sl.y), d, y[e]);
               }
             }
-            if (a.mod.slopes) {
+            if (whole) {
 #pragma unroll
-              for (int e = 0; e < 16; ++e) y[e] = fmaf(-row_slope2[c0 + e], fabsf(row_pos[c0 + e] - fkey), y[e]);
-            }
-          }
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float w = fast_exp2(y[e] - row_lse2[c0 + e]);
-            if (unmasked) {
-              sum += c0 + e < p.n_rows ? w : 0.f;
+              for (int e = 0; e < 8; ++e) sum2 = add2(sum2, make_float2(fast_exp2(y[e].x), fast_exp2(y[e].y)));
             } else {
-              const bool vis = (key < pfx || (key >= row_lo[c0 + e] && key <= row_hi[c0 + e])) && c0 + e < p.n_rows;
-              sum += vis ? w : 0.f;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const int c = c0 + 2 * e;
+                const bool v0 = key < lim.pfx || (key >= row_lo[c] && key <= row_hi[c]);
+                const bool v1 = key < lim.pfx || (key >= row_lo[c + 1] && key <= row_hi[c + 1]);
+                sum2.x += v0 ? fast_exp2(y[e].x) : 0.f;
+                sum2.y += v1 ? fast_exp2(y[e].y) : 0.f;
+              }
             }
           }
         }
+        if (key < L && !*abort_flag) acc[key] = (reads(key) ? p.decay * old : 0.f) + (sum2.x + sum2.y);
+        t = t_next;
+        old = old_next;
       }
-      if (key < L && !*abort_flag) acc[key] = (reads ? p.decay * old : 0.f) + sum;
     }
   }
 
@@ -413,18 +588,17 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 template <bool kQe4m3, bool kMod>
-cudaError_t launch_kw(const KwArgs& p, const CUtensorMap& mk, size_t smem, cudaStream_t stream) {
+cudaError_t launch_kw(const KwArgs& p, const CUtensorMap& mk, int ctas, size_t smem, cudaStream_t stream) {
   auto kern = key_weights_kernel<kQe4m3, kMod>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(p.d.num_work) * p.d.h_k, 1, 1), dim3(kThreads, 1, 1), smem, stream,
-                    p, mk);
+  return launch_pdl(kern, dim3(static_cast<unsigned>(ctas), 1, 1), dim3(kThreads, 1, 1), smem, stream, p, mk);
 }
 
 }  // namespace
 
 cudaError_t launch_key_weights(const DecodeModDev& a, bool q_e4m3, bool has_mod, int n0, int n_rows, const float* lse,
-                               float* acc, int64_t acc_seq, int64_t acc_head, float decay, int fresh,
+                               float* acc, int64_t acc_seq, int64_t acc_head, float decay, int fresh, int sm_count,
                                cudaStream_t stream) {
   KwArgs p{};
   p.d = a;
@@ -439,22 +613,30 @@ cudaError_t launch_key_weights(const DecodeModDev& a, bool q_e4m3, bool has_mod,
   p.n_mma = (n_rows + 15) / 16 * 16;
   p.tmem_cols = 32;
   while (p.tmem_cols < 2 * p.n_mma) p.tmem_cols *= 2;
-  const int q_bytes = p.n_mma * 128 * (q_e4m3 ? 1 : 2);
-  const int tail = 5 * kMaxRows * 4 + 8 * (2 * kMaxStages + 8) + 128;
-  // two CTAs an SM when their shared memory and TMEM allow it
-  const int limit = n_rows <= 128 ? 112 * 1024 : 224 * 1024;
+  const int per_sm = n_rows <= kTwoCtaRows ? 2 : 1;
+  const int q_bytes = 2 * p.n_mma * 128 * (q_e4m3 ? 1 : 2);  // two segments' rows
+  const int row_bytes = 2 * 5 * p.n_mma * 4;
+  const int tail = row_bytes + 8 * (2 * kMaxStages + 8) + 256;
+  const int limit = (per_sm == 2 ? 112 : 224) * 1024;
   p.stages = (limit - 1024 - q_bytes - tail) / kTileBytes;
   if (p.stages > kMaxStages) p.stages = kMaxStages;
   p.off_q = p.stages * kTileBytes;
   p.off_row = p.off_q + q_bytes;
-  p.off_bar = p.off_row + 5 * kMaxRows * 4;
+  p.off_bar = p.off_row + row_bytes;
   const size_t smem = 1024 + static_cast<size_t>(p.off_q) + q_bytes + tail;
   const int box_rows = a.page_size < kKeys ? a.page_size : kKeys;
   CUtensorMap mk;
   if (!make_kv_map(&mk, a.k, a.page_size, a.h_k, a.num_pages, a.k_row, a.k_head, a.k_page, box_rows, 1, a.kv_format))
     return cudaErrorInvalidValue;
-  if (q_e4m3) return has_mod ? launch_kw<true, true>(p, mk, smem, stream) : launch_kw<true, false>(p, mk, smem, stream);
-  return has_mod ? launch_kw<false, true>(p, mk, smem, stream) : launch_kw<false, false>(p, mk, smem, stream);
+  // one share a resident CTA, the same cuts for every head; never more shares
+  // than tiles could be (an item holds at most all of a sequence's)
+  const int64_t tiles = static_cast<int64_t>(a.num_work) * ((a.max_blocks * a.page_size + kKeys - 1) / kKeys);
+  int64_t shares = sm_count * per_sm / a.h_k;
+  shares = shares < 1 ? 1 : (shares > tiles ? tiles : shares);
+  const int ctas = static_cast<int>(shares) * a.h_k;
+  if (q_e4m3)
+    return has_mod ? launch_kw<true, true>(p, mk, ctas, smem, stream) : launch_kw<true, false>(p, mk, ctas, smem, stream);
+  return has_mod ? launch_kw<false, true>(p, mk, ctas, smem, stream) : launch_kw<false, false>(p, mk, ctas, smem, stream);
 }
 
 }  // namespace mj

@@ -271,13 +271,15 @@ extern "C" mj_status mj_key_weights(const mj_decode_params* params, const mj_sco
   d.causal = p.causal;
   d.kv_evict_first = kv_evict_first(p);
   d.kv_format = p.kv_format;
+  const int sms = device_sm_count();
+  if (sms < 1) return MJ_ERR_CUDA;
   const NvtxRange range("mj_key_weights");
   for (int n0 = 0; n0 < n_q; n0 += 256) {
     const int rows = std::min(256, n_q - n0);
     // later row groups add onto what the first one wrote
     const cudaError_t e =
         launch_key_weights(d, p.q_dtype == MJ_E4M3, mod != nullptr, n0, rows, a.lse, acc, acc_seq, acc_head,
-                           n0 == 0 ? decay : 1.f, n0 == 0 ? fresh : 0, reinterpret_cast<cudaStream_t>(stream));
+                           n0 == 0 ? decay : 1.f, n0 == 0 ? fresh : 0, sms, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return MJ_ERR_CUDA;
   }
   return MJ_OK;

@@ -77,7 +77,7 @@ cudaError_t launch_score_spans(const ScoreModDev& m, const int32_t* seq_lens, in
 // Accumulated attention weights of packed rows n0 .. n0 + n_rows - 1 (at
 // most 256): acc[b][g][j] of a.work's tiles.
 cudaError_t launch_key_weights(const DecodeModDev& a, bool q_e4m3, bool has_mod, int n0, int n_rows, const float* lse,
-                               float* acc, int64_t acc_seq, int64_t acc_head, float decay, int fresh,
+                               float* acc, int64_t acc_seq, int64_t acc_head, float decay, int fresh, int sm_count,
                                cudaStream_t stream);
 
 cudaError_t launch_rope_append(const RopeDev& a, cudaStream_t stream);

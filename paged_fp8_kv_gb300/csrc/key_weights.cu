@@ -24,7 +24,8 @@
 // Roles (320 threads): warp 0 issues the K tiles into a ring, warp 1 (TMEM
 // allocator) the MMAs, warps 2-5 and 6-9 take alternate tiles.  Up to 64 rows
 // two CTAs fit an SM, one's segment starts under the other's stream.  Q parts
-// and row constants are double-buffered over segments.  Tiles that no row sees
+// and row constants are double-buffered over segments, the next segment's Q
+// rows and scalars fetched during one.  Tiles that no row sees
 // (a window, documents) are neither loaded nor multiplied; their weights only
 // decay.
 
@@ -58,7 +59,8 @@ struct KwArgs {
   int32_t n_mma;       // n_rows rounded up to 16: the MMA's N
   int32_t stages;
   int32_t tmem_cols;
-  int32_t off_q, off_row, off_bar;  // shared memory, from the 1 KB boundary
+  int32_t s_bufs;      // S buffers of each group: 2, or 1 above 128 rows
+  int32_t off_q, off_stage, off_row, off_bar;  // shared memory, from the 1 KB boundary
 };
 
 __device__ __forceinline__ void set_abort(volatile int* abort, int32_t* status) {
@@ -162,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t sbase = ptx::smem_u32(sm);
   // per-row constants of a segment, two buffers of [5][n_mma]
   float* const row_base = reinterpret_cast<float*>(sm + p.off_row);
-  uint8_t* const misc = sm + p.off_bar + 8 * (2 * kMaxStages + 8);
+  uint8_t* const misc = sm + p.off_bar + 8 * (2 * kMaxStages + 12);
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(misc);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(misc + 4);
   float* const amax_red = reinterpret_cast<float*>(misc + 32);      // [8]
@@ -172,10 +174,16 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t bar0 = sbase + p.off_bar;
   auto kfull = [&](int s) { return bar0 + 8u * s; };
   auto kempty = [&](int s) { return bar0 + 8u * (kMaxStages + s); };
-  auto sfull = [&](int wg) { return bar0 + 8u * (2 * kMaxStages + wg); };
-  auto sfree = [&](int wg) { return bar0 + 8u * (2 * kMaxStages + 2 + wg); };
-  auto qready = [&](int s) { return bar0 + 8u * (2 * kMaxStages + 4 + s); };
-  const uint32_t drain = bar0 + 8u * (2 * kMaxStages + 6);
+  auto sfull = [&](int buf) { return bar0 + 8u * (2 * kMaxStages + buf); };  // buf: group * 2 + its buffer
+  auto sfree = [&](int buf) { return bar0 + 8u * (2 * kMaxStages + 4 + buf); };
+  auto qready = [&](int s) { return bar0 + 8u * (2 * kMaxStages + 8 + s); };
+  const uint32_t drain = bar0 + 8u * (2 * kMaxStages + 10);
+  // a group's n-th seen tile: its buffer, and that barrier's phase
+  const int two = p.s_bufs - 1;
+  const int buf_cols = p.tmem_cols >> (1 + two);
+  auto buf_of = [&](int wg, int n) { return wg * 2 + (n & two); };
+  auto phase_of = [&](int n) { return static_cast<uint32_t>((n >> two) & 1); };
+  auto s_cols = [&](int wg, int n) { return static_cast<uint32_t>((wg * p.s_bufs + (n & two)) * buf_cols); };
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int stages = p.stages;
@@ -186,14 +194,18 @@ __global__ void __launch_bounds__(kThreads, 2)
       ptx::mbar_init(kfull(s), 1);
       ptx::mbar_init(kempty(s), 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       ptx::mbar_init(sfull(i), 1);
       ptx::mbar_init(sfree(i), 4);
-      ptx::mbar_init(qready(i), 1);
     }
+    for (int i = 0; i < 2; ++i) ptx::mbar_init(qready(i), 1);
     ptx::mbar_init(drain, 1);
     *abort_flag = 0;
     ptx::fence_mbar_init();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), p.tmem_cols);
+    ptx::tmem_relinquish();
   }
   // ---- this CTA's share: tiles [first, last) of the items' tiles in order,
   // for one kv head; the CTAs of the other heads' shares run beside it
@@ -237,11 +249,6 @@ __global__ void __launch_bounds__(kThreads, 2)
         before += tiles;
       }
     }
-  }
-  if (first == last) return;  // nothing to do (uniform over the CTA, before TMEM)
-  if (warp == 1) {
-    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), p.tmem_cols);
-    ptx::tmem_relinquish();
   }
   ptx::tc_fence_before();
   __syncthreads();
@@ -333,20 +340,21 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (!lim.seen(t * kKeys)) continue;
           const int st = u % stages, wg = u & 1, n = u >> 1;
           if (!ptx::mbar_wait_bounded(kfull(st), (u / stages) & 1, abort_flag, kWaitNs) ||
-              (n >= 1 && !ptx::mbar_wait_bounded(sfree(wg), (n - 1) & 1, abort_flag, kWaitNs))) {
+              (n > two &&
+               !ptx::mbar_wait_bounded(sfree(buf_of(wg, n)), phase_of(n - 1 - two), abort_flag, kWaitNs))) {
             ok = false;
             break;
           }
           ptx::tc_fence_after();
           const uint64_t kdesc = kdesc0 + static_cast<uint64_t>((st * kTileBytes) >> 4);
-          const uint32_t d = tmem + wg * (p.tmem_cols >> 1);
+          const uint32_t d = tmem + s_cols(wg, n);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
 #pragma unroll
             for (int part = 0; part < kParts; ++part)
               ptx::mma_e4m3(d, kdesc + 2 * kk, qdesc + part * part_step + 2 * kk, idesc, (kk > 0 || part > 0) ? 1u : 0u);
           }
-          ptx::mma_commit(sfull(wg));
+          ptx::mma_commit(sfull(buf_of(wg, n)));
           ptx::mma_commit(kempty(st));
           ++u;
         }
@@ -365,16 +373,39 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int ct = tid - 64;  // consumer thread
     const int wg = ct >> 7, quarter = warp & 3;
     const int key_in_tile = quarter * 32 + lane;
-    const uint32_t tmem_s = tmem + wg * (p.tmem_cols >> 1) + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t tmem_w = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    bool far = false;  // the last capped tile held scores past the polynomial's range
     const float cap2 = kMod ? a.mod.softcap * kLog2e : 0.f;
     const float2 cap22 = make_float2(cap2, cap2);
     int u = 0, s = 0;
-    while (walk.next(sg)) {
-      const int b = sg.b;
-      const int L = length_of(b);
+    // the next segment's raw Q rows (this thread's 16-element chunks, by
+    // asynchronous copies) and scalars are on their way during a segment
+    constexpr int kChunkBytes = kQe4m3 ? 16 : 32;
+    uint8_t* const stage = sm + p.off_stage;
+    int L_next = 0;
+    float kd_next = 0.f, qd_next = 0.f, lse_next = 0.f;
+    auto fetch = [&](int b) {
+      const uint8_t* src = static_cast<const uint8_t*>(a.q) +
+                           (b * a.q_seq + (static_cast<int64_t>(g) * a.n_q + p.n0) * kHeadDimDev) * (kQe4m3 ? 1 : 2);
+      for (int id = ct; id < p.n_rows * 8; id += 256) {
+        cp_async16(stage + id * kChunkBytes, src + id * kChunkBytes, true);
+        if (!kQe4m3) cp_async16(stage + id * kChunkBytes + 16, src + id * kChunkBytes + 16, true);
+      }
+      cp_async_commit();
+      L_next = length_of(b);
+      kd_next = a.kd[b * a.kd_seq + g * a.kd_head];
+      qd_next = a.qd[b * a.qd_seq + g * a.qd_head];
+      if (ct < p.n_rows) lse_next = p.lse[(static_cast<int64_t>(b) * a.h_k + g) * a.n_q + p.n0 + ct];
+    };
+    Segment upcoming;
+    bool more = walk.next(upcoming);
+    if (more) fetch(upcoming.b);
+    while (more) {
+      sg = upcoming;
+      const int b = sg.b, L = L_next;
+      const float kd = kd_next, qd = qd_next;
       const Limits lim = warp_limits<kMod>(p, b, L, lane);
-      const float kd = a.kd[b * a.kd_seq + g * a.kd_head];
-      const float qd = a.qd[b * a.qd_seq + g * a.qd_head];
+      cp_async_wait<0>();
       float* const row_nlse2 = row_base + (s & 1) * 5 * p.n_mma;  // -lse in log2 units
       float* const row_slope2 = row_nlse2 + p.n_mma;
       float* const row_pos = row_slope2 + p.n_mma;
@@ -386,12 +417,11 @@ __global__ void __launch_bounds__(kThreads, 2)
       // ---- Q rows -> one (e4m3) or two (bf16: hi + lo) operand rows, a
       // 16-element chunk a thread and round
       if (lim.any(sg.t0, sg.t1)) {
-        const int64_t q_at = b * a.q_seq + (static_cast<int64_t>(g) * a.n_q + p.n0) * kHeadDimDev;
         const int chunks = p.n_mma * 8;
         if constexpr (!kQe4m3) {
           uint32_t mbits = 0;  // bf16 |q| maximum: integer maximum of the magnitude bits
           for (int id = ct; id < p.n_rows * 8; id += 256) {
-            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + q_at + id * 16);
+            const uint4* src = reinterpret_cast<const uint4*>(stage + id * kChunkBytes);
             const uint4 r0 = src[0], r1 = src[1];
             const uint32_t v8[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
 #pragma unroll
@@ -418,10 +448,10 @@ __global__ void __launch_bounds__(kThreads, 2)
           const int r = id >> 3, cc = id & 7;
           const bool live = r < p.n_rows;
           if constexpr (kQe4m3) {
-            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.q) + q_at + id * 16);
+            const uint4* src = reinterpret_cast<const uint4*>(stage + id * kChunkBytes);
             *reinterpret_cast<uint4*>(swz(qbase, r, cc)) = live ? *src : make_uint4(0u, 0u, 0u, 0u);
           } else {
-            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + q_at + id * 16);
+            const uint4* src = reinterpret_cast<const uint4*>(stage + id * kChunkBytes);
             const uint4 z = make_uint4(0u, 0u, 0u, 0u);
             const uint4 r0 = live ? src[0] : z, r1 = live ? src[1] : z;
             const uint32_t w8[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
@@ -462,8 +492,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             } else {
               hi = a.causal && pos < L - 1 ? pos : L - 1;
             }
-            const float lse = p.lse[(static_cast<int64_t>(b) * a.h_k + g) * a.n_q + n];
-            nlse2 = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
+            nlse2 = lse_next == -INFINITY ? -INFINITY : -lse_next * kLog2e;
           }
           row_nlse2[ct] = nlse2;
           row_slope2[ct] = slope2;
@@ -476,6 +505,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (ct == 0) ptx::mbar_arrive(qready(s & 1));
         ++s;
       }
+      more = walk.next(upcoming);
+      if (more) fetch(upcoming.b);  // (this thread has read its staged chunks)
 
       const float to_logit = a.softmax_scale * qd * kd * ldexpf(1.f, -shift);
       const float c1 = cap2 > 0.f ? to_logit / a.mod.softcap : to_logit * kLog2e;
@@ -510,69 +541,87 @@ __global__ void __launch_bounds__(kThreads, 2)
             t_next < sg.t1 && reads(t_next * kKeys + key_in_tile) ? acc[t_next * kKeys + key_in_tile] : 0.f;
         float2 sum2 = make_float2(0.f, 0.f);
         if (is_seen) {
-          if (!ptx::mbar_wait_bounded(sfull(wg), n & 1, abort_flag, kWaitNs)) set_abort(abort_flag, a.status);
+          const int sb = buf_of(wg, n);
+          const uint32_t tmem_s = tmem_w + s_cols(wg, n);
+          if (!ptx::mbar_wait_bounded(sfull(sb), phase_of(n), abort_flag, kWaitNs)) set_abort(abort_flag, a.status);
           ptx::tc_fence_after();
           const bool whole = lim.whole(key0);  // uniform
           const float fkey = static_cast<float>(key);
           const float2 nkey2 = make_float2(-fkey, -fkey);
           const bool ahead = key0 + kKeys - 1 > pos_min;  // some distance may be negative
-          for (int c0 = 0; c0 < p.n_mma; c0 += 16) {
-            uint32_t r[16];
-            MJ_TMEM_LD16(tmem_s + c0, r);
-            ptx::tmem_ld_wait();
-            if (c0 + 16 >= p.n_mma) {  // read whole: the next MMA may overwrite it
-              ptx::tc_fence_before();
-              __syncwarp();
-              if (lane == 0) ptx::mbar_arrive(sfree(wg));
-            }
-            float2 y[8];
-            if (kMod && cap2 > 0.f) {
-              float top = 0.f;
+          // the tile's row sums; capped scores by the polynomial (near) or by
+          // the exponential form; returns whether all lay in its range
+          auto tile_sums = [&](bool near) {
+            float top = 0.f;  // largest square of a score over the cap
+            sum2 = make_float2(0.f, 0.f);
+            for (int c0 = 0; c0 < p.n_mma; c0 += 16) {
+              uint32_t r[16];
+              MJ_TMEM_LD16(tmem_s + c0, r);
+              ptx::tmem_ld_wait();
+              float2 y[8];
+              if (kMod && cap2 > 0.f) {
+                if (near) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                y[e] = mul2(make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])), c12);
-                top = fmax3(top, fabsf(y[e].x), fabsf(y[e].y));
-              }
-              // scores small against the cap (most, in practice) need no exponential
-              if (__all_sync(0xffffffffu, top < kTanhSmall)) {
+                  for (int e = 0; e < 8; ++e) {
+                    const float2 t = mul2(make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])), c12);
+                    const float2 sq = mul2(t, t);
+                    top = fmax3(top, sq.x, sq.y);
+                    y[e] = mul2(t, tanh_ratio2(sq));
+                  }
+                } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = tanh_small2(y[e]);
+                  for (int e = 0; e < 8; ++e) {
+                    const float2 t = mul2(make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])), c12);
+                    const float2 sq = mul2(t, t);
+                    top = fmax3(top, sq.x, sq.y);
+                    y[e] = make_float2(tanh_any(t.x), tanh_any(t.y));
+                  }
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  y[e] = fma2(y[e], cap22, *reinterpret_cast<const float2*>(row_nlse2 + c0 + 2 * e));
               } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = make_float2(tanh_any(y[e].x), tanh_any(y[e].y));
+                for (int e = 0; e < 8; ++e)
+                  y[e] = fma2(make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])), c12,
+                              *reinterpret_cast<const float2*>(row_nlse2 + c0 + 2 * e));
               }
+              if (kMod && a.mod.slopes) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                y[e] = fma2(y[e], cap22, *reinterpret_cast<const float2*>(row_nlse2 + c0 + 2 * e));
-            } else {
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                y[e] = fma2(make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])), c12,
-                            *reinterpret_cast<const float2*>(row_nlse2 + c0 + 2 * e));
-            }
-            if (kMod && a.mod.slopes) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float2 sl = *reinterpret_cast<const float2*>(row_slope2 + c0 + 2 * e);
-                float2 d = add2(*reinterpret_cast<const float2*>(row_pos + c0 + 2 * e), nkey2);
-                if (ahead) d = make_float2(fabsf(d.x), fabsf(d.y));
-                y[e] = fma2(make_float2(-sl.x, -sl.y), d, y[e]);
+                for (int e = 0; e < 8; ++e) {
+                  const float2 sl = *reinterpret_cast<const float2*>(row_slope2 + c0 + 2 * e);
+                  float2 d = add2(*reinterpret_cast<const float2*>(row_pos + c0 + 2 * e), nkey2);
+                  if (ahead) d = make_float2(fabsf(d.x), fabsf(d.y));
+                  y[e] = fma2(make_float2(-sl.x, -sl.y), d, y[e]);
+                }
               }
-            }
-            if (whole) {
+              if (whole) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e) sum2 = add2(sum2, make_float2(fast_exp2(y[e].x), fast_exp2(y[e].y)));
-            } else {
+                for (int e = 0; e < 8; ++e) sum2 = add2(sum2, make_float2(fast_exp2(y[e].x), fast_exp2(y[e].y)));
+              } else {
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const int c = c0 + 2 * e;
-                const bool v0 = key < lim.pfx || (key >= row_lo[c] && key <= row_hi[c]);
-                const bool v1 = key < lim.pfx || (key >= row_lo[c + 1] && key <= row_hi[c + 1]);
-                sum2.x += v0 ? fast_exp2(y[e].x) : 0.f;
-                sum2.y += v1 ? fast_exp2(y[e].y) : 0.f;
+                for (int e = 0; e < 8; ++e) {
+                  const int c = c0 + 2 * e;
+                  const bool v0 = key < lim.pfx || (key >= row_lo[c] && key <= row_hi[c]);
+                  const bool v1 = key < lim.pfx || (key >= row_lo[c + 1] && key <= row_hi[c + 1]);
+                  sum2.x += v0 ? fast_exp2(y[e].x) : 0.f;
+                  sum2.y += v1 ? fast_exp2(y[e].y) : 0.f;
+                }
               }
             }
+            return __all_sync(0xffffffffu, top < kTanhSmall * kTanhSmall);
+          };
+          if (kMod && cap2 > 0.f) {
+            // most scores are small against a cap; a tile that holds others is
+            // done again, and the next one starts with the exponential form
+            if (!far && !tile_sums(true)) far = true;
+            if (far) far = !tile_sums(false);
+          } else {
+            tile_sums(true);
           }
+          ptx::tc_fence_before();  // the buffer is read
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(sfree(sb));
         }
         if (key < L && !*abort_flag) acc[key] = (reads(key) ? p.decay * old : 0.f) + (sum2.x + sum2.y);
         t = t_next;
@@ -611,17 +660,21 @@ cudaError_t launch_key_weights(const DecodeModDev& a, bool q_e4m3, bool has_mod,
   p.n0 = n0;
   p.n_rows = n_rows;
   p.n_mma = (n_rows + 15) / 16 * 16;
+  // S buffers: two of each group (the MMA runs a tile ahead), one above 128 rows
+  p.s_bufs = p.n_mma <= 128 ? 2 : 1;
   p.tmem_cols = 32;
-  while (p.tmem_cols < 2 * p.n_mma) p.tmem_cols *= 2;
+  while (p.tmem_cols < 2 * p.s_bufs * p.n_mma) p.tmem_cols *= 2;
   const int per_sm = n_rows <= kTwoCtaRows ? 2 : 1;
   const int q_bytes = 2 * p.n_mma * 128 * (q_e4m3 ? 1 : 2);  // two segments' rows
   const int row_bytes = 2 * 5 * p.n_mma * 4;
-  const int tail = row_bytes + 8 * (2 * kMaxStages + 8) + 256;
+  const int stage_bytes = p.n_mma * 128 * (q_e4m3 ? 1 : 2);
+  const int tail = stage_bytes + row_bytes + 8 * (2 * kMaxStages + 12) + 256;
   const int limit = (per_sm == 2 ? 112 : 224) * 1024;
   p.stages = (limit - 1024 - q_bytes - tail) / kTileBytes;
   if (p.stages > kMaxStages) p.stages = kMaxStages;
   p.off_q = p.stages * kTileBytes;
-  p.off_row = p.off_q + q_bytes;
+  p.off_stage = p.off_q + q_bytes;
+  p.off_row = p.off_stage + stage_bytes;
   p.off_bar = p.off_row + row_bytes;
   const size_t smem = 1024 + static_cast<size_t>(p.off_q) + q_bytes + tail;
   const int box_rows = a.page_size < kKeys ? a.page_size : kKeys;

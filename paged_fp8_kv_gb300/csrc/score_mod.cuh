@@ -80,15 +80,14 @@ __device__ __forceinline__ float rcp_approx(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float2 tanh_small2(float2 t) {  // two of tanh_small, the same roundings
-  const float2 u = mul2(t, t);
+// tanh(t) / t of two values of u = t^2, the same polynomial
+__device__ __forceinline__ float2 tanh_ratio2(float2 u) {
   float2 p = make_float2(-5.852168662e-03f, -5.852168662e-03f);
   p = fma2(p, u, make_float2(2.075362916e-02f, 2.075362916e-02f));
   p = fma2(p, u, make_float2(-5.376870490e-02f, -5.376870490e-02f));
   p = fma2(p, u, make_float2(1.333168896e-01f, 1.333168896e-01f));
   p = fma2(p, u, make_float2(-3.333328326e-01f, -3.333328326e-01f));
-  p = fma2(p, u, make_float2(9.999999975e-01f, 9.999999975e-01f));
-  return mul2(t, p);
+  return fma2(p, u, make_float2(9.999999975e-01f, 9.999999975e-01f));
 }
 constexpr float kTanhSmall = 0.6f;
 __device__ __forceinline__ float tanh_any(float t) {

@@ -775,10 +775,18 @@ class _Call:
     _name = ""
 
     def _bind(self, fn, args, keep) -> None:
+        import torch
+
         self._fn, self._args, self._keep = fn, args, keep  # keep: the tensors behind the pointers
+        self._device, self._current_device = torch.cuda.current_device(), torch.cuda.current_device
+        # the current stream's handle without a Stream object around it (3 us of a call that takes 6)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self._raw_stream = raw or (lambda device: torch.cuda.current_stream(device).cuda_stream)
 
     def __call__(self, stream=None) -> None:
-        st = self._fn(*self._args, _stream_handle(stream))
+        if self._current_device() != self._device:
+            raise ValueError(f"{self._name}: its tensors are on CUDA device {self._device}, which is not the current one")
+        st = self._fn(*self._args, self._raw_stream(self._device) if stream is None else stream.cuda_stream)
         if st != MJ_OK:
             raise MjError(st, self._name)
 

@@ -29,7 +29,8 @@
 namespace mj {
 namespace {
 
-constexpr int kMaxTokens = 16;     // tokens per CTA
+constexpr int kMaxTokens = 8;      // tokens per CTA
+constexpr int kLongCtas = 1024;    // CTAs from which they take more tokens instead
 constexpr int kRopeThreads = 384;  // 48 heads at a time
 constexpr int kStatusInvalidArg = 1;  // MJ_ERR_INVALID_ARG
 
@@ -61,15 +62,47 @@ __device__ __forceinline__ uint4 pack8(const float* x) {
   return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-__device__ __forceinline__ uint2 codes8(const float* x, float descale) {
+__device__ __forceinline__ uint2 to_codes8(const float* q) {
   uint32_t u[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const uint16_t lo = ptx::f32x2_to_e4m3x2(__fdiv_rn(x[4 * i], descale), __fdiv_rn(x[4 * i + 1], descale));
-    const uint16_t hi = ptx::f32x2_to_e4m3x2(__fdiv_rn(x[4 * i + 2], descale), __fdiv_rn(x[4 * i + 3], descale));
+    const uint16_t lo = ptx::f32x2_to_e4m3x2(q[4 * i], q[4 * i + 1]);
+    const uint16_t hi = ptx::f32x2_to_e4m3x2(q[4 * i + 2], q[4 * i + 3]);
     u[i] = static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
   }
   return make_uint2(u[0], u[1]);
+}
+
+// x[i] / d for sixteen values, each as the IEEE division gives it, at three
+// operations a value: with r = 1/d and q = x r rounded, x - q d is exact in an
+// fma and q + (x - q d) r rounds to the quotient (Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000 processor", 1990, theorem
+// 7).  It needs r, q and the remainder clear of overflow and underflow: d
+// outside [2^-60, 2^60] or a quotient past 2^40 takes the division itself; a
+// remainder that underflows then belongs to a quotient below 2^-18, which
+// every e4m3 rounding makes zero.  (The divisions were most of the kernel's
+// instructions: on the prompt above 95 us with them, 77 so.)
+__device__ __forceinline__ void divide16(float* x, float d) {
+  const float r = __frcp_rn(d);
+  const float2 r2 = make_float2(r, r), nd2 = make_float2(-d, -d);
+  float2 q[8];
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    q[i] = mul2(make_float2(x[2 * i], x[2 * i + 1]), r2);
+    top = fmax3(top, fabsf(q[i].x), fabsf(q[i].y));
+  }
+  if (d >= 0x1p-60f && d <= 0x1p60f && top <= 0x1p40f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      q[i] = fma2(fma2(q[i], nd2, make_float2(x[2 * i], x[2 * i + 1])), r2, q[i]);
+      x[2 * i] = q[i].x;
+      x[2 * i + 1] = q[i].y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = __fdiv_rn(x[i], d);
+  }
 }
 
 // kPairs: neighbouring elements are a pair
@@ -160,8 +193,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeDev
     }
     info[back] = f;
   }
-  // the first head's rows, in flight across the barrier (padding rows are
-  // inside the input: reading them is harmless, they are not written)
+  // the first heads' rows, in flight across the barrier (padding rows are
+  // inside the input: reading them is harmless, they are not written); one
+  // head in flight a group of eight lanes (with two, their registers cost a
+  // CTA an SM: 77 us for 64 on a prompt of 15005 tokens and 48 heads)
   const int items = nt * heads;
   int item = threadIdx.x >> 3;
   int tl = 0, head = 0;
@@ -238,8 +273,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeDev
         if (a.key_pos && lane8 == 0) a.key_pos[f.seq * a.kp_seq + g * a.kp_head + f.slot] = f.pos0;
       }
       uint2* dst = reinterpret_cast<uint2*>(row);
-      dst[c0] = codes8(x, descale);
-      dst[c1] = codes8(x + 8, descale);
+      divide16(x, descale);
+      dst[c0] = to_codes8(x);
+      dst[c1] = to_codes8(x + 8);
     }
   }
 }
@@ -249,9 +285,12 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeDev
 cudaError_t launch_rope_append(const RopeDev& a, cudaStream_t stream) {
   if (a.num_tokens == 0) return cudaSuccess;
   const int heads = a.h_k * (a.h_r + 2);
-  // whole tokens, about one head per group of eight lanes
+  // whole tokens: about one head per group of eight lanes, and more of them
+  // once the CTAs fill the GPU several times over (they share one
+  // chain of dependent loads: one token a CTA took 152 us where eight take 64)
   int per_cta = (kRopeThreads / 8) / heads;
   per_cta = per_cta < 1 ? 1 : (per_cta > kMaxTokens ? kMaxTokens : per_cta);
+  while (per_cta < kMaxTokens && a.num_tokens >= kLongCtas * per_cta * 2) per_cta *= 2;
   int threads = per_cta * heads * 8;
   threads = (threads + 31) / 32 * 32;
   if (threads > kRopeThreads) threads = kRopeThreads;

@@ -221,6 +221,30 @@ def test_nonfinite_values():
     assert row[0] & 0x7F == 0x7F and row[1] == 0x7E and row[2] == 0xFE
 
 
+def test_codes_are_those_of_the_division():
+    """K (turned by nothing) and V codes equal torch's division and rounding,
+    bit for bit, for descales over the whole range."""
+    n = 4096
+    rng = np.random.default_rng(5)
+    c = Case([n], [0], h_k=4, h_r=1, seed=9, max_pos=1, page_size=128)
+    c.pos[:] = 0
+    c.dev["positions"].zero_()
+    c.dev["cos_sin"][:, :64], c.dev["cos_sin"][:, 64:] = 1.0, 0.0
+    for exps in ((-3, 3), (-70, 70), (-126, 127)):
+        d = torch.from_numpy((2.0 ** rng.uniform(*exps, (1, 4))).astype(np.float32)).cuda()
+        scale = torch.from_numpy(2.0 ** rng.uniform(-12, 12, (n, 4, 1))).cuda()
+        x = (torch.from_numpy(rng.standard_normal((n, 4, 128))).cuda() * scale * d[..., None].double()).to(torch.bfloat16)
+        c.call(k=x, v=x, k_descale=d, v_descale=d)()
+        torch.cuda.synchronize()
+        want = (x.float() / d[..., None]).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+        page = c.dev["block_table"][0, torch.arange(n, device="cuda") // 128].long()
+        row = torch.arange(n, device="cuda") % 128
+        for got in (c.kc, c.vc):
+            g = got[page, row]
+            nan = torch.isnan(x.float() / d[..., None])
+            assert torch.equal(torch.where(nan, 0x7F, g), torch.where(nan, 0x7F, want)), exps
+
+
 def test_graph_and_stream():
     c = Case([4, 4], [100, 3], packed=True, axes=3)
     call = c.call()

@@ -246,13 +246,16 @@ decode_tc_kernel(const std::conditional_t<kMod, DecodeModDev, DecodeDev> a, cons
       tile_jump = tile_jump > 0 ? tile_jump : 0;
     }
   }
-  // the sequence's tile of the item's tile i
+  // the sequence's tile of the item's i-th; modified scores go from the last
+  // to the first (a distance bias grows towards a row's own position: in
+  // rising order nearly every tile would move the maxima and correct O)
   auto seq_tile = [&](int i) {
-    const int v = t_begin + i;
-    if constexpr (kMod)
+    if constexpr (kMod) {
+      const int v = t_end - 1 - i;
       return v < prefix_tiles ? v : v + tile_jump;
-    else
-      return v;
+    } else {
+      return t_begin + i;
+    }
   };
   int first_page_raw = 0;
   if (warp == 0 && lane < ppt && seq_tile(0) * ppt + lane < a.max_blocks)

@@ -97,36 +97,82 @@ __device__ __forceinline__ float tanh_any(float t) {
   return at < kTanhSmall ? tanh_small(t) : big;
 }
 
+// Scores s[0..N) (N even) over the cap, t = s c1, -> cap2 tanh(t) + b, where
+// b(e) gives the addend of score e.  Scores small against the cap (most, in
+// practice) take the polynomial, two a time; a warp with others takes the
+// exponential form for all of them.
+template <int N, typename Bias>
+__device__ __forceinline__ void cap_scores(float* s, float c1, float cap2, Bias b) {
+  const float2 c12 = make_float2(c1, c1), cap22 = make_float2(cap2, cap2);
+  float2 sq[N / 2];
+  float top = 0.f;
+#pragma unroll
+  for (int e = 0; e < N / 2; ++e) {
+    const float2 t = mul2(make_float2(s[2 * e], s[2 * e + 1]), c12);
+    sq[e] = mul2(t, t);
+    top = fmax3(top, sq[e].x, sq[e].y);
+    s[2 * e] = t.x;
+    s[2 * e + 1] = t.y;
+  }
+  if (__all_sync(0xffffffffu, top < kTanhSmall * kTanhSmall)) {
+#pragma unroll
+    for (int e = 0; e < N / 2; ++e) {
+      const float2 y = mul2(make_float2(s[2 * e], s[2 * e + 1]), tanh_ratio2(sq[e]));
+      const float2 o = fma2(y, cap22, make_float2(b(2 * e), b(2 * e + 1)));
+      s[2 * e] = o.x;
+      s[2 * e + 1] = o.y;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e) s[e] = fmaf(tanh_any(s[e]), cap2, b(e));
+  }
+}
+
 // Raw scores r[0..N) (fp32 bits) of one row at keys j0 .. j0 + N - 1 -> logits
 // in log2 units, in place.
 //   c1: raw score -> t = z / softcap, or (no cap) -> log2 units
 //   cap2: softcap in log2 units (0: no cap)
-//   slope2, pos: distance bias in log2 units (0: none)
+//   slope2, pos_minus_j0: the row's bias in log2 units per position (0: none)
 template <int N>
-__device__ __forceinline__ void modify_scores(uint32_t* r, float c1, float cap2, float slope2, float pos_minus_j0) {
+__device__ __forceinline__ void modify_scores(uint32_t* r, float c1, float cap2, bool bias, float slope2,
+                                              float pos_minus_j0) {
   float s[N];
 #pragma unroll
   for (int e = 0; e < N; ++e) s[e] = __uint_as_float(r[e]);
-  if (cap2 > 0.f) {
-    float top = 0.f;
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
-      s[e] *= c1;
-      top = fmaxf(top, fabsf(s[e]));
-    }
-    // scores small against the cap (most, in practice) need no exponential
-    if (__all_sync(0xffffffffu, top < kTanhSmall)) {
-#pragma unroll
-      for (int e = 0; e < N; ++e) s[e] = cap2 * tanh_small(s[e]);
+  if (!bias) {
+    if (cap2 > 0.f) {
+      cap_scores<N>(s, c1, cap2, [](int) { return 0.f; });
     } else {
 #pragma unroll
-      for (int e = 0; e < N; ++e) s[e] = cap2 * tanh_any(s[e]);
+      for (int e = 0; e < N; ++e) s[e] *= c1;
+    }
+  } else if (__all_sync(0xffffffffu, pos_minus_j0 >= static_cast<float>(N - 1))) {
+    // no key past its row (a warp's usual case): -slope (pos - j0 - e) is
+    // linear in e, one fma a score
+    const float base = -slope2 * pos_minus_j0;
+    auto linear = [&](int e) { return fmaf(slope2, static_cast<float>(e), base); };
+    if (cap2 > 0.f) {
+      cap_scores<N>(s, c1, cap2, linear);
+    } else {  // four running pairs of addends
+      const float2 c12 = make_float2(c1, c1), step = make_float2(8.f * slope2, 8.f * slope2);
+      float2 b[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) b[i] = make_float2(linear(2 * i), linear(2 * i + 1));
+#pragma unroll
+      for (int e = 0; e < N / 2; ++e) {
+        const float2 o = fma2(make_float2(s[2 * e], s[2 * e + 1]), c12, b[e & 3]);
+        b[e & 3] = add2(b[e & 3], step);
+        s[2 * e] = o.x;
+        s[2 * e + 1] = o.y;
+      }
     }
   } else {
+    if (cap2 > 0.f) {
+      cap_scores<N>(s, c1, cap2, [](int) { return 0.f; });
+    } else {
 #pragma unroll
-    for (int e = 0; e < N; ++e) s[e] *= c1;
-  }
-  if (slope2 != 0.f) {
+      for (int e = 0; e < N; ++e) s[e] *= c1;
+    }
 #pragma unroll
     for (int e = 0; e < N; ++e) s[e] = fmaf(-slope2, fabsf(pos_minus_j0 - static_cast<float>(e)), s[e]);
   }
@@ -139,19 +185,11 @@ __device__ __forceinline__ void modify_scores(uint32_t* r, float c1, float cap2,
 template <int N>
 __device__ __forceinline__ void modify_columns(float* s, float c1, float cap2, bool bias, const float* slope2,
                                                const float* pos, float key) {
-#pragma unroll
-  for (int c = 0; c < N; ++c) s[c] *= c1;
   if (cap2 > 0.f) {
-    float top = 0.f;
+    cap_scores<N>(s, c1, cap2, [](int) { return 0.f; });
+  } else {
 #pragma unroll
-    for (int c = 0; c < N; ++c) top = fmaxf(top, fabsf(s[c]));
-    if (__all_sync(0xffffffffu, top < kTanhSmall)) {
-#pragma unroll
-      for (int c = 0; c < N; ++c) s[c] = cap2 * tanh_small(s[c]);
-    } else {
-#pragma unroll
-      for (int c = 0; c < N; ++c) s[c] = cap2 * tanh_any(s[c]);
-    }
+    for (int c = 0; c < N; ++c) s[c] *= c1;
   }
   if (bias) {
 #pragma unroll

@@ -237,7 +237,8 @@ def _prepare_rope(c, gen):
 
 def _decode_params(mj, c, s):
     return mj.make_params(c["seqs"], c["q_len"], c["h_k"], c["h_r"], c["page"], int(s["table"].shape[1]), s["pages"],
-                          causal=c.get("causal", True), q_dtype=mj.MJ_E4M3 if c["q8"] else mj.MJ_BF16, max_splits=64)
+                          causal=c.get("causal", True), q_dtype=mj.MJ_E4M3 if c["q8"] else mj.MJ_BF16,
+                          max_splits=256 if c["seqs"] * c["h_k"] <= 64 else 64)  # few heads: as many as the library takes
 
 
 def _prepare_attn(c, gen):

@@ -442,29 +442,39 @@ decode_qm_kernel(const std::conditional_t<kMod, DecodeModDev, DecodeDev> a, cons
     const float kd = a.kd[b * a.kd_seq + g * a.kd_head];
     const float vd = a.vd[b * a.vd_seq + g * a.vd_head];
 
-    // ---- Q row r -> two (bf16) or one (e4m3) K-major operand rows (group 0;
-    // paired q tiles: each group its own tile, with its own scaling)
+    // ---- Q rows -> two (bf16) or one (e4m3) K-major operand rows (group 0;
+    // paired q tiles: each group its own tile, with its own scaling).  A warp
+    // lays out its 32 rows, the lanes of a load side by side in a row (whole
+    // lines; a row a lane would take 32 of them an instruction).
     uint8_t* const qbase = sm + C::kOffQ + (kPair ? wg * C::kQParts * kPartBytes : 0);
     int* const q_shift_g = q_shift + (kPair ? wg : 0);
     float* const amax_g = amax_red + (kPair ? 4 * wg : 0);
     if (kPair || wg == 0) {
-      uint4 raw[kQe4m3 ? 8 : 16];
-      const int64_t off = b * a.q_seq + (static_cast<int64_t>(g) * a.n_q + (live ? qrow : 0)) * kHeadDimDev;
+      constexpr int kLanes = kQe4m3 ? 8 : 16;  // lanes of 16 bytes a row
+      constexpr int kLoads = kLanes;           // loads of 32 / kLanes rows each
+      const int piece = lane % kLanes;
+      const int first_row = n0 + (kPair ? wg * kRows : 0);
+      uint4 raw[kLoads];
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k) {
+        const int rr = quarter * 32 + k * (32 / kLanes) + lane / kLanes;  // row of the tile
+        const int n = first_row + rr % kR;
+        raw[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (n < a.n_q) {
+          const int64_t off = b * a.q_seq + (static_cast<int64_t>(g) * a.n_q + n) * kHeadDimDev;
+          raw[k] = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.q) + off * (kQe4m3 ? 1 : 2))[piece];
+        }
+      }
       if (kQe4m3) {
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.q) + off);
 #pragma unroll
-        for (int cc = 0; cc < 8; ++cc) raw[cc] = live ? src[cc] : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int cc = 0; cc < 8; ++cc) *reinterpret_cast<uint4*>(swz(qbase, r, cc)) = raw[cc];
+        for (int k = 0; k < kLoads; ++k)
+          *reinterpret_cast<uint4*>(swz(qbase, quarter * 32 + k * (32 / kLanes) + lane / kLanes, piece)) = raw[k];
         if (st_tid == 0) *q_shift_g = 0;
       } else {
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + off);
-#pragma unroll
-        for (int w = 0; w < 16; ++w) raw[w] = live ? src[w] : make_uint4(0u, 0u, 0u, 0u);
         uint32_t mbits = 0;  // bf16 |q| max: integer max of the magnitude bits
 #pragma unroll
-        for (int w = 0; w < 16; ++w) {
-          const uint32_t v4[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
+        for (int k = 0; k < kLoads; ++k) {
+          const uint32_t v4[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) mbits = max(mbits, max(v4[e] & 0x7FFFu, (v4[e] >> 16) & 0x7FFFu));
         }
@@ -482,27 +492,28 @@ decode_qm_kernel(const std::conditional_t<kMod, DecodeModDev, DecodeDev> a, cons
         }
         const float qscale = ldexpf(1.f, shift);
 #pragma unroll
-        for (int cc = 0; cc < 8; ++cc) {  // 16 elements = two 16-byte words of bf16
-          uint32_t hw[4], lw[4];
-          const uint32_t w8[8] = {raw[2 * cc].x,     raw[2 * cc].y,     raw[2 * cc].z,     raw[2 * cc].w,
-                                  raw[2 * cc + 1].x, raw[2 * cc + 1].y, raw[2 * cc + 1].z, raw[2 * cc + 1].w};
+        for (int k = 0; k < kLoads; ++k) {  // eight elements: half a 16-byte chunk of each part
+          const int rr = quarter * 32 + k * (32 / kLanes) + lane / kLanes;
+          const uint32_t w4[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+          uint32_t hw[2], lw[2];
 #pragma unroll
-          for (int wi = 0; wi < 4; ++wi) {
+          for (int wi = 0; wi < 2; ++wi) {
             float x[4], hf[4];
-            x[0] = __uint_as_float(w8[2 * wi] << 16) * qscale;
-            x[1] = __uint_as_float(w8[2 * wi] & 0xFFFF0000u) * qscale;
-            x[2] = __uint_as_float(w8[2 * wi + 1] << 16) * qscale;
-            x[3] = __uint_as_float(w8[2 * wi + 1] & 0xFFFF0000u) * qscale;
+            x[0] = __uint_as_float(w4[2 * wi] << 16) * qscale;
+            x[1] = __uint_as_float(w4[2 * wi] & 0xFFFF0000u) * qscale;
+            x[2] = __uint_as_float(w4[2 * wi + 1] << 16) * qscale;
+            x[3] = __uint_as_float(w4[2 * wi + 1] & 0xFFFF0000u) * qscale;
             const uint16_t h01 = ptx::f32x2_to_e4m3x2(x[0], x[1]);
             const uint16_t h23 = ptx::f32x2_to_e4m3x2(x[2], x[3]);
-            e4m3x4_to_f32(static_cast<uint32_t>(h01) | (static_cast<uint32_t>(h23) << 16), hf);
+            hw[wi] = static_cast<uint32_t>(h01) | (static_cast<uint32_t>(h23) << 16);
+            e4m3x4_to_f32(hw[wi], hf);
             const uint16_t l01 = ptx::f32x2_to_e4m3x2(x[0] - hf[0], x[1] - hf[1]);
             const uint16_t l23 = ptx::f32x2_to_e4m3x2(x[2] - hf[2], x[3] - hf[3]);
-            hw[wi] = static_cast<uint32_t>(h01) | (static_cast<uint32_t>(h23) << 16);
             lw[wi] = static_cast<uint32_t>(l01) | (static_cast<uint32_t>(l23) << 16);
           }
-          *reinterpret_cast<uint4*>(swz(qbase, r, cc)) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-          *reinterpret_cast<uint4*>(swz(qbase + kPartBytes, r, cc)) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+          const int half = (piece & 1) * 8;
+          *reinterpret_cast<uint2*>(swz(qbase, rr, piece >> 1) + half) = make_uint2(hw[0], hw[1]);
+          *reinterpret_cast<uint2*>(swz(qbase + kPartBytes, rr, piece >> 1) + half) = make_uint2(lw[0], lw[1]);
         }
         if (st_tid == 0) *q_shift_g = shift;
       }
@@ -578,12 +589,17 @@ decode_qm_kernel(const std::conditional_t<kMod, DecodeModDev, DecodeDev> a, cons
     #pragma unroll
             for (int c0 = 0; c0 < kCh; c0 += 16) MJ_TMEM_LD16(tmem_s + h0 + c0, (rr + c0));
             ptx::tmem_ld_wait();
-            if constexpr (kMod) {  // logits, back over S for pass 2
-              modify_scores<kCh>(rr, mod_c1, cap2, a.mod.slopes != nullptr, slope2, row_pos - static_cast<float>(key0 + h0));
+            if constexpr (kMod) {  // logits, masked, back over S for pass 2
+              modify_scores<kCh>(rr, mod_c1, cap2, a.mod.slopes != nullptr, slope2,
+                                 row_pos - static_cast<float>(key0 + h0));
+              if (!unmasked) {
+#pragma unroll
+                for (int e = 0; e < kCh; ++e) rr[e] = visible(key0 + h0 + e) ? rr[e] : 0xFF800000u;  // -inf
+              }
 #pragma unroll
               for (int c0 = 0; c0 < kCh; c0 += 16) MJ_TMEM_ST16(tmem_s + h0 + c0, (rr + c0));
             }
-            if (unmasked) {
+            if (kMod || unmasked) {
     #pragma unroll
               for (int e = 0; e < kCh; e += 2) mt = fmax3(mt, __uint_as_float(rr[e]), __uint_as_float(rr[e + 1]));
             } else {
@@ -655,7 +671,7 @@ decode_qm_kernel(const std::conditional_t<kMod, DecodeModDev, DecodeDev> a, cons
                 for (int pr = 0; pr < 2; ++pr) {
                   const int e0 = q * 16 + wi * 4 + pr * 2;
                   float s0 = __uint_as_float(rr[e0]), s1 = __uint_as_float(rr[e0 + 1]);
-                  if (!unmasked) {
+                  if (!kMod && !unmasked) {
                     const int c = h0 + e0;
                     s0 = visible(key0 + c) ? s0 : -INFINITY;
                     s1 = visible(key0 + c + 1) ? s1 : -INFINITY;
@@ -734,40 +750,53 @@ decode_qm_kernel(const std::conditional_t<kMod, DecodeModDev, DecodeDev> a, cons
         const float l = lraw * kPScaleInv;
         const float f = vd * kPScaleInv * (final_out ? a.scale_o / (l + 1e-30f) : 1.f);
         const bool writer = live;
+        // A thread holds a row, and a row's 16-byte pieces stored by 32 lanes
+        // 256 or 512 bytes apart are 32 half-used sectors an instruction: the
+        // rows go through the warp's part of the group's P buffers (free by
+        // now), 64 columns at a time, 16-byte chunk c of row r at chunk
+        // c ^ (r % 16), and leave as whole lines
+        float4* const rows_x = reinterpret_cast<float4*>(pbuf + quarter * 8192);  // [32][16]
 #pragma unroll 1
-        for (int c0 = 0; c0 < kRows; c0 += 16) {
-          uint32_t ra[16], rb[16];
-          MJ_TMEM_LD16(tmem_o + c0, ra);
-          if constexpr (kPair) {
+        for (int h0 = 0; h0 < kRows; h0 += 64) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) rb[e] = 0u;  // no second group's state (f1 = 0)
-          } else {
-            MJ_TMEM_LD16(o1 + c0, rb);
-          }
-          ptx::tmem_ld_wait();
-          float v[16];
-          // select, not multiply: a group with no key left its O stale
+          for (int c0 = 0; c0 < 64; c0 += 16) {
+            uint32_t ra[16], rb[16];
+            MJ_TMEM_LD16(tmem_o + h0 + c0, ra);
+            if constexpr (kPair) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            v[e] = ((f0 > 0.f ? __uint_as_float(ra[e]) * f0 : 0.f) + (f1 > 0.f ? __uint_as_float(rb[e]) * f1 : 0.f));
-          if (!writer) continue;
-#pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] *= f;
-          if (final_out) {
-            uint32_t pk[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const __nv_bfloat162 v2 = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
-              pk[e] = *reinterpret_cast<const uint32_t*>(&v2);
+              for (int e = 0; e < 16; ++e) rb[e] = 0u;  // no second group's state (f1 = 0)
+            } else {
+              MJ_TMEM_LD16(o1 + h0 + c0, rb);
             }
-            uint4* dst = reinterpret_cast<uint4*>(a.o + orow + c0);
-            dst[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-            dst[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-          } else {
-            float4* dst = reinterpret_cast<float4*>(a.o_part + orow + c0);
+            ptx::tmem_ld_wait();
+            float v[16];
+            // select, not multiply: a group with no key left its O stale
 #pragma unroll
-            for (int e = 0; e < 4; ++e) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            for (int e = 0; e < 16; ++e)
+              v[e] = ((f0 > 0.f ? __uint_as_float(ra[e]) * f0 : 0.f) + (f1 > 0.f ? __uint_as_float(rb[e]) * f1 : 0.f));
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] *= f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              rows_x[lane * 16 + ((c0 / 4 + e) ^ (lane & 15))] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
           }
+          __syncwarp();
+          // 16 lanes a row of 64 columns, two rows at a time
+#pragma unroll 4
+          for (int rr = lane >> 4; rr < 32; rr += 2) {
+            const float4 x = rows_x[rr * 16 + ((lane & 15) ^ (rr & 15))];
+            const int64_t at = __shfl_sync(0xffffffffu, orow, rr) + h0 + (lane & 15) * 4;
+            const bool on = __shfl_sync(0xffffffffu, static_cast<int>(writer), rr) != 0;
+            if (!on) continue;
+            if (final_out) {
+              const __nv_bfloat162 lo2 = __floats2bfloat162_rn(x.x, x.y), hi2 = __floats2bfloat162_rn(x.z, x.w);
+              *reinterpret_cast<uint2*>(a.o + at) =
+                  make_uint2(*reinterpret_cast<const uint32_t*>(&lo2), *reinterpret_cast<const uint32_t*>(&hi2));
+            } else {
+              *reinterpret_cast<float4*>(a.o_part + at) = x;
+            }
+          }
+          __syncwarp();
         }
         if (writer) {
           const float m_logit = mrow * scale_l;
@@ -819,8 +848,14 @@ decode_qm_kernel(const std::conditional_t<kMod, DecodeModDev, DecodeDev> a, cons
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(wgbar(wg, 1));
         if (warp_live) {
-          if constexpr (kMod) modify_scores<kR>(sv, mod_c1, cap2, a.mod.slopes != nullptr, slope2, row_pos - static_cast<float>(key0 + cb));
-          if (unmasked) {
+          if constexpr (kMod) {  // logits, masked here for both passes
+            modify_scores<kR>(sv, mod_c1, cap2, a.mod.slopes != nullptr, slope2, row_pos - static_cast<float>(key0 + cb));
+            if (!unmasked) {
+#pragma unroll
+              for (int e = 0; e < kR; ++e) sv[e] = visible(key0 + cb + e) ? sv[e] : 0xFF800000u;  // -inf
+            }
+          }
+          if (kMod || unmasked) {
   #pragma unroll
             for (int e = 0; e < kR; e += 2) mt = fmax3(mt, __uint_as_float(sv[e]), __uint_as_float(sv[e + 1]));
           } else {
@@ -886,7 +921,7 @@ decode_qm_kernel(const std::conditional_t<kMod, DecodeModDev, DecodeDev> a, cons
               for (int pr = 0; pr < 2; ++pr) {
                 const int e0 = q * 16 + wi * 4 + pr * 2;
                 float s0 = __uint_as_float(sv[e0]), s1 = __uint_as_float(sv[e0 + 1]);
-                if (!unmasked) {
+                if (!kMod && !unmasked) {
                   s0 = visible(key0 + cb + e0) ? s0 : -INFINITY;
                   s1 = visible(key0 + cb + e0 + 1) ? s1 : -INFINITY;
                 }

@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
       k_max = k > k_max && k != 0xFFFFFFFFu ? k : k_max;
     };
     const int quads = wide ? n / 4 : 0;
-    constexpr int kBatch = 4;  // loads in flight a thread, before any of their stores
+    constexpr int kBatch = 2;  // loads in flight a thread, before any of their stores
     for (int v0 = tid; v0 < quads; v0 += kBatch * kSelThreads) {
       float4 w[kBatch];
       int4 p[kBatch];
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
   // prefix found so far are kept
   uint32_t prefix = 0;
   int need = fresh;
-  int left_bits = bits;
+  int left_bits = bits, last_pass = 0;
   for (int pass = 0; pass < passes; ++pass) {
     const int width = left_bits < 11 ? left_bits : 11, above = left_bits;
     left_bits -= width;
@@ -301,9 +301,11 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
     __syncthreads();
     prefix |= s.bin << shift;
     need = s.need;
+    last_pass = pass;
+    if (s.bin_count == need) break;  // the whole bin is kept: the lower digits do not matter
   }
   static_assert(kSelThreads * 4 == kBins, "four bins a thread");
-  const int* const last_hist = s.hist[(passes - 1) & 1];
+  const int* const last_hist = s.hist[last_pass & 1];
   const uint32_t last_bin = s.bin;
   // keys above the threshold are kept, and of the ties (equal to it) the
   // first `need`; those of lower runs are in the last histogram

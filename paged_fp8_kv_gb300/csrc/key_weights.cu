@@ -7,7 +7,11 @@
 // the rows' e4m3 parts operand B), so a TMEM lane is a key, its row sum is
 // thread-local, and one coalesced 4-byte store a key is all that leaves.  The
 // logits and the row sums are fp32; bf16 Q is split into hi + lo e4m3 parts
-// as in the decode kernels (exact down to 2^-10 of the scaled row maximum).
+// as in the decode kernels (exact down to 2^-10 of the scaled row maximum),
+// up to 16 rows side by side in one MMA a K step with their products added in
+// registers (half the MMA issues, 70 to 100 cycles each: 4 rows 65 -> 61 us;
+// at 32 rows the additions cost as much as they save: 126 -> 130), else into
+// one accumulator.
 // With lse known there is no running maximum and nothing to merge, so the
 // plan's items are only a list of tiles: it is cut evenly, whatever the items'
 // lengths, into shares for which every kv head has a resident CTA, and a CTA
@@ -32,6 +36,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "mj_kernels.h"
 #include "score_mod.cuh"
 #include "sm100_ptx.cuh"
@@ -46,6 +52,7 @@ constexpr int kStatusTimeout = 5;            // MJ_ERR_TIMEOUT
 constexpr int kThreads = 64 + 256;
 constexpr int kMaxStages = 8;
 constexpr int kBarCons = 1;  // named barrier of the 256 consumer threads
+constexpr int kStackRows = 16;   // bf16 rows up to which both parts go into one MMA
 constexpr int kTwoCtaRows = 64;  // rows up to which two CTAs share an SM
 
 struct KwArgs {
@@ -56,10 +63,12 @@ struct KwArgs {
   float decay;
   int32_t fresh;
   int32_t n0, n_rows;  // packed rows of this launch
-  int32_t n_mma;       // n_rows rounded up to 16: the MMA's N
+  int32_t rows;        // n_rows rounded up: 8, or a multiple of 16
+  int32_t n_mma;       // the MMA's N: rows (at least 16), or both parts of them
+  int32_t stacked;     // bf16 Q: hi and lo rows side by side in one MMA
   int32_t stages;
   int32_t tmem_cols;
-  int32_t s_bufs;      // S buffers of each group: 2, or 1 above 128 rows
+  int32_t s_bufs;      // S buffers of each group: 1 or 2
   int32_t off_q, off_stage, off_row, off_bar;  // shared memory, from the 1 KB boundary
 };
 
@@ -326,14 +335,16 @@ __global__ void __launch_bounds__(kThreads, 2)
     // (the whole warp walks and takes the limits; lane 0 waits and issues)
     const uint32_t idesc = ptx::idesc_f8f6f4(kKeys, p.n_mma, false, false, kv_mma_format(a.kv_format), 0);
     const uint64_t kdesc0 = ptx::smem_desc(sbase, 16, 1024, ptx::kSwizzle128B);
-    const uint64_t part_step = static_cast<uint64_t>(p.n_mma * 128) >> 4;
+    const uint64_t part_step = static_cast<uint64_t>(p.rows * 128) >> 4;
+    const int parts = kParts == 2 && !p.stacked ? 2 : 1;  // MMAs a K step
+    const int q_bytes = (kParts == 2 ? 2 * p.rows : p.n_mma) * 128;  // of one segment's operand rows
     int u = 0, s = 0;  // tiles, segments with a seen tile (only those have a Q buffer)
     bool ok = true;
     while (ok && walk.next(sg)) {
       const Limits lim = warp_limits<kMod>(p, sg.b, length_of(sg.b), lane);
       if (!lim.any(sg.t0, sg.t1)) continue;
       const uint64_t qdesc =
-          ptx::smem_desc(sbase + p.off_q + (s & 1) * p.n_mma * 128 * kParts, 16, 1024, ptx::kSwizzle128B);
+          ptx::smem_desc(sbase + p.off_q + (s & 1) * q_bytes, 16, 1024, ptx::kSwizzle128B);
       if (lane == 0) {
         ok = ptx::mbar_wait_bounded(qready(s & 1), (s >> 1) & 1, abort_flag, kWaitNs);
         for (int t = sg.t0; ok && t < sg.t1; ++t) {
@@ -350,9 +361,8 @@ __global__ void __launch_bounds__(kThreads, 2)
           const uint32_t d = tmem + s_cols(wg, n);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
-#pragma unroll
-            for (int part = 0; part < kParts; ++part)
-              ptx::mma_e4m3(d, kdesc + 2 * kk, qdesc + part * part_step + 2 * kk, idesc, (kk > 0 || part > 0) ? 1u : 0u);
+            ptx::mma_e4m3(d, kdesc + 2 * kk, qdesc + 2 * kk, idesc, kk > 0 ? 1u : 0u);
+            if (parts == 2) ptx::mma_e4m3(d, kdesc + 2 * kk, qdesc + part_step + 2 * kk, idesc, 1u);
           }
           ptx::mma_commit(sfull(buf_of(wg, n)));
           ptx::mma_commit(kempty(st));
@@ -377,6 +387,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     bool far = false;  // the last capped tile held scores past the polynomial's range
     const float cap2 = kMod ? a.mod.softcap * kLog2e : 0.f;
     const float2 cap22 = make_float2(cap2, cap2);
+    const TanhRatio ratio(cap2);
     int u = 0, s = 0;
     // the next segment's raw Q rows (this thread's 16-element chunks, by
     // asynchronous copies) and scalars are on their way during a segment
@@ -406,18 +417,18 @@ __global__ void __launch_bounds__(kThreads, 2)
       const float kd = kd_next, qd = qd_next;
       const Limits lim = warp_limits<kMod>(p, b, L, lane);
       cp_async_wait<0>();
-      float* const row_nlse2 = row_base + (s & 1) * 5 * p.n_mma;  // -lse in log2 units
-      float* const row_slope2 = row_nlse2 + p.n_mma;
-      float* const row_pos = row_slope2 + p.n_mma;
-      int* const row_lo = reinterpret_cast<int*>(row_pos + p.n_mma);
-      int* const row_hi = row_lo + p.n_mma;
-      uint8_t* const qbase = sm + p.off_q + (s & 1) * p.n_mma * 128 * kParts;
+      float* const row_nlse2 = row_base + (s & 1) * 5 * p.rows;  // -lse in log2 units
+      float* const row_slope2 = row_nlse2 + p.rows;
+      float* const row_pos = row_slope2 + p.rows;
+      int* const row_lo = reinterpret_cast<int*>(row_pos + p.rows);
+      int* const row_hi = row_lo + p.rows;
+      uint8_t* const qbase = sm + p.off_q + (s & 1) * (kParts == 2 ? 2 * p.rows : p.n_mma) * 128;
 
       int shift = 0;
       // ---- Q rows -> one (e4m3) or two (bf16: hi + lo) operand rows, a
       // 16-element chunk a thread and round
       if (lim.any(sg.t0, sg.t1)) {
-        const int chunks = p.n_mma * 8;
+        const int chunks = p.rows * 8;
         if constexpr (!kQe4m3) {
           uint32_t mbits = 0;  // bf16 |q| maximum: integer maximum of the magnitude bits
           for (int id = ct; id < p.n_rows * 8; id += 256) {
@@ -472,12 +483,12 @@ __global__ void __launch_bounds__(kThreads, 2)
               lw[wi] = static_cast<uint32_t>(l01) | (static_cast<uint32_t>(l23) << 16);
             }
             *reinterpret_cast<uint4*>(swz(qbase, r, cc)) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-            *reinterpret_cast<uint4*>(swz(qbase + p.n_mma * 128, r, cc)) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+            *reinterpret_cast<uint4*>(swz(qbase + p.rows * 128, r, cc)) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
           }
         }
         // ---- the rows' constants; a row past n_rows or without keys adds
         // 2^-inf (its scores are finite: Q's rows are zeros or data)
-        if (ct < p.n_mma) {
+        if (ct < p.rows) {
           const int n = p.n0 + ct;
           float nlse2 = -INFINITY, slope2 = 0.f;
           int lo = 0, hi = -1, pos = 0;
@@ -551,44 +562,62 @@ __global__ void __launch_bounds__(kThreads, 2)
           const bool ahead = key0 + kKeys - 1 > pos_min;  // some distance may be negative
           // the tile's row sums; capped scores by the polynomial (near) or by
           // the exponential form; returns whether all lay in its range
-          auto tile_sums = [&](bool near) {
+          auto sums_of = [&](auto width, bool near) {
+            constexpr int W = decltype(width)::value;  // columns at a time
             float top = 0.f;  // largest square of a score over the cap
             sum2 = make_float2(0.f, 0.f);
-            for (int c0 = 0; c0 < p.n_mma; c0 += 16) {
-              uint32_t r[16];
-              MJ_TMEM_LD16(tmem_s + c0, r);
-              ptx::tmem_ld_wait();
-              float2 y[8];
+            for (int c0 = 0; c0 < p.rows; c0 += W) {
+              uint32_t r[W];
+              if constexpr (W == 8)
+                MJ_TMEM_LD8(tmem_s + c0, r);
+              else
+                MJ_TMEM_LD16(tmem_s + c0, r);
+              if (!kQe4m3 && p.stacked) {  // the lo rows' products
+                uint32_t lo[W];
+                if constexpr (W == 8)
+                  MJ_TMEM_LD8(tmem_s + p.rows + c0, lo);
+                else
+                  MJ_TMEM_LD16(tmem_s + p.rows + c0, lo);
+                ptx::tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < W; e += 2) {
+                  const float2 x = add2(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])),
+                                        make_float2(__uint_as_float(lo[e]), __uint_as_float(lo[e + 1])));
+                  r[e] = __float_as_uint(x.x);
+                  r[e + 1] = __float_as_uint(x.y);
+                }
+              } else {
+                ptx::tmem_ld_wait();
+              }
+              float2 y[W / 2];
               if (kMod && cap2 > 0.f) {
                 if (near) {
 #pragma unroll
-                  for (int e = 0; e < 8; ++e) {
+                  for (int e = 0; e < W / 2; ++e) {
                     const float2 t = mul2(make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])), c12);
                     const float2 sq = mul2(t, t);
                     top = fmax3(top, sq.x, sq.y);
-                    y[e] = mul2(t, tanh_ratio2(sq));
+                    y[e] = fma2(t, ratio(sq), *reinterpret_cast<const float2*>(row_nlse2 + c0 + 2 * e));
                   }
                 } else {
 #pragma unroll
-                  for (int e = 0; e < 8; ++e) {
+                  for (int e = 0; e < W / 2; ++e) {
                     const float2 t = mul2(make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])), c12);
                     const float2 sq = mul2(t, t);
                     top = fmax3(top, sq.x, sq.y);
-                    y[e] = make_float2(tanh_any(t.x), tanh_any(t.y));
+                    y[e] = fma2(make_float2(tanh_any(t.x), tanh_any(t.y)), cap22,
+                                *reinterpret_cast<const float2*>(row_nlse2 + c0 + 2 * e));
                   }
                 }
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                  y[e] = fma2(y[e], cap22, *reinterpret_cast<const float2*>(row_nlse2 + c0 + 2 * e));
               } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
+                for (int e = 0; e < W / 2; ++e)
                   y[e] = fma2(make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])), c12,
                               *reinterpret_cast<const float2*>(row_nlse2 + c0 + 2 * e));
               }
               if (kMod && a.mod.slopes) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
+                for (int e = 0; e < W / 2; ++e) {
                   const float2 sl = *reinterpret_cast<const float2*>(row_slope2 + c0 + 2 * e);
                   float2 d = add2(*reinterpret_cast<const float2*>(row_pos + c0 + 2 * e), nkey2);
                   if (ahead) d = make_float2(fabsf(d.x), fabsf(d.y));
@@ -597,10 +626,10 @@ __global__ void __launch_bounds__(kThreads, 2)
               }
               if (whole) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) sum2 = add2(sum2, make_float2(fast_exp2(y[e].x), fast_exp2(y[e].y)));
+                for (int e = 0; e < W / 2; ++e) sum2 = add2(sum2, make_float2(fast_exp2(y[e].x), fast_exp2(y[e].y)));
               } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
+                for (int e = 0; e < W / 2; ++e) {
                   const int c = c0 + 2 * e;
                   const bool v0 = key < lim.pfx || (key >= row_lo[c] && key <= row_hi[c]);
                   const bool v1 = key < lim.pfx || (key >= row_lo[c + 1] && key <= row_hi[c + 1]);
@@ -610,6 +639,10 @@ __global__ void __launch_bounds__(kThreads, 2)
               }
             }
             return __all_sync(0xffffffffu, top < kTanhSmall * kTanhSmall);
+          };
+          auto tile_sums = [&](bool near) {
+            return p.rows == 8 ? sums_of(std::integral_constant<int, 8>{}, near)
+                               : sums_of(std::integral_constant<int, 16>{}, near);
           };
           if (kMod && cap2 > 0.f) {
             // most scores are small against a cap; a tile that holds others is
@@ -659,15 +692,19 @@ cudaError_t launch_key_weights(const DecodeModDev& a, bool q_e4m3, bool has_mod,
   p.fresh = fresh;
   p.n0 = n0;
   p.n_rows = n_rows;
-  p.n_mma = (n_rows + 15) / 16 * 16;
-  // S buffers: two of each group (the MMA runs a tile ahead), one above 128 rows
-  p.s_bufs = p.n_mma <= 128 ? 2 : 1;
+  p.rows = n_rows <= 8 ? 8 : (n_rows + 15) / 16 * 16;
+  p.stacked = !q_e4m3 && p.rows <= kStackRows;
+  p.n_mma = p.stacked ? 2 * p.rows : (p.rows < 16 ? 16 : p.rows);
+  const int per_sm = n_rows <= kTwoCtaRows ? 2 : 1;
+  // S buffers: two of each group (the MMA runs a tile ahead) where TMEM has
+  // the columns
+  p.s_bufs = 4 * p.n_mma <= 512 / per_sm ? 2 : 1;
   p.tmem_cols = 32;
   while (p.tmem_cols < 2 * p.s_bufs * p.n_mma) p.tmem_cols *= 2;
-  const int per_sm = n_rows <= kTwoCtaRows ? 2 : 1;
-  const int q_bytes = 2 * p.n_mma * 128 * (q_e4m3 ? 1 : 2);  // two segments' rows
-  const int row_bytes = 2 * 5 * p.n_mma * 4;
-  const int stage_bytes = p.n_mma * 128 * (q_e4m3 ? 1 : 2);
+  const int part_bytes = (q_e4m3 ? p.n_mma : 2 * p.rows) * 128;  // a segment's operand rows
+  const int q_bytes = 2 * part_bytes;                            // two segments'
+  const int row_bytes = 2 * 5 * p.rows * 4;
+  const int stage_bytes = p.rows * 128 * (q_e4m3 ? 1 : 2);
   const int tail = stage_bytes + row_bytes + 8 * (2 * kMaxStages + 12) + 256;
   const int limit = (per_sm == 2 ? 112 : 224) * 1024;
   p.stages = (limit - 1024 - q_bytes - tail) / kTileBytes;

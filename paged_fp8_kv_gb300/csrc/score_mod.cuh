@@ -80,15 +80,21 @@ __device__ __forceinline__ float rcp_approx(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// tanh(t) / t of two values of u = t^2, the same polynomial
-__device__ __forceinline__ float2 tanh_ratio2(float2 u) {
-  float2 p = make_float2(-5.852168662e-03f, -5.852168662e-03f);
-  p = fma2(p, u, make_float2(2.075362916e-02f, 2.075362916e-02f));
-  p = fma2(p, u, make_float2(-5.376870490e-02f, -5.376870490e-02f));
-  p = fma2(p, u, make_float2(1.333168896e-01f, 1.333168896e-01f));
-  p = fma2(p, u, make_float2(-3.333328326e-01f, -3.333328326e-01f));
-  return fma2(p, u, make_float2(9.999999975e-01f, 9.999999975e-01f));
-}
+// scale tanh(t) / t of two values of u = t^2: the same polynomial with its
+// coefficients times `scale` (one rounding each; a multiplication a pair less
+// than scaling the result)
+struct TanhRatio {
+  float c[6];
+  __device__ __forceinline__ explicit TanhRatio(float scale)
+      : c{-5.852168662e-03f * scale, 2.075362916e-02f * scale, -5.376870490e-02f * scale,
+          1.333168896e-01f * scale,  -3.333328326e-01f * scale, 9.999999975e-01f * scale} {}
+  __device__ __forceinline__ float2 operator()(float2 u) const {
+    float2 p = make_float2(c[0], c[0]);
+#pragma unroll
+    for (int i = 1; i < 6; ++i) p = fma2(p, u, make_float2(c[i], c[i]));
+    return p;
+  }
+};
 constexpr float kTanhSmall = 0.6f;
 __device__ __forceinline__ float tanh_any(float t) {
   const float at = fabsf(t);
@@ -103,7 +109,7 @@ __device__ __forceinline__ float tanh_any(float t) {
 // exponential form for all of them.
 template <int N, typename Bias>
 __device__ __forceinline__ void cap_scores(float* s, float c1, float cap2, Bias b) {
-  const float2 c12 = make_float2(c1, c1), cap22 = make_float2(cap2, cap2);
+  const float2 c12 = make_float2(c1, c1);
   float2 sq[N / 2];
   float top = 0.f;
 #pragma unroll
@@ -115,10 +121,10 @@ __device__ __forceinline__ void cap_scores(float* s, float c1, float cap2, Bias 
     s[2 * e + 1] = t.y;
   }
   if (__all_sync(0xffffffffu, top < kTanhSmall * kTanhSmall)) {
+    const TanhRatio ratio(cap2);
 #pragma unroll
     for (int e = 0; e < N / 2; ++e) {
-      const float2 y = mul2(make_float2(s[2 * e], s[2 * e + 1]), tanh_ratio2(sq[e]));
-      const float2 o = fma2(y, cap22, make_float2(b(2 * e), b(2 * e + 1)));
+      const float2 o = fma2(make_float2(s[2 * e], s[2 * e + 1]), ratio(sq[e]), make_float2(b(2 * e), b(2 * e + 1)));
       s[2 * e] = o.x;
       s[2 * e + 1] = o.y;
     }

@@ -53,6 +53,7 @@ constexpr int kThreads = 64 + 256;
 constexpr int kMaxStages = 8;
 constexpr int kBarCons = 1;  // named barrier of the 256 consumer threads
 constexpr int kStackRows = 16;   // bf16 rows up to which both parts go into one MMA
+constexpr int kItemCost = 3;     // tiles that a segment takes to start (0: 62 us for 55 on a decode batch; 2, 4 the same)
 constexpr int kTwoCtaRows = 64;  // rows up to which two CTAs share an SM
 
 struct KwArgs {
@@ -86,23 +87,23 @@ struct Segment {
 };
 struct Walk {
   const int4* work;
-  int num_work;
-  int w, t;      // where the next segment starts
-  int64_t left;  // tiles of the share still to come
+  int w, t;          // where the next segment starts
+  int w_end, t_end;  // the share ends before tile t_end of item w_end
   __device__ __forceinline__ bool next(Segment& s) {
-    while (left > 0 && w < num_work) {
+    while (w < w_end || (w == w_end && t < t_end)) {
       const int4 item = work[w];
-      const int tiles = item.z - item.y;
-      if (t >= tiles) {
-        t = 0;
+      const int tiles = w == w_end ? t_end : item.z - item.y;
+      const int t0 = t;
+      if (w == w_end) {
+        t = t_end;
+      } else {
         ++w;
-        continue;
+        t = 0;
       }
-      const int n = tiles - t < left ? tiles - t : static_cast<int>(left);
-      s = Segment{item.y + t, item.y + t + n, item.x};
-      t += n;
-      left -= n;
-      return true;
+      if (t0 < tiles) {
+        s = Segment{item.y + t0, item.y + tiles, item.x};
+        return true;
+      }
     }
     return false;
   }
@@ -178,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(misc + 4);
   float* const amax_red = reinterpret_cast<float*>(misc + 32);      // [8]
   int64_t* const scan_red = reinterpret_cast<int64_t*>(misc + 64);  // [10]
-  int* const walk_s = reinterpret_cast<int*>(misc + 160);           // w, t of the share's first tile
+  int* const walk_s = reinterpret_cast<int*>(misc + 160);           // (w, t) of the share's start and end
 
   const uint32_t bar0 = sbase + p.off_bar;
   auto kfull = [&](int s) { return bar0 + 8u * s; };
@@ -216,19 +217,21 @@ __global__ void __launch_bounds__(kThreads, 2)
     ptx::tmem_alloc(ptx::smem_u32(tmem_slot), p.tmem_cols);
     ptx::tmem_relinquish();
   }
-  // ---- this CTA's share: tiles [first, last) of the items' tiles in order,
-  // for one kv head; the CTAs of the other heads' shares run beside it
+  // ---- this CTA's share of the items' tiles in order, for one kv head; the
+  // CTAs of the other heads' shares run beside it.  An item costs its tiles
+  // and kItemCost more (the start of a segment); a cut inside that start falls
+  // on the item's first tile.
   const int g = blockIdx.x % a.h_k;
-  int64_t first, last;
   {
     const int per = (a.num_work + kThreads - 1) / kThreads;
     const int w0 = tid * per < a.num_work ? tid * per : a.num_work;
     const int w1 = w0 + per < a.num_work ? w0 + per : a.num_work;
-    int64_t mine = 0;
-    for (int w = w0; w < w1; ++w) {
+    auto cost = [&](int w) -> int64_t {
       const int4 item = work[w];
-      mine += item.z > item.y ? item.z - item.y : 0;
-    }
+      return item.z > item.y ? item.z - item.y + kItemCost : 0;
+    };
+    int64_t mine = 0;
+    for (int w = w0; w < w1; ++w) mine += cost(w);
     int64_t x = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -236,6 +239,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (lane >= o) x += y;
     }
     if (lane == 31) scan_red[warp] = x;
+    if (tid < 2) {  // a cut past every item (the last share's end)
+      walk_s[2 * tid] = a.num_work;
+      walk_s[2 * tid + 1] = 0;
+    }
     __syncthreads();
     int64_t before = x - mine, total = 0;
 #pragma unroll
@@ -244,18 +251,14 @@ __global__ void __launch_bounds__(kThreads, 2)
       total += scan_red[w];
     }
     const int shares = gridDim.x / a.h_k, share = blockIdx.x / a.h_k;
-    first = total * share / shares;
-    last = total * (share + 1) / shares;
-    if (before <= first && first < before + mine) {  // one thread: where the share starts
-      for (int w = w0;; ++w) {
-        const int4 item = work[w];
-        const int64_t tiles = item.z > item.y ? item.z - item.y : 0;
-        if (first < before + tiles) {
-          walk_s[0] = w;
-          walk_s[1] = static_cast<int>(first - before);
-          break;
-        }
-        before += tiles;
+    for (int cut = 0; cut < 2; ++cut) {
+      const int64_t at = total * (share + cut) / shares;
+      if (before <= at && at < before + mine) {  // one thread
+        int64_t c = before;
+        int w = w0;
+        while (at >= c + cost(w)) c += cost(w++);
+        walk_s[2 * cut] = w;
+        walk_s[2 * cut + 1] = at - c > kItemCost ? static_cast<int>(at - c) - kItemCost : 0;
       }
     }
   }
@@ -263,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  Walk walk{work, a.num_work, walk_s[0], walk_s[1], last - first};
+  Walk walk{work, walk_s[0], walk_s[1], walk_s[2], walk_s[3]};
   Segment sg;
   const int max_len = a.max_blocks * a.page_size;  // acc has no more slots
   auto length_of = [&](int b) {

@@ -41,8 +41,6 @@ namespace {
 
 constexpr int kThreads = 256;     // of the move kernel
 constexpr int kWarps = kThreads / 32;
-constexpr int kSelThreads = 512;  // of the selection
-constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxKeys = 49152;  // keys of a run in shared memory
@@ -61,13 +59,17 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
-__device__ __forceinline__ int4 ld_cluster_v4(uint32_t addr) {
-  int4 v;
-  asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
+template <int N>
+__device__ __forceinline__ void ld_cluster_n(uint32_t addr, int* v) {
+  static_assert(N == 2 || N == 4, "vector width");
+  if constexpr (N == 4) {
+    asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(addr)
+                 : "memory");
+  } else {
+    asm volatile("ld.shared::cluster.v2.b32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(addr) : "memory");
+  }
 }
 __device__ __forceinline__ int ld_cluster(uint32_t addr) {
   int v;
@@ -92,7 +94,8 @@ __device__ __forceinline__ int warp_sum_before(int v, int lane, int& total) {
 
 struct Shared {
   int hist[2][kBins];
-  int warp_sums[kSelWarps];
+  int warp_sums[32];
+  int warp_holes[32];
   int totals[4];  // holes, movers of this CTA
   uint32_t range[2];  // smallest key, largest unprotected key of this CTA
   uint32_t bin;
@@ -100,10 +103,14 @@ struct Shared {
   int bin_count;
 };
 
-__global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const EvictDev a, int cluster, int key_cap) {
+// T threads: 512, two CTAs an SM, or 1024 when the groups do not fill the GPU
+template <int T>
+__global__ void __launch_bounds__(T, 1024 / T) evict_select_kernel(const EvictDev a, int cluster, int key_cap) {
   // a programmatic dependent: no global access before the grid ahead is done
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
+  constexpr int kSelWarps = T / 32;
+  constexpr int kPer = kBins / T;  // bins a thread
   __shared__ __align__(16) Shared s;
   extern __shared__ uint32_t keys[];  // [key_cap] of this CTA's run
   const int bg = blockIdx.x / cluster, rank = blockIdx.x - bg * cluster;
@@ -128,7 +135,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
 
   if (L <= a.budget) {  // nothing leaves (uniform over the cluster)
     if (rank == 0 && tid == 0) a.counts[bg] = 0;
-    for (int i = tid; i < n; i += kSelThreads) {
+    for (int i = tid; i < n; i += T) {
       const int j = begin + i;
       if (copy_acc) a.acc_out[off + j] = acc[j];
       if (copy_pos) a.key_pos_out[off + j] = pos[j];
@@ -161,18 +168,18 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
     };
     const int quads = wide ? n / 4 : 0;
     constexpr int kBatch = 2;  // loads in flight a thread, before any of their stores
-    for (int v0 = tid; v0 < quads; v0 += kBatch * kSelThreads) {
+    for (int v0 = tid; v0 < quads; v0 += kBatch * T) {
       float4 w[kBatch];
       int4 p[kBatch];
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        const int v = v0 + u * kSelThreads, j = begin + 4 * v;
+        const int v = v0 + u * T, j = begin + 4 * v;
         if (v < quads) w[u] = *reinterpret_cast<const float4*>(acc + j);
         p[u] = pos && v < quads ? *reinterpret_cast<const int4*>(pos + j) : make_int4(j, j + 1, j + 2, j + 3);
       }
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        const int v = v0 + u * kSelThreads, j = begin + 4 * v;
+        const int v = v0 + u * T, j = begin + 4 * v;
         if (v >= quads) break;
         take(4 * v, w[u].x, p[u].x);
         take(4 * v + 1, w[u].y, p[u].y);
@@ -193,7 +200,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
         }
       }
     }
-    for (int i = 4 * quads + tid; i < n; i += kSelThreads) {
+    for (int i = 4 * quads + tid; i < n; i += T) {
       const int j = begin + i;
       const float w = acc[j];
       const int p = pos ? pos[j] : j;
@@ -204,7 +211,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
       }
     }
   }
-  for (int i = tid; i < 2 * kBins; i += kSelThreads) (&s.hist[0][0])[i] = 0;
+  for (int i = tid; i < 2 * kBins; i += T) (&s.hist[0][0])[i] = 0;
   if (tid < 2) s.range[tid] = tid == 0 ? 0xFFFFFFFFu : 0u;
   __syncthreads();
   k_min = __reduce_min_sync(0xffffffffu, k_min);
@@ -241,13 +248,13 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
     const int shift = left_bits;
     int* const hist = s.hist[pass & 1];
     if (pass == 2) {  // every CTA has read pass 0's counts (it passed pass 1's barrier)
-      for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
+      for (int i = tid; i < kBins; i += T) hist[i] = 0;
       __syncthreads();
     }
     const uint32_t mask = (1u << width) - 1u;
     // (above = 32 only when every bit is left: then all keys match)
 #pragma unroll 8
-    for (int i = tid; i < n; i += kSelThreads) {
+    for (int i = tid; i < n; i += T) {
       const uint32_t k = digits_of(key_of(i));
       if (pass == 0 || (k >> above) == (prefix >> above)) atomicAdd(&hist[(k >> shift) & mask], 1);
     }
@@ -255,31 +262,32 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
       cluster_sync();
     else
       __syncthreads();
-    // every CTA sums the cluster's counts: thread t four bins, the highest
+    // every CTA sums the cluster's counts: thread t a few bins, the highest
     // first, so that a prefix sum over the threads counts the larger keys
-    const int q = kSelThreads - 1 - tid;
-    int4 v = *reinterpret_cast<const int4*>(hist + 4 * q);
-    int c[4] = {v.w, v.z, v.y, v.x};
+    const int q = T - 1 - tid;
+    int c[kPer];
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) c[e] = hist[kPer * q + kPer - 1 - e];
     if (cluster > 1) {
       // (three other CTAs' counts in flight, each CTA going round from its own
       // neighbour: all reading one at a time would queue on that one's SM)
-      const uint32_t mine = ptx::smem_u32(hist + 4 * q);
+      const uint32_t mine = ptx::smem_u32(hist + kPer * q);
       for (int r0 = 1; r0 < cluster; r0 += 3) {
-        int4 o[3];
+        int o[3][kPer];
 #pragma unroll
         for (int u = 0; u < 3; ++u)
-          if (r0 + u < cluster) o[u] = ld_cluster_v4(map_rank(mine, (rank + r0 + u) & (cluster - 1)));
+          if (r0 + u < cluster) ld_cluster_n<kPer>(map_rank(mine, (rank + r0 + u) & (cluster - 1)), o[u]);
 #pragma unroll
         for (int u = 0; u < 3; ++u) {
           if (r0 + u >= cluster) break;
-          c[0] += o[u].w;
-          c[1] += o[u].z;
-          c[2] += o[u].y;
-          c[3] += o[u].x;
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) c[e] += o[u][kPer - 1 - e];
         }
       }
     }
-    const int sum = c[0] + c[1] + c[2] + c[3];
+    int sum = 0;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) sum += c[e];
     int total;
     int before = warp_sum_before(sum, lane, total);
     if (lane == 31) s.warp_sums[warp] = total;
@@ -289,9 +297,9 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
     if (before < need && need <= before + sum) {  // one thread: the threshold's digit is among its bins
       int left = need - before;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
+      for (int e = 0; e < kPer; ++e) {
         if (left > 0 && left <= c[e]) {
-          s.bin = 4 * q + 3 - e;
+          s.bin = kPer * q + kPer - 1 - e;
           s.need = left;
           s.bin_count = c[e];
         }
@@ -304,7 +312,6 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
     last_pass = pass;
     if (s.bin_count == need) break;  // the whole bin is kept: the lower digits do not matter
   }
-  static_assert(kSelThreads * 4 == kBins, "four bins a thread");
   const int* const last_hist = s.hist[last_pass & 1];
   const uint32_t last_bin = s.bin;
   // keys above the threshold are kept, and of the ties (equal to it) the
@@ -330,11 +337,10 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
     __syncthreads();
     for (int w = 0; w < warp; ++w) tie_rank += s.warp_sums[w];
   }
-  // keep flags of a row of 32 slots, as ballots: holes and movers
-  auto flags = [&](int r, int& ties, uint32_t& holes, uint32_t& movers) {
+  // keep flags of a row of 32 slots (key offsets k), as ballots: holes and movers
+  auto flags = [&](int r, uint32_t k, int& ties, uint32_t& holes, uint32_t& movers) {
     const int i = r * 32 + lane;
     const bool in = i < n;
-    const uint32_t k = in ? digits_of(key_of(i)) : 0u;
     bool keep = in && k >= prefix;
     if (!all_ties) {
       const uint32_t tie = __ballot_sync(0xffffffffu, in && k == prefix);
@@ -345,21 +351,37 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
     holes = __ballot_sync(0xffffffffu, in && j < fresh && !keep);
     movers = __ballot_sync(0xffffffffu, keep && j >= fresh);
   };
+  auto row_key = [&](int r) {
+    const int i = r * 32 + lane;
+    return r < row1 && i < n ? digits_of(key_of(i)) : 0u;
+  };
   int n_holes = 0, n_movers = 0, ties = tie_rank;
-#pragma unroll 4
-  for (int r = row0; r < row1; ++r) {
-    uint32_t h, m;
-    flags(r, ties, h, m);
-    n_holes += __popc(h);
-    n_movers += __popc(m);
-    if (cached && lane < 2) keys[r * 32 + lane] = lane == 0 ? h : m;  // over the row's keys, done with
+  constexpr int kRows = 4;  // rows' keys read before any of their flags is stored
+  for (int r0 = row0; r0 < row1; r0 += kRows) {
+    uint32_t k[kRows];
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) k[u] = row_key(r0 + u);
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const int r = r0 + u;
+      if (r >= row1) break;
+      uint32_t h, m;
+      flags(r, k[u], ties, h, m);
+      n_holes += __popc(h);
+      n_movers += __popc(m);
+      if (cached && lane < 2) keys[r * 32 + lane] = lane == 0 ? h : m;  // over the row's keys, done with
+    }
   }
   __syncthreads();
-  if (lane == 0) s.warp_sums[warp] = n_holes | (n_movers << 16);
+  if (lane == 0) {
+    s.warp_holes[warp] = n_holes;
+    s.warp_sums[warp] = n_movers;
+  }
   __syncthreads();
   int hole_at = 0, mover_at = 0, cta_holes = 0, cta_movers = 0;
+#pragma unroll
   for (int w = 0; w < kSelWarps; ++w) {
-    const int v = s.warp_sums[w], h = v & 0xFFFF, m = v >> 16;
+    const int h = s.warp_holes[w], m = s.warp_sums[w];
     if (w < warp) {
       hole_at += h;
       mover_at += m;
@@ -398,7 +420,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
       h = keys[r * 32];
       m = keys[r * 32 + 1];
     } else {
-      flags(r, ties, h, m);
+      flags(r, row_key(r), ties, h, m);
     }
     const int j = begin + r * 32 + lane;
     const bool is_hole = (h >> lane) & 1u, is_mover = (m >> lane) & 1u;
@@ -539,11 +561,15 @@ cudaError_t launch_evict(const EvictDev& a, int sm_count, cudaStream_t stream) {
   // are made again from the weights, in L2, by every pass)
   const int64_t run = (max_len + cluster - 1) / cluster + 32;
   const int key_cap = run <= kMaxKeys ? static_cast<int>(run) : 0;
-  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxKeys * 4);
+  // (four caches of two heads and up to 131072 keys: the call 54 us with 512
+  // threads, 48 with 1024)
+  const bool large = groups * cluster <= sm_count;
+  auto kern = large ? evict_select_kernel<1024> : evict_select_kernel<512>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxKeys * 4);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(groups * cluster), 1, 1);
-  cfg.blockDim = dim3(kSelThreads, 1, 1);
+  cfg.blockDim = dim3(large ? 1024 : 512, 1, 1);
   cfg.dynamicSmemBytes = static_cast<size_t>(key_cap) * 4;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -555,7 +581,7 @@ cudaError_t launch_evict(const EvictDev& a, int sm_count, cudaStream_t stream) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a, cluster, key_cap);
+  e = cudaLaunchKernelEx(&cfg, kern, a, cluster, key_cap);
   if (e != cudaSuccess || a.moves_cap == 0) return e;
   const int64_t most = (groups * a.moves_cap + 15) / 16;  // CTAs with one move a half warp
   const int64_t ctas = most < sm_count * 4 ? most : sm_count * 4;

@@ -144,6 +144,20 @@ def test_one_sequence_longer_than_shared_memory_holds():
     c.check()
 
 
+def test_runs_too_long_for_shared_memory():
+    """Every CTA's run is read again from the weights in each pass."""
+    c = Case([500003], 250000, h_k=1, page_size=128, first=3, last=1000, weights="mixed")
+    c.call()()
+    c.check()
+
+
+def test_more_groups_than_the_gpu_holds():
+    rng = np.random.default_rng(8)
+    c = Case(rng.integers(0, 700, 90).tolist(), 150, h_k=8, first=2, last=20, pos=True)
+    c.call()()
+    c.check()
+
+
 def test_everything_protected_in_excess_keeps_the_lowest_slots():
     """More slots hold a protected position than the budget: the lowest stay."""
     c = Case([200], 50, h_k=1, pos=True, last=50)

@@ -165,6 +165,13 @@ def test_ragged_padded_and_empty_sequences():
     c.check()
 
 
+def test_long_ragged_prompts():
+    """Several tokens a CTA, sequences ending inside one."""
+    c = Case([9001, 1, 12003], [0, 5, 77], h_k=1, h_r=2, axes=3, page_size=64, pad=5, max_pos=2000)
+    c.call()()
+    c.check()
+
+
 def test_more_new_tokens_than_the_length_counts():
     """Rows whose slot would be negative: Q is written, no cache row is."""
     c = Case([4, 4], [0, 7], packed=True)

@@ -915,6 +915,9 @@ class ScoreMod:
         return ScoreModArgs(float(self.softcap), int(self.window), _ptr(self.alibi_slopes), _ptr(self.key_begin),
                             _ptr(self.key_end), _ptr(self.prefix))
 
+    def _tensors(self):
+        return self.alibi_slopes, self.key_begin, self.key_end, self.prefix
+
 
 def score_spans(params: DecodeParams, mod: ScoreMod, seq_lens: Sequence[int]) -> Tuple[np.ndarray, np.ndarray]:
     """mj_score_spans on host seq_lens: (spans (num_seqs, 4), plan_lens
@@ -1006,7 +1009,7 @@ class DecodeAttnMod(_Call):
             workspace=workspace, softmax_scale=softmax_scale, scale_o=scale_o, status=status, max_n_splits=max_n_splits,
         )
         self._bind(lib().mj_decode_attn_mod, (ctypes.byref(params), ctypes.byref(m), _ptr(spans), ctypes.byref(a)),
-                   (params, mod, m, a, spans, q, k_cache, v_cache, block_table, seq_lens, work, n_splits, q_descale,
+                   (params, mod._tensors(), m, a, spans, q, k_cache, v_cache, block_table, seq_lens, work, n_splits, q_descale,
                     k_descale, v_descale, o, lse, workspace, status))
 
 
@@ -1050,7 +1053,7 @@ class KeyWeights(_Call):
         self._bind(lib().mj_key_weights,
                    (ctypes.byref(params), None if m is None else ctypes.byref(m), ctypes.byref(a), _ptr(acc), seq, head,
                     float(decay), int(fresh)),
-                   (params, mod, m, a, q, k_cache, block_table, seq_lens, work, q_descale, k_descale, lse, acc, status))
+                   (params, None if mod is None else mod._tensors(), m, a, q, k_cache, block_table, seq_lens, work, q_descale, k_descale, lse, acc, status))
 
 
 def key_weights(params: DecodeParams, mod: Optional[ScoreMod] = None, *, stream=None, **tensors) -> None:

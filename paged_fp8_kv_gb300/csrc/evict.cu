@@ -504,8 +504,8 @@ __global__ void __launch_bounds__(kThreads, 4) evict_move_kernel(const EvictDev 
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         const int i = i0 + u * step;
-        dst[u] = i < stop ? to[i] : make_int2(0, -2);  // page -2: no move
-        src[u] = i < stop ? from[i] : make_int2(0, -2);
+        dst[u] = i < stop ? to[i] : make_int2(-1, 0);  // slot -1: no move
+        src[u] = i < stop ? from[i] : make_int2(0, 0);
       }
     };
     if (start < stop) fetch(start);
@@ -513,34 +513,35 @@ __global__ void __launch_bounds__(kThreads, 4) evict_move_kernel(const EvictDev 
       uint4 row[kUnroll];
       uint32_t word[kUnroll];
       int2 to_now[kUnroll];
+      bool ok[kUnroll];  // both pages are pages
       int sp[kUnroll];
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         to_now[u] = dst[u];
         sp[u] = src[u].y;
-        const bool ok = static_cast<uint32_t>(dst[u].y) < static_cast<uint32_t>(a.num_pages) &&
-                        static_cast<uint32_t>(sp[u]) < static_cast<uint32_t>(a.num_pages);
-        if (!ok && sp[u] != -2) sp[u] = -1;  // a page that is none
-        if (sp[u] >= 0 && has_vec)
+        ok[u] = static_cast<uint32_t>(dst[u].y) < static_cast<uint32_t>(a.num_pages) &&
+                static_cast<uint32_t>(sp[u]) < static_cast<uint32_t>(a.num_pages);
+        if (dst[u].x >= 0 && ok[u] && has_vec)
           row[u] = *reinterpret_cast<const uint4*>(pool + sp[u] * page_step + (src[u].x & page_mask) * row_step);
-        if (sp[u] != -2 && has_word) word[u] = word_in[src[u].x];
+        if (dst[u].x >= 0 && has_word) word[u] = word_in[src[u].x];
       }
       if (a.ks && l8 == 0) {  // nvfp4: the rows' eight scales, K's and V's
         uint8_t* const plane = is_v ? a.vs + g * a.vs_head : a.ks + g * a.ks_head;
         const int64_t step_s = is_v ? a.vs_page : a.ks_page;
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u)
-          if (sp[u] >= 0)
+          if (to_now[u].x >= 0 && ok[u])
             *reinterpret_cast<uint2*>(plane + to_now[u].y * step_s + (to_now[u].x & page_mask) * 8) =
                 *reinterpret_cast<const uint2*>(plane + sp[u] * step_s + (src[u].x & page_mask) * 8);
       }
       if (i0 + step * kUnroll < stop) fetch(i0 + step * kUnroll);  // the next round's list entries
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
-        if (sp[u] >= 0 && has_vec)
+        if (to_now[u].x < 0) continue;
+        if (ok[u] && has_vec)
           *reinterpret_cast<uint4*>(pool + to_now[u].y * page_step + (to_now[u].x & page_mask) * row_step) = row[u];
-        if (sp[u] != -2 && has_word) word_out[to_now[u].x] = word[u];
-        if (sp[u] == -1 && l16 == 0 && a.status) atomicExch(a.status, kStatusInvalidArg);
+        if (has_word) word_out[to_now[u].x] = word[u];
+        if (!ok[u] && l16 == 0 && a.status) atomicExch(a.status, kStatusInvalidArg);
       }
     }
     group_begin = group_end;

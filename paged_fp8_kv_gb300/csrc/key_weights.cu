@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int max_len = a.max_blocks * a.page_size;  // acc has no more slots
   auto length_of = [&](int b) {
     const int L = a.seq_lens[b];
-    return L < max_len ? L : max_len;
+    return L < 0 ? 0 : (L < max_len ? L : max_len);
   };
 
   if (warp == 0) {

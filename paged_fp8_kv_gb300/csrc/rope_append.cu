@@ -290,7 +290,7 @@ cudaError_t launch_rope_append(const RopeDev& a, cudaStream_t stream) {
   // chain of dependent loads: one token a CTA took 152 us where eight take 64)
   int per_cta = (kRopeThreads / 8) / heads;
   per_cta = per_cta < 1 ? 1 : (per_cta > kMaxTokens ? kMaxTokens : per_cta);
-  while (per_cta < kMaxTokens && a.num_tokens >= kLongCtas * per_cta * 2) per_cta *= 2;
+  while (per_cta * 2 <= kMaxTokens && a.num_tokens >= kLongCtas * per_cta * 2) per_cta *= 2;
   int threads = per_cta * heads * 8;
   threads = (threads + 31) / 32 * 32;
   if (threads > kRopeThreads) threads = kRopeThreads;

@@ -1,14 +1,18 @@
-// The query-rows decode kernel on modified scores (see decode_qm.cuh), and the
-// spans of keys that a plan for it covers.
+// The keys that any query token of a sequence sees under modified scores, and
+// the length a plan has to cover (see mj_score_spans_device): one CTA a
+// sequence takes the extremes of its tokens' ranges.
 
-#include "decode_qm.cuh"
+#include <cuda_runtime.h>
+
+#include "mj_kernels.h"
+#include "score_mod.cuh"
+#include "sm100_ptx.cuh"
 
 namespace mj {
 namespace {
 
 constexpr int kSpanThreads = 128;
 
-// One CTA a sequence: the keys any of its query tokens sees.
 __global__ void __launch_bounds__(kSpanThreads)
     score_spans_kernel(const ScoreModDev m, const int32_t* seq_lens, int q_len, int causal, int64_t max_len, int4* spans,
                        int32_t* plan_lens) {
@@ -39,11 +43,6 @@ __global__ void __launch_bounds__(kSpanThreads)
 }
 
 }  // namespace
-
-cudaError_t launch_decode_qm_mod(const DecodeModDev& a, int rows_per_cta, int n_q_tiles, bool q_e4m3,
-                                 cudaStream_t stream) {
-  return launch_qm_rows<true>(a, rows_per_cta, n_q_tiles, q_e4m3, stream);
-}
 
 cudaError_t launch_score_spans(const ScoreModDev& m, const int32_t* seq_lens, int num_seqs, int q_len, int causal,
                                int64_t max_len, int4* spans, int32_t* plan_lens, cudaStream_t stream) {

@@ -168,7 +168,7 @@ def test_everything_protected_in_excess_keeps_the_lowest_slots():
 
 
 def test_bad_pages_are_not_moved():
-    for entry in (-1, 2**31 - 1):
+    for entry in (-1, -2, 2**31 - 1):
         c = Case([300, 200], 64, h_k=2, seed=5)
         c.table[0, 2] = entry
         c.table[0, 10] = entry

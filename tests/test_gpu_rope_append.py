@@ -167,9 +167,10 @@ def test_ragged_padded_and_empty_sequences():
 
 def test_long_ragged_prompts():
     """Several tokens a CTA, sequences ending inside one."""
-    c = Case([9001, 1, 12003], [0, 5, 77], h_k=1, h_r=2, axes=3, page_size=64, pad=5, max_pos=2000)
-    c.call()()
-    c.check()
+    for h_r in (2, 6):  # 12 and 6 tokens a CTA would have room for
+        c = Case([9001, 1, 12003], [0, 5, 77], h_k=1, h_r=h_r, axes=3, page_size=64, pad=5, max_pos=2000)
+        c.call()()
+        c.check()
 
 
 def test_more_new_tokens_than_the_length_counts():

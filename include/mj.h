@@ -604,8 +604,8 @@ mj_status mj_decode_attn_mod(const mj_decode_params* params, const mj_score_mod*
  *   decay         0 <= decay <= 1; with 0 (and for fresh keys) acc is not read
  *   fresh         >= 0: the newest keys, whose accumulators start from zero
  *                 (q_len after a decode step that appended q_len tokens)
- * A row with lse = -inf adds nothing.  One launch per 256 packed rows; every
- * sum in a fixed order.
+ * A row with lse = -inf adds nothing.  One launch per 128 packed rows (256 of
+ * e4m3 Q); every sum in a fixed order.
  * Errors: MJ_ERR_INVALID_ARG, MJ_ERR_UNSUPPORTED, MJ_ERR_CUDA. */
 mj_status mj_key_weights(const mj_decode_params* params, const mj_score_mod* mod, const mj_decode_args* args,
                          float* acc, int64_t acc_seq, int64_t acc_head, float decay, int32_t fresh,

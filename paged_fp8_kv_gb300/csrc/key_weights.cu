@@ -21,9 +21,10 @@
 // of them (shares cut across the heads read a quarter more from HBM).
 //
 // Bound: 128 bytes of K a key and head against one exponential per row and
-// key: HBM up to about 64 rows, the exponential units and the MMA above.  256
-// packed rows a launch (TMEM holds two buffers of 256 columns); more rows are
-// further launches that add on, in order.
+// key: HBM up to about 64 rows, the exponential units and the MMA above.  A
+// launch takes 256 packed rows of e4m3 Q or 128 of bf16 Q (two segments'
+// operand rows beside a ring of seven K tiles); more rows are further launches
+// that add on, in order.
 //
 // Roles (320 threads): warp 0 issues the K tiles into a ring, warp 1 (TMEM
 // allocator) the MMAs, warps 2-5 and 6-9 take alternate tiles.  Up to 64 rows

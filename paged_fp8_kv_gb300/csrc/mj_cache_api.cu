@@ -274,8 +274,9 @@ extern "C" mj_status mj_key_weights(const mj_decode_params* params, const mj_sco
   const int sms = device_sm_count();
   if (sms < 1) return MJ_ERR_CUDA;
   const NvtxRange range("mj_key_weights");
-  for (int n0 = 0; n0 < n_q; n0 += 256) {
-    const int rows = std::min(256, n_q - n0);
+  const int step = p.q_dtype == MJ_E4M3 ? 256 : 128;  // rows a launch takes
+  for (int n0 = 0; n0 < n_q; n0 += step) {
+    const int rows = std::min(step, n_q - n0);
     // later row groups add onto what the first one wrote
     const cudaError_t e =
         launch_key_weights(d, p.q_dtype == MJ_E4M3, mod != nullptr, n0, rows, a.lse, acc, acc_seq, acc_head,

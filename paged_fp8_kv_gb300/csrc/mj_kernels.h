@@ -75,7 +75,7 @@ cudaError_t launch_score_spans(const ScoreModDev& m, const int32_t* seq_lens, in
                                int64_t max_len, int4* spans, int32_t* plan_lens, cudaStream_t stream);
 
 // Accumulated attention weights of packed rows n0 .. n0 + n_rows - 1 (at
-// most 256): acc[b][g][j] of a.work's tiles.
+// most 256, or 128 of bf16 Q): acc[b][g][j] of a.work's tiles.
 cudaError_t launch_key_weights(const DecodeModDev& a, bool q_e4m3, bool has_mod, int n0, int n_rows, const float* lse,
                                float* acc, int64_t acc_seq, int64_t acc_head, float decay, int fresh, int sm_count,
                                cudaStream_t stream);

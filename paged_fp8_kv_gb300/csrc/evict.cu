@@ -24,12 +24,17 @@
 // counts are summed over distributed shared memory.  It writes the kept slots'
 // weights, and the move lists with their pages looked up.  Long caches of few
 // heads get their CTAs from the cluster, short ones of many heads from the
-// grid, two CTAs an SM.
+// grid, two CTAs an SM; when those do not all fit, the longest sequences start
+// first, so that the last ones to run are short (64 sequences of 8 heads and
+// 512 to 8192 keys, cut to 2048: the call 82 us, in batch order 86).
+// Bound: on that batch, the second wave of CTAs (34 us for 9 MB of weights);
+// on a few long caches, the chain of cluster barriers between the passes.
 // Kernel 2 moves the rows: the moves of all groups are one list, cut evenly
 // over the CTAs (a group's share differs by its length and its luck), sixteen
-// lanes a move, two in flight a thread (GB300: 86 us for the whole call on a
-// decode batch; one in flight 95, four 90, eight 87).  Bound: the round trip of
-// dependent loads (list, then rows at random places), so bytes in flight.
+// lanes a move, two in flight a thread (the same batch, before the order by
+// length: 86 us; one in flight 95, four 90, eight 87).  Bound: DRAM, at rows of
+// 64 to 128 bytes in random places, read once and written once; more of them in
+// flight, or other cache hints, are no faster.
 
 #include <cuda_runtime.h>
 
@@ -105,7 +110,8 @@ struct Shared {
 
 // T threads: 512, two CTAs an SM, or 1024 when the groups do not fill the GPU
 template <int T>
-__global__ void __launch_bounds__(T, 1024 / T) evict_select_kernel(const EvictDev a, int cluster, int key_cap) {
+__global__ void __launch_bounds__(T, 1024 / T)
+    evict_select_kernel(const EvictDev a, int cluster, int key_cap, bool by_length) {
   // a programmatic dependent: no global access before the grid ahead is done
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
@@ -113,10 +119,26 @@ __global__ void __launch_bounds__(T, 1024 / T) evict_select_kernel(const EvictDe
   constexpr int kPer = kBins / T;  // bins a thread
   __shared__ __align__(16) Shared s;
   extern __shared__ uint32_t keys[];  // [key_cap] of this CTA's run
-  const int bg = blockIdx.x / cluster, rank = blockIdx.x - bg * cluster;
-  const int b = bg / a.h_k, g = bg - b * a.h_k;
+  int bg = blockIdx.x / cluster;
+  const int rank = blockIdx.x - bg * cluster;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t max_len = static_cast<int64_t>(a.max_blocks) * a.page_size;
+  int b = bg / a.h_k;
+  const int g = bg - b * a.h_k;
+  if (by_length) {  // the b-th longest sequence (at most T of them); ties by index
+    int* const lens = s.hist[0];
+    if (tid < a.num_seqs) lens[tid] = a.seq_lens[tid];
+    __syncthreads();
+    if (tid < a.num_seqs) {
+      int rank_of = 0;
+      for (int j = 0; j < a.num_seqs; ++j) rank_of += lens[j] > lens[tid] || (lens[j] == lens[tid] && j < tid);
+      if (rank_of == b) s.need = tid;
+    }
+    __syncthreads();
+    b = s.need;
+    bg = b * a.h_k + g;
+    __syncthreads();
+  }
   int L = a.seq_lens[b];
   if (L < 0 || L > max_len) {
     if (tid == 0 && a.status) atomicExch(a.status, kStatusInvalidArg);
@@ -582,7 +604,9 @@ cudaError_t launch_evict(const EvictDev& a, int sm_count, cudaStream_t stream) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, kern, a, cluster, key_cap);
+  // more CTAs than one wave: by length, where a thread can rank a sequence
+  const bool by_length = groups > 2 * sm_count && a.num_seqs <= 512;
+  e = cudaLaunchKernelEx(&cfg, kern, a, cluster, key_cap, by_length);
   if (e != cudaSuccess || a.moves_cap == 0) return e;
   const int64_t most = (groups * a.moves_cap + 15) / 16;  // CTAs with one move a half warp
   const int64_t ctas = most < sm_count * 4 ? most : sm_count * 4;

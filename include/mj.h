@@ -446,7 +446,7 @@ typedef struct {
  *   q, k, v      bf16 rows of 128: token t, head h at x + t*x_tok + h*x_head
  *                (strides in elements, multiples of 8; 16-byte aligned; the
  *                three may be slices of one projection's output)
- *   num_tokens   tokens in q, k, v
+ *   num_tokens   tokens in q, k, v; 0: nothing is done (with cu_tokens)
  *   positions    int32, axis a of token t at a*pos_axis + t
  *   cos_sin      fp32 [max_pos][rot_dim], 16-byte aligned: row p holds
  *                cos(p w_i) for i < rot_dim/2, then sin(p w_i)
@@ -463,8 +463,9 @@ typedef struct {
  *                apart (at least h_k*q_len*h_r*128; cu_tokens NULL);
  *                q_packed = 0: (num_tokens, h_k*h_r, 128), tokens
  *                q_out_stride apart (at least h_k*h_r*128); it may then be q
- *                itself (same base, q_head 128, q_tok == q_out_stride), else
- *                no output overlaps an input
+ *                itself (same base, q_head 128, q_tok == q_out_stride; k and
+ *                v of the same projection beside it: the same token stride),
+ *                else no output overlaps an input
  *   k_cache, v_cache, k_page .. v_head   e4m3 pools as in mj_decode_args,
  *                strides in bytes, multiples of 16
  *   block_table, seq_lens, k_descale, v_descale and their strides   as in
@@ -629,7 +630,9 @@ mj_status mj_key_weights(const mj_decode_params* params, const mj_score_mod* mod
  *   keep_first, keep_last   >= 0, together at most budget: slots with position
  *                < keep_first or >= next_pos - keep_last rank above all others
  *   workspace    >= mj_evict_workspace_bytes, 16-byte aligned; need not be
- *                initialised
+ *                initialised; in use until the call's second launch is done
+ *                (calls, or replayed graphs, that may run at the same time
+ *                need one each)
  *   status       optional int32, caller-zeroed: MJ_ERR_INVALID_ARG when a
  *                length is out of range or a page of a row to move is outside
  *                [0, num_pages) (that row is not moved) */

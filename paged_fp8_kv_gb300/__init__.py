@@ -774,6 +774,11 @@ class _Call:
 
     _name = ""
 
+    @staticmethod
+    def _own(params):
+        """A copy: the caller may change its own for the next call."""
+        return type(params).from_buffer_copy(params)
+
     def _bind(self, fn, args, keep) -> None:
         import torch
 
@@ -825,6 +830,7 @@ class RopeAppend(_Call):
 
     def __init__(self, params: RopeParams, *, q, k, v, positions, cos_sin, q_out, k_cache, v_cache, block_table, seq_lens,
                  k_descale, v_descale, freq_axis=None, cu_tokens=None, key_pos=None, status=None):
+        params = self._own(params)
         bf16, f32, i32, _ = _dtypes()
         nb, hk, hq = int(params.num_seqs), int(params.h_k), int(params.h_k) * int(params.h_r)
         n = int(q.shape[0])
@@ -985,6 +991,7 @@ class DecodeAttnMod(_Call):
                  scale_o: float = 1.0, status=None, max_n_splits: int = 0):
         import torch
 
+        params = self._own(params)
         bf16, f32, i32, _ = _dtypes()
         nb, hk, rows = int(params.num_seqs), int(params.h_k), int(params.q_len) * int(params.h_r)
         _check_queries(params, q)
@@ -1027,6 +1034,7 @@ class KeyWeights(_Call):
 
     def __init__(self, params: DecodeParams, mod: Optional[ScoreMod], *, q, k_cache, block_table, seq_lens, work, q_descale,
                  k_descale, lse, acc, softmax_scale: float, decay: float = 1.0, fresh: int = 0, status=None):
+        params = self._own(params)
         _, f32, i32, _ = _dtypes()
         nb, hk, rows = int(params.num_seqs), int(params.h_k), int(params.q_len) * int(params.h_r)
         _check_queries(params, q)
@@ -1080,9 +1088,10 @@ class Evict(_Call):
     def __init__(self, params: DecodeParams, *, k_cache, v_cache, block_table, seq_lens, acc, new_lens, budget: int,
                  workspace, acc_out=None, key_pos=None, key_pos_out=None, next_pos=None, keep_first: int = 0,
                  keep_last: int = 0, status=None, k_scales=None, v_scales=None):
-        _, f32, i32, _ = _dtypes()
         import torch
 
+        params = self._own(params)
+        _, f32, i32, codes = _dtypes()
         nb, hk = int(params.num_seqs), int(params.h_k)
         _check_pools(params, k_cache, v_cache, _row_bytes(params))
         _check_tables(params, block_table, seq_lens)
@@ -1098,6 +1107,10 @@ class Evict(_Call):
             if _per_slot(name, t, dtype, params) != strides or t.shape != acc.shape:
                 raise ValueError(f"{name}: the layout of acc")
         _tensor("workspace", workspace, (torch.uint8,))
+        for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+            if t is not None:
+                shape = (int(params.num_pages), hk, int(params.page_size), 8)
+                _tensor(name, t, codes, shape, strided=True)
         _check_status(status)
         a = EvictArgs()
         a.k, a.v = _ptr(k_cache), _ptr(v_cache)

@@ -70,9 +70,10 @@ extern "C" mj_status mj_rope_append(const mj_rope_params* params, const mj_rope_
   if (static_cast<int64_t>(p.max_blocks) * p.page_size > (int64_t{1} << 30)) return MJ_ERR_UNSUPPORTED;
   const int64_t h_q = static_cast<int64_t>(p.h_k) * p.h_r;
   if (h_q + 2 * static_cast<int64_t>(p.h_k) > 4096) return MJ_ERR_UNSUPPORTED;
-  if (!a.q || !a.k || !a.v || !a.positions || !a.cos_sin || !a.q_out || !a.k_cache || !a.v_cache || !a.block_table ||
-      !a.seq_lens || !a.k_descale || !a.v_descale)
+  if (!a.cos_sin || !a.k_cache || !a.v_cache || !a.block_table || !a.seq_lens || !a.k_descale || !a.v_descale)
     return MJ_ERR_INVALID_ARG;
+  // (a batch without tokens has none of these)
+  if (a.num_tokens != 0 && (!a.q || !a.k || !a.v || !a.positions || !a.q_out)) return MJ_ERR_INVALID_ARG;
   if (a.num_tokens < 0 || (a.q_packed != 0 && a.q_packed != 1)) return MJ_ERR_INVALID_ARG;
   if (!a.cu_tokens && static_cast<int64_t>(p.num_seqs) * p.q_len != a.num_tokens) return MJ_ERR_INVALID_ARG;
   if (a.cu_tokens && a.q_packed) return MJ_ERR_INVALID_ARG;  // packed rows need one q_len
@@ -112,9 +113,16 @@ extern "C" mj_status mj_rope_append(const mj_rope_params* params, const mj_rope_
   };
   const bool in_place = a.q_out == a.q && !a.q_packed && a.q_tok == a.q_out_stride && (h_q == 1 || a.q_head == kHeadDim);
   if (!in_place && overlap(a.q_out, out_bytes, a.q, in_bytes(a.q_tok, a.q_head, h_q))) return MJ_ERR_INVALID_ARG;
-  // (in place, Q's rows may lie between K's and V's of the same projection)
-  if (!in_place && (overlap(a.q_out, out_bytes, a.k, in_bytes(a.k_tok, a.k_head_in, p.h_k)) ||
-                    overlap(a.q_out, out_bytes, a.v, in_bytes(a.v_tok, a.v_head_in, p.h_k))))
+  // (in place, Q's rows may lie between K's and V's of the same projection:
+  // a token's rows of x then fall behind its Q rows and before the next's)
+  auto beside = [&](const void* x, int64_t tok, int64_t head) {
+    if (!in_place || tok != a.q_tok || tok == 0) return false;
+    int64_t at = (static_cast<const char*>(x) - static_cast<const char*>(a.q)) / 2 % tok;
+    if (at < 0) at += tok;
+    return at >= h_q * kHeadDim && at + (p.h_k - 1) * head + kHeadDim <= tok;
+  };
+  if ((overlap(a.q_out, out_bytes, a.k, in_bytes(a.k_tok, a.k_head_in, p.h_k)) && !beside(a.k, a.k_tok, a.k_head_in)) ||
+      (overlap(a.q_out, out_bytes, a.v, in_bytes(a.v_tok, a.v_head_in, p.h_k)) && !beside(a.v, a.v_tok, a.v_head_in)))
     return MJ_ERR_INVALID_ARG;
 
   d.q = static_cast<const __nv_bfloat16*>(a.q);

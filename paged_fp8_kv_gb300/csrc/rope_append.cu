@@ -77,27 +77,29 @@ __device__ __forceinline__ uint2 to_codes8(const float* q) {
 // operations a value: with r = 1/d and q = x r rounded, x - q d is exact in an
 // fma and q + (x - q d) r rounds to the quotient (Markstein, "Computation of
 // elementary functions on the IBM RISC System/6000 processor", 1990, theorem
-// 7).  It needs r, q and the remainder clear of overflow and underflow: d
+// 7).  The steps run on -q and -r, so that a zero keeps its sign: for x = -0
+// the remainder is +0, and +0 (-r) - (-0) is +0, the quotient's negative.
+// It needs r, q and the remainder clear of overflow and underflow: d
 // outside [2^-60, 2^60] or a quotient past 2^40 takes the division itself; a
 // remainder that underflows then belongs to a quotient below 2^-18, which
 // every e4m3 rounding makes zero.  (The divisions were most of the kernel's
 // instructions: on the prompt above 95 us with them, 77 so.)
 __device__ __forceinline__ void divide16(float* x, float d) {
   const float r = __frcp_rn(d);
-  const float2 r2 = make_float2(r, r), nd2 = make_float2(-d, -d);
-  float2 q[8];
+  const float2 nr2 = make_float2(-r, -r), d2 = make_float2(d, d);
+  float2 q[8];  // negative quotients
   float top = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    q[i] = mul2(make_float2(x[2 * i], x[2 * i + 1]), r2);
+    q[i] = mul2(make_float2(x[2 * i], x[2 * i + 1]), nr2);
     top = fmax3(top, fabsf(q[i].x), fabsf(q[i].y));
   }
   if (d >= 0x1p-60f && d <= 0x1p60f && top <= 0x1p40f) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      q[i] = fma2(fma2(q[i], nd2, make_float2(x[2 * i], x[2 * i + 1])), r2, q[i]);
-      x[2 * i] = q[i].x;
-      x[2 * i + 1] = q[i].y;
+      q[i] = fma2(fma2(q[i], d2, make_float2(x[2 * i], x[2 * i + 1])), nr2, q[i]);
+      x[2 * i] = -q[i].x;
+      x[2 * i + 1] = -q[i].y;
     }
   } else {
 #pragma unroll

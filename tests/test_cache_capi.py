@@ -100,6 +100,20 @@ def test_rope_layout_and_axes_refused():
     p, a = _rope()
     a.cu_tokens, a.q_packed, a.q_out_stride, a.num_tokens = _ptr(), 0, 8 * 128, 0
     assert _rope_status(p, a) == mj.MJ_OK  # nothing to do, nothing launched
+    a.q = a.k = a.v = a.positions = a.q_out = None  # an empty tensor has no address
+    assert _rope_status(p, a) == mj.MJ_OK
+
+
+def test_rope_in_place_refuses_k_or_v_under_the_output():
+    rows = 8 + 2 + 2  # heads of one projection's token
+    for name, tok, head in (("k", "k_tok", "k_head_in"), ("v", "v_tok", "v_head_in")):
+        for at, step in ((0, rows * 128), (7 * 128, rows * 128), (11 * 128, rows * 128), (-128, rows * 128),
+                         (8 * 128, 2 * 128), (8 * 128, rows * 256)):
+            p, a = _rope()
+            a.cu_tokens = _ptr()
+            _set(a, q_packed=0, q_tok=rows * 128, q_out_stride=rows * 128, q_out=a.q)
+            _set(a, **{name: a.q + 2 * at, tok: step})
+            assert _rope_status(p, a) == BAD, (name, at, step)
 
 
 # ---------------------------------------------------------- modified scores

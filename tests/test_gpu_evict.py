@@ -225,3 +225,6 @@ def test_binding_refuses():
     with pytest.raises(mj.MjError):
         mj.evict(c.params, k_cache=c.k, v_cache=c.v, block_table=c.table, seq_lens=c.seq_lens, acc=c.acc, new_lens=c.new_lens,
                  budget=16, workspace=c.ws[:16])
+    with pytest.raises(ValueError):
+        mj.Evict(c.params, k_cache=c.k, v_cache=c.v, block_table=c.table, seq_lens=c.seq_lens, acc=c.acc, new_lens=c.new_lens,
+                 budget=16, workspace=c.ws, k_scales=c.k, v_scales=c.v)

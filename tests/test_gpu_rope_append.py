@@ -253,6 +253,38 @@ def test_codes_are_those_of_the_division():
             assert torch.equal(torch.where(nan, 0x7F, g), torch.where(nan, 0x7F, want)), exps
 
 
+def test_signed_zeros_keep_their_sign():
+    c = Case([3, 3], [5, 40], h_k=2, h_r=1, packed=False)
+    v = c.v.clone()
+    v[:, :, 0::4], v[:, :, 1::4] = 0.0, -0.0
+    c.call(v=v)()
+    torch.cuda.synchronize()
+    for b in range(2):
+        for i in range(3):
+            slot = int(c.lens[b]) - 3 + i
+            row = c.vc.cpu().numpy()[c.bt[b, slot // 16], slot % 16]
+            assert (row[:, 0::4] == 0x00).all() and (row[:, 1::4] == 0x80).all()
+
+
+def test_no_tokens():
+    c = Case([3, 3], [5, 40], packed=False)
+    before = c.kc.clone(), c.vc.clone()
+    empty = {n: c.dev[n][..., :0] if n == "positions" else getattr(c, n)[:0] for n in ("q", "k", "v", "positions", "q_out")}
+    cu = torch.zeros(3, dtype=torch.int32, device="cuda")
+    c.call(**empty, cu_tokens=cu)()
+    torch.cuda.synchronize()
+    assert torch.equal(c.kc, before[0]) and torch.equal(c.vc, before[1]) and int(c.status.item()) == 0
+
+
+def test_a_call_keeps_its_shape():
+    """Parameters changed after the call was made do not change it."""
+    c = Case([4, 4], [100, 3])
+    call = c.call()
+    c.params.interleaved, c.params.rot_dim = 1, 64
+    call()
+    c.check()
+
+
 def test_graph_and_stream():
     c = Case([4, 4], [100, 3], packed=True, axes=3)
     call = c.call()

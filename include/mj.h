@@ -536,7 +536,7 @@ mj_status mj_rope_append(const mj_rope_params* params, const mj_rope_args* args,
  * in the sequence's span (mj_score_spans; without spans: every key below
  * L_b), also where some rows do not see it; outside the span V may hold
  * anything.  A row that sees no key gets O = 0 and LSE = -inf.
- *   softcap       0 = off; finite, >= 0
+ *   softcap       0 = off; else 2^-20 to 2^60
  *   window        0 = off; > 0 needs params.causal
  *   alibi_slopes  device fp32[h_k*h_r], finite, or NULL
  *   key_begin, key_end   device int32[num_seqs*q_len] or NULL

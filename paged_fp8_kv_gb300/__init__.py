@@ -899,7 +899,7 @@ def rope_append(params: RopeParams, *, stream=None, **tensors) -> None:
 class ScoreMod:
     """mj_score_mod: device tensors (alibi_slopes (h_k*h_r,) float32,
     key_begin / key_end (num_seqs, q_len) int32, prefix (num_seqs,) int32) or
-    None, softcap and window 0 = off."""
+    None, softcap (else 2^-20 to 2^60) and window 0 = off."""
 
     softcap: float = 0.0
     window: int = 0

@@ -5,7 +5,6 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include <algorithm>
-#include <cmath>
 #include <cstring>
 
 #include "mj.h"
@@ -38,7 +37,8 @@ struct NvtxRange {
 }  // namespace
 
 mj_status score_mod_dev(const mj_decode_params& p, const mj_score_mod& mod, const int32_t* spans, ScoreModDev* out) {
-  if (!(mod.softcap >= 0.f) || std::isinf(mod.softcap)) return MJ_ERR_INVALID_ARG;
+  // a cap for which neither 1 / softcap nor a score over it leaves fp32's range
+  if (mod.softcap != 0.f && !(mod.softcap >= 0x1p-20f && mod.softcap <= 0x1p60f)) return MJ_ERR_INVALID_ARG;
   if (mod.window < 0 || (mod.window > 0 && p.causal == 0)) return MJ_ERR_INVALID_ARG;
   if (!aligned4(mod.alibi_slopes) || !aligned4(mod.key_begin) || !aligned4(mod.key_end) || !aligned4(mod.prefix) ||
       !aligned16(spans))

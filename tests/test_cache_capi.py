@@ -135,7 +135,8 @@ def _mod_status(p, m, a, spans=None):
 
 def test_decode_attn_mod_refused():
     inf = float("inf")
-    for bad in (dict(softcap=-1.0), dict(softcap=float("nan")), dict(softcap=inf), dict(window=-1), dict(alibi_slopes=_ptr() + 2),
+    for bad in (dict(softcap=-1.0), dict(softcap=float("nan")), dict(softcap=inf), dict(softcap=1e-40), dict(softcap=1e38),
+                dict(window=-1), dict(alibi_slopes=_ptr() + 2),
                 dict(key_begin=_ptr() + 1), dict(key_end=_ptr() + 2), dict(prefix=_ptr() + 3)):
         p, a = _attn()
         assert _mod_status(p, _set(mj.ScoreModArgs(), **bad), a) == BAD, bad

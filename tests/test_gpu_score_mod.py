@@ -211,3 +211,17 @@ def test_long_sequence_splits():
     w = syn.make_workload("mod", [20011, 600], 1, 1, 16, 128, seed=4, max_splits=32)
     check(w, dict(softcap=30.0, alibi=True))
     check(w, dict(softcap=30.0, window=9000, prefix=700))
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("q_len,h_r", [(2, 8), (5, 8), (3, 48)], ids=["r16", "r40", "r144"])
+def test_slopes_of_either_sign(q_len, h_r, causal):
+    """Biases that grow with the distance, that leave a row one key, and none:
+    the running maximum moves both ways along the keys."""
+    w = syn.make_workload("mod", [2, 500, 1300], q_len, 1, h_r, 16, seed=41, causal=causal, max_splits=4)
+    mod, host = make_mod(w, np.random.default_rng(0), softcap=30.0)
+    slopes = np.resize(np.float32([-0.5, 3.0, 0.0, -0.001, 100.0]), h_r)
+    host["slopes"], mod.alibi_slopes = slopes, torch.from_numpy(slopes).cuda()
+    ref = Reference(w, host)
+    for kernel, splits in itertools.product(families(w), (0, 3)):
+        ref.check(*ModStep(w, mod, kernel=kernel, force_splits=splits).run())

@@ -97,6 +97,13 @@ __device__ __forceinline__ int warp_sum_before(int v, int lane, int& total) {
   return x - v;
 }
 
+// Sum of the warps' values before `warp`, and of all N (N <= 32).
+template <int N>
+__device__ __forceinline__ int warps_before(const int* sums, int warp, int lane, int& total) {
+  const int before = warp_sum_before(lane < N ? sums[lane] : 0, lane, total);
+  return __shfl_sync(0xffffffffu, before, warp);
+}
+
 struct Shared {
   int hist[2][kBins];
   int warp_sums[32];
@@ -314,8 +321,7 @@ __global__ void __launch_bounds__(T, 1024 / T)
     int before = warp_sum_before(sum, lane, total);
     if (lane == 31) s.warp_sums[warp] = total;
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kSelWarps; ++w) before += w < warp ? s.warp_sums[w] : 0;
+    before += warps_before<kSelWarps>(s.warp_sums, warp, lane, total);
     if (before < need && need <= before + sum) {  // one thread: the threshold's digit is among its bins
       int left = need - before;
 #pragma unroll
@@ -400,17 +406,9 @@ __global__ void __launch_bounds__(T, 1024 / T)
     s.warp_sums[warp] = n_movers;
   }
   __syncthreads();
-  int hole_at = 0, mover_at = 0, cta_holes = 0, cta_movers = 0;
-#pragma unroll
-  for (int w = 0; w < kSelWarps; ++w) {
-    const int h = s.warp_holes[w], m = s.warp_sums[w];
-    if (w < warp) {
-      hole_at += h;
-      mover_at += m;
-    }
-    cta_holes += h;
-    cta_movers += m;
-  }
+  int cta_holes, cta_movers;
+  int hole_at = warps_before<kSelWarps>(s.warp_holes, warp, lane, cta_holes);
+  int mover_at = warps_before<kSelWarps>(s.warp_sums, warp, lane, cta_movers);
   if (tid == 0) {
     s.totals[0] = cta_holes;
     s.totals[1] = cta_movers;

@@ -128,3 +128,89 @@ def test_serving_loop():
                 newest = set(range(max(0, int(next_pos[i]) - 6), int(next_pos[i])))
                 assert newest <= set(got.tolist())  # the newest six are still there
     assert cuts >= 2
+
+
+class Loop:
+    """A decode step of every operator, budget 40, on state of its own."""
+
+    def __init__(self):
+        gen = torch.Generator("cuda").manual_seed(3)
+        i32 = dict(dtype=torch.int32, device="cuda")
+        lens, b, max_blocks = [33, 1, 40], 3, 4
+        pages, h_q = b * max_blocks, H_K * H_R
+        rand = lambda *shape: torch.rand(*shape, generator=gen, device="cuda")  # noqa: E731
+        self.kc = torch.randint(0, 0x7F, (pages, PS, H_K, 128), generator=gen, device="cuda").to(torch.uint8)
+        self.vc = torch.randint(0, 0x7F, (pages, PS, H_K, 128), generator=gen, device="cuda").to(torch.uint8)
+        table = torch.randperm(pages, generator=gen, device="cuda").reshape(b, max_blocks).to(torch.int32)
+        kd, vd, qd = rand(b, H_K) * 1e-3 + 1e-3, rand(b, H_K) * 1e-3 + 1e-3, torch.ones(1, device="cuda")
+        self.acc = rand(b, H_K, max_blocks * PS)
+        self.key_pos = torch.arange(max_blocks * PS, **i32).expand(b, H_K, -1).contiguous()
+        self.lens, self.next_pos = torch.tensor(lens, **i32), torch.tensor(lens, **i32)
+        self.new_lens, self.status = torch.zeros(b, **i32), torch.zeros(1, **i32)
+        ang = torch.outer(torch.arange(100.0, device="cuda"), 10000.0 ** (-torch.arange(64.0, device="cuda") / 64))
+        cos_sin = torch.cat([ang.cos(), ang.sin()], 1)
+        self.x = torch.empty(b, h_q + 2 * H_K, 128, dtype=torch.bfloat16, device="cuda")
+        q = torch.empty(b, H_K, H_R, 128, dtype=torch.bfloat16, device="cuda")
+        self.o, self.lse = torch.zeros_like(q), torch.zeros(b, H_K, H_R, device="cuda")
+        self.params = params = mj.make_params(b, 1, H_K, H_R, PS, max_blocks, pages, max_splits=4)
+        self.mod = mj.ScoreMod(softcap=CAP)
+        self.pad = pad = mj.decode_plan_max_items(params)
+        self.work, self.all_work = torch.zeros(pad, 4, **i32), torch.zeros(pad, 4, **i32)
+        self.n_splits, self.spans, self.plan_lens = torch.zeros(b, **i32), torch.zeros(b, 4, **i32), torch.zeros(b, **i32)
+        self.ws = torch.empty(mj.workspace_bytes(params), dtype=torch.uint8, device="cuda")
+        self.ews = torch.empty(mj.evict_workspace_bytes(params, 40), dtype=torch.uint8, device="cuda")
+        cache = dict(block_table=table, seq_lens=self.lens, status=self.status)
+        self.append = mj.RopeAppend(
+            mj.make_rope_params(b, 1, H_K, H_R, PS, max_blocks, pages, max_pos=100), q=self.x[:, :h_q],
+            k=self.x[:, h_q : h_q + H_K], v=self.x[:, h_q + H_K :], positions=self.next_pos, cos_sin=cos_sin, q_out=q,
+            k_cache=self.kc, v_cache=self.vc, k_descale=kd, v_descale=vd, key_pos=self.key_pos, **cache)
+        self.attn = mj.DecodeAttnMod(params, self.mod, q=q, k_cache=self.kc, v_cache=self.vc, work=self.work, n_splits=self.n_splits,
+                                     q_descale=qd, k_descale=kd, v_descale=vd, o=self.o, lse=self.lse, softmax_scale=SCALE,
+                                     workspace=self.ws, spans=self.spans, max_n_splits=4, **cache)
+        self.weigh = mj.KeyWeights(params, self.mod, q=q, k_cache=self.kc, work=self.all_work, q_descale=qd, k_descale=kd, lse=self.lse,
+                                   acc=self.acc, softmax_scale=SCALE, decay=0.9, fresh=1, **cache)
+        self.cut = mj.Evict(params, k_cache=self.kc, v_cache=self.vc, acc=self.acc, key_pos=self.key_pos, next_pos=self.next_pos,
+                            new_lens=self.new_lens, budget=40, keep_first=1, keep_last=4, workspace=self.ews, **cache)
+
+    def step(self):
+        self.lens += 1
+        self.append()
+        self.next_pos += 1
+        mj.score_spans_device(self.params, self.mod, self.lens, self.spans, self.plan_lens)
+        mj.decode_plan_device(self.params, self.plan_lens, self.work, self.n_splits, self.pad, status=self.status)
+        self.attn()
+        mj.decode_plan_device(self.params, self.lens, self.all_work, self.plan_lens, self.pad, status=self.status)
+        self.weigh()
+        self.cut()
+        self.lens.copy_(self.new_lens)
+
+    def state(self):
+        torch.cuda.synchronize()
+        return [t.clone() for t in (self.kc, self.vc, self.acc, self.key_pos, self.lens, self.next_pos, self.o, self.lse, self.status)]
+
+
+def test_captured_steps_give_the_eager_steps_bytes():
+    """Two graphs of the same step, which share its workspaces, replayed in
+    turn while the caches grow to the budget and are cut at every step."""
+    gen = torch.Generator("cuda").manual_seed(5)
+    xs = torch.randn(16, 3, (H_R + 2) * H_K, 128, generator=gen, device="cuda").to(torch.bfloat16)
+    eager, replayed = Loop(), Loop()
+    graphs = []
+    side = torch.cuda.Stream()
+    start = [t.clone() for t in (replayed.lens, replayed.next_pos)]
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.graph(graph, stream=side):
+            replayed.step()
+        graphs.append(graph)
+    assert torch.equal(replayed.lens, start[0]) and torch.equal(replayed.next_pos, start[1])  # capture ran nothing
+    for i, x in enumerate(xs):
+        eager.x.copy_(x)
+        eager.step()
+        replayed.x.copy_(x)
+        graphs[i % 2].replay()
+    got, want = replayed.state(), eager.state()
+    assert int(want[-1].item()) == 0 and want[4].tolist() == [40, 17, 40]
+    for a, b in zip(got, want):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))

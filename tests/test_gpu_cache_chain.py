@@ -131,17 +131,21 @@ def test_serving_loop():
 
 
 class Loop:
-    """A decode step of every operator, budget 40, on state of its own."""
+    """A decode step of every operator, budget 40, on state of its own, whose
+    pages are the pool's from `base` on."""
 
-    def __init__(self):
+    def __init__(self, base=0):
         gen = torch.Generator("cuda").manual_seed(3)
         i32 = dict(dtype=torch.int32, device="cuda")
         lens, b, max_blocks = [33, 1, 40], 3, 4
         pages, h_q = b * max_blocks, H_K * H_R
         rand = lambda *shape: torch.rand(*shape, generator=gen, device="cuda")  # noqa: E731
-        self.kc = torch.randint(0, 0x7F, (pages, PS, H_K, 128), generator=gen, device="cuda").to(torch.uint8)
-        self.vc = torch.randint(0, 0x7F, (pages, PS, H_K, 128), generator=gen, device="cuda").to(torch.uint8)
-        table = torch.randperm(pages, generator=gen, device="cuda").reshape(b, max_blocks).to(torch.int32)
+        self.base, pools = base, torch.empty(2, base + pages, PS, H_K, 128, dtype=torch.uint8, device="cuda")
+        for pool in pools:
+            pool[base:] = torch.randint(0, 0x7F, (pages, PS, H_K, 128), generator=gen, device="cuda").to(torch.uint8)
+        self.kc, self.vc = pools
+        table = (base + torch.randperm(pages, generator=gen, device="cuda")).reshape(b, max_blocks).to(torch.int32)
+        pages += base
         kd, vd, qd = rand(b, H_K) * 1e-3 + 1e-3, rand(b, H_K) * 1e-3 + 1e-3, torch.ones(1, device="cuda")
         self.acc = rand(b, H_K, max_blocks * PS)
         self.key_pos = torch.arange(max_blocks * PS, **i32).expand(b, H_K, -1).contiguous()
@@ -186,7 +190,7 @@ class Loop:
 
     def state(self):
         torch.cuda.synchronize()
-        return [t.clone() for t in (self.kc, self.vc, self.acc, self.key_pos, self.lens, self.next_pos, self.o, self.lse, self.status)]
+        return [t.clone() for t in (self.kc[self.base :], self.vc[self.base :], self.acc, self.key_pos, self.lens, self.next_pos, self.o, self.lse, self.status)]
 
 
 def test_captured_steps_give_the_eager_steps_bytes():
@@ -212,5 +216,20 @@ def test_captured_steps_give_the_eager_steps_bytes():
         graphs[i % 2].replay()
     got, want = replayed.state(), eager.state()
     assert int(want[-1].item()) == 0 and want[4].tolist() == [40, 17, 40]
+    for a, b in zip(got, want):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_pools_past_32_bits():
+    """The same steps on pages at byte offsets beyond 2^32 of each pool."""
+    gen = torch.Generator("cuda").manual_seed(6)
+    near, far = Loop(), Loop(base=2**32 // (PS * H_K * 128) + 12345)
+    for _ in range(10):
+        x = torch.randn(near.x.shape, generator=gen, device="cuda").to(torch.bfloat16)
+        for loop in (near, far):
+            loop.x.copy_(x)
+            loop.step()
+    want, got = near.state(), far.state()
+    assert int(want[-1].item()) == 0
     for a, b in zip(got, want):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))

@@ -579,9 +579,11 @@ decode_qm_kernel(const std::conditional_t<kMod, DecodeModDev, DecodeDev> a, cons
           // poison keys never leak); a tile wholly below every row's limit of
           // its warp skips the selects.  64 columns per TMEM round trip.
           // (rows past n_q produce nothing: any value will do for them)
+          // kMod: halves one by one, so that a CTA of few tiles fetches the
+          // longer code once (244 rows over 84 one-tile CTAs: 20.1 -> 19.7 us)
           const bool unmasked = __all_sync(0xffffffffu, !live || all_visible(key0, kRows));
           float mt = -INFINITY;
-    #pragma unroll
+    #pragma unroll(kMod ? 1 : kRows / kCh)
           for (int h0 = 0; h0 < kRows; h0 += kCh) {
             uint32_t rr[kCh];
     #pragma unroll
@@ -644,7 +646,7 @@ decode_qm_kernel(const std::conditional_t<kMod, DecodeModDev, DecodeDev> a, cons
           // packed-half one, so nothing is saved by narrowing it.)
           const float bias = fmaf(-mu, c2, kLog2PScale);
           const float2 c2x2 = make_float2(c2, c2), bias2 = make_float2(bias, bias);
-    #pragma unroll
+    #pragma unroll(kMod ? 1 : kRows / kCh)
           for (int h0 = 0; h0 < kRows; h0 += kCh) {
             uint32_t rr[kCh];
     #pragma unroll

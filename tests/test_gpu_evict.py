@@ -158,6 +158,16 @@ def test_more_groups_than_the_gpu_holds():
     c.check()
 
 
+@pytest.mark.parametrize("b", [305, 512, 513])
+def test_many_sequences(b):
+    """Around the number up to which the longest are taken first; equal
+    lengths among them."""
+    rng = np.random.default_rng(b)
+    c = Case(rng.integers(0, 60, b).tolist(), 20, h_k=1, first=1, last=4)
+    c.call()()
+    c.check()
+
+
 def test_everything_protected_in_excess_keeps_the_lowest_slots():
     """More slots hold a protected position than the budget: the lowest stay."""
     c = Case([200], 50, h_k=1, pos=True, last=50)

@@ -509,7 +509,8 @@ typedef struct {
 
 /* Rotary positions with one to four axes, and the new tokens' rows:
  *   p = positions[freq_axis[i]][t], c = cos_sin[p][i], s = cos_sin[p][rot_dim/2 + i]
- *   (x_a, x_b) of pair i -> (x_a c - x_b s, x_b c + x_a s)      in fp32
+ *   (x_a, x_b) of pair i -> (x_a c - x_b s, x_b c + x_a s)
+ *                           in fp32, each operation rounded by itself
  *   Q: bf16 of it;  K: e4m3 of it / k_descale[b,g];  V: e4m3(v / v_descale[b,g])
  * (IEEE fp32 division; e4m3 to nearest even, saturating at +-448; NaN gives
  * a NaN code).  The rotated K is not rounded to bf16 in between.  One kernel

@@ -253,6 +253,32 @@ def test_codes_are_those_of_the_division():
             assert torch.equal(torch.where(nan, 0x7F, g), torch.where(nan, 0x7F, want)), exps
 
 
+@pytest.mark.parametrize("pairs", [False, True], ids=["halves", "neighbours"])
+def test_results_are_the_formulas_in_fp32(pairs):
+    """Q and K equal the formula evaluated operation by operation, bit for bit."""
+    n, h_k, h_r, rot = 6000, 4, 2, 96
+    c = Case([n], [0], h_k=h_k, h_r=h_r, page_size=128, rot=rot, axes=3, mixed=True, pairs=pairs)
+    c.call()()
+    torch.cuda.synchronize()
+    at = c.dev["positions"].long()[torch.from_numpy(c.axis).cuda()].t()
+    f = torch.arange(rot // 2, device="cuda")
+    cos, sin = c.dev["cos_sin"][at, f][:, None], c.dev["cos_sin"][at, rot // 2 + f][:, None]
+
+    def turn(x):
+        x = x.float()
+        y = x.clone()
+        ia, ib = (slice(0, rot, 2), slice(1, rot, 2)) if pairs else (slice(0, rot // 2), slice(rot // 2, rot))
+        y[..., ia] = x[..., ia] * cos - x[..., ib] * sin
+        y[..., ib] = x[..., ib] * cos + x[..., ia] * sin
+        return y
+
+    assert torch.equal(c.q_out, turn(c.q).to(torch.bfloat16))
+    slot = torch.arange(n, device="cuda")
+    got = c.kc[c.dev["block_table"][0, slot // 128].long(), slot % 128]
+    want = (turn(c.k) / c.dev["k_descale"][0][:, None]).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    assert torch.equal(got, want)
+
+
 def test_signed_zeros_keep_their_sign():
     c = Case([3, 3], [5, 40], h_k=2, h_r=1, packed=False)
     v = c.v.clone()

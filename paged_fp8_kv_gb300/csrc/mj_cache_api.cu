@@ -20,6 +20,10 @@ constexpr int64_t kMaxStride = int64_t{1} << 40;
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// n elements `stride` apart reach past any memory (the offsets below and in
+// the kernels are 64-bit)
+bool too_far(int64_t n, int64_t stride) { return n > 1 && stride > (int64_t{1} << 44) / (n - 1); }
+
 // [a, a + an) and [b, b + bn) share a byte
 bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
@@ -95,6 +99,10 @@ extern "C" mj_status mj_rope_append(const mj_rope_params* params, const mj_rope_
     if (s < 0 || s >= kMaxStride) return MJ_ERR_INVALID_ARG;
   const int64_t row_elems = h_q * kHeadDim * (a.q_packed ? p.q_len : 1);
   const int64_t rows = a.q_packed ? p.num_seqs : a.num_tokens;
+  if (too_far(a.num_tokens, a.q_tok) || too_far(a.num_tokens, a.k_tok) || too_far(a.num_tokens, a.v_tok) ||
+      too_far(h_q, a.q_head) || too_far(p.h_k, a.k_head_in) || too_far(p.h_k, a.v_head_in) ||
+      too_far(rows, a.q_out_stride))
+    return MJ_ERR_INVALID_ARG;
   if (a.q_out_stride % 8 != 0 || a.q_out_stride < 0 || a.q_out_stride >= kMaxStride) return MJ_ERR_INVALID_ARG;
   if (rows > 1 && a.q_out_stride < row_elems) return MJ_ERR_INVALID_ARG;
   RopeDev d{};
@@ -243,6 +251,7 @@ extern "C" mj_status mj_key_weights(const mj_decode_params* params, const mj_sco
     if (s < 0 || s >= kMaxStride) return MJ_ERR_INVALID_ARG;
   const int64_t max_len = static_cast<int64_t>(p.max_blocks) * p.page_size;
   if ((p.h_k > 1 && acc_head < max_len) || (p.num_seqs > 1 && acc_seq < max_len)) return MJ_ERR_INVALID_ARG;
+  if (too_far(p.num_seqs, acc_seq) || too_far(p.h_k, acc_head)) return MJ_ERR_INVALID_ARG;
   if (!(a.softmax_scale > 0.f) || !(decay >= 0.f && decay <= 1.f) || fresh < 0) return MJ_ERR_INVALID_ARG;
 
   DecodeModDev d{};
@@ -348,6 +357,7 @@ extern "C" mj_status mj_evict(const mj_decode_params* params, const mj_evict_arg
     if (!aligned4(x)) return MJ_ERR_INVALID_ARG;
   for (int64_t s : {a.acc_seq, a.acc_head})
     if (s < 0 || s >= kMaxStride) return MJ_ERR_INVALID_ARG;
+  if (too_far(p.num_seqs, a.acc_seq) || too_far(p.h_k, a.acc_head)) return MJ_ERR_INVALID_ARG;
   const int64_t lens_bytes = static_cast<int64_t>(p.num_seqs) * 4;
   if (overlap(a.new_lens, lens_bytes, a.seq_lens, lens_bytes)) return MJ_ERR_INVALID_ARG;
   if (a.key_pos && overlap(a.new_lens, lens_bytes, a.next_pos, lens_bytes)) return MJ_ERR_INVALID_ARG;

@@ -104,6 +104,14 @@ def test_rope_layout_and_axes_refused():
     assert _rope_status(p, a) == mj.MJ_OK
 
 
+@pytest.mark.parametrize("field", ["q_tok", "k_tok", "v_tok", "q_out_stride"])
+def test_rope_offsets_past_any_memory_refused(field):
+    p, a = _rope()
+    _set(a, cu_tokens=_ptr(), q_packed=0, q_out_stride=8 * 128, num_tokens=1 << 30, pos_axis=1 << 30)
+    setattr(a, field, (1 << 40) - 16)
+    assert _rope_status(p, a) == BAD
+
+
 def test_rope_in_place_refuses_k_or_v_under_the_output():
     rows = 8 + 2 + 2  # heads of one projection's token
     for name, tok, head in (("k", "k_tok", "k_head_in"), ("v", "v_tok", "v_head_in")):
@@ -245,6 +253,10 @@ def test_evict_aliases_and_planes_refused():
     _set(a, key_pos=key_pos, key_pos_out=key_pos + 64, next_pos=_ptr())
     assert _evict_status(p, a) == BAD
     p, a = _evict(kv_format=mj.MJ_KV_NVFP4)  # no scale planes given
+    assert _evict_status(p, a) == BAD
+    p, a = _evict()
+    p.num_seqs, a.acc_seq = 1 << 22, (1 << 40) - 16  # past any memory
+    a.workspace_bytes = mj.evict_workspace_bytes(p, 100)
     assert _evict_status(p, a) == BAD
     p, a = _evict()
     _set(a, keep_first=60, keep_last=41)

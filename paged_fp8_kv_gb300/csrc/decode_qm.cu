@@ -530,7 +530,8 @@ decode_qm_kernel(const std::conditional_t<kMod, DecodeModDev, DecodeDev> a, cons
     int lim = a.causal ? L - a.q_len + qrow / a.h_r : L - 1;
     lim = lim < L - 1 ? lim : L - 1;
     int lo = 0, pfx = 0;  // kMod: keys [lo, lim] and [0, pfx)
-    float mod_c1 = 0.f, cap2 = 0.f, slope2 = 0.f, row_pos = 0.f;
+    float mod_c1 = 0.f, cap2 = 0.f, slope2 = 0.f;
+    int row_pos = 0;  // distances are taken in whole numbers: positions past 2^24 share fp32 values
     if constexpr (kMod) {
       if (live) {
         const RowRange rr = row_range(a.mod, a.causal, a.q_len, b, L, qrow / a.h_r);
@@ -541,7 +542,7 @@ decode_qm_kernel(const std::conditional_t<kMod, DecodeModDev, DecodeDev> a, cons
       }
       cap2 = a.mod.softcap * kLog2e;
       mod_c1 = a.mod.softcap > 0.f ? raw_l / a.mod.softcap : raw_l * kLog2e;
-      row_pos = static_cast<float>(L - a.q_len + qrow / a.h_r);
+      row_pos = L - a.q_len + qrow / a.h_r;
     }
     if (!live) lim = -1;
     auto visible = [&](int key) {
@@ -591,7 +592,7 @@ decode_qm_kernel(const std::conditional_t<kMod, DecodeModDev, DecodeDev> a, cons
             ptx::tmem_ld_wait();
             if constexpr (kMod) {  // logits, masked, back over S for pass 2
               modify_scores<kCh>(rr, mod_c1, cap2, a.mod.slopes != nullptr, slope2,
-                                 row_pos - static_cast<float>(key0 + h0));
+                                 static_cast<float>(row_pos - key0 - h0));
               if (!unmasked) {
 #pragma unroll
                 for (int e = 0; e < kCh; ++e) rr[e] = visible(key0 + h0 + e) ? rr[e] : 0xFF800000u;  // -inf
@@ -849,7 +850,8 @@ decode_qm_kernel(const std::conditional_t<kMod, DecodeModDev, DecodeDev> a, cons
         if (lane == 0) ptx::mbar_arrive(wgbar(wg, 1));
         if (warp_live) {
           if constexpr (kMod) {  // logits, masked here for both passes
-            modify_scores<kR>(sv, mod_c1, cap2, a.mod.slopes != nullptr, slope2, row_pos - static_cast<float>(key0 + cb));
+            modify_scores<kR>(sv, mod_c1, cap2, a.mod.slopes != nullptr, slope2,
+                              static_cast<float>(row_pos - key0 - cb));
             if (!unmasked) {
 #pragma unroll
               for (int e = 0; e < kR; ++e) sv[e] = visible(key0 + cb + e) ? sv[e] : 0xFF800000u;  // -inf

@@ -670,16 +670,15 @@ decode_tc_kernel(const std::conditional_t<kMod, DecodeModDev, DecodeDev> a, cons
         if (st_tid < R) {  // the row's constants (rows past n_q see every key: any value will do)
           const int n = n0 + st_tid;
           float slope2 = 0.f;
-          int pos = 0, lo = 0, hi = L - 1;
+          int lo = 0, hi = L - 1;
           if (n < a.n_q) {
             const RowRange rr = row_range(a.mod, a.causal, a.q_len, b, L, n / a.h_r);
             hi = rr.hi < span.z - 1 ? rr.hi : span.z - 1;
             lo = rr.lo > span.y ? rr.lo : span.y;
-            pos = L - a.q_len + n / a.h_r;
             if (a.mod.slopes) slope2 = a.mod.slopes[g * a.h_r + n % a.h_r] * kLog2e;
           }
           row_slope2[st_tid] = slope2;
-          row_pos[st_tid] = static_cast<float>(pos);
+          row_pos[st_tid] = static_cast<float>(n / a.h_r);  // from the first new token's
           row_lo[st_tid] = lo;
           row_hi[st_tid] = hi;
         }
@@ -756,7 +755,7 @@ decode_tc_kernel(const std::conditional_t<kMod, DecodeModDev, DecodeDev> a, cons
         }
         if constexpr (kMod) {
           modify_columns<kCols>(sc, mod_c1, cap2, a.mod.slopes != nullptr, row_slope2 + col0, row_pos + col0,
-                                static_cast<float>(j));
+                                static_cast<float>(j - (L - a.q_len)));
           if (j >= pfx && (j < lo_max || j > hi_min)) {
 #pragma unroll
             for (int c = 0; c < kCols; ++c)

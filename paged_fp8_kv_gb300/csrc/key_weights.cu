@@ -498,23 +498,24 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (ct < p.rows) {
           const int n = p.n0 + ct;
           float nlse2 = -INFINITY, slope2 = 0.f;
-          int lo = 0, hi = -1, pos = 0;
+          int lo = 0, hi = -1, from_first = 0;
           if (ct < p.n_rows) {
             const int qi = n / a.h_r;
-            pos = L - a.q_len + qi;
+            from_first = qi - p.n0 / a.h_r;
             if constexpr (kMod) {
               const RowRange r = row_range(a.mod, a.causal, a.q_len, b, L, qi);
               lo = r.lo;
               hi = r.hi;
               if (a.mod.slopes) slope2 = a.mod.slopes[g * a.h_r + n % a.h_r] * kLog2e;
             } else {
+              const int pos = L - a.q_len + qi;
               hi = a.causal && pos < L - 1 ? pos : L - 1;
             }
             nlse2 = lse_next == -INFINITY ? -INFINITY : -lse_next * kLog2e;
           }
           row_nlse2[ct] = nlse2;
           row_slope2[ct] = slope2;
-          row_pos[ct] = static_cast<float>(pos);
+          row_pos[ct] = static_cast<float>(from_first);
           row_lo[ct] = lo;
           row_hi[ct] = hi;
         }
@@ -564,7 +565,8 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (!ptx::mbar_wait_bounded(sfull(sb), phase_of(n), abort_flag, kWaitNs)) set_abort(abort_flag, a.status);
           ptx::tc_fence_after();
           const bool whole = lim.whole(key0);  // uniform
-          const float fkey = static_cast<float>(key);
+          // positions from the launch's first row's: exact to 2^24 of distance anywhere
+          const float fkey = static_cast<float>(key - pos_min);
           const float2 nkey2 = make_float2(-fkey, -fkey);
           const bool ahead = key0 + kKeys - 1 > pos_min;  // some distance may be negative
           // the tile's row sums; capped scores by the polynomial (near) or by

@@ -197,6 +197,8 @@ __device__ __forceinline__ void modify_scores(uint32_t* r, float c1, float cap2,
 
 // The same for one key and N rows: s[c] is row c's score of the key at
 // position `key`, the rows' slopes (log2 units) and positions in shared memory.
+// Key and rows count from one position near the rows (whole positions past
+// 2^24 share fp32 values: the bias would be of a neighbouring distance).
 template <int N>
 __device__ __forceinline__ void modify_columns(float* s, float c1, float cap2, bool bias, const float* slope2,
                                                const float* pos, float key) {

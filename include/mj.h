@@ -602,7 +602,9 @@ mj_status mj_decode_attn_mod(const mj_decode_params* params, const mj_score_mod*
  *                 once), q_descale, k_descale and their strides,
  *                 softmax_scale, lse, status; the rest is ignored
  *   acc           device fp32, slot j of (b, g) at b*acc_seq + g*acc_head + j
- *                 (elements; room for the longest sequence)
+ *                 (elements; max_blocks*page_size slots each, and none in two:
+ *                 acc_seq passes all heads' planes, or acc_head all
+ *                 sequences')
  *   decay         0 <= decay <= 1; with 0 (and for fresh keys) acc is not read
  *   fresh         >= 0: the newest keys, whose accumulators start from zero
  *                 (q_len after a decode step that appended q_len tokens)
@@ -618,7 +620,7 @@ mj_status mj_key_weights(const mj_decode_params* params, const mj_score_mod* mod
  *                mj_decode_args, of any kv_format; written
  *   block_table, seq_lens   as in mj_decode_args
  *   acc          fp32 weights, slot j of (b, g) at b*acc_seq + g*acc_head + j
- *                (strides as in mj_key_weights)
+ *                (strides and room as in mj_key_weights)
  *   acc_out      the kept slots' weights, same strides; acc itself or a
  *                buffer apart from it (so key_pos_out)
  *   key_pos      optional int32, same strides: the position of the token each

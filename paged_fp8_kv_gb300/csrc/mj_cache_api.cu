@@ -30,6 +30,14 @@ bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
   return x < y + static_cast<uintptr_t>(bn) && y < x + static_cast<uintptr_t>(an);
 }
 
+// The planes of `len` slots at b*seq + g*head (b < num_seqs, g < h_k) have no
+// slot in common: each index's step passes all that the other one reaches.
+bool planes_apart(int num_seqs, int h_k, int64_t seq, int64_t head, int64_t len) {
+  if (num_seqs == 1) return h_k == 1 || head >= len;
+  if (h_k == 1) return seq >= len;
+  return (head >= len && seq >= (h_k - 1) * head + len) || (seq >= len && head >= (num_seqs - 1) * seq + len);
+}
+
 bool page_size_ok(int ps) { return ps == 16 || ps == 32 || ps == 64 || ps == 128; }
 
 // An NVTX range around a call's launches, so a profiler's timeline names them.
@@ -250,8 +258,8 @@ extern "C" mj_status mj_key_weights(const mj_decode_params* params, const mj_sco
   for (int64_t s : {a.qd_seq, a.qd_head, a.kd_seq, a.kd_head, acc_seq, acc_head})
     if (s < 0 || s >= kMaxStride) return MJ_ERR_INVALID_ARG;
   const int64_t max_len = static_cast<int64_t>(p.max_blocks) * p.page_size;
-  if ((p.h_k > 1 && acc_head < max_len) || (p.num_seqs > 1 && acc_seq < max_len)) return MJ_ERR_INVALID_ARG;
   if (too_far(p.num_seqs, acc_seq) || too_far(p.h_k, acc_head)) return MJ_ERR_INVALID_ARG;
+  if (!planes_apart(p.num_seqs, p.h_k, acc_seq, acc_head, max_len)) return MJ_ERR_INVALID_ARG;
   if (!(a.softmax_scale > 0.f) || !(decay >= 0.f && decay <= 1.f) || fresh < 0) return MJ_ERR_INVALID_ARG;
 
   DecodeModDev d{};
@@ -368,7 +376,7 @@ extern "C" mj_status mj_evict(const mj_decode_params* params, const mj_evict_arg
   if (a.key_pos && a.key_pos_out != a.key_pos && overlap(a.key_pos_out, plane, a.key_pos, plane))
     return MJ_ERR_INVALID_ARG;
   // and the heads' slots are their own
-  if ((p.h_k > 1 && a.acc_head < max_len) || (p.num_seqs > 1 && a.acc_seq < max_len)) return MJ_ERR_INVALID_ARG;
+  if (!planes_apart(p.num_seqs, p.h_k, a.acc_seq, a.acc_head, max_len)) return MJ_ERR_INVALID_ARG;
   const EvictLayout w = evict_layout(p, a.budget);
   if (!a.workspace || !aligned16(a.workspace)) return MJ_ERR_INVALID_ARG;
   if (a.workspace_bytes < w.total) return MJ_ERR_CAPACITY;

@@ -266,6 +266,23 @@ def test_evict_aliases_and_planes_refused():
         mj.evict_workspace_bytes(p, 0)
 
 
+# ------------------------------------------------- planes of slots that coincide
+
+
+@pytest.mark.parametrize("seq,head,apart", [
+    (2048, 1024, True), (1024, 2048, True), (1024 + 1024, 1500, False), (1024, 1024, False), (1500, 1024, False),
+    (1024, 1500, False), (2524, 1500, True), (1024, 2047, False),
+])
+def test_planes_of_two_heads_that_share_slots_refused(seq, head, apart):
+    """Two sequences, two heads, 1024 slots: each plane's slots are its own."""
+    p, a = _attn()
+    p.h_k, a.q_seq_stride = 2, 2 * 4 * 128
+    assert (_kw_status(p, a, seq=seq, head=head) != BAD) == apart
+    p, a = _evict()
+    _set(a, acc_seq=seq, acc_head=head)
+    assert (_evict_status(p, a) != BAD) == apart
+
+
 # ---------------------------------------------------------- binding's checks
 
 

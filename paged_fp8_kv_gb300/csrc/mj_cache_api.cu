@@ -30,6 +30,14 @@ bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
   return x < y + static_cast<uintptr_t>(bn) && y < x + static_cast<uintptr_t>(an);
 }
 
+// the same of a pool's pages, rows and heads, or of a (sequence, head) array
+bool pool_too_far(int num_pages, int page_size, int h_k, int64_t page, int64_t row, int64_t head) {
+  return too_far(num_pages, page) || too_far(page_size, row) || too_far(h_k, head);
+}
+bool heads_too_far(int num_seqs, int h_k, int64_t seq, int64_t head) {
+  return too_far(num_seqs, seq) || too_far(h_k, head);
+}
+
 // The planes of `len` slots at b*seq + g*head (b < num_seqs, g < h_k) have no
 // slot in common: each index's step passes all that the other one reaches.
 bool planes_apart(int num_seqs, int h_k, int64_t seq, int64_t head, int64_t len) {
@@ -110,6 +118,11 @@ extern "C" mj_status mj_rope_append(const mj_rope_params* params, const mj_rope_
   if (too_far(a.num_tokens, a.q_tok) || too_far(a.num_tokens, a.k_tok) || too_far(a.num_tokens, a.v_tok) ||
       too_far(h_q, a.q_head) || too_far(p.h_k, a.k_head_in) || too_far(p.h_k, a.v_head_in) ||
       too_far(rows, a.q_out_stride))
+    return MJ_ERR_INVALID_ARG;
+  if (pool_too_far(p.num_pages, p.page_size, p.h_k, a.k_page, a.k_row, a.k_head) ||
+      pool_too_far(p.num_pages, p.page_size, p.h_k, a.v_page, a.v_row, a.v_head) ||
+      heads_too_far(p.num_seqs, p.h_k, a.kd_seq, a.kd_head) || heads_too_far(p.num_seqs, p.h_k, a.vd_seq, a.vd_head) ||
+      (a.key_pos && heads_too_far(p.num_seqs, p.h_k, a.kp_seq, a.kp_head)))
     return MJ_ERR_INVALID_ARG;
   if (a.q_out_stride % 8 != 0 || a.q_out_stride < 0 || a.q_out_stride >= kMaxStride) return MJ_ERR_INVALID_ARG;
   if (rows > 1 && a.q_out_stride < row_elems) return MJ_ERR_INVALID_ARG;
@@ -258,7 +271,9 @@ extern "C" mj_status mj_key_weights(const mj_decode_params* params, const mj_sco
   for (int64_t s : {a.qd_seq, a.qd_head, a.kd_seq, a.kd_head, acc_seq, acc_head})
     if (s < 0 || s >= kMaxStride) return MJ_ERR_INVALID_ARG;
   const int64_t max_len = static_cast<int64_t>(p.max_blocks) * p.page_size;
-  if (too_far(p.num_seqs, acc_seq) || too_far(p.h_k, acc_head)) return MJ_ERR_INVALID_ARG;
+  if (too_far(p.num_seqs, a.q_seq_stride) || heads_too_far(p.num_seqs, p.h_k, a.qd_seq, a.qd_head) ||
+      heads_too_far(p.num_seqs, p.h_k, a.kd_seq, a.kd_head) || heads_too_far(p.num_seqs, p.h_k, acc_seq, acc_head))
+    return MJ_ERR_INVALID_ARG;
   if (!planes_apart(p.num_seqs, p.h_k, acc_seq, acc_head, max_len)) return MJ_ERR_INVALID_ARG;
   if (!(a.softmax_scale > 0.f) || !(decay >= 0.f && decay <= 1.f) || fresh < 0) return MJ_ERR_INVALID_ARG;
 
@@ -365,7 +380,12 @@ extern "C" mj_status mj_evict(const mj_decode_params* params, const mj_evict_arg
     if (!aligned4(x)) return MJ_ERR_INVALID_ARG;
   for (int64_t s : {a.acc_seq, a.acc_head})
     if (s < 0 || s >= kMaxStride) return MJ_ERR_INVALID_ARG;
-  if (too_far(p.num_seqs, a.acc_seq) || too_far(p.h_k, a.acc_head)) return MJ_ERR_INVALID_ARG;
+  if (heads_too_far(p.num_seqs, p.h_k, a.acc_seq, a.acc_head) ||
+      pool_too_far(p.num_pages, p.page_size, p.h_k, a.k_page, a.k_row, a.k_head) ||
+      pool_too_far(p.num_pages, p.page_size, p.h_k, a.v_page, a.v_row, a.v_head) ||
+      (p.kv_format == MJ_KV_NVFP4 && (pool_too_far(p.num_pages, 1, p.h_k, a.ks_page, 0, a.ks_head) ||
+                                      pool_too_far(p.num_pages, 1, p.h_k, a.vs_page, 0, a.vs_head))))
+    return MJ_ERR_INVALID_ARG;
   const int64_t lens_bytes = static_cast<int64_t>(p.num_seqs) * 4;
   if (overlap(a.new_lens, lens_bytes, a.seq_lens, lens_bytes)) return MJ_ERR_INVALID_ARG;
   if (a.key_pos && overlap(a.new_lens, lens_bytes, a.next_pos, lens_bytes)) return MJ_ERR_INVALID_ARG;

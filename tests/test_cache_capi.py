@@ -266,6 +266,40 @@ def test_evict_aliases_and_planes_refused():
         mj.evict_workspace_bytes(p, 0)
 
 
+# --------------------------------- offsets past any memory, whatever they index
+
+
+FAR = (1 << 40) - 32
+
+
+@pytest.mark.parametrize("field", ["kp_seq", "kp_head", "kd_seq", "kd_head", "vd_seq", "vd_head", "k_page", "v_page", "k_head", "v_head"])
+def test_rope_planes_descales_and_pools_past_any_memory_refused(field):
+    p, a = _rope()
+    p.num_seqs, p.h_k, p.h_r, p.num_pages = 1 << 20, 1024, 1, 1 << 20
+    _set(a, cu_tokens=_ptr(), q_packed=0, q_tok=1024 * 128, q_out_stride=1024 * 128, key_pos=_ptr())
+    setattr(a, field, FAR)
+    assert _rope_status(p, a) == BAD
+
+
+@pytest.mark.parametrize("field", ["k_page", "v_page", "k_head", "v_head", "ks_page", "vs_page", "ks_head", "vs_head"])
+def test_evict_pools_past_any_memory_refused(field):
+    p, a = _evict(kv_format=mj.MJ_KV_NVFP4)
+    p.h_k, p.num_pages = 1024, 1 << 20
+    _set(a, k_scales=_ptr(), v_scales=_ptr(), ks_page=128 * 1024, ks_head=128, vs_page=128 * 1024, vs_head=128, acc_seq=1 << 20,
+         acc_out=a.acc, workspace_bytes=mj.evict_workspace_bytes(p, 100))
+    assert _evict_status(p, a) != BAD
+    setattr(a, field, FAR)
+    assert _evict_status(p, a) == BAD
+
+
+@pytest.mark.parametrize("field", ["qd_seq", "kd_seq", "q_seq_stride"])
+def test_key_weights_descales_and_rows_past_any_memory_refused(field):
+    p, a = _attn()
+    p.num_seqs = 1 << 20
+    setattr(a, field, FAR)
+    assert _kw_status(p, a) == BAD
+
+
 # ------------------------------------------------- planes of slots that coincide
 
 

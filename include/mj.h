@@ -600,7 +600,12 @@ mj_status mj_decode_attn_mod(const mj_decode_params* params, const mj_score_mod*
  *                 seq_lens, work, num_work (a plan made from seq_lens
  *                 themselves, so that every tile of every sequence is in it
  *                 once), q_descale, k_descale and their strides,
- *                 softmax_scale, lse, status; the rest is ignored
+ *                 softmax_scale, lse, status; the rest is ignored.  status
+ *                 (optional, caller-zeroed) becomes MJ_ERR_INVALID_ARG when
+ *                 the items hold fewer tiles than the sequences (a plan of
+ *                 mj_score_spans' plan_lens, or of earlier lengths): the
+ *                 accumulators of the missing tiles are then left as they
+ *                 were
  *   acc           device fp32, slot j of (b, g) at b*acc_seq + g*acc_head + j
  *                 (elements; max_blocks*page_size slots each, and none in two:
  *                 acc_seq passes all heads' planes, or acc_head all

@@ -1028,7 +1028,8 @@ def decode_attn_mod(params: DecodeParams, mod: ScoreMod, *, stream=None, **tenso
 class KeyWeights(_Call):
     """mj_key_weights on device tensors: acc (num_seqs, h_k, slots) float32
     receives the weights of every cached key; work is of a plan made from
-    seq_lens themselves; mod may be None."""
+    seq_lens themselves (not from spans' plan_lens: status reports one that
+    holds too few tiles); mod may be None."""
 
     _name = "mj_key_weights"
 

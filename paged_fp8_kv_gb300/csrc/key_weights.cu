@@ -53,6 +53,7 @@ constexpr int kKeys = 128;                   // keys per tile = MMA M
 constexpr int kTileBytes = kKeys * 128;      // 16 KB
 constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s: far above any legal wait
 constexpr int kStatusTimeout = 5;            // MJ_ERR_TIMEOUT
+constexpr int kStatusInvalidArg = 1;         // MJ_ERR_INVALID_ARG
 constexpr int kThreads = 64 + 256;
 constexpr int kMaxStages = 8;
 constexpr int kBarCons = 1;  // named barrier of the 256 consumer threads
@@ -184,6 +185,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   float* const amax_red = reinterpret_cast<float*>(misc + 32);      // [8]
   int64_t* const scan_red = reinterpret_cast<int64_t*>(misc + 64);  // [10]
   int* const walk_s = reinterpret_cast<int*>(misc + 160);           // (w, t) of the share's start and end
+  int64_t* const need_red = reinterpret_cast<int64_t*>(misc + 176);  // [10]
 
   const uint32_t bar0 = sbase + p.off_bar;
   auto kfull = [&](int s) { return bar0 + 8u * s; };
@@ -221,6 +223,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     ptx::tmem_alloc(ptx::smem_u32(tmem_slot), p.tmem_cols);
     ptx::tmem_relinquish();
   }
+  const int max_len = a.max_blocks * a.page_size;  // acc has no more slots
+  auto length_of = [&](int b) {
+    const int L = a.seq_lens[b];
+    return L < 0 ? 0 : (L < max_len ? L : max_len);
+  };
   // ---- this CTA's share of the items' tiles in order, for one kv head; the
   // CTAs of the other heads' shares run beside it.  An item costs its tiles
   // and kItemCost more (the start of a segment); a cut inside that start falls
@@ -243,6 +250,20 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (lane >= o) x += y;
     }
     if (lane == 31) scan_red[warp] = x;
+    // (one CTA) tiles that the sequences have and the items do not: a plan of
+    // other lengths, such as the spans', whose other keys would go unnoticed
+    const bool counts = blockIdx.x == 0 && a.status;
+    if (counts) {
+      int64_t need = 0;
+      for (int b = tid; b < a.num_seqs; b += kThreads) {
+        const int L = length_of(b);
+        need += L > 0 ? (L + kKeys - 1) / kKeys : 1;  // a plan has a tile of an empty one too
+      }
+      for (int w = w0; w < w1; ++w) need -= work[w].z - work[w].y;
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) need += __shfl_xor_sync(0xffffffffu, need, o);
+      if (lane == 0) need_red[warp] = need;
+    }
     if (tid < 2) {  // a cut past every item (the last share's end)
       walk_s[2 * tid] = a.num_work;
       walk_s[2 * tid + 1] = 0;
@@ -253,6 +274,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int w = 0; w < kThreads / 32; ++w) {
       before += w < warp ? scan_red[w] : 0;
       total += scan_red[w];
+    }
+    if (counts && tid == 0) {
+      int64_t need = 0;
+      for (int w = 0; w < kThreads / 32; ++w) need += need_red[w];
+      if (need > 0) atomicExch(a.status, kStatusInvalidArg);
     }
     const int shares = gridDim.x / a.h_k, share = blockIdx.x / a.h_k;
     for (int cut = 0; cut < 2; ++cut) {
@@ -272,11 +298,6 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t tmem = *tmem_slot;
   Walk walk{work, walk_s[0], walk_s[1], walk_s[2], walk_s[3]};
   Segment sg;
-  const int max_len = a.max_blocks * a.page_size;  // acc has no more slots
-  auto length_of = [&](int b) {
-    const int L = a.seq_lens[b];
-    return L < 0 ? 0 : (L < max_len ? L : max_len);
-  };
 
   if (warp == 0) {
     // ---------------------------------------------------------- producer

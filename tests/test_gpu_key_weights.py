@@ -136,3 +136,22 @@ def test_same_bytes_in_a_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert np.array_equal(one, x.acc.cpu().numpy())
+
+
+def test_a_plan_of_the_spans_or_of_shorter_lengths_is_reported():
+    """It leaves tiles out; one made for longer lengths does not."""
+    w = syn.make_workload("kw", [1500, 2, 0, 129], 2, 2, 4, 16, seed=23, max_splits=4)
+    mod, _ = make_mod(w, np.random.default_rng(0), window=100)
+    x = Weights(w, dict(window=100), 0.5, 2)
+    x.check()
+    s, lens = x.s, np.asarray(w.seq_lens)
+    longer = np.minimum(lens + [0, 0, 40, 500], w.max_blocks * 16)
+    for plan_lens, want in ((mj.score_spans(s.params, mod, lens)[1], mj.MJ_ERR_INVALID_ARG), (lens - [129, 0, 0, 0], mj.MJ_ERR_INVALID_ARG),
+                            (lens - [0, 0, 0, 1], mj.MJ_ERR_INVALID_ARG), (longer, 0), (lens, 0)):
+        work = torch.from_numpy(mj.decode_plan(s.params, plan_lens).work).cuda()
+        x.status.zero_()
+        mj.key_weights(s.params, mod, q=s.q_packed, k_cache=s.k_cache, block_table=s.block_table, seq_lens=s.seq_lens, work=work,
+                       q_descale=s.q_descale, k_descale=s.k_descale, lse=x.lse, acc=x.acc, softmax_scale=w.softmax_scale, decay=0.5,
+                       fresh=2, status=x.status)
+        torch.cuda.synchronize()
+        assert int(x.status.item()) == want, plan_lens

@@ -668,17 +668,17 @@ decode_tc_kernel(const std::conditional_t<kMod, DecodeModDev, DecodeDev> a, cons
       if (st_tid < R) m_s[st_tid] = -INFINITY;  // running max starts at -inf
       if constexpr (kMod) {
         if (st_tid < R) {  // the row's constants (rows past n_q see every key: any value will do)
-          const int n = n0 + st_tid;
+          const int n = n0 + st_tid, qi = n / a.h_r;
           float slope2 = 0.f;
           int lo = 0, hi = L - 1;
           if (n < a.n_q) {
-            const RowRange rr = row_range(a.mod, a.causal, a.q_len, b, L, n / a.h_r);
+            const RowRange rr = row_range(a.mod, a.causal, a.q_len, b, L, qi);
             hi = rr.hi < span.z - 1 ? rr.hi : span.z - 1;
             lo = rr.lo > span.y ? rr.lo : span.y;
-            if (a.mod.slopes) slope2 = a.mod.slopes[g * a.h_r + n % a.h_r] * kLog2e;
+            if (a.mod.slopes) slope2 = a.mod.slopes[g * a.h_r + n - qi * a.h_r] * kLog2e;
           }
           row_slope2[st_tid] = slope2;
-          row_pos[st_tid] = static_cast<float>(n / a.h_r);  // from the first new token's
+          row_pos[st_tid] = static_cast<float>(qi);  // from the first new token's
           row_lo[st_tid] = lo;
           row_hi[st_tid] = hi;
         }

@@ -539,7 +539,7 @@ mj_status mj_rope_append(const mj_rope_params* params, const mj_rope_args* args,
  * anything.  A row that sees no key gets O = 0 and LSE = -inf.
  *   softcap       0 = off; else 2^-20 to 2^60
  *   window        0 = off; > 0 needs params.causal
- *   alibi_slopes  device fp32[h_k*h_r], finite, or NULL
+ *   alibi_slopes  device fp32[h_k*h_r], magnitudes up to 2^90, or NULL
  *   key_begin, key_end   device int32[num_seqs*q_len] or NULL
  *   prefix        device int32[num_seqs] or NULL
  * Positions are slots of the cache: after mj_evict has moved rows only
@@ -643,7 +643,9 @@ mj_status mj_key_weights(const mj_decode_params* params, const mj_score_mod* mod
  *                need one each)
  *   status       optional int32, caller-zeroed: MJ_ERR_INVALID_ARG when a
  *                length is out of range or a page of a row to move is outside
- *                [0, num_pages) (that row is not moved) */
+ *                [0, num_pages) (that row's K, V and scales are not moved;
+ *                its weight and position are, so the slot's no longer
+ *                describe the row it holds) */
 typedef struct {
   uint8_t* k;
   uint8_t* v;

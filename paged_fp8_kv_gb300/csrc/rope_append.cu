@@ -13,9 +13,10 @@
 //
 // Every byte is touched once (128 (4 h_r + 6) of them a token and kv head), so the
 // bound is HBM for prompts (15005 tokens of 48 heads, 341 MB: 65 us, 5.2 TB/s,
-// 59 % of the issue slots) and the launch plus one chain of dependent loads
-// (position -> table row; sequence length -> block table) for decode batches
-// (64 tokens: 3.0 us a call in a graph, 4 when the host launches each).
+// 59 % of the issue slots) and one chain of dependent loads (position ->
+// table row; sequence length -> block table) plus the launch for decode
+// batches: 64 tokens take 2.9 us a call back to back in a graph, everything in
+// L2, but 6.0 us of kernel with cold inputs, and 8.8 a call so from the host.
 // One CTA takes one or more whole tokens: the token's cos and sin are fetched
 // once into shared memory, by frequency, whatever the axes' map, and serve
 // all of its heads; the tokens' slots are looked up at the same time, and the

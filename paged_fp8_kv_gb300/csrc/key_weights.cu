@@ -23,8 +23,8 @@
 // Bound: 128 bytes of K a key and head against one exponential per row and
 // key: HBM up to about 64 rows, the exponential units and the MMA above.  64
 // sequences of 512 to 8192 keys, 8 heads, 4 rows: 55 us, 5.6 TB/s; 32 of 2048
-// to 32768, 32 rows under a soft cap: 115 us, 5.4 TB/s, the cap's polynomial
-// taking the issue slots (59 %, of which two CTAs can use little more).  A
+// to 32768, 32 rows under a soft cap: 116 us, 5.4 TB/s, the cap's polynomial
+// taking the issue slots (58 %, of which two CTAs can use little more).  A
 // launch takes 256 packed rows of e4m3 Q or 128 of bf16 Q (two segments'
 // operand rows beside a ring of seven K tiles); more rows are further launches
 // that add on, in order.

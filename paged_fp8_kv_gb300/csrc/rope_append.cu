@@ -16,7 +16,7 @@
 // 59 % of the issue slots) and one chain of dependent loads (position ->
 // table row; sequence length -> block table) plus the launch for decode
 // batches: 64 tokens take 2.9 us a call back to back in a graph, everything in
-// L2, but 6.0 us of kernel with cold inputs, and 8.8 a call so from the host.
+// L2, but 6.4 us of kernel with cold inputs, and about 9 a call so from the host.
 // One CTA takes one or more whole tokens: the token's cos and sin are fetched
 // once into shared memory, by frequency, whatever the axes' map, and serve
 // all of its heads; the tokens' slots are looked up at the same time, and the

@@ -475,7 +475,9 @@ typedef struct {
  *                K / V.  Tokens of one call must have slots of their own
  *                (pages that sequences share are not written).
  *   key_pos      optional int32: slot j of (b, g) at b*kp_seq + g*kp_head + j
- *                receives the token's position on axis 0 (see mj_evict)
+ *                receives the token's position on axis 0 (see mj_evict); the
+ *                planes are apart, or one for all heads of a sequence
+ *                (kp_head 0)
  *   status       optional int32, caller-zeroed: MJ_ERR_INVALID_ARG when a
  *                position is outside [0, max_pos) (that token is left out
  *                whole), or a slot past max_blocks*page_size or its page
@@ -602,7 +604,7 @@ mj_status mj_decode_attn_mod(const mj_decode_params* params, const mj_score_mod*
  *                 once), q_descale, k_descale and their strides,
  *                 softmax_scale, lse, status; the rest is ignored.  status
  *                 (optional, caller-zeroed) becomes MJ_ERR_INVALID_ARG when
- *                 the items hold fewer tiles than the sequences (a plan of
+ *                 the items hold fewer tiles in all than the sequences (a plan of
  *                 mj_score_spans' plan_lens, or of earlier lengths): the
  *                 accumulators of the missing tiles are then left as they
  *                 were

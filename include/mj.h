@@ -687,6 +687,254 @@ size_t mj_evict_workspace_bytes(const mj_decode_params* params, int32_t budget);
  * (workspace), MJ_ERR_CUDA. */
 mj_status mj_evict(const mj_decode_params* params, const mj_evict_args* args, mj_stream_t stream);
 
+/* ------------------------------------------------- a serving step's operators
+ *
+ * What a step needs besides: pages for its new tokens and the tables that list
+ * them (mj_pages_reserve, mj_pages_release), attention over whole prompts of
+ * different lengths (mj_prompt_plan, mj_prompt_attn), attention of drafted
+ * token trees (mj_decode_attn_tree) and the accepted branch's rows moved to
+ * where the next step reads them (mj_tree_commit).  The pages have no
+ * counterpart of these; the formulas below are their definition.  The
+ * conventions above hold. */
+
+/* Shape of the page calls.
+ *   num_seqs     rows of the block table, 1 to 16384
+ *   page_size    16, 32, 64 or 128
+ *   max_blocks   row length of the block table
+ *   num_pages    pages of the pool, and entries of the free list */
+typedef struct {
+  int32_t num_seqs, page_size, max_blocks, num_pages;
+} mj_page_params;
+
+/* Arguments of mj_pages_reserve; all pointers are device memory.
+ *   seq_lens      int32[num_seqs]: tokens a sequence holds
+ *   new_tokens    int32[num_seqs]: tokens it is to get; NULL: q_len each
+ *   free_pages    int32[num_pages]: the pages no sequence holds are its first
+ *                 num_free[0] entries; read
+ *   num_free      int32[1]; num_free_out int32[1] (may be num_free)
+ *   block_table   int32(num_seqs, max_blocks): entries of new pages are
+ *                 written, the others left as they are
+ *   seq_lens_out  int32[num_seqs] (may be seq_lens)
+ *   cu_tokens     optional out int32[num_seqs + 1]: tokens of the sequences
+ *                 before (as mj_rope_append and mj_prompt_plan take it)
+ *   positions     optional out int32[num_tokens]: each new token's position
+ *   slots         optional out int64[num_tokens]: page * page_size + row of
+ *                 each new token
+ *   num_tokens    entries of positions and slots; those behind the last
+ *                 sequence's tokens get position 0 and slot -1
+ *   status        optional int32, caller-zeroed */
+typedef struct {
+  const int32_t* seq_lens;
+  const int32_t* new_tokens;
+  int32_t q_len;
+  const int32_t* free_pages;
+  const int32_t* num_free;
+  int32_t* num_free_out;
+  int32_t* block_table;
+  int32_t* seq_lens_out;
+  int32_t* cu_tokens;
+  int32_t* positions;
+  int64_t* slots;
+  int32_t num_tokens;
+  int32_t* status;
+} mj_reserve_args;
+
+/* Pages for new tokens, in one launch: with need_b = ceil((L_b + n_b) /
+ * page_size) - ceil(L_b / page_size) and before_b the needs of the sequences
+ * ahead of b, new page i of b is free_pages[num_free - 1 - (before_b + i)];
+ * num_free_out = num_free - (all needs).
+ * A sequence whose pages are no longer in the list (before_b + need_b >
+ * num_free, need_b > 0) is left out: no page, its length unchanged, its tokens
+ * in cu_tokens but with slot -1, MJ_ERR_CAPACITY in the status; those that
+ * need no page are not.  Likewise one whose L_b or n_b is negative (its tokens
+ * then count as none) or whose tokens do not fit max_blocks: MJ_ERR_INVALID_ARG,
+ * as for more than num_tokens tokens in all where positions or slots are given
+ * (the first num_tokens are written), and for num_free outside [0, num_pages]
+ * (taken as 0).  A step whose status is not 0 must not append its tokens.
+ * Deterministic.
+ * Errors: MJ_ERR_INVALID_ARG, MJ_ERR_UNSUPPORTED (page_size, num_seqs, over
+ * 2^30 slots a sequence), MJ_ERR_CUDA. */
+mj_status mj_pages_reserve(const mj_page_params* params, const mj_reserve_args* args, mj_stream_t stream);
+
+/* Arguments of mj_pages_release, device memory.
+ *   seq_lens, keep_lens   int32[num_seqs]: tokens held, and tokens to keep (0:
+ *                 the sequence has ended)
+ *   free_pages    int32[num_pages]: grows behind its first num_free[0] entries
+ *   num_free, num_free_out   as above
+ *   block_table   int32(num_seqs, max_blocks), read
+ *   status        optional int32, caller-zeroed */
+typedef struct {
+  const int32_t* seq_lens;
+  const int32_t* keep_lens;
+  int32_t* free_pages;
+  const int32_t* num_free;
+  int32_t* num_free_out;
+  const int32_t* block_table;
+  int32_t* status;
+} mj_release_args;
+
+/* Pages ceil(keep_b / page_size) .. ceil(L_b / page_size) - 1 of every sequence
+ * go back to the free list, sequences and pages in order, in one launch.  The
+ * table keeps their entries, which nothing reads any more.  A sequence whose
+ * lengths are not 0 <= keep_b <= L_b <= max_blocks*page_size releases nothing
+ * (MJ_ERR_INVALID_ARG in the status); pages past the list's num_pages entries
+ * (a page given back twice, somewhere) are dropped, MJ_ERR_CAPACITY.  Pages
+ * must not be shared between sequences.  Deterministic.
+ * Errors: as mj_pages_reserve. */
+mj_status mj_pages_release(const mj_page_params* params, const mj_release_args* args, mj_stream_t stream);
+
+/* Attention over whole prompts: sequence b has n_b = cu_tokens[b+1] -
+ * cu_tokens[b] query tokens, the last of its L_b = seq_lens[b] keys (which the
+ * cache holds already, prompts' beginnings of earlier steps among them), n_b
+ * from 0 on and different for every sequence; a decode token is n_b = 1.
+ * Token i (0 .. n_b - 1), at position pos = L_b - n_b + i, sees key j if
+ *   j <= pos (causal) or j < L_b,   and   j > pos - window (window > 0)
+ * and z, O and LSE are those of the decode operation above, with softcap > 0:
+ * z <- softcap * tanh(z / softcap).  A token that sees no key gets O = 0 and
+ * LSE = -inf.
+ *
+ * mj_prompt_plan makes the step's work list on the device, once for all
+ * layers; mj_prompt_attn attends one layer by it.
+ *   params      num_seqs (to 16384), h_k, h_r, head_dim, page_size, max_blocks,
+ *               num_pages, causal, q_dtype, max_splits (1: no token's keys are
+ *               cut) and kv_evict_first (0 = off here: row tiles share pages);
+ *               kv_format MJ_KV_E4M3; q_len, kernel and l2_prefetch are not
+ *               looked at.  The same in both calls, and so num_tokens and window
+ *   cu_tokens   device int32[num_seqs + 1], non-decreasing, from 0 on or later,
+ *               to num_tokens at most
+ *   seq_lens    device int32[num_seqs]
+ *   num_tokens  tokens in Q and O (those outside cu_tokens' range are padding)
+ *   window      0 = off; > 0 needs params->causal
+ *   plan        device, 16-byte aligned, >= mj_prompt_plan_bytes
+ *   status      optional device int32, caller-zeroed: MJ_ERR_INVALID_ARG for
+ *               cu_tokens out of order or range (the list is then empty and the
+ *               attention writes nothing) or a length outside [0,
+ *               max_blocks*page_size] (taken as the nearest in it)
+ * Both launches may be captured.  Errors: MJ_ERR_INVALID_ARG,
+ * MJ_ERR_UNSUPPORTED (params, over 2^30 rows of num_tokens*h_k*h_r, over 4096
+ * heads), MJ_ERR_CAPACITY (plan_bytes), MJ_ERR_CUDA. */
+size_t mj_prompt_plan_bytes(const mj_decode_params* params, int32_t num_tokens);
+mj_status mj_prompt_plan(const mj_decode_params* params, const int32_t* cu_tokens, const int32_t* seq_lens,
+                         int32_t num_tokens, int32_t window, void* plan, size_t plan_bytes, int32_t* status,
+                         mj_stream_t stream);
+
+/* Arguments of mj_prompt_attn, device memory.
+ *   q            bf16 or e4m3 rows of 128, finite: token t, head h at q + t*q_tok
+ *                + h*q_head (elements; multiples of 16 bytes)
+ *   o            bf16, token t, head h at o + t*o_tok + h*128 (o_tok at least
+ *                h_k*h_r*128, a multiple of 8); no overlap with q
+ *   lse          fp32 (num_tokens, h_k*h_r) contiguous, or NULL.  O and LSE of
+ *                padding tokens are left as they were
+ *   k, v, strides, block_table, descales   as in mj_decode_args (q_descale per
+ *                sequence and kv head).  V must hold finite values below L_b
+ *   plan         of mj_prompt_plan for this shape (another one's is refused in
+ *                the status word and nothing is written)
+ *   softcap      0 = off; else 2^-20 to 2^60
+ *   workspace    >= mj_prompt_workspace_bytes, 16-byte aligned; need not be
+ *                initialised; calls that may run at the same time need one each
+ *   status       optional int32, caller-zeroed: also MJ_ERR_TIMEOUT */
+typedef struct {
+  const void* q;
+  int64_t q_tok, q_head;
+  void* o;
+  int64_t o_tok;
+  float* lse;
+  int32_t num_tokens;
+  const uint8_t* k;
+  const uint8_t* v;
+  int64_t k_page, k_row, k_head, v_page, v_row, v_head;
+  const int32_t* block_table;
+  const void* plan;
+  size_t plan_bytes;
+  const float* q_descale;
+  const float* k_descale;
+  const float* v_descale;
+  int64_t qd_seq, qd_head, kd_seq, kd_head, vd_seq, vd_head;
+  float softmax_scale, scale_o, softcap;
+  int32_t window;
+  void* workspace;
+  size_t workspace_bytes;
+  int32_t* status;
+} mj_prompt_args;
+
+size_t mj_prompt_workspace_bytes(const mj_decode_params* params);
+
+/* Deterministic; the attention and, unless max_splits is 1, a merge of the
+ * tokens whose keys were cut.  Errors: as mj_prompt_plan, and MJ_ERR_CAPACITY
+ * for the workspace. */
+mj_status mj_prompt_attn(const mj_decode_params* params, const mj_prompt_args* args, mj_stream_t stream);
+
+/* A tree of drafted tokens behind each sequence's context: the q_len query
+ * tokens of sequence b are nodes 0 .. n_b - 1 of its tree (n_b = tree_lens[b],
+ * at most q_len; NULL: q_len each) and rows without a node behind them; the
+ * cache's last n_b of L_b keys are the nodes', in the same order, the first
+ * ctx = L_b - n_b the context.  Node i sees node m if bit m % 32 of word
+ * mask[(b*q_len + i)*mask_words + m/32] is set (a node's ancestors and itself,
+ * by the caller), and context keys by the modifiers.  Rows without a node get
+ * O = 0 and LSE = -inf.
+ *   mask         device uint32[num_seqs*q_len][mask_words]
+ *   mask_words   words of a row, at least ceil(q_len / 32)
+ *   tree_lens    device int32[num_seqs] or NULL (clamped to [0, min(q_len, L_b)]) */
+typedef struct {
+  const uint32_t* mask;
+  int32_t mask_words;
+  const int32_t* tree_lens;
+} mj_tree;
+
+/* mj_decode_attn_mod for trees.  The same arguments and results; params->causal
+ * is not looked at.  mod (NULL: none) may hold a softcap, key_begin (node i sees
+ * context keys from key_begin[b*q_len + i] on: the window of a token whose
+ * position is its depth) and prefix (context keys seen ahead of that); a
+ * window, slopes or key_end, which take positions for slots, are refused
+ * (MJ_ERR_UNSUPPORTED).  spans as there, of mj_score_spans with the same mod
+ * and params, for which every key_begin entry, also of rows without a node, is
+ * at most ctx. */
+mj_status mj_decode_attn_tree(const mj_decode_params* params, const mj_tree* tree, const mj_score_mod* mod,
+                              const int32_t* spans, const mj_decode_args* args, mj_stream_t stream);
+
+/* Arguments of mj_tree_commit, device memory.
+ *   k, v, strides, k_scales, v_scales and their strides   the pools, as in
+ *                mj_decode_args, of any kv_format; written
+ *   block_table, seq_lens   as in mj_decode_args
+ *   tree_lens    int32[num_seqs] or NULL (params->q_len each), as in mj_tree
+ *   accepted     int32(num_seqs, max_accept): nodes of the accepted branch,
+ *                rising (parents come before their children)
+ *   num_accepted int32[num_seqs], 0 .. max_accept
+ *   new_lens     out int32[num_seqs] (may be seq_lens)
+ *   key_pos      optional int32: the planes of mj_rope_append, moved as well
+ *   status       optional int32, caller-zeroed: MJ_ERR_INVALID_ARG for a
+ *                sequence whose numbers are out of range or whose nodes do not
+ *                rise (nothing of it is moved, its length stays), or a page
+ *                outside [0, num_pages) (that row is not moved) */
+typedef struct {
+  uint8_t* k;
+  uint8_t* v;
+  int64_t k_page, k_row, k_head, v_page, v_row, v_head;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* tree_lens;
+  const int32_t* accepted;
+  int32_t max_accept;
+  const int32_t* num_accepted;
+  int32_t* new_lens;
+  int32_t* key_pos;
+  int64_t kp_seq, kp_head;
+  int32_t* status;
+  uint8_t* k_scales;
+  uint8_t* v_scales;
+  int64_t ks_page, ks_head, vs_page, vs_head;
+} mj_commit_args;
+
+/* Moves the accepted branch to the front of the tree, in place and in one
+ * launch: slot ctx + i gets the row (K, V, scales, position) of slot ctx +
+ * accepted[b][i], i < num_accepted[b]; new_lens[b] = ctx + num_accepted[b].
+ * Slots behind keep what they held.  Pages must not be shared between
+ * sequences.
+ *   params   num_seqs, q_len, h_k, head_dim, page_size, max_blocks, num_pages
+ *            and kv_format are used
+ * Errors: MJ_ERR_INVALID_ARG, MJ_ERR_UNSUPPORTED, MJ_ERR_CUDA. */
+mj_status mj_tree_commit(const mj_decode_params* params, const mj_commit_args* args, mj_stream_t stream);
+
 /* Static text for a status code. */
 const char* mj_status_string(mj_status status);
 

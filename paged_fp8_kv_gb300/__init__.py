@@ -239,6 +239,107 @@ class EvictArgs(ctypes.Structure):
     ]
 
 
+class PageParams(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int32) for name in ("num_seqs", "page_size", "max_blocks", "num_pages")]
+
+
+class ReserveArgs(ctypes.Structure):
+    _fields_ = [
+        ("seq_lens", _vp),
+        ("new_tokens", _vp),
+        ("q_len", ctypes.c_int32),
+        ("free_pages", _vp),
+        ("num_free", _vp),
+        ("num_free_out", _vp),
+        ("block_table", _vp),
+        ("seq_lens_out", _vp),
+        ("cu_tokens", _vp),
+        ("positions", _vp),
+        ("slots", _vp),
+        ("num_tokens", ctypes.c_int32),
+        ("status", _vp),
+    ]
+
+
+class ReleaseArgs(ctypes.Structure):
+    _fields_ = [
+        (name, _vp) for name in ("seq_lens", "keep_lens", "free_pages", "num_free", "num_free_out", "block_table", "status")
+    ]
+
+
+class PromptArgs(ctypes.Structure):
+    _fields_ = [
+        ("q", _vp),
+        ("q_tok", _i64),
+        ("q_head", _i64),
+        ("o", _vp),
+        ("o_tok", _i64),
+        ("lse", _vp),
+        ("num_tokens", ctypes.c_int32),
+        ("k", _vp),
+        ("v", _vp),
+        ("k_page", _i64),
+        ("k_row", _i64),
+        ("k_head", _i64),
+        ("v_page", _i64),
+        ("v_row", _i64),
+        ("v_head", _i64),
+        ("block_table", _vp),
+        ("plan", _vp),
+        ("plan_bytes", ctypes.c_size_t),
+        ("q_descale", _vp),
+        ("k_descale", _vp),
+        ("v_descale", _vp),
+        ("qd_seq", _i64),
+        ("qd_head", _i64),
+        ("kd_seq", _i64),
+        ("kd_head", _i64),
+        ("vd_seq", _i64),
+        ("vd_head", _i64),
+        ("softmax_scale", ctypes.c_float),
+        ("scale_o", ctypes.c_float),
+        ("softcap", ctypes.c_float),
+        ("window", ctypes.c_int32),
+        ("workspace", _vp),
+        ("workspace_bytes", ctypes.c_size_t),
+        ("status", _vp),
+    ]
+
+
+class TreeArgs(ctypes.Structure):
+    _fields_ = [("mask", _vp), ("mask_words", ctypes.c_int32), ("tree_lens", _vp)]
+
+
+class CommitArgs(ctypes.Structure):
+    _fields_ = [
+        ("k", _vp),
+        ("v", _vp),
+        ("k_page", _i64),
+        ("k_row", _i64),
+        ("k_head", _i64),
+        ("v_page", _i64),
+        ("v_row", _i64),
+        ("v_head", _i64),
+        ("block_table", _vp),
+        ("seq_lens", _vp),
+        ("tree_lens", _vp),
+        ("accepted", _vp),
+        ("max_accept", ctypes.c_int32),
+        ("num_accepted", _vp),
+        ("new_lens", _vp),
+        ("key_pos", _vp),
+        ("kp_seq", _i64),
+        ("kp_head", _i64),
+        ("status", _vp),
+        ("k_scales", _vp),
+        ("v_scales", _vp),
+        ("ks_page", _i64),
+        ("ks_head", _i64),
+        ("vs_page", _i64),
+        ("vs_head", _i64),
+    ]
+
+
 _lib = None
 
 
@@ -294,6 +395,22 @@ def lib() -> ctypes.CDLL:
         L.mj_evict_workspace_bytes.argtypes = [P(DecodeParams), ctypes.c_int32]
         L.mj_evict.restype = ctypes.c_int
         L.mj_evict.argtypes = [P(DecodeParams), P(EvictArgs), _vp]
+        L.mj_pages_reserve.restype = ctypes.c_int
+        L.mj_pages_reserve.argtypes = [P(PageParams), P(ReserveArgs), _vp]
+        L.mj_pages_release.restype = ctypes.c_int
+        L.mj_pages_release.argtypes = [P(PageParams), P(ReleaseArgs), _vp]
+        L.mj_prompt_plan_bytes.restype = ctypes.c_size_t
+        L.mj_prompt_plan_bytes.argtypes = [P(DecodeParams), ctypes.c_int32]
+        L.mj_prompt_plan.restype = ctypes.c_int
+        L.mj_prompt_plan.argtypes = [P(DecodeParams), _vp, _vp, ctypes.c_int32, ctypes.c_int32, _vp, ctypes.c_size_t, _vp, _vp]
+        L.mj_prompt_workspace_bytes.restype = ctypes.c_size_t
+        L.mj_prompt_workspace_bytes.argtypes = [P(DecodeParams)]
+        L.mj_prompt_attn.restype = ctypes.c_int
+        L.mj_prompt_attn.argtypes = [P(DecodeParams), P(PromptArgs), _vp]
+        L.mj_decode_attn_tree.restype = ctypes.c_int
+        L.mj_decode_attn_tree.argtypes = [P(DecodeParams), P(TreeArgs), P(ScoreModArgs), _vp, P(DecodeArgs), _vp]
+        L.mj_tree_commit.restype = ctypes.c_int
+        L.mj_tree_commit.argtypes = [P(DecodeParams), P(CommitArgs), _vp]
         L.mj_kernel_name.restype = ctypes.c_int
         L.mj_kernel_name.argtypes = [P(DecodeParams), ctypes.c_char_p, ctypes.c_int32]
         _lib = L
@@ -989,9 +1106,17 @@ class DecodeAttnMod(_Call):
     def __init__(self, params: DecodeParams, mod: ScoreMod, *, q, k_cache, v_cache, block_table, seq_lens, work, n_splits,
                  q_descale, k_descale, v_descale, o, lse, softmax_scale: float, workspace=None, spans=None,
                  scale_o: float = 1.0, status=None, max_n_splits: int = 0):
+        params = self._own(params)
+        m, a, keep = self._marshal(params, mod, q, k_cache, v_cache, block_table, seq_lens, work, n_splits, q_descale,
+                                   k_descale, v_descale, o, lse, softmax_scale, workspace, spans, scale_o, status, max_n_splits)
+        self._bind(lib().mj_decode_attn_mod, (ctypes.byref(params), ctypes.byref(m), _ptr(spans), ctypes.byref(a)), (params, keep))
+
+    @staticmethod
+    def _marshal(params, mod, q, k_cache, v_cache, block_table, seq_lens, work, n_splits, q_descale, k_descale, v_descale, o,
+                 lse, softmax_scale, workspace, spans, scale_o, status, max_n_splits):
+        """The checked modifiers and arguments, and all that they point to."""
         import torch
 
-        params = self._own(params)
         bf16, f32, i32, _ = _dtypes()
         nb, hk, rows = int(params.num_seqs), int(params.h_k), int(params.q_len) * int(params.h_r)
         _check_queries(params, q)
@@ -1015,14 +1140,43 @@ class DecodeAttnMod(_Call):
             n_splits=n_splits, q_descale=q_descale, k_descale=k_descale, v_descale=v_descale, o=o, lse=lse,
             workspace=workspace, softmax_scale=softmax_scale, scale_o=scale_o, status=status, max_n_splits=max_n_splits,
         )
-        self._bind(lib().mj_decode_attn_mod, (ctypes.byref(params), ctypes.byref(m), _ptr(spans), ctypes.byref(a)),
-                   (params, mod._tensors(), m, a, spans, q, k_cache, v_cache, block_table, seq_lens, work, n_splits, q_descale,
-                    k_descale, v_descale, o, lse, workspace, status))
+        return m, a, (mod._tensors(), m, a, spans, q, k_cache, v_cache, block_table, seq_lens, work, n_splits, q_descale,
+                      k_descale, v_descale, o, lse, workspace, status)
 
 
 def decode_attn_mod(params: DecodeParams, mod: ScoreMod, *, stream=None, **tensors) -> None:
     """One DecodeAttnMod call."""
     DecodeAttnMod(params, mod, **tensors)(stream)
+
+
+class DecodeAttnTree(DecodeAttnMod):
+    """mj_decode_attn_tree on device tensors: DecodeAttnMod's (mod None, or
+    with softcap, key_begin and prefix alone), tree_mask (num_seqs, q_len,
+    words) int32, bit m of a token's words set if it sees node m, and tree_lens
+    (num_seqs,) int32 (None: q_len nodes each)."""
+
+    _name = "mj_decode_attn_tree"
+
+    def __init__(self, params: DecodeParams, mod: Optional[ScoreMod] = None, *, tree_mask, q, k_cache, v_cache, block_table,
+                 seq_lens, work, n_splits, q_descale, k_descale, v_descale, o, lse, softmax_scale: float, tree_lens=None,
+                 workspace=None, spans=None, scale_o: float = 1.0, status=None, max_n_splits: int = 0):
+        params = self._own(params)
+        i32 = _dtypes()[2]
+        m, a, keep = self._marshal(params, ScoreMod() if mod is None else mod, q, k_cache, v_cache, block_table, seq_lens, work,
+                                   n_splits, q_descale, k_descale, v_descale, o, lse, softmax_scale, workspace, spans, scale_o,
+                                   status, max_n_splits)
+        _tensor("tree_mask", tree_mask, (i32,), (int(params.num_seqs), int(params.q_len), None))
+        if tree_lens is not None:
+            _tensor("tree_lens", tree_lens, (i32,), (int(params.num_seqs),))
+        t = TreeArgs(_ptr(tree_mask), int(tree_mask.shape[2]), _ptr(tree_lens))
+        self._bind(lib().mj_decode_attn_tree,
+                   (ctypes.byref(params), ctypes.byref(t), ctypes.byref(m), _ptr(spans), ctypes.byref(a)),
+                   (params, t, tree_mask, tree_lens, keep))
+
+
+def decode_attn_tree(params: DecodeParams, mod: Optional[ScoreMod] = None, *, stream=None, **tensors) -> None:
+    """One DecodeAttnTree call."""
+    DecodeAttnTree(params, mod, **tensors)(stream)
 
 
 class KeyWeights(_Call):
@@ -1135,3 +1289,233 @@ class Evict(_Call):
 def evict(params: DecodeParams, *, stream=None, **tensors) -> None:
     """One Evict call."""
     Evict(params, **tensors)(stream)
+
+
+# ------------------------------------------- a serving step's operators
+
+
+def make_page_params(num_seqs: int, page_size: int, max_blocks: int, num_pages: int) -> PageParams:
+    return PageParams(num_seqs, page_size, max_blocks, num_pages)
+
+
+def _check_page_list(params, seq_lens, free_pages, num_free, num_free_out, block_table, status):
+    i32, nb = _dtypes()[2], int(params.num_seqs)
+    _tensor("seq_lens", seq_lens, (i32,), (nb,))
+    _tensor("free_pages", free_pages, (i32,), (int(params.num_pages),))
+    _tensor("num_free", num_free, (i32,), (1,))
+    _tensor("num_free_out", num_free_out, (i32,), (1,))
+    _tensor("block_table", block_table, (i32,), (nb, int(params.max_blocks)))
+    _check_status(status)
+
+
+class PagesReserve(_Call):
+    """mj_pages_reserve on device tensors: pages from the free list
+    (free_pages (num_pages,) int32, of which the first num_free (1,) int32)
+    for new_tokens (num_seqs,) int32 (None: q_len each) behind seq_lens.
+    seq_lens_out and num_free_out may be (and are, if None) seq_lens and
+    num_free themselves; cu_tokens (num_seqs + 1,) int32, positions (tokens,)
+    int32 and slots (tokens,) int64 are optional outputs."""
+
+    _name = "mj_pages_reserve"
+
+    def __init__(self, params: PageParams, *, seq_lens, free_pages, num_free, block_table, new_tokens=None, q_len: int = 1,
+                 num_free_out=None, seq_lens_out=None, cu_tokens=None, positions=None, slots=None, status=None):
+        import torch
+
+        params = self._own(params)
+        i32, nb = _dtypes()[2], int(params.num_seqs)
+        num_free_out = num_free if num_free_out is None else num_free_out
+        seq_lens_out = seq_lens if seq_lens_out is None else seq_lens_out
+        _check_page_list(params, seq_lens, free_pages, num_free, num_free_out, block_table, status)
+        _tensor("seq_lens_out", seq_lens_out, (i32,), (nb,))
+        if new_tokens is not None:
+            _tensor("new_tokens", new_tokens, (i32,), (nb,))
+        if cu_tokens is not None:
+            _tensor("cu_tokens", cu_tokens, (i32,), (nb + 1,))
+        n = 0
+        for name, t, dtype in (("positions", positions, i32), ("slots", slots, torch.int64)):
+            if t is not None:
+                _tensor(name, t, (dtype,), (None,))
+                n = int(t.shape[0])
+        if positions is not None and slots is not None and positions.shape != slots.shape:
+            raise ValueError(f"slots: {slots.shape[0]} entries, positions has {positions.shape[0]}")
+        a = ReserveArgs(_ptr(seq_lens), _ptr(new_tokens), int(q_len), _ptr(free_pages), _ptr(num_free), _ptr(num_free_out),
+                        _ptr(block_table), _ptr(seq_lens_out), _ptr(cu_tokens), _ptr(positions), _ptr(slots), n, _ptr(status))
+        self._bind(lib().mj_pages_reserve, (ctypes.byref(params), ctypes.byref(a)),
+                   (params, a, seq_lens, new_tokens, free_pages, num_free, num_free_out, block_table, seq_lens_out, cu_tokens,
+                    positions, slots, status))
+
+
+def pages_reserve(params: PageParams, *, stream=None, **tensors) -> None:
+    """One PagesReserve call."""
+    PagesReserve(params, **tensors)(stream)
+
+
+class PagesRelease(_Call):
+    """mj_pages_release on device tensors: the pages behind keep_lens
+    (num_seqs,) int32 of sequences of seq_lens tokens go back to the free
+    list; num_free_out None: num_free itself."""
+
+    _name = "mj_pages_release"
+
+    def __init__(self, params: PageParams, *, seq_lens, keep_lens, free_pages, num_free, block_table, num_free_out=None,
+                 status=None):
+        params = self._own(params)
+        num_free_out = num_free if num_free_out is None else num_free_out
+        _check_page_list(params, seq_lens, free_pages, num_free, num_free_out, block_table, status)
+        _tensor("keep_lens", keep_lens, (_dtypes()[2],), (int(params.num_seqs),))
+        a = ReleaseArgs(_ptr(seq_lens), _ptr(keep_lens), _ptr(free_pages), _ptr(num_free), _ptr(num_free_out),
+                        _ptr(block_table), _ptr(status))
+        self._bind(lib().mj_pages_release, (ctypes.byref(params), ctypes.byref(a)),
+                   (params, a, seq_lens, keep_lens, free_pages, num_free, num_free_out, block_table, status))
+
+
+def pages_release(params: PageParams, *, stream=None, **tensors) -> None:
+    """One PagesRelease call."""
+    PagesRelease(params, **tensors)(stream)
+
+
+def prompt_plan_bytes(params: DecodeParams, num_tokens: int) -> int:
+    """mj_prompt_plan_bytes."""
+    n = int(lib().mj_prompt_plan_bytes(ctypes.byref(params), int(num_tokens)))
+    if n == 0:
+        raise MjError(MJ_ERR_INVALID_ARG, "mj_prompt_plan_bytes")
+    return n
+
+
+def prompt_workspace_bytes(params: DecodeParams) -> int:
+    """mj_prompt_workspace_bytes (0 when max_splits is 1)."""
+    return int(lib().mj_prompt_workspace_bytes(ctypes.byref(params)))
+
+
+class PromptPlan(_Call):
+    """mj_prompt_plan on device tensors: cu_tokens (num_seqs + 1,) and seq_lens
+    (num_seqs,) int32 into plan (prompt_plan_bytes,) uint8."""
+
+    _name = "mj_prompt_plan"
+
+    def __init__(self, params: DecodeParams, *, cu_tokens, seq_lens, num_tokens: int, plan, window: int = 0, status=None):
+        import torch
+
+        params = self._own(params)
+        i32, nb = _dtypes()[2], int(params.num_seqs)
+        _tensor("cu_tokens", cu_tokens, (i32,), (nb + 1,))
+        _tensor("seq_lens", seq_lens, (i32,), (nb,))
+        _tensor("plan", plan, (torch.uint8,))
+        _check_status(status)
+        self._bind(lib().mj_prompt_plan,
+                   (ctypes.byref(params), _ptr(cu_tokens), _ptr(seq_lens), int(num_tokens), int(window), _ptr(plan),
+                    int(plan.numel()), _ptr(status)),
+                   (params, cu_tokens, seq_lens, plan, status))
+
+
+def prompt_plan(params: DecodeParams, *, stream=None, **tensors) -> None:
+    """One PromptPlan call."""
+    PromptPlan(params, **tensors)(stream)
+
+
+class PromptAttn(_Call):
+    """mj_prompt_attn on device tensors: q (tokens, h_k*h_r, 128) bf16, or
+    e4m3 codes for params of that q_dtype (a slice of a projection's output, or
+    rope_append's); o (tokens, h_k*h_r, 128) bf16 with contiguous rows; lse
+    (tokens, h_k*h_r) float32 or None; plan of prompt_plan for the same params,
+    tokens and window."""
+
+    _name = "mj_prompt_attn"
+
+    def __init__(self, params: DecodeParams, *, q, k_cache, v_cache, block_table, plan, q_descale, k_descale, v_descale, o,
+                 softmax_scale: float, lse=None, softcap: float = 0.0, window: int = 0, scale_o: float = 1.0, workspace=None,
+                 status=None):
+        import torch
+
+        params = self._own(params)
+        bf16, f32, i32, codes = _dtypes()
+        nb, hk, hq = int(params.num_seqs), int(params.h_k), int(params.h_k) * int(params.h_r)
+        n = int(q.shape[0])
+        _tensor("q", q, codes if int(params.q_dtype) == MJ_E4M3 else (bf16,), (n, hq, 128), strided=True)
+        if q.stride(2) != 1:
+            raise ValueError("q: the head dimension must be contiguous")
+        _tensor("o", o, (bf16,), (n, hq, 128), strided=True)
+        if n and not o[0].is_contiguous():
+            raise ValueError("o: a token's rows must be contiguous")
+        if lse is not None:
+            _tensor("lse", lse, (f32,), (n, hq))
+        _check_pools(params, k_cache, v_cache)
+        _tensor("block_table", block_table, (i32,), (nb, int(params.max_blocks)))
+        for name, t in (("q_descale", q_descale), ("k_descale", k_descale), ("v_descale", v_descale)):
+            _check_descale(name, t, nb, hk)
+        _tensor("plan", plan, (torch.uint8,))
+        if workspace is not None:
+            _tensor("workspace", workspace, (torch.uint8,))
+        _check_status(status)
+        a = PromptArgs()
+        a.q, a.q_tok, a.q_head = _ptr(q), int(q.stride(0)), int(q.stride(1))
+        a.o, a.o_tok = _ptr(o), int(o.stride(0))
+        a.lse, a.num_tokens = _ptr(lse), n
+        a.k, a.v = _ptr(k_cache), _ptr(v_cache)
+        a.k_page, a.k_row, a.k_head = kv_strides(k_cache)
+        a.v_page, a.v_row, a.v_head = kv_strides(v_cache)
+        a.block_table = _ptr(block_table)
+        a.plan, a.plan_bytes = _ptr(plan), int(plan.numel())
+        a.q_descale, a.k_descale, a.v_descale = _ptr(q_descale), _ptr(k_descale), _ptr(v_descale)
+        a.qd_seq, a.qd_head = descale_strides(q_descale, nb, hk)
+        a.kd_seq, a.kd_head = descale_strides(k_descale, nb, hk)
+        a.vd_seq, a.vd_head = descale_strides(v_descale, nb, hk)
+        a.softmax_scale, a.scale_o, a.softcap, a.window = float(softmax_scale), float(scale_o), float(softcap), int(window)
+        if workspace is not None:
+            a.workspace, a.workspace_bytes = _ptr(workspace), int(workspace.numel())
+        a.status = _ptr(status)
+        self._bind(lib().mj_prompt_attn, (ctypes.byref(params), ctypes.byref(a)),
+                   (params, a, q, k_cache, v_cache, block_table, plan, q_descale, k_descale, v_descale, o, lse, workspace, status))
+
+
+def prompt_attn(params: DecodeParams, *, stream=None, **tensors) -> None:
+    """One PromptAttn call."""
+    PromptAttn(params, **tensors)(stream)
+
+
+class TreeCommit(_Call):
+    """mj_tree_commit on device tensors: the rows of nodes accepted (num_seqs,
+    max_accept) int32, num_accepted (num_seqs,) of each, move to the front of
+    their trees (tree_lens (num_seqs,) int32; None: params.q_len nodes each);
+    new_lens (num_seqs,) int32, None: seq_lens itself.  key_pos (num_seqs, h_k,
+    slots) int32 moves along."""
+
+    _name = "mj_tree_commit"
+
+    def __init__(self, params: DecodeParams, *, k_cache, v_cache, block_table, seq_lens, accepted, num_accepted, tree_lens=None,
+                 new_lens=None, key_pos=None, status=None, k_scales=None, v_scales=None):
+        params = self._own(params)
+        i32, codes = _dtypes()[2:]
+        nb = int(params.num_seqs)
+        new_lens = seq_lens if new_lens is None else new_lens
+        _check_pools(params, k_cache, v_cache, _row_bytes(params))
+        _check_tables(params, block_table, seq_lens)
+        _tensor("accepted", accepted, (i32,), (nb, None))
+        for name, t in (("num_accepted", num_accepted), ("new_lens", new_lens), ("tree_lens", tree_lens)):
+            if t is not None:
+                _tensor(name, t, (i32,), (nb,))
+        for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+            if t is not None:
+                _tensor(name, t, codes, (int(params.num_pages), int(params.h_k), int(params.page_size), 8), strided=True)
+        _check_status(status)
+        a = CommitArgs()
+        a.k, a.v = _ptr(k_cache), _ptr(v_cache)
+        a.k_page, a.k_row, a.k_head = kv_strides(k_cache)
+        a.v_page, a.v_row, a.v_head = kv_strides(v_cache)
+        a.block_table, a.seq_lens, a.tree_lens = _ptr(block_table), _ptr(seq_lens), _ptr(tree_lens)
+        a.accepted, a.max_accept, a.num_accepted = _ptr(accepted), int(accepted.shape[1]), _ptr(num_accepted)
+        a.new_lens = _ptr(new_lens)
+        if key_pos is not None:
+            a.kp_seq, a.kp_head = _per_slot("key_pos", key_pos, i32, params)
+            a.key_pos = _ptr(key_pos)
+        a.status = _ptr(status)
+        _set_scales(a, k_scales, v_scales)
+        self._bind(lib().mj_tree_commit, (ctypes.byref(params), ctypes.byref(a)),
+                   (params, a, k_cache, v_cache, block_table, seq_lens, tree_lens, accepted, num_accepted, new_lens, key_pos,
+                    status, k_scales, v_scales))
+
+
+def tree_commit(params: DecodeParams, *, stream=None, **tensors) -> None:
+    """One TreeCommit call."""
+    TreeCommit(params, **tensors)(stream)

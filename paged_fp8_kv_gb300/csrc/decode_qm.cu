@@ -47,6 +47,11 @@
 // that pass 1 writes them back over S for pass 2.  Tiles outside the
 // sequence's span are not in the plan: the item's tiles count the span's
 // prefix tiles first, then those from its first seen key on.
+//
+// kTree (with kMod): the sequence's last keys are a drafted tree's nodes; a row
+// sees context keys by its range and, in the tiles that reach the tree, nodes by
+// its bits of the mask, two words for 64 keys.  Rows without a node of their
+// own compute like rows past n_q and are written as rows without a key.
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -128,10 +133,14 @@ __device__ __forceinline__ uint8_t* swz(uint8_t* part, int r, int cc) {
 // covers 1 / kDup of the keys.  The copies of a row share its reference
 // maximum, write their key slices into one P row per packed row, and GEMM2
 // runs as O^T = V^T P^T with the kR packed rows on N.
-template <bool kQe4m3, int kDup, bool kPair, bool kMod>
+template <bool kMod, bool kTree>
+using QmArgs = std::conditional_t<kTree, DecodeTreeDev, std::conditional_t<kMod, DecodeModDev, DecodeDev>>;
+
+template <bool kQe4m3, int kDup, bool kPair, bool kMod, bool kTree>
 __global__ void __launch_bounds__(kThreads, 1)
-decode_qm_kernel(const std::conditional_t<kMod, DecodeModDev, DecodeDev> a, const __grid_constant__ CUtensorMap tmap_k,
+decode_qm_kernel(const QmArgs<kMod, kTree> a, const __grid_constant__ CUtensorMap tmap_k,
                  const __grid_constant__ CUtensorMap tmap_v, int n_q_tiles) {
+  static_assert(!kTree || kMod, "a tree is a kind of modified scores");
   static_assert(!kPair || kDup == 1, "paired q tiles: one copy of each row");
   constexpr int kR = kRows / kDup;   // packed rows per q tile; also keys per copy
   constexpr int kCh = kR < 64 ? kR : 64;  // S columns per TMEM round trip
@@ -435,7 +444,8 @@ decode_qm_kernel(const std::conditional_t<kMod, DecodeModDev, DecodeDev> a, cons
     uint8_t* const pbuf = sm + C::kOffP + wg * 2 * kPartBytes;
     const int qrow = n0 + (kPair ? wg * kRows : 0) + r % kR;  // paired: group w owns q tile w
     const int cb = (r / kR) * kR;  // first key of this row's copy (uniform over a warp)
-    const bool live = qrow < a.n_q;
+    const bool in_range = qrow < a.n_q;
+    bool live = in_range;  // kTree: and a node of the sequence's tree
     const float qd = a.qd[b * a.qd_seq + g * a.qd_head];
     const float kd = a.kd[b * a.kd_seq + g * a.kd_head];
     const float vd = a.vd[b * a.vd_seq + g * a.vd_head];
@@ -532,7 +542,22 @@ decode_qm_kernel(const std::conditional_t<kMod, DecodeModDev, DecodeDev> a, cons
     int lo = 0, pfx = 0;  // kMod: keys [lo, lim] and [0, pfx)
     float mod_c1 = 0.f, cap2 = 0.f, slope2 = 0.f;
     int row_pos = 0;  // distances are taken in whole numbers: positions past 2^24 share fp32 values
-    if constexpr (kMod) {
+    const uint32_t* tree_row = nullptr;  // kTree: the node's row of the mask
+    TreeShape tree{0, 0};
+    if constexpr (kTree) {
+      tree = tree_shape(a, b, L);
+      const int qi = qrow / a.h_r;
+      live = in_range && qi < tree.nodes;
+      if (live) {
+        const RowRange rr = tree_range(a, b, qi, tree.ctx);
+        lim = rr.hi < span.z - 1 ? rr.hi : span.z - 1;
+        lo = rr.lo > span.y ? rr.lo : span.y;
+        pfx = rr.pfx < span.x ? rr.pfx : span.x;
+        tree_row = a.mask + (static_cast<int64_t>(b) * a.q_len + qi) * a.mask_words;
+      }
+      cap2 = a.mod.softcap * kLog2e;
+      mod_c1 = a.mod.softcap > 0.f ? raw_l / a.mod.softcap : raw_l * kLog2e;
+    } else if constexpr (kMod) {
       if (live) {
         const RowRange rr = row_range(a.mod, a.causal, a.q_len, b, L, qrow / a.h_r);
         lim = rr.hi < span.z - 1 ? rr.hi : span.z - 1;
@@ -558,6 +583,17 @@ decode_qm_kernel(const std::conditional_t<kMod, DecodeModDev, DecodeDev> a, cons
       else
         return key0 + n - 1 <= lim;
     };
+
+    // kTree: the mask's words of up to 64 keys from k0 on, and whether the node
+    // sees key k0 + e of them (e a constant of the unrolled loops)
+    uint32_t word0 = 0, word1 = 0;
+    auto see_words = [&](int k0) {
+      if (tree_row) {
+        word0 = tree_bits(tree_row, tree.nodes, k0 - tree.ctx);
+        word1 = tree_bits(tree_row, tree.nodes, k0 + 32 - tree.ctx);
+      }
+    };
+    auto node_sees = [&](int k0, int e) { return visible(k0 + e) || (((e < 32 ? word0 : word1) >> (e & 31)) & 1u) != 0; };
 
     float m_run = -INFINITY;  // reference row maximum (raw units)
     float l_run = 0.f;        // running row sum of x = 448 p 2^-kTau
@@ -594,8 +630,14 @@ decode_qm_kernel(const std::conditional_t<kMod, DecodeModDev, DecodeDev> a, cons
               modify_scores<kCh>(rr, mod_c1, cap2, a.mod.slopes != nullptr, slope2,
                                  static_cast<float>(row_pos - key0 - h0));
               if (!unmasked) {
+                if constexpr (kTree) {
+                  see_words(key0 + h0);
 #pragma unroll
-                for (int e = 0; e < kCh; ++e) rr[e] = visible(key0 + h0 + e) ? rr[e] : 0xFF800000u;  // -inf
+                  for (int e = 0; e < kCh; ++e) rr[e] = node_sees(key0 + h0, e) ? rr[e] : 0xFF800000u;
+                } else {
+#pragma unroll
+                  for (int e = 0; e < kCh; ++e) rr[e] = visible(key0 + h0 + e) ? rr[e] : 0xFF800000u;  // -inf
+                }
               }
 #pragma unroll
               for (int c0 = 0; c0 < kCh; c0 += 16) MJ_TMEM_ST16(tmem_s + h0 + c0, (rr + c0));
@@ -725,6 +767,7 @@ decode_qm_kernel(const std::conditional_t<kMod, DecodeModDev, DecodeDev> a, cons
         if (!ok) set_abort(abort_flag, a.status);
       }
 
+      if (kTree && !live) l_run = 0.f;  // a row without a node: what it summed may be anything
       // ---- epilogue: this group's O is final once its last GEMM2 is done;
       // group 0 merges both groups' rows (row r's state of group 1 through
       // shared memory, its O from group 1's TMEM columns, same lanes).  With
@@ -744,13 +787,13 @@ decode_qm_kernel(const std::conditional_t<kMod, DecodeModDev, DecodeDev> a, cons
         const float f1 = (m1 == -INFINITY) ? 0.f : fast_exp2((m1 - mx) * c2);
         const float lraw = l_run * f0 + l1 * f1;  // row sum of x, both groups
         const bool final_out = a.n_splits[b] <= 1;
-        const int64_t orow = final_out ? b * a.o_seq + (static_cast<int64_t>(g) * a.n_q + (live ? qrow : 0)) * kHeadDimDev
-                                       : part_row(a, b, g, slot, live ? qrow : 0) * kHeadDimDev;
+        const int64_t orow = final_out ? b * a.o_seq + (static_cast<int64_t>(g) * a.n_q + (in_range ? qrow : 0)) * kHeadDimDev
+                                       : part_row(a, b, g, slot, in_range ? qrow : 0) * kHeadDimDev;
         const uint32_t o1 = tmem + C::kWgCols + kRows + lane_off;  // group 1's O, same lanes
         const float mrow = mx;
         const float l = lraw * kPScaleInv;
         const float f = vd * kPScaleInv * (final_out ? a.scale_o / (l + 1e-30f) : 1.f);
-        const bool writer = live;
+        const bool writer = in_range;
         // A thread holds a row, and a row's 16-byte pieces stored by 32 lanes
         // 256 or 512 bytes apart are 32 half-used sectors an instruction: the
         // rows go through the warp's part of the group's P buffers (free by
@@ -853,8 +896,14 @@ decode_qm_kernel(const std::conditional_t<kMod, DecodeModDev, DecodeDev> a, cons
             modify_scores<kR>(sv, mod_c1, cap2, a.mod.slopes != nullptr, slope2,
                               static_cast<float>(row_pos - key0 - cb));
             if (!unmasked) {
+              if constexpr (kTree) {
+                see_words(key0 + cb);
 #pragma unroll
-              for (int e = 0; e < kR; ++e) sv[e] = visible(key0 + cb + e) ? sv[e] : 0xFF800000u;  // -inf
+                for (int e = 0; e < kR; ++e) sv[e] = node_sees(key0 + cb, e) ? sv[e] : 0xFF800000u;
+              } else {
+#pragma unroll
+                for (int e = 0; e < kR; ++e) sv[e] = visible(key0 + cb + e) ? sv[e] : 0xFF800000u;  // -inf
+              }
             }
           }
           if (kMod || unmasked) {
@@ -963,6 +1012,7 @@ decode_qm_kernel(const std::conditional_t<kMod, DecodeModDev, DecodeDev> a, cons
         if (!ok) set_abort(abort_flag, a.status);
       }
 
+      if (kTree && !live) l_run = 0.f;
       // ---- epilogue: a row's sum over its copies (one scale), then group 0
       // merges both groups' rows (group 1's state through shared memory, its
       // O^T from its TMEM columns) and lane d writes element d of every row
@@ -992,7 +1042,7 @@ decode_qm_kernel(const std::conditional_t<kMod, DecodeModDev, DecodeDev> a, cons
           // 0 marks a group with no key for the row (its O^T column is stale)
           fx[qr] = f0 > 0.f ? f0 * f : 0.f;
           fx[kR + qr] = f1 > 0.f ? f1 * f : 0.f;
-          if (live) {
+          if (in_range) {
             const float m_logit = mx * scale_l;
             if (final_out) {
               a.lse[(static_cast<int64_t>(b) * a.h_k + g) * a.n_q + qrow] = m_logit + logf(l);
@@ -1037,8 +1087,8 @@ decode_qm_kernel(const std::conditional_t<kMod, DecodeModDev, DecodeDev> a, cons
   if (warp == 1) ptx::tmem_dealloc(tmem, C::kTmemCols);
 }
 
-template <bool kQe4m3, int kDup, bool kPair, bool kMod>
-cudaError_t launch_qm(const std::conditional_t<kMod, DecodeModDev, DecodeDev>& a, int n_q_tiles, cudaStream_t stream) {
+template <bool kQe4m3, int kDup, bool kPair, bool kMod, bool kTree>
+cudaError_t launch_qm(const QmArgs<kMod, kTree>& a, int n_q_tiles, cudaStream_t stream) {
   using C = QmCfg<kQe4m3, kPair, kDup>;
   const int box_rows = a.page_size < kRows ? a.page_size : kRows;
   CUtensorMap mk, mv;
@@ -1047,29 +1097,29 @@ cudaError_t launch_qm(const std::conditional_t<kMod, DecodeModDev, DecodeDev>& a
       !make_kv_map(&mv, a.v, a.page_size, a.h_k, a.num_pages, a.v_row, a.v_head, a.v_page, box_rows, 1,
                    a.kv_format))
     return cudaErrorInvalidValue;
-  auto kern = decode_qm_kernel<kQe4m3, kDup, kPair, kMod>;
+  auto kern = decode_qm_kernel<kQe4m3, kDup, kPair, kMod, kTree>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
   if (e != cudaSuccess) return e;
   dim3 grid(static_cast<unsigned>(a.num_work) * n_q_tiles * a.h_k, 1, 1);
   return launch_pdl(kern, grid, dim3(kThreads, 1, 1), C::kBytes, stream, a, mk, mv, n_q_tiles);
 }
 
-template <bool kMod>
-cudaError_t launch_qm_rows(const std::conditional_t<kMod, DecodeModDev, DecodeDev>& a, int rows_per_cta, int n_q_tiles,
-                           bool q_e4m3, cudaStream_t stream) {
+template <bool kMod, bool kTree>
+cudaError_t launch_qm_rows(const QmArgs<kMod, kTree>& a, int rows_per_cta, int n_q_tiles, bool q_e4m3,
+                           cudaStream_t stream) {
   switch (rows_per_cta) {
     case 256:  // two q tiles of 128 rows per CTA
-      return q_e4m3 ? launch_qm<true, 1, true, kMod>(a, n_q_tiles, stream)
-                    : launch_qm<false, 1, true, kMod>(a, n_q_tiles, stream);
+      return q_e4m3 ? launch_qm<true, 1, true, kMod, kTree>(a, n_q_tiles, stream)
+                    : launch_qm<false, 1, true, kMod, kTree>(a, n_q_tiles, stream);
     case 128:
-      return q_e4m3 ? launch_qm<true, 1, false, kMod>(a, n_q_tiles, stream)
-                    : launch_qm<false, 1, false, kMod>(a, n_q_tiles, stream);
+      return q_e4m3 ? launch_qm<true, 1, false, kMod, kTree>(a, n_q_tiles, stream)
+                    : launch_qm<false, 1, false, kMod, kTree>(a, n_q_tiles, stream);
     case 64:
-      return q_e4m3 ? launch_qm<true, 2, false, kMod>(a, n_q_tiles, stream)
-                    : launch_qm<false, 2, false, kMod>(a, n_q_tiles, stream);
+      return q_e4m3 ? launch_qm<true, 2, false, kMod, kTree>(a, n_q_tiles, stream)
+                    : launch_qm<false, 2, false, kMod, kTree>(a, n_q_tiles, stream);
     case 32:
-      return q_e4m3 ? launch_qm<true, 4, false, kMod>(a, n_q_tiles, stream)
-                    : launch_qm<false, 4, false, kMod>(a, n_q_tiles, stream);
+      return q_e4m3 ? launch_qm<true, 4, false, kMod, kTree>(a, n_q_tiles, stream)
+                    : launch_qm<false, 4, false, kMod, kTree>(a, n_q_tiles, stream);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -1077,12 +1127,17 @@ cudaError_t launch_qm_rows(const std::conditional_t<kMod, DecodeModDev, DecodeDe
 }  // namespace
 
 cudaError_t launch_decode_qm(const DecodeDev& a, int rows_per_cta, int n_q_tiles, bool q_e4m3, cudaStream_t stream) {
-  return launch_qm_rows<false>(a, rows_per_cta, n_q_tiles, q_e4m3, stream);
+  return launch_qm_rows<false, false>(a, rows_per_cta, n_q_tiles, q_e4m3, stream);
 }
 
 cudaError_t launch_decode_qm_mod(const DecodeModDev& a, int rows_per_cta, int n_q_tiles, bool q_e4m3,
                                  cudaStream_t stream) {
-  return launch_qm_rows<true>(a, rows_per_cta, n_q_tiles, q_e4m3, stream);
+  return launch_qm_rows<true, false>(a, rows_per_cta, n_q_tiles, q_e4m3, stream);
+}
+
+cudaError_t launch_decode_qm_tree(const DecodeTreeDev& a, int rows_per_cta, int n_q_tiles, bool q_e4m3,
+                                  cudaStream_t stream) {
+  return launch_qm_rows<true, true>(a, rows_per_cta, n_q_tiles, q_e4m3, stream);
 }
 
 int qm_smem_bytes(bool q_e4m3) { return q_e4m3 ? QmCfg<true>::kBytes : QmCfg<false>::kBytes; }

@@ -46,6 +46,10 @@
 // with a unit scale.  Tiles outside the sequence's span are not in the plan:
 // the item's tiles count the span's prefix tiles first, then those from its
 // first seen key on.
+//
+// kTree (with kMod): the sequence's last keys are a drafted tree's nodes, at
+// most 16 here; a row's bits of the mask are one word in shared memory, looked
+// at by the threads whose key is not in every row's range.
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -129,6 +133,7 @@ constexpr int kTileKV = 128;                 // KV rows per tile (MMA M)
 constexpr int kKVTileBytes = kTileKV * 128;  // one K or V tile: 16 KB
 constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s: far above any legal wait
 constexpr int kStatusTimeout = 5;            // MJ_ERR_TIMEOUT
+constexpr uint32_t kNode = 1u << 31;         // kTree: the row is a node of its sequence's tree
 // P is produced as x = 448 p 2^-kTau: a column's reference maximum m moves
 // only when a score passes m + kTau (log2 units), so x stays within e4m3's
 // range and most tiles need neither the column reduction nor an O
@@ -220,9 +225,12 @@ __device__ __forceinline__ void set_abort(volatile int* abort, int32_t* status) 
   if (status) atomicExch(status, kStatusTimeout);
 }
 
-template <int R, bool kQe4m3, bool kNv, bool kMod>
+template <bool kMod, bool kTree>
+using TcArgs = std::conditional_t<kTree, DecodeTreeDev, std::conditional_t<kMod, DecodeModDev, DecodeDev>>;
+
+template <int R, bool kQe4m3, bool kNv, bool kMod, bool kTree>
 __global__ void __launch_bounds__((TcCfg<R, kQe4m3, kNv, kMod>::kThreads), (TcCfg<R, kQe4m3, kNv, kMod>::kMinBlocks))
-decode_tc_kernel(const std::conditional_t<kMod, DecodeModDev, DecodeDev> a, const __grid_constant__ CUtensorMap tmap_k,
+decode_tc_kernel(const TcArgs<kMod, kTree> a, const __grid_constant__ CUtensorMap tmap_k,
                  const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_ks,
                  const __grid_constant__ CUtensorMap tmap_vs, int n_q_tiles) {
   // Launched as a programmatic dependent: no global load or store before
@@ -241,6 +249,7 @@ decode_tc_kernel(const std::conditional_t<kMod, DecodeModDev, DecodeDev> a, cons
   float* row_pos = row_slope2 + R;
   int* row_lo = reinterpret_cast<int*>(row_pos + R);
   int* row_hi = row_lo + R;
+  uint32_t* row_bits = reinterpret_cast<uint32_t*>(row_pos);  // kTree: the node's bits of the mask
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + C::kOffMisc + 4);
   int* q_shift = reinterpret_cast<int*>(sm + C::kOffMisc + 8);
@@ -666,7 +675,23 @@ decode_tc_kernel(const std::conditional_t<kMod, DecodeModDev, DecodeDev> a, cons
       }
       if (st_tid == 0) *q_shift = shift;
       if (st_tid < R) m_s[st_tid] = -INFINITY;  // running max starts at -inf
-      if constexpr (kMod) {
+      if constexpr (kTree) {
+        if (st_tid < R) {  // a tree of up to 16 nodes: one word; rows without a node see nothing
+          const int n = n0 + st_tid, qi = n / a.h_r;
+          const TreeShape tree = tree_shape(a, b, L);
+          int lo = INT32_MAX, hi = -1;
+          uint32_t bits = 0;
+          if (n < a.n_q && qi < tree.nodes) {
+            const RowRange rr = tree_range(a, b, qi, tree.ctx);
+            hi = rr.hi < span.z - 1 ? rr.hi : span.z - 1;
+            lo = rr.lo > span.y ? rr.lo : span.y;
+            bits = tree_bits(a.mask + (static_cast<int64_t>(b) * a.q_len + qi) * a.mask_words, tree.nodes, 0) | kNode;
+          }
+          row_bits[st_tid] = bits;
+          row_lo[st_tid] = lo;
+          row_hi[st_tid] = hi;
+        }
+      } else if constexpr (kMod) {
         if (st_tid < R) {  // the row's constants (rows past n_q see every key: any value will do)
           const int n = n0 + st_tid, qi = n / a.h_r;
           float slope2 = 0.f;
@@ -703,12 +728,15 @@ decode_tc_kernel(const std::conditional_t<kMod, DecodeModDev, DecodeDev> a, cons
     bool ok = true;
     const int vis_all = a.causal ? L - a.q_len : L - 1;  // keys every row sees
     float cap2 = 0.f, mod_c1 = 0.f;
+    TreeShape tree{0, 0};
+    if constexpr (kTree) tree = tree_shape(a, b, L);
     int pfx = 0, lo_max = 0, hi_min = L - 1;  // kMod: keys [lo_max, hi_min] and [0, pfx) are seen by every row
     if constexpr (kMod) {
       cap2 = a.mod.softcap * kLog2e;
       mod_c1 = a.mod.softcap > 0.f ? raw_l / a.mod.softcap : raw_l * kLog2e;
       if (a.mod.prefix) pfx = a.mod.prefix[b];
       pfx = pfx < span.x ? pfx : span.x;
+      if (kTree && pfx > tree.ctx) pfx = tree.ctx;
 #pragma unroll
       for (int c = 0; c < R; ++c) {
         lo_max = row_lo[c] > lo_max ? row_lo[c] : lo_max;
@@ -756,7 +784,18 @@ decode_tc_kernel(const std::conditional_t<kMod, DecodeModDev, DecodeDev> a, cons
         if constexpr (kMod) {
           modify_columns<kCols>(sc, mod_c1, cap2, a.mod.slopes != nullptr, row_slope2 + col0, row_pos + col0,
                                 static_cast<float>(j - (L - a.q_len)));
-          if (j >= pfx && (j < lo_max || j > hi_min)) {
+          if constexpr (kTree) {
+            if (j < lo_max || j > hi_min) {
+              const int m = j - tree.ctx;  // node; bits past the tree are clear
+#pragma unroll
+              for (int c = 0; c < kCols; ++c) {
+                const uint32_t bits = row_bits[col0 + c];
+                const bool seen = (j >= row_lo[col0 + c] && j <= row_hi[col0 + c]) || (j < pfx && (bits & kNode) != 0) ||
+                                  (m >= 0 && m < 16 && ((bits >> m) & 1u) != 0);
+                if (!seen) sc[c] = -INFINITY;
+              }
+            }
+          } else if (j >= pfx && (j < lo_max || j > hi_min)) {
 #pragma unroll
             for (int c = 0; c < kCols; ++c)
               if (j < row_lo[col0 + c] || j > row_hi[col0 + c]) sc[c] = -INFINITY;
@@ -1056,8 +1095,8 @@ decode_tc_kernel(const std::conditional_t<kMod, DecodeModDev, DecodeDev> a, cons
   if (warp == 1) ptx::tmem_dealloc(tmem, C::kTmemCols);
 }
 
-template <int R, bool kQe4m3, bool kNv, bool kMod>
-cudaError_t launch_tc(const std::conditional_t<kMod, DecodeModDev, DecodeDev>& a, int n_q_tiles, cudaStream_t stream) {
+template <int R, bool kQe4m3, bool kNv, bool kMod, bool kTree = false>
+cudaError_t launch_tc(const TcArgs<kMod, kTree>& a, int n_q_tiles, cudaStream_t stream) {
   CUtensorMap mk, mv, mks, mvs;
   if (kNv) {
     if (!make_nv_map(&mk, a.k, false, a.page_size, a.h_k, a.num_pages, a.k_row, a.k_head, a.k_page) ||
@@ -1075,7 +1114,7 @@ cudaError_t launch_tc(const std::conditional_t<kMod, DecodeModDev, DecodeDev>& a
     mvs = mv;
   }
   using C = TcCfg<R, kQe4m3, kNv, kMod>;
-  auto kern = decode_tc_kernel<R, kQe4m3, kNv, kMod>;
+  auto kern = decode_tc_kernel<R, kQe4m3, kNv, kMod, kTree>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
   if (e != cudaSuccess) return e;
   dim3 grid(static_cast<unsigned>(a.num_work) * n_q_tiles * a.h_k, 1, 1);
@@ -1255,6 +1294,19 @@ cudaError_t launch_decode_tc_mod(const DecodeModDev& a, int rows_per_cta, int n_
     case 16:
       return q_e4m3 ? launch_tc<16, true, false, true>(a, n_q_tiles, stream)
                     : launch_tc<16, false, false, true>(a, n_q_tiles, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+cudaError_t launch_decode_tc_tree(const DecodeTreeDev& a, int rows_per_cta, int n_q_tiles, bool q_e4m3,
+                                  cudaStream_t stream) {
+  switch (rows_per_cta) {
+    case 8:
+      return q_e4m3 ? launch_tc<8, true, false, true, true>(a, n_q_tiles, stream)
+                    : launch_tc<8, false, false, true, true>(a, n_q_tiles, stream);
+    case 16:
+      return q_e4m3 ? launch_tc<16, true, false, true, true>(a, n_q_tiles, stream)
+                    : launch_tc<16, false, false, true, true>(a, n_q_tiles, stream);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -219,7 +219,7 @@ namespace {
 
 // One decode step for checked params; with `mod` non-null on modified scores
 // (the query-rows kernel's instances for them).
-mj_status decode_step(const mj_decode_params& p, const mj_decode_args& a, const ScoreModDev* mod,
+mj_status decode_step(const mj_decode_params& p, const mj_decode_args& a, const ScoreModDev* mod, const mj_tree* tree,
                       mj_stream_t stream_) {
   if (!a.q || !a.k || !a.v || !a.block_table || !a.seq_lens || !a.work || !a.n_splits || !a.q_descale ||
       !a.k_descale || !a.v_descale || !a.o || !a.lse)
@@ -247,8 +247,14 @@ mj_status decode_step(const mj_decode_params& p, const mj_decode_args& a, const 
     if ((reinterpret_cast<uintptr_t>(a.workspace) & (kAlign - 1)) != 0) return MJ_ERR_INVALID_ARG;
   }
 
-  DecodeModDev d{};
+  DecodeTreeDev d{};
   if (mod) d.mod = *mod;
+  if (tree) {
+    d.mask = tree->mask;
+    d.mask_words = tree->mask_words;
+    d.tree_lens = tree->tree_lens;
+  }
+  const char* const name = tree ? "mj_decode_attn_tree" : (mod ? "mj_decode_attn_mod" : "mj_decode_attn");
   d.q = a.q;
   d.q_seq = a.q_seq_stride;
   d.k = a.k;
@@ -317,19 +323,23 @@ mj_status decode_step(const mj_decode_params& p, const mj_decode_args& a, const 
     std::fprintf(stderr,
                  "%s: kernel=%s num_seqs=%d h_k=%d n_q=%d (q_len %d x h_r %d) page_size=%d %s "
                  "q=%s kv=%s work_items=%d merge=%s (max_n_splits %d of max_splits %d) kv_evict_first=%d\n",
-                 mod ? "mj_decode_attn_mod" : "mj_decode_attn", kc.name, p.num_seqs, p.h_k, p.q_len * p.h_r, p.q_len,
+                 name, kc.name, p.num_seqs, p.h_k, p.q_len * p.h_r, p.q_len,
                  p.h_r, p.page_size,
                  p.causal ? "causal" : "non-causal", p.q_dtype == MJ_E4M3 ? "e4m3" : "bf16",
                  kv_format_name(p.kv_format), a.num_work, merge ? "yes" : "no", merge_splits, p.max_splits,
                  d.kv_evict_first);
   // an NVTX range around the launches, so a profiler's timeline names them
-  nvtxRangePushA(mod ? "mj_decode_attn_mod" : "mj_decode_attn");
+  nvtxRangePushA(name);
   struct RangeEnd {
     ~RangeEnd() { nvtxRangePop(); }
   } range_end;
   cudaError_t e = cudaSuccess;
   if (ev[0] && (e = cudaEventRecord(ev[0], stream)) != cudaSuccess) return MJ_ERR_CUDA;
-  if (mod) {
+  if (tree) {
+    e = kc.kind == KernelKind::kTensorCore
+            ? launch_decode_tc_tree(d, kc.rows_per_cta, kc.n_q_tiles, p.q_dtype == MJ_E4M3, stream)
+            : launch_decode_qm_tree(d, kc.rows_per_cta, kc.n_q_tiles, p.q_dtype == MJ_E4M3, stream);
+  } else if (mod) {
     e = kc.kind == KernelKind::kTensorCore
             ? launch_decode_tc_mod(d, kc.rows_per_cta, kc.n_q_tiles, p.q_dtype == MJ_E4M3, stream)
             : launch_decode_qm_mod(d, kc.rows_per_cta, kc.n_q_tiles, p.q_dtype == MJ_E4M3, stream);
@@ -363,7 +373,7 @@ extern "C" mj_status mj_decode_attn(const mj_decode_params* params, const mj_dec
   const mj_status st = check_params(params);
   if (st != MJ_OK) return st;
   if (!args) return MJ_ERR_INVALID_ARG;
-  return decode_step(*params, *args, nullptr, stream);
+  return decode_step(*params, *args, nullptr, nullptr, stream);
 }
 
 extern "C" mj_status mj_decode_attn_mod(const mj_decode_params* params, const mj_score_mod* mod, const int32_t* spans,
@@ -379,7 +389,28 @@ extern "C" mj_status mj_decode_attn_mod(const mj_decode_params* params, const mj
   ScoreModDev m{};
   st = score_mod_dev(*params, *mod, spans, &m);
   if (st != MJ_OK) return st;
-  return decode_step(*params, *args, &m, stream);
+  return decode_step(*params, *args, &m, nullptr, stream);
+}
+
+extern "C" mj_status mj_decode_attn_tree(const mj_decode_params* params, const mj_tree* tree, const mj_score_mod* mod,
+                                         const int32_t* spans, const mj_decode_args* args, mj_stream_t stream) {
+  mj_status st = check_params(params);
+  if (st != MJ_OK) return st;
+  if (!args || !tree || !tree->mask) return MJ_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(tree->mask) & 3) != 0 || (reinterpret_cast<uintptr_t>(tree->tree_lens) & 3) != 0)
+    return MJ_ERR_INVALID_ARG;
+  if (tree->mask_words < (params->q_len + 31) / 32) return MJ_ERR_INVALID_ARG;
+  const KernelChoice kc = choose_kernel(*params);
+  if (params->kv_format == MJ_KV_NVFP4 ||
+      !(kc.kind == KernelKind::kTensorCoreQRows || (kc.kind == KernelKind::kTensorCore && kc.rows_per_cta <= 16)))
+    return MJ_ERR_UNSUPPORTED;
+  // these take positions for slots, which a tree's are not
+  if (mod && (mod->window != 0 || mod->alibi_slopes || mod->key_end)) return MJ_ERR_UNSUPPORTED;
+  ScoreModDev m{};
+  const mj_score_mod none{};
+  st = score_mod_dev(*params, mod ? *mod : none, spans, &m);
+  if (st != MJ_OK) return st;
+  return decode_step(*params, *args, &m, tree, stream);
 }
 
 namespace {

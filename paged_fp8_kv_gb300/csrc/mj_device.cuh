@@ -56,6 +56,13 @@ struct DecodeModDev : DecodeDev {
   ScoreModDev mod;
 };
 
+// mj_decode_attn_tree: which of the last keys, the tree's, each token sees.
+struct DecodeTreeDev : DecodeModDev {
+  const uint32_t* mask;  // [num_seqs * q_len][mask_words]
+  const int32_t* tree_lens;  // or null: q_len each
+  int32_t mask_words;
+};
+
 // mj_rope_append (mj_rope_params, mj_rope_args).
 struct RopeDev {
   const __nv_bfloat16* q;
@@ -110,6 +117,46 @@ struct EvictDev {
   uint8_t* ks;  // nvfp4 scale planes or null
   uint8_t* vs;
   int64_t ks_page, ks_head, vs_page, vs_head;
+};
+
+// mj_pages_reserve and mj_pages_release (whose keep_lens are new_tokens here).
+struct PagesDev {
+  const int32_t* seq_lens;
+  const int32_t* new_tokens;
+  const int32_t* free_pages;
+  int32_t* free_pages_out;
+  const int32_t* num_free;
+  int32_t* num_free_out;
+  const int32_t* block_table;
+  int32_t* block_table_out;
+  int32_t* seq_lens_out;
+  int32_t* cu_tokens;
+  int32_t* positions;
+  int64_t* slots;
+  int32_t* status;
+  int64_t max_len;
+  int32_t num_seqs, q_len, page_shift, max_blocks, num_pages, num_tokens;
+};
+
+// mj_tree_commit.
+struct CommitDev {
+  uint8_t* k;
+  uint8_t* v;
+  int64_t k_page, k_row, k_head, v_page, v_row, v_head;
+  uint8_t* ks;  // nvfp4 scale planes or null
+  uint8_t* vs;
+  int64_t ks_page, ks_head, vs_page, vs_head;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* tree_lens;
+  const int32_t* accepted;
+  const int32_t* num_accepted;
+  int32_t* new_lens;
+  int32_t* key_pos;
+  int64_t kp_seq, kp_head;
+  int32_t* status;
+  int64_t max_len;
+  int32_t num_seqs, q_len, max_accept, h_k, row_bytes, page_shift, max_blocks, num_pages;
 };
 
 // Bits per K/V code of a pool format (mj_kv_format: e4m3, e3m2, e2m3, e2m1,

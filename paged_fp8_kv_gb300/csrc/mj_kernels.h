@@ -70,6 +70,12 @@ cudaError_t launch_decode_tc_mod(const DecodeModDev& a, int rows_per_cta, int n_
 cudaError_t launch_decode_qm_mod(const DecodeModDev& a, int rows_per_cta, int n_q_tiles, bool q_e4m3,
                                  cudaStream_t stream);
 
+// Modified scores and, of the last keys, a drafted tree's.
+cudaError_t launch_decode_tc_tree(const DecodeTreeDev& a, int rows_per_cta, int n_q_tiles, bool q_e4m3,
+                                  cudaStream_t stream);
+cudaError_t launch_decode_qm_tree(const DecodeTreeDev& a, int rows_per_cta, int n_q_tiles, bool q_e4m3,
+                                  cudaStream_t stream);
+
 // Spans of the keys any row sees and the lengths to plan with.
 cudaError_t launch_score_spans(const ScoreModDev& m, const int32_t* seq_lens, int num_seqs, int q_len, int causal,
                                int64_t max_len, int4* spans, int32_t* plan_lens, cudaStream_t stream);
@@ -80,7 +86,17 @@ cudaError_t launch_key_weights(const DecodeModDev& a, bool q_e4m3, bool has_mod,
                                float* acc, int64_t acc_seq, int64_t acc_head, float decay, int fresh, int sm_count,
                                cudaStream_t stream);
 
+// Attention over whole prompts: the work list, then the attention and the
+// merge of the row tiles whose keys were cut.
+struct PromptPlanDev;
+struct PromptDev;
+cudaError_t launch_prompt_plan(const PromptPlanDev& a, cudaStream_t stream);
+cudaError_t launch_prompt_attn(const PromptDev& a, bool q_e4m3, int sm_count, cudaStream_t stream);
+
 cudaError_t launch_rope_append(const RopeDev& a, cudaStream_t stream);
+cudaError_t launch_pages_reserve(const PagesDev& a, cudaStream_t stream);
+cudaError_t launch_pages_release(const PagesDev& a, cudaStream_t stream);
+cudaError_t launch_tree_commit(const CommitDev& a, cudaStream_t stream);
 cudaError_t launch_evict(const EvictDev& a, int sm_count, cudaStream_t stream);
 
 // TMA descriptor of a paged e4m3 pool seen as (d bytes, rows in page, kv

@@ -1,0 +1,279 @@
+// Pages handed out for new tokens and taken back (see mj_pages_reserve,
+// mj_pages_release).
+//
+// What a call reads and writes is a few words a sequence, page and token (under
+// 0.2 us at HBM's rate for 65000 tokens): it is bound by the launch and a chain
+// of cold loads, lengths -> table entry -> store.  One launch therefore does it
+// all: a cluster of CTAs each of which makes the prefix sums over all sequences
+// for itself (a thousand threads, one sequence each in a decode batch) and then
+// takes its share of the tokens and pages, finding each one's sequence by a
+// binary search in shared memory.  The lengths and the list's size may be
+// written where they were read: the cluster's barrier is between.
+
+#include <cuda_runtime.h>
+
+#include "mj_kernels.h"
+#include "sm100_ptx.cuh"
+
+namespace mj {
+namespace {
+
+constexpr int kThreads = 1024;
+constexpr int kWarps = kThreads / 32;
+constexpr int kCluster = 8;  // CTAs of a call with many tokens or pages
+constexpr int kStatusInvalid = 1;   // MJ_ERR_INVALID_ARG
+constexpr int kStatusCapacity = 3;  // MJ_ERR_CAPACITY
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += x;
+  }
+  return v;
+}
+
+struct Pair {
+  int64_t a, b;
+};
+
+// Inclusive prefix sums of two values over the block, and the block's totals.
+__device__ __forceinline__ Pair block_scan(Pair v, Pair* red, Pair* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  Pair inc{warp_scan(v.a, lane), warp_scan(v.b, lane)};
+  __syncthreads();  // red is free
+  if (lane == 31) red[warp] = inc;
+  __syncthreads();
+  if (warp == 0) {
+    const Pair x = red[lane];
+    red[lane] = Pair{warp_scan(x.a, lane), warp_scan(x.b, lane)};
+  }
+  __syncthreads();
+  *total = red[kWarps - 1];
+  if (warp > 0) {
+    inc.a += red[warp - 1].a;
+    inc.b += red[warp - 1].b;
+  }
+  return inc;
+}
+
+// The last b with off[b] <= x (off[0] = 0; sequences without an element share
+// the offset of the one behind them).
+__device__ __forceinline__ int find(const int32_t* off, int n, int x) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (off[mid] <= x)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ int32_t clamp32(int64_t x) {
+  return x > INT32_MAX ? INT32_MAX : static_cast<int32_t>(x);
+}
+
+__device__ __forceinline__ void report(int32_t* status, int what) {
+  if (status) atomicExch(status, what);
+}
+
+__global__ void __launch_bounds__(kThreads, 1) reserve_kernel(const PagesDev a) {
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  extern __shared__ int32_t smem[];
+  int32_t* const tok = smem;                       // [num_seqs + 1] tokens before b
+  int32_t* const need = tok + a.num_seqs + 1;      // [num_seqs + 1] pages before b
+  int32_t* const held = need + a.num_seqs + 1;     // [num_seqs] tokens held; -1: gets no slots
+  __shared__ Pair red[kWarps];
+  __shared__ int wrong, taken;  // bit 0: an invalid length, bit 1: too few pages
+  const int tid = threadIdx.x, rank = blockIdx.x, ctas = gridDim.x;
+  const int shift = a.page_shift, row_mask = (1 << shift) - 1;
+  if (tid == 0) {
+    wrong = taken = 0;
+    tok[0] = need[0] = 0;
+  }
+  int n_free = a.num_free[0];
+  if (n_free < 0 || n_free > a.num_pages) {
+    n_free = 0;
+    if (tid == 0) wrong = 1;
+  }
+  __syncthreads();
+  Pair base{0, 0};
+  for (int b0 = 0; b0 < a.num_seqs; b0 += kThreads) {
+    const int b = b0 + tid;
+    Pair v{0, 0};
+    int old = -1;
+    if (b < a.num_seqs) {
+      const int L = a.seq_lens[b], n = a.new_tokens ? a.new_tokens[b] : a.q_len;
+      if (L < 0 || n < 0) {
+        atomicOr(&wrong, 1);
+      } else {
+        v.a = n;
+        if (static_cast<int64_t>(L) + n > a.max_len) {
+          atomicOr(&wrong, 1);
+        } else {
+          old = L;
+          v.b = ((static_cast<int64_t>(L) + n + row_mask) >> shift) - ((static_cast<int64_t>(L) + row_mask) >> shift);
+        }
+      }
+    }
+    Pair total;
+    const Pair inc = block_scan(v, red, &total);
+    if (b < a.num_seqs) {
+      const int64_t end = base.b + inc.b;
+      if (v.b > 0 && end > n_free) {  // its pages are no longer in the list
+        old = -1;
+        atomicOr(&wrong, 2);
+      } else if (v.b > 0) {
+        atomicMax(&taken, static_cast<int>(end));
+      }
+      tok[b + 1] = clamp32(base.a + inc.a);
+      need[b + 1] = clamp32(end);
+      held[b] = old;
+    }
+    base.a += total.a;
+    base.b += total.b;
+  }
+  __syncthreads();
+  const int tokens = tok[a.num_seqs];
+  if (tid == 0 && rank == 0) {
+    if ((wrong & 1) || ((a.positions || a.slots) && tokens > a.num_tokens))
+      report(a.status, kStatusInvalid);
+    else if (wrong)
+      report(a.status, kStatusCapacity);
+  }
+  auto free_page = [&](int x) { return a.free_pages[n_free - 1 - x]; };
+  // the new tokens' positions and slots
+  if (a.positions || a.slots) {
+    for (int t = rank * kThreads + tid; t < a.num_tokens; t += ctas * kThreads) {
+      int pos = 0;
+      int64_t slot = -1;
+      if (t < tokens) {
+        const int b = find(tok, a.num_seqs, t);
+        const int old = held[b];
+        if (old >= 0) {
+          pos = old + t - tok[b];
+          const int blk = pos >> shift, have = (old + row_mask) >> shift;
+          if (a.slots) {
+            const int page = blk < have ? a.block_table[static_cast<int64_t>(b) * a.max_blocks + blk]
+                                        : free_page(need[b] + blk - have);
+            slot = (static_cast<int64_t>(page) << shift) + (pos & row_mask);
+          }
+        }
+      }
+      if (a.positions) a.positions[t] = pos;
+      if (a.slots) a.slots[t] = slot;
+    }
+  }
+  // the new pages' entries
+  for (int x = rank * kThreads + tid; x < taken; x += ctas * kThreads) {
+    const int b = find(need, a.num_seqs, x);
+    const int blk = ((held[b] + row_mask) >> shift) + x - need[b];
+    a.block_table_out[static_cast<int64_t>(b) * a.max_blocks + blk] = free_page(x);
+  }
+  // every CTA of the cluster has read the lengths and the list's size
+  if (ctas > 1) cluster_sync();
+  for (int b = rank * kThreads + tid; b < a.num_seqs; b += ctas * kThreads) {
+    const int old = held[b];
+    a.seq_lens_out[b] = old >= 0 ? old + tok[b + 1] - tok[b] : a.seq_lens[b];
+  }
+  if (a.cu_tokens)
+    for (int b = rank * kThreads + tid; b <= a.num_seqs; b += ctas * kThreads) a.cu_tokens[b] = tok[b];
+  if (rank == 0 && tid == 0) a.num_free_out[0] = n_free - taken;
+}
+
+__global__ void __launch_bounds__(kThreads, 1) release_kernel(const PagesDev a) {
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  extern __shared__ int32_t smem[];
+  int32_t* const gone = smem;                   // [num_seqs + 1] pages before b
+  int32_t* const kept = gone + a.num_seqs + 1;  // [num_seqs] pages that stay
+  __shared__ Pair red[kWarps];
+  __shared__ int wrong;
+  const int tid = threadIdx.x, rank = blockIdx.x, ctas = gridDim.x;
+  const int shift = a.page_shift, row_mask = (1 << shift) - 1;
+  if (tid == 0) {
+    wrong = 0;
+    gone[0] = 0;
+  }
+  int n_free = a.num_free[0];
+  if (n_free < 0 || n_free > a.num_pages) {
+    n_free = 0;
+    if (tid == 0) wrong = kStatusInvalid;
+  }
+  __syncthreads();
+  int64_t base = 0;
+  for (int b0 = 0; b0 < a.num_seqs; b0 += kThreads) {
+    const int b = b0 + tid;
+    Pair v{0, 0};
+    if (b < a.num_seqs) {
+      const int L = a.seq_lens[b], keep = a.new_tokens[b];
+      if (keep < 0 || keep > L || L > a.max_len) {
+        wrong = kStatusInvalid;
+      } else {
+        kept[b] = (keep + row_mask) >> shift;
+        v.a = ((L + row_mask) >> shift) - kept[b];
+      }
+    }
+    Pair total;
+    const Pair inc = block_scan(v, red, &total);
+    if (b < a.num_seqs) gone[b + 1] = clamp32(base + inc.a);
+    base += total.a;
+  }
+  __syncthreads();
+  int pages = gone[a.num_seqs];
+  if (pages > a.num_pages - n_free) {  // more than the pool has: some were given back before
+    pages = a.num_pages - n_free;
+    if (tid == 0 && rank == 0) report(a.status, kStatusCapacity);
+  } else if (wrong && tid == 0 && rank == 0) {
+    report(a.status, wrong);
+  }
+  for (int x = rank * kThreads + tid; x < pages; x += ctas * kThreads) {
+    const int b = find(gone, a.num_seqs, x);
+    a.free_pages_out[n_free + x] = a.block_table[static_cast<int64_t>(b) * a.max_blocks + kept[b] + x - gone[b]];
+  }
+  if (ctas > 1) cluster_sync();  // every CTA has read the list's size
+  if (rank == 0 && tid == 0) a.num_free_out[0] = n_free + pages;
+}
+
+cudaError_t launch(void (*kern)(PagesDev), const PagesDev& a, size_t smem, int64_t elements, cudaStream_t stream) {
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  const unsigned ctas = elements > 4 * kThreads ? kCluster : 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+}  // namespace
+
+cudaError_t launch_pages_reserve(const PagesDev& a, cudaStream_t stream) {
+  const int64_t tokens = a.positions || a.slots ? a.num_tokens : 0;
+  return launch(reserve_kernel, a, (3 * static_cast<size_t>(a.num_seqs) + 2) * 4, tokens, stream);
+}
+
+cudaError_t launch_pages_release(const PagesDev& a, cudaStream_t stream) {
+  const int64_t most = static_cast<int64_t>(a.num_seqs) * a.max_blocks;  // pages, at most
+  return launch(release_kernel, a, (2 * static_cast<size_t>(a.num_seqs) + 1) * 4, most < a.num_pages ? most : a.num_pages,
+                stream);
+}
+
+}  // namespace mj

@@ -1,0 +1,748 @@
+// Attention of whole prompts over the paged e4m3 cache (see mj_prompt_attn):
+// many query rows a sequence, sequences of different lengths packed one behind
+// the other, each against its own pages.
+//
+//   S[row, key] = Q[row] . K[key]         O[row, d] += P[row, key] V[key, d]
+//
+// A work item is 256 packed rows (token, head of the group) of one sequence
+// and one kv head against its keys, 128 at a time: one read of a K and V tile
+// serves both groups of 128 rows, one MMA warp and one softmax warpgroup each,
+// which go through their tiles half a period apart.  Operands:
+//   S   Q as hi + lo e4m3 parts (q 2^s = hi + lo, s by row) against the K codes
+//       as they lie in the cache, kind::f8f6f4: K is never converted, and the
+//       two parts cost what one bf16 product would
+//   O   P in half precision from TMEM, where it overwrites its scores, against
+//       V in half precision (every e4m3 value is one), kind::f16.  A converter
+//       warpgroup turns each V tile once for both groups.  Splitting P into
+//       e4m3 parts instead would cost the softmax threads four conversions a
+//       pair of scores for one, and keeps 8 bits of P for 11.
+//
+// Bound: per pair of row groups and key tile the tensor core runs 4 x 512
+// cycles; the softmax threads 2 x (128 exponentials, a maximum, a fused
+// multiply-add, a sum and half a conversion each) on the other pipes.
+//
+// Roles (512 threads, one CTA an SM): warps 0-3 and 4-7 softmax of the two row
+// groups (thread = row = TMEM lane; S and O 128 columns each, a group's S, P
+// and next S in the same columns); 8-11 Q and V conversion; 12 and 13 issue a
+// group's MMAs (one warp alone issues an MMA every 70 to 100 cycles); 14 and
+// 15 load K and V tiles by TMA, one box a page.  The CTA takes items in turns,
+// forth and back through a list ordered by length; the loads, conversions and
+// first products of an item run under the end of the one before it.
+//
+// Every wait is bounded: a role that gives up sets the abort flag and the
+// status word, the others stop at their next wait, copies and MMAs in flight
+// are drained and TMEM is freed.
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "mj_kernels.h"
+#include "prompt.cuh"
+#include "score_mod.cuh"
+#include "sm100_ptx.cuh"
+
+namespace mj {
+namespace {
+
+constexpr int kRows = 128;               // rows of a group = MMA M; keys of a tile = MMA N
+constexpr int kTile = 128 * 128;         // bytes of a K tile, a raw V tile, an e4m3 part of a group's Q
+constexpr int kVfTile = 2 * kTile;       // a V tile in half precision
+constexpr int kThreads = 512;
+constexpr int kConvWarp = 8, kMmaWarp = 12, kKWarp = 14;
+constexpr int kVf = 2;                   // converted V tiles held
+constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s: far above any legal wait
+constexpr int kStatusTimeout = 5;        // MJ_ERR_TIMEOUT
+constexpr int kStatusInvalid = 1;        // MJ_ERR_INVALID_ARG
+// P is 2^kPBias 2^(s - m): the reference m of a row moves only when a score
+// passes it by kTau (log2 units), so P stays below 2^15, and an entry keeps
+// half precision's 11 bits down to 2^-21 of the reference.
+constexpr float kPBias = 7.f;
+constexpr float kTau = 8.f;
+
+template <bool kQe4m3>
+struct Cfg {
+  static constexpr int kParts = kQe4m3 ? 1 : 2;
+  static constexpr int kSK = kQe4m3 ? 4 : 3, kSV = kQe4m3 ? 4 : 3;  // K and raw V rings
+  static constexpr int kOffK = 0;
+  static constexpr int kOffV = kOffK + kSK * kTile;
+  static constexpr int kOffVf = kOffV + kSV * kTile;
+  static constexpr int kOffQ = kOffVf + kVf * kVfTile;           // [group][part]
+  static constexpr int kOffShift = kOffQ + 2 * kParts * kTile;   // [2][256] s of each row
+  static constexpr int kOffBar = kOffShift + 2 * 256;
+  static constexpr int kBars = 2 * (kSK + kSV + kVf) + 2 + 4 * 2 + 2;
+  static constexpr int kOffMisc = kOffBar + kBars * 8;
+  static constexpr int kBytes = kOffMisc + 16 + 1024;
+  static_assert(kBytes <= 232448, "shared memory");
+};
+
+__device__ __forceinline__ void give_up(volatile int* abort, int32_t* status) {
+  *abort = 1;
+  if (status) atomicExch(status, kStatusTimeout);
+}
+
+// chunk cc (16 bytes) of row r in a 128-byte-swizzled tile
+__device__ __forceinline__ uint32_t swz(int r, int cc) { return r * 128 + ((cc ^ (r & 7)) << 4); }
+
+// D (fp32, TMEM) += A (half precision, TMEM) B (half precision, shared memory)
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+template <bool kQe4m3, bool kCap>
+__global__ void __launch_bounds__(kThreads, 1)
+prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k,
+                   const __grid_constant__ CUtensorMap tmap_v) {
+  using C = Cfg<kQe4m3>;
+  constexpr int SK = C::kSK, SV = C::kSV;
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  if (!prompt_plan_fits(a)) {
+    if (threadIdx.x == 0 && blockIdx.x == 0 && a.status) atomicExch(a.status, kStatusInvalid);
+    return;
+  }
+  const int units = a.head->n_items * a.h_k;
+  if (static_cast<int>(blockIdx.x) >= units) return;
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = ptx::smem_u32(sm);
+  int8_t* const q_shift = reinterpret_cast<int8_t*>(sm + C::kOffShift);
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(sm + C::kOffMisc);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(sm + C::kOffMisc + 4);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  const uint32_t bar0 = sbase + C::kOffBar;
+  auto kfull = [&](int s) { return bar0 + 8u * s; };
+  auto kempty = [&](int s) { return bar0 + 8u * (SK + s); };
+  auto vfull = [&](int s) { return bar0 + 8u * (2 * SK + s); };
+  auto vempty = [&](int s) { return bar0 + 8u * (2 * SK + SV + s); };
+  auto ffull = [&](int s) { return bar0 + 8u * (2 * SK + 2 * SV + s); };   // converted V
+  auto fempty = [&](int s) { return bar0 + 8u * (2 * SK + 2 * SV + kVf + s); };
+  constexpr int kB = 2 * (SK + SV + kVf);
+  const uint32_t qfull = bar0 + 8u * kB, qempty = qfull + 8u;
+  auto gbar = [&](int w, int k) { return bar0 + 8u * (kB + 2 + 4 * w + k); };
+  // of each group: 0 scores written, 1 P written, 2 O final, 3 O read out
+  const uint32_t drain = bar0 + 8u * (kB + 10);  // [group]
+
+  if (tid == 0) {
+    for (int s = 0; s < SK; ++s) {
+      ptx::mbar_init(kfull(s), 1);
+      ptx::mbar_init(kempty(s), 2);
+    }
+    for (int s = 0; s < SV; ++s) {
+      ptx::mbar_init(vfull(s), 1);
+      ptx::mbar_init(vempty(s), 4);
+    }
+    for (int s = 0; s < kVf; ++s) {
+      ptx::mbar_init(ffull(s), 4);
+      ptx::mbar_init(fempty(s), 2);
+    }
+    ptx::mbar_init(qfull, 4);
+    ptx::mbar_init(qempty, 2);
+    for (int w = 0; w < 2; ++w) {
+      ptx::mbar_init(gbar(w, 0), 1);
+      ptx::mbar_init(gbar(w, 1), 4);
+      ptx::mbar_init(gbar(w, 2), 1);
+      ptx::mbar_init(gbar(w, 3), 4);
+      ptx::mbar_init(drain + 8u * w, 1);
+    }
+    *abort_flag = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    ptx::tmem_alloc(sbase + C::kOffMisc, 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;  // group w: S at 256 w, O at 256 w + 128
+
+  auto wait = [&](uint32_t bar, uint32_t parity) { return ptx::mbar_wait_bounded(bar, parity, abort_flag, kWaitNs); };
+  // the CTA's k-th unit: forth and back through the list (longest first)
+  const int G = gridDim.x, me = blockIdx.x;
+  auto unit_at = [&](int k) { return k * G + ((k & 1) ? G - 1 - me : me); };
+  auto load_item = [&](int u) {
+    PromptItem it;
+    const int4* src = reinterpret_cast<const int4*>(a.items + u / a.h_k);
+    reinterpret_cast<int4*>(&it)[0] = src[0];
+    reinterpret_cast<int4*>(&it)[1] = src[1];
+    return it;
+  };
+  // the tiles of the item that group w's rows see any key of
+  auto group_tiles = [&](const PromptItem& it, int w, int* g0, int* g1) {
+    prompt_tiles(it.len, it.n_tok, a.h_r, it.row0 + w * kRows, kRows, a.causal, a.window, g0, g1);
+    *g0 = *g0 > it.t0 ? *g0 : it.t0;
+    *g1 = *g1 < it.t1 ? *g1 : it.t1;
+    if (*g1 < *g0) *g1 = *g0;
+  };
+
+  // a warpgroup's share of the launch's 512 x 128 registers: 2 x 176 + 104 + 56
+  // = 4 x 128 (the softmax threads hold 64 scores and their 32 pairs of P)
+  if (warp >= kMmaWarp)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+  else if (warp >= kConvWarp)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+  else
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+
+  if (warp >= kKWarp) {
+    // ------------------------------------------------------------- TMA loads
+    const bool is_k = warp == kKWarp;
+    const int NS = is_k ? SK : SV;
+    const uint32_t ring = sbase + (is_k ? C::kOffK : C::kOffV);
+    const CUtensorMap* const tmap = is_k ? &tmap_k : &tmap_v;
+    auto full = [&](int s) { return is_k ? kfull(s) : vfull(s); };
+    auto empty = [&](int s) { return is_k ? kempty(s) : vempty(s); };
+    const int PS = a.page_size;
+    const int nbox = kRows / PS;  // pages of a tile
+    if (lane == 0) ptx::prefetch_tmap(tmap);
+    const bool evict_first = a.kv_evict_first != 0;
+    const uint64_t policy = ptx::policy_evict_first();
+    int n = 0;  // tiles issued
+    bool ok = true;
+    for (int k = 0; ok && unit_at(k) < units; ++k) {
+      const int u = unit_at(k), g = u % a.h_k;
+      const PromptItem it = load_item(u);
+      const int64_t table = static_cast<int64_t>(it.b) * a.max_blocks;
+      // lane l loads the tile's l-th page; its table entry comes a tile ahead
+      auto page_of = [&](int t) {
+        const int key = t * kRows + lane * PS;
+        return t < it.t1 && lane < nbox && key < it.len ? a.block_table[table + key / PS] : a.num_pages;
+      };
+      int page = page_of(it.t0);
+      for (int t = it.t0; t < it.t1; ++t, ++n) {
+        const int st = n % NS;
+        const int next = page_of(t + 1);
+        if (n >= NS && !wait(empty(st), ((n / NS) - 1) & 1)) ok = false;
+        if (__any_sync(0xffffffffu, !ok)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) ptx::mbar_arrive_expect_tx(full(st), kTile);
+        __syncwarp();
+        if (lane < nbox)
+          ptx::tma_load_kv(ring + st * kTile + lane * PS * 128, tmap, full(st), 0, 0, g, page, evict_first, policy);
+        page = next;
+      }
+    }
+    if (!ok) {
+      if (lane == 0) {
+        give_up(abort_flag, a.status);
+        volatile int never = 0;
+        for (int i = n > NS ? n - NS : 0; i < n; ++i)
+          ptx::mbar_wait_bounded(full(i % NS), (i / NS) & 1, &never, kWaitNs / 4);
+      }
+    } else if (*abort_flag && lane == 0) {
+      volatile int never = 0;
+      for (int i = n > NS ? n - NS : 0; i < n; ++i)
+        ptx::mbar_wait_bounded(full(i % NS), (i / NS) & 1, &never, kWaitNs / 4);
+    }
+  } else if (warp >= kMmaWarp) {
+    // ------------------------------------------------------------------- MMA
+    // A group's S, its P and its next S share their columns: the products run
+    // in the order of issue, S of tile t + 1 after O of tile t.
+    const int w = warp - kMmaWarp;
+    if (lane == 0) {
+      const uint32_t idesc_s = ptx::idesc_e4m3(kRows, kRows, false, false);
+      const uint32_t idesc_o = ptx::idesc_e4m3(kRows, kRows, false, true);  // formats 0: half precision in kind::f16
+      const uint64_t qdesc = ptx::smem_desc(sbase + C::kOffQ + w * C::kParts * kTile, 16, 1024, ptx::kSwizzle128B);
+      const uint64_t kdesc0 = ptx::smem_desc(sbase + C::kOffK, 16, 1024, ptx::kSwizzle128B);
+      // V, d-major: 64 elements of d a 128-byte row, the other 64 a tile half further
+      const uint64_t vdesc0 = ptx::smem_desc(sbase + C::kOffVf, kTile, 1024, ptx::kSwizzle128B);
+      const uint32_t ts = tmem + w * 256, to = ts + 128;
+      int n = 0, live_tiles = 0, live_items = 0, items = 0;
+      bool ok = true;
+      for (int k = 0; ok && unit_at(k) < units; ++k) {
+        const PromptItem it = load_item(unit_at(k));
+        if (it.t1 <= it.t0) continue;
+        int g0, g1;
+        group_tiles(it, w, &g0, &g1);
+        ok = wait(qfull, items & 1);
+        ++items;
+        for (int t = it.t0; ok && t < it.t1; ++t, ++n) {
+          const int st = n % SK, vf = n % kVf;
+          const bool on = t >= g0 && t < g1;
+          if (!wait(kfull(st), (n / SK) & 1)) {
+            ok = false;
+            break;
+          }
+          if (on) {
+            ptx::tc_fence_after();
+            const uint64_t kd = kdesc0 + static_cast<uint64_t>((st * kTile) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+              for (int part = 0; part < C::kParts; ++part)
+                ptx::mma_e4m3(ts, qdesc + part * (kTile >> 4) + 2 * kk, kd + 2 * kk, idesc_s, kk > 0 || part > 0);
+            ptx::mma_commit(gbar(w, 0));
+            ptx::mma_commit(kempty(st));
+          } else {
+            ptx::mbar_arrive(kempty(st));
+          }
+          if (t + 1 == it.t1) {  // the item's Q is read
+            if (g1 > g0)
+              ptx::mma_commit(qempty);
+            else
+              ptx::mbar_arrive(qempty);
+          }
+          if (!wait(ffull(vf), (n / kVf) & 1) || (on && !wait(gbar(w, 1), live_tiles & 1)) ||
+              (on && t == g0 && live_items > 0 && !wait(gbar(w, 3), (live_items - 1) & 1))) {
+            ok = false;
+            break;
+          }
+          if (on) {
+            ptx::tc_fence_after();
+            const uint64_t vd = vdesc0 + static_cast<uint64_t>((vf * kVfTile) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)  // 16 keys: 8 columns of P, 16 rows of V
+              mma_f16_ts(to, ts + 8 * kk, vd + 128 * kk, idesc_o, t > g0 || kk > 0);
+            ptx::mma_commit(fempty(vf));
+            if (t + 1 == g1) ptx::mma_commit(gbar(w, 2));
+            ++live_tiles;
+          } else {
+            ptx::mbar_arrive(fempty(vf));
+          }
+        }
+        if (g1 > g0) ++live_items;
+      }
+      if (!ok) give_up(abort_flag, a.status);
+      ptx::mma_commit(drain + 8u * w);
+      volatile int never = 0;
+      ptx::mbar_wait_bounded(drain + 8u * w, 0, &never, kWaitNs);
+    }
+  } else if (warp >= kConvWarp) {
+    // ------------------------------------------------ Q and V conversion
+    const int cw = warp - kConvWarp;
+    int n = 0, items = 0;
+    bool ok = true;
+    for (int k = 0; ok && unit_at(k) < units; ++k) {
+      const int u = unit_at(k), g = u % a.h_k;
+      const PromptItem it = load_item(u);
+      if (it.t1 <= it.t0) continue;
+      // ---- Q: this warp lays out 64 of the 256 rows, the lanes of a load
+      // side by side in a row (16, or 8 of e4m3)
+      {
+        constexpr int kLanes = kQe4m3 ? 8 : 16;
+        constexpr int kPer = 32 / kLanes;       // rows a load
+        constexpr int kLoads = 64 / kPer;
+        constexpr int kBatch = 8;               // loads in flight
+        const int piece = lane % kLanes;
+        const int rows = it.n_tok * a.h_r;
+        uint4 raw[kBatch];
+        auto load = [&](int l0) {
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const int row = it.row0 + cw * 64 + (l0 + i) * kPer + lane / kLanes;
+            raw[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (row < rows) {
+              const int tok = row / a.h_r;
+              const int64_t at = prompt_at(a.q_rows, it.b, it.tok0 + tok, g, row - tok * a.h_r);
+              raw[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.q) + at * (kQe4m3 ? 1 : 2)) + piece);
+            }
+          }
+        };
+        load(0);
+        if (items > 0 && !wait(qempty, (items - 1) & 1)) ok = false;
+        if (__any_sync(0xffffffffu, !ok)) {
+          ok = false;
+          break;
+        }
+        int8_t* const shifts = q_shift + (items & 1) * 256;
+#pragma unroll 1
+        for (int l0 = 0; l0 < kLoads; l0 += kBatch) {
+          if (l0 > 0) load(l0);
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const int r256 = cw * 64 + (l0 + i) * kPer + lane / kLanes;
+            uint8_t* const part = sm + C::kOffQ + (r256 >> 7) * C::kParts * kTile;
+            const int r = r256 & 127;
+            if constexpr (kQe4m3) {
+              *reinterpret_cast<uint4*>(part + swz(r, piece)) = raw[i];
+            } else {
+              // the row's largest |q| goes to [128, 256): hi + lo then hold
+              // every bit of an element down to 2^-9 of it, and 2^-18 of it below
+              const uint32_t v4[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+              uint32_t top = 0;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) top = max(top, max(v4[e] & 0x7FFFu, (v4[e] >> 16) & 0x7FFFu));
+#pragma unroll
+              for (int o = 8; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+              int shift = 134 - static_cast<int>(top >> 7);  // 7 - exponent
+              shift = top == 0 ? 0 : (shift > 126 ? 126 : (shift < -126 ? -126 : shift));
+              const float qs = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
+              uint32_t hw[2], lw[2];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                float x[4], f[4];
+                x[0] = __uint_as_float(v4[2 * h] << 16) * qs;
+                x[1] = __uint_as_float(v4[2 * h] & 0xFFFF0000u) * qs;
+                x[2] = __uint_as_float(v4[2 * h + 1] << 16) * qs;
+                x[3] = __uint_as_float(v4[2 * h + 1] & 0xFFFF0000u) * qs;
+                hw[h] = static_cast<uint32_t>(ptx::f32x2_to_e4m3x2(x[0], x[1])) |
+                        (static_cast<uint32_t>(ptx::f32x2_to_e4m3x2(x[2], x[3])) << 16);
+                e4m3x4_to_f32(hw[h], f);
+                lw[h] = static_cast<uint32_t>(ptx::f32x2_to_e4m3x2(x[0] - f[0], x[1] - f[1])) |
+                        (static_cast<uint32_t>(ptx::f32x2_to_e4m3x2(x[2] - f[2], x[3] - f[3])) << 16);
+              }
+              const uint32_t at = swz(r, piece >> 1) + (piece & 1) * 8;
+              *reinterpret_cast<uint2*>(part + at) = make_uint2(hw[0], hw[1]);
+              *reinterpret_cast<uint2*>(part + kTile + at) = make_uint2(lw[0], lw[1]);
+              if (piece == 0) shifts[r256] = static_cast<int8_t>(shift);
+            }
+          }
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(qfull);
+        ++items;
+      }
+      // ---- V tiles: this warp turns 32 keys, four rows a load, 16 codes a lane
+      for (int t = it.t0; t < it.t1; ++t, ++n) {
+        const int st = n % SV, vf = n % kVf;
+        if (!wait(vfull(st), (n / SV) & 1) || (n >= kVf && !wait(fempty(vf), ((n / kVf) - 1) & 1))) ok = false;
+        if (__any_sync(0xffffffffu, !ok)) {
+          ok = false;
+          break;
+        }
+        const uint8_t* const src = sm + C::kOffV + st * kTile;
+        uint8_t* const dst = sm + C::kOffVf + vf * kVfTile;
+        const int cc = lane & 7;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = cw * 32 + i * 4 + (lane >> 3);
+          uint4 x = *reinterpret_cast<const uint4*>(src + swz(r, cc));
+          if (t * kRows + r >= it.len) x = make_uint4(0u, 0u, 0u, 0u);  // 0 x what lies there must not reach O
+          const uint32_t v4[4] = {x.x, x.y, x.z, x.w};
+          uint32_t h[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            h[2 * e] = e4m3x2_to_f16x2(static_cast<uint16_t>(v4[e] & 0xFFFFu));
+            h[2 * e + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(v4[e] >> 16));
+          }
+          // codes 16 cc ..: chunks 2 (cc % 4) and the next of half cc / 4; the
+          // halves' lanes take theirs in opposite order (they share banks)
+          uint8_t* const half = dst + (cc >> 2) * kTile;
+          const int c0 = 2 * (cc & 3), flip = cc >> 2;
+          *reinterpret_cast<uint4*>(half + swz(r, c0 + flip)) =
+              flip ? make_uint4(h[4], h[5], h[6], h[7]) : make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(half + swz(r, c0 + 1 - flip)) =
+              flip ? make_uint4(h[0], h[1], h[2], h[3]) : make_uint4(h[4], h[5], h[6], h[7]);
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          ptx::mbar_arrive(ffull(vf));
+          ptx::mbar_arrive(vempty(st));
+        }
+      }
+    }
+    if (!ok && lane == 0) give_up(abort_flag, a.status);
+  } else {
+    // --------------------------------------------------------------- softmax
+    const int w = warp >> 2;
+    const int quarter = warp & 3;
+    const int r = quarter * 32 + lane;  // row of the group = TMEM lane
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t ts = tmem + w * 256 + lane_off, to = ts + 128;
+    int live_tiles = 0, live_items = 0, items = 0;
+    bool ok = true;
+    for (int k = 0; ok && unit_at(k) < units; ++k) {
+      const int u = unit_at(k), g = u % a.h_k;
+      const PromptItem it = load_item(u);
+      const int row = it.row0 + w * kRows + r;
+      const int rows = it.n_tok * a.h_r;
+      const bool live = row < rows;
+      const int tok = live ? row / a.h_r : 0;
+      const int hr = live ? row - tok * a.h_r : 0;
+      int g0 = 0, g1 = 0;
+      group_tiles(it, w, &g0, &g1);
+      int lo = 0, lim = -1;  // the row sees keys lo .. lim
+      if (live) prompt_range(it.len, it.n_tok, tok, tok, a.causal, a.window, &lo, &lim);
+      const float raw_l0 = a.softmax_scale * a.qd[it.b * a.qd_seq + g * a.qd_head] * a.kd[it.b * a.kd_seq + g * a.kd_head];
+      const float vd = a.vd[it.b * a.vd_seq + g * a.vd_head];
+      float m_run = -INFINITY, l_run = 0.f;  // reference (units of the scores as read), sum of 2^kPBias p
+      float scale_l = 1.f, c2 = 1.f, head_c = kTau, cap_c1 = 0.f;
+      for (int t = g0; t < g1; ++t) {
+        const int key0 = t * kRows;
+        if (!wait(gbar(w, 0), live_tiles & 1)) ok = false;
+        if (__any_sync(0xffffffffu, !ok)) {
+          ok = false;
+          break;
+        }
+        ptx::tc_fence_after();
+        if (t == g0) {  // the row's scale is there since its Q was laid out
+          float raw_l = raw_l0;
+          if constexpr (!kQe4m3) raw_l *= __uint_as_float(static_cast<uint32_t>(127 - q_shift[(items & 1) * 256 + w * kRows + r]) << 23);
+          if constexpr (kCap) {  // scores become logits in log2 units as they are read
+            cap_c1 = raw_l / a.softcap;
+            scale_l = 1.f / kLog2e;
+          } else {
+            scale_l = raw_l;
+            c2 = raw_l * kLog2e;
+            head_c = fminf(kTau / c2, 0x1p126f);  // finite: -inf + head_c stays -inf
+          }
+        }
+        const bool unmasked = __all_sync(0xffffffffu, !live || (key0 >= lo && key0 + kRows - 1 <= lim));
+        auto visible = [&](int key) { return key >= lo && key <= lim; };
+        float mt = -INFINITY;
+#pragma unroll(kCap ? 1 : 2)
+        for (int h0 = 0; h0 < kRows; h0 += 64) {
+          uint32_t s[64];
+#pragma unroll
+          for (int c = 0; c < 64; c += 16) MJ_TMEM_LD16(ts + h0 + c, (s + c));
+          ptx::tmem_ld_wait();
+          if constexpr (kCap) {
+            modify_scores<64>(s, cap_c1, a.softcap * kLog2e, false, 0.f, 0.f);
+#pragma unroll
+            for (int c = 0; c < 64; c += 16) MJ_TMEM_ST16(ts + h0 + c, (s + c));
+          }
+          if (unmasked) {
+#pragma unroll
+            for (int e = 0; e < 64; e += 2) mt = fmax3(mt, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 64; e += 2)
+              mt = fmax3(mt, visible(key0 + h0 + e) ? __uint_as_float(s[e]) : -INFINITY,
+                         visible(key0 + h0 + e + 1) ? __uint_as_float(s[e + 1]) : -INFINITY);
+          }
+        }
+        if constexpr (kCap) ptx::tmem_st_wait();
+        if (!live) mt = -INFINITY;
+        const bool moved = mt > m_run + head_c;
+        const float m_new = moved ? mt : m_run;
+        const float mu = m_new == -INFINITY ? 0.f : m_new;
+        const float corr = moved ? fast_exp2((m_run - mu) * c2) : 1.f;  // 0 for a row that had seen no key
+        l_run *= corr;
+        m_run = m_new;
+        // O of the tiles before is complete (its products were issued ahead
+        // of this tile's scores); a warp corrects it when any row moved
+        if (t > g0 && __any_sync(0xffffffffu, moved)) {
+#pragma unroll 1
+          for (int h0 = 0; h0 < kRows; h0 += 32) {
+            uint32_t o[32];
+            MJ_TMEM_LD16(to + h0, o);
+            MJ_TMEM_LD16(to + h0 + 16, (o + 16));
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+            MJ_TMEM_ST16(to + h0, o);
+            MJ_TMEM_ST16(to + h0 + 16, (o + 16));
+          }
+        }
+        // P over the scores it was made of: columns h0 / 2 .. from columns h0 ..
+        const float bias = fmaf(-mu, c2, kPBias);
+        const float2 c22 = make_float2(c2, c2), bias2 = make_float2(bias, bias);
+        float2 sum2 = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int h0 = 0; h0 < kRows; h0 += 64) {
+          uint32_t s[64];
+#pragma unroll
+          for (int c = 0; c < 64; c += 16) MJ_TMEM_LD16(ts + h0 + c, (s + c));
+          ptx::tmem_ld_wait();
+          uint32_t p[32];
+#pragma unroll
+          for (int e = 0; e < 64; e += 2) {
+            float s0 = __uint_as_float(s[e]), s1 = __uint_as_float(s[e + 1]);
+            if (!unmasked) {
+              s0 = visible(key0 + h0 + e) ? s0 : -INFINITY;
+              s1 = visible(key0 + h0 + e + 1) ? s1 : -INFINITY;
+            }
+            const float2 y = fma2(make_float2(s0, s1), c22, bias2);
+            const float2 x = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+            sum2 = add2(sum2, x);
+            p[e / 2] = f32x2_to_f16x2(x.x, x.y);
+          }
+          MJ_TMEM_ST16(ts + h0 / 2, p);
+          MJ_TMEM_ST16(ts + h0 / 2 + 16, (p + 16));
+        }
+        l_run += sum2.x + sum2.y;
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(gbar(w, 1));
+        ++live_tiles;
+      }
+      if (it.t1 > it.t0) ++items;
+      if (!ok) break;
+      // ---- epilogue: O, or its part, of this group's rows
+      const bool any = g1 > g0;
+      if (any && !wait(gbar(w, 2), live_items & 1)) ok = false;
+      if (__any_sync(0xffffffffu, !ok)) {
+        ok = false;
+        break;
+      }
+      ptx::tc_fence_after();
+      const bool final_out = it.part < 0;
+      const float l = l_run * (1.f / 128.f);  // 2^-kPBias
+      const bool seen = m_run > -INFINITY;
+      const float f = vd * (1.f / 128.f) * (final_out ? a.scale_o / (seen ? l : 1.f) : 1.f);
+      const int64_t part_row = (static_cast<int64_t>(it.part) * a.h_k + g) * kPromptRows + w * kRows + r;
+      const int64_t orow = final_out ? prompt_at(a.o_rows, it.b, it.tok0 + tok, g, hr) : part_row * kHeadDimDev;
+#pragma unroll 1
+      for (int h0 = 0; h0 < kRows; h0 += 32) {
+        uint32_t o[32];
+        if (any) {
+          MJ_TMEM_LD16(to + h0, o);
+          MJ_TMEM_LD16(to + h0 + 16, (o + 16));
+          ptx::tmem_ld_wait();
+        }
+        if (!live) continue;
+        float x[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) x[e] = any && seen ? __uint_as_float(o[e]) * f : 0.f;
+        if (final_out) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint32_t b4[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const __nv_bfloat162 v = __floats2bfloat162_rn(x[e + 2 * i], x[e + 2 * i + 1]);
+              b4[i] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+            *reinterpret_cast<uint4*>(a.o + orow + h0 + e) = make_uint4(b4[0], b4[1], b4[2], b4[3]);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4*>(a.o_part + orow + h0 + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+        }
+      }
+      if (any) {
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(gbar(w, 3));
+        ++live_items;
+      }
+      if (live) {
+        const float top = m_run * scale_l;
+        if (!final_out) {
+          a.m_part[part_row] = top;
+          a.l_part[part_row] = l;
+        } else if (a.lse) {
+          a.lse[prompt_at(a.lse_rows, it.b, it.tok0 + tok, g, hr)] = seen ? top + logf(l) : -INFINITY;
+        }
+      }
+    }
+    if (!ok && lane == 0) give_up(abort_flag, a.status);
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, 512);
+}
+
+// Row tiles whose keys were cut: parts rescaled to their common maximum and
+// added in order, O and LSE of every row.  Eight warps take eight rows of few
+// parts, or one row's parts in turn; each lane holds 4 of the 128 elements.
+constexpr int kMergeWarps = 8;
+
+__global__ void __launch_bounds__(kMergeWarps * 32) prompt_merge_kernel(const PromptDev a) {
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  __shared__ float s_m[kMergeWarps], s_l[kMergeWarps];
+  __shared__ float4 s_o[kMergeWarps][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (!prompt_plan_fits(a)) return;
+  const int groups = a.head->n_merges * a.h_k * (kPromptRows / kMergeWarps);  // of eight rows
+  for (int x = blockIdx.x; x < groups; x += gridDim.x) {
+    const int r0 = x % (kPromptRows / kMergeWarps) * kMergeWarps;
+    const int g = x / (kPromptRows / kMergeWarps) % a.h_k;
+    const PromptMerge m = a.merges[x / (kPromptRows / kMergeWarps) / a.h_k];
+    const int rows = m.n_tok * a.h_r - m.row0;
+    const bool together = m.n_parts > 8;  // the warps share a row
+    const int64_t stride = static_cast<int64_t>(a.h_k) * kPromptRows;  // rows between a row's parts
+    const int64_t base = static_cast<int64_t>(m.part0) * stride + g * kPromptRows;
+    for (int i = 0; i < (together ? kMergeWarps : 1); ++i) {
+      const int r = r0 + (together ? i : warp);
+      if (r >= rows) break;  // uniform over the CTA (together) or the warp
+      const int p0 = together ? warp : 0, step = together ? kMergeWarps : 1;
+      float mx = -INFINITY, l = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int p = p0 + lane * step; p < m.n_parts; p += 32 * step) mx = fmaxf(mx, a.m_part[base + r + p * stride]);
+#pragma unroll
+      for (int off = 16; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+#pragma unroll 4
+      for (int p = p0; p < m.n_parts; p += step) {
+        const int64_t at = base + r + p * stride;
+        const float mp = a.m_part[at];
+        const float wt = mp == -INFINITY ? 0.f : __expf(mp - mx);
+        const float4 v = *reinterpret_cast<const float4*>(a.o_part + at * kHeadDimDev + lane * 4);
+        l = fmaf(wt, a.l_part[at], l);
+        o.x = fmaf(wt, v.x, o.x);
+        o.y = fmaf(wt, v.y, o.y);
+        o.z = fmaf(wt, v.z, o.z);
+        o.w = fmaf(wt, v.w, o.w);
+      }
+      if (together) {
+        if (lane == 0) {
+          s_m[warp] = mx;
+          s_l[warp] = l;
+        }
+        s_o[warp][lane] = o;
+        __syncthreads();
+        if (warp == 0) {
+          mx = -INFINITY;
+          for (int v = 0; v < kMergeWarps; ++v) mx = fmaxf(mx, s_m[v]);
+          l = 0.f;
+          o = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int v = 0; v < kMergeWarps; ++v) {
+            const float f = s_m[v] == -INFINITY ? 0.f : __expf(s_m[v] - mx);
+            const float4 ov = s_o[v][lane];
+            l = fmaf(f, s_l[v], l);
+            o.x = fmaf(f, ov.x, o.x);
+            o.y = fmaf(f, ov.y, o.y);
+            o.z = fmaf(f, ov.z, o.z);
+            o.w = fmaf(f, ov.w, o.w);
+          }
+        }
+      }
+      if (!together || warp == 0) {
+        const int row = m.row0 + r, tok = row / a.h_r, hr = row - tok * a.h_r;
+        const float inv = l > 0.f ? a.scale_o / l : 0.f;
+        const __nv_bfloat162 lo2 = __floats2bfloat162_rn(o.x * inv, o.y * inv);
+        const __nv_bfloat162 hi2 = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+        *reinterpret_cast<uint2*>(a.o + prompt_at(a.o_rows, m.b, m.tok0 + tok, g, hr) + lane * 4) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&lo2), *reinterpret_cast<const uint32_t*>(&hi2));
+        if (lane == 0 && a.lse)
+          a.lse[prompt_at(a.lse_rows, m.b, m.tok0 + tok, g, hr)] = l > 0.f ? mx + logf(l) : -INFINITY;
+      }
+      if (together) __syncthreads();  // s_o is read
+    }
+  }
+}
+
+template <bool kQe4m3, bool kCap>
+cudaError_t launch(const PromptDev& a, int sm_count, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t stream) {
+  constexpr int smem = Cfg<kQe4m3>::kBytes;
+  auto kern = prompt_attn_kernel<kQe4m3, kCap>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(static_cast<unsigned>(sm_count), 1, 1), dim3(kThreads, 1, 1), smem, stream, a, mk, mv);
+}
+
+}  // namespace
+
+cudaError_t launch_prompt_attn(const PromptDev& a, bool q_e4m3, int sm_count, cudaStream_t stream) {
+  CUtensorMap mk, mv;
+  if (!make_kv_map(&mk, a.k, a.page_size, a.h_k, a.num_pages, a.k_row, a.k_head, a.k_page, a.page_size, 1, 0) ||
+      !make_kv_map(&mv, a.v, a.page_size, a.h_k, a.num_pages, a.v_row, a.v_head, a.v_page, a.page_size, 1, 0))
+    return cudaErrorInvalidValue;
+  const bool cap = a.softcap > 0.f;
+  cudaError_t e;
+  if (q_e4m3)
+    e = cap ? launch<true, true>(a, sm_count, mk, mv, stream) : launch<true, false>(a, sm_count, mk, mv, stream);
+  else
+    e = cap ? launch<false, true>(a, sm_count, mk, mv, stream) : launch<false, false>(a, sm_count, mk, mv, stream);
+  if (e != cudaSuccess || a.max_splits == 1) return e;
+  return launch_pdl(prompt_merge_kernel, dim3(static_cast<unsigned>(4 * sm_count), 1, 1), dim3(kMergeWarps * 32, 1, 1), 0,
+                    stream, a);
+}
+
+}  // namespace mj

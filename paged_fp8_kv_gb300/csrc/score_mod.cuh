@@ -54,6 +54,48 @@ __host__ __device__ __forceinline__ RowRange row_range(const ScoreModDev& m, int
   return r;
 }
 
+// A drafted tree of `nodes` tokens behind ctx context keys.
+struct TreeShape {
+  int nodes, ctx;
+};
+__device__ __forceinline__ TreeShape tree_shape(const DecodeTreeDev& a, int b, int L) {
+  TreeShape t;
+  t.nodes = a.tree_lens ? a.tree_lens[b] : a.q_len;
+  t.nodes = t.nodes > a.q_len ? a.q_len : t.nodes;
+  t.nodes = t.nodes > L ? L : t.nodes;
+  t.nodes = t.nodes < 0 ? 0 : t.nodes;
+  t.ctx = L - t.nodes;
+  return t;
+}
+
+// Nodes m .. m + 31 of a row of the tree's mask (m may be negative), those that
+// exist.
+__device__ __forceinline__ uint32_t tree_bits(const uint32_t* row, int nodes, int m) {
+  if (m <= -32 || m >= nodes) return 0u;
+  const int w = m >> 5, last = (nodes - 1) >> 5;
+  const uint32_t lo = w >= 0 ? row[w] : 0u;
+  const uint32_t hi = w < last ? row[w + 1] : 0u;
+  const uint32_t x = __funnelshift_r(lo, hi, m & 31);
+  return nodes - m >= 32 ? x : x & ((1u << (nodes - m)) - 1u);
+}
+
+// The context keys a node sees: those from its first one on, and the prefix.
+__device__ __forceinline__ RowRange tree_range(const DecodeTreeDev& a, int b, int qi, int ctx) {
+  RowRange r;
+  r.hi = ctx - 1;
+  r.lo = 0;
+  if (a.mod.key_begin) {
+    const int k = a.mod.key_begin[static_cast<int64_t>(b) * a.q_len + qi];
+    r.lo = k > 0 ? k : 0;
+  }
+  r.pfx = 0;
+  if (a.mod.prefix) {
+    const int p = a.mod.prefix[b];
+    r.pfx = p < 0 ? 0 : (p > ctx ? ctx : p);
+  }
+  return r;
+}
+
 // The span of a sequence whose rows see keys [first, last] between them
 // (last < first: none) and [0, pfx), and the length to plan with: its tiles
 // are the prefix's, then those from first / 128 to the end.

@@ -825,8 +825,8 @@ mj_status mj_prompt_plan(const mj_decode_params* params, const int32_t* cu_token
  *                h_k*h_r*128, a multiple of 8); no overlap with q
  *   lse          fp32 (num_tokens, h_k*h_r) contiguous, or NULL.  O and LSE of
  *                padding tokens are left as they were
- *   k, v, strides, block_table, descales   as in mj_decode_args (q_descale per
- *                sequence and kv head).  V must hold finite values below L_b
+ *   k, v, strides, block_table, descales   as in mj_decode_args, q_descale by
+ *                sequence and kv head too; V must hold finite values below L_b
  *   plan         of mj_prompt_plan for this shape (another one's is refused in
  *                the status word and nothing is written)
  *   softcap      0 = off; else 2^-20 to 2^60

@@ -69,7 +69,7 @@ struct Cfg {
   static constexpr int kOffQ = kOffVf + kVf * kVfTile;           // [group][part]
   static constexpr int kOffShift = kOffQ + 2 * kParts * kTile;   // [2][256] s of each row
   static constexpr int kOffBar = kOffShift + 2 * 256;
-  static constexpr int kBars = 2 * (kSK + kSV + kVf) + 2 + 4 * 2 + 2;
+  static constexpr int kBars = 2 * (kSK + kSV + kVf) + 2 + 4 * 2 + 2 + 2;
   static constexpr int kOffMisc = kOffBar + kBars * 8;
   static constexpr int kBytes = kOffMisc + 16 + 1024;
   static_assert(kBytes <= 232448, "shared memory");
@@ -126,8 +126,9 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
   constexpr int kB = 2 * (SK + SV + kVf);
   const uint32_t qfull = bar0 + 8u * kB, qempty = qfull + 8u;
   auto gbar = [&](int w, int k) { return bar0 + 8u * (kB + 2 + 4 * w + k); };
-  // of each group: 0 scores written, 1 P written, 2 O final, 3 O read out
-  const uint32_t drain = bar0 + 8u * (kB + 10);  // [group]
+  // of each group: 0 scores written, 1 P's first half written, 2 O final, 3 O read out
+  auto phalf = [&](int w) { return bar0 + 8u * (kB + 10 + w); };  // P's second half written
+  const uint32_t drain = bar0 + 8u * (kB + 12);  // [group]
 
   if (tid == 0) {
     for (int s = 0; s < SK; ++s) {
@@ -149,6 +150,7 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
       ptx::mbar_init(gbar(w, 1), 4);
       ptx::mbar_init(gbar(w, 2), 1);
       ptx::mbar_init(gbar(w, 3), 4);
+      ptx::mbar_init(phalf(w), 4);
       ptx::mbar_init(drain + 8u * w, 1);
     }
     *abort_flag = 0;
@@ -182,14 +184,14 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
     if (*g1 < *g0) *g1 = *g0;
   };
 
-  // a warpgroup's share of the launch's 512 x 128 registers: 2 x 176 + 104 + 56
-  // = 4 x 128 (the softmax threads hold 64 scores and their 32 pairs of P)
+  // a warpgroup's share of the launch's 512 x 128 registers: 2 x 192 + 80 + 48
+  // = 4 x 128 (the softmax threads hold 128 scores)
   if (warp >= kMmaWarp)
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
   else if (warp >= kConvWarp)
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
   else
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
 
   if (warp >= kKWarp) {
     // ------------------------------------------------------------- TMA loads
@@ -247,34 +249,42 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
     // ------------------------------------------------------------------- MMA
     // A group's S, its P and its next S share their columns: the products run
     // in the order of issue, S of tile t + 1 after O of tile t.
-    const int w = warp - kMmaWarp;
-    if (lane == 0) {
-      const uint32_t idesc_s = ptx::idesc_e4m3(kRows, kRows, false, false);
-      const uint32_t idesc_o = ptx::idesc_e4m3(kRows, kRows, false, true);  // formats 0: half precision in kind::f16
-      const uint64_t qdesc = ptx::smem_desc(sbase + C::kOffQ + w * C::kParts * kTile, 16, 1024, ptx::kSwizzle128B);
-      const uint64_t kdesc0 = ptx::smem_desc(sbase + C::kOffK, 16, 1024, ptx::kSwizzle128B);
-      // V, d-major: 64 elements of d a 128-byte row, the other 64 a tile half further
-      const uint64_t vdesc0 = ptx::smem_desc(sbase + C::kOffVf, kTile, 1024, ptx::kSwizzle128B);
-      const uint32_t ts = tmem + w * 256, to = ts + 128;
-      int n = 0, live_tiles = 0, live_items = 0, items = 0;
-      bool ok = true;
-      for (int k = 0; ok && unit_at(k) < units; ++k) {
-        const PromptItem it = load_item(unit_at(k));
-        if (it.t1 <= it.t0) continue;
-        int g0, g1;
-        group_tiles(it, w, &g0, &g1);
-        ok = wait(qfull, items & 1);
-        ++items;
-        for (int t = it.t0; ok && t < it.t1; ++t, ++n) {
-          const int st = n % SK, vf = n % kVf;
-          const bool on = t >= g0 && t < g1;
-          if (!wait(kfull(st), (n / SK) & 1)) {
-            ok = false;
-            break;
-          }
-          if (on) {
-            ptx::tc_fence_after();
-            const uint64_t kd = kdesc0 + static_cast<uint64_t>((st * kTile) >> 4);
+    // The whole warp goes through the loop and one lane issues, so that
+    // descriptors and addresses stay in uniform registers: inside a branch of
+    // one lane each MMA took 118 cycles to issue.
+    const int w = __shfl_sync(0xffffffffu, warp - kMmaWarp, 0);
+    const bool leader = ptx::elect_one() != 0;
+    const uint32_t idesc_s = ptx::idesc_e4m3(kRows, kRows, false, false);
+    const uint32_t idesc_o = ptx::idesc_e4m3(kRows, kRows, false, true);  // formats 0: half precision in kind::f16
+    const uint64_t qdesc = ptx::smem_desc(sbase + C::kOffQ + w * C::kParts * kTile, 16, 1024, ptx::kSwizzle128B);
+    const uint64_t kdesc0 = ptx::smem_desc(sbase + C::kOffK, 16, 1024, ptx::kSwizzle128B);
+    // V, d-major: 64 elements of d a 128-byte row, the other 64 a tile half further
+    const uint64_t vdesc0 = ptx::smem_desc(sbase + C::kOffVf, kTile, 1024, ptx::kSwizzle128B);
+    const uint32_t ts = __shfl_sync(0xffffffffu, tmem, 0) + w * 256, to = ts + 128;
+    auto wait_all = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+    int n = 0, live_tiles = 0, live_items = 0, items = 0;
+    bool ok = true;
+    for (int k = 0; ok && unit_at(k) < units; ++k) {
+      const PromptItem it = load_item(unit_at(k));
+      const int t0 = __shfl_sync(0xffffffffu, it.t0, 0), t1 = __shfl_sync(0xffffffffu, it.t1, 0);
+      if (t1 <= t0) continue;
+      int g0, g1;
+      group_tiles(it, w, &g0, &g1);
+      g0 = __shfl_sync(0xffffffffu, g0, 0);
+      g1 = __shfl_sync(0xffffffffu, g1, 0);
+      ok = wait_all(qfull, items & 1);
+      ++items;
+      for (int t = t0; ok && t < t1; ++t, ++n) {
+        const int st = n % SK, vf = n % kVf;
+        const bool on = t >= g0 && t < g1;
+        if (!wait_all(kfull(st), (n / SK) & 1)) {
+          ok = false;
+          break;
+        }
+        if (on) {
+          ptx::tc_fence_after();
+          const uint64_t kd = kdesc0 + static_cast<uint64_t>((st * kTile) >> 4);
+          if (leader) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
@@ -282,40 +292,57 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
                 ptx::mma_e4m3(ts, qdesc + part * (kTile >> 4) + 2 * kk, kd + 2 * kk, idesc_s, kk > 0 || part > 0);
             ptx::mma_commit(gbar(w, 0));
             ptx::mma_commit(kempty(st));
-          } else {
-            ptx::mbar_arrive(kempty(st));
           }
-          if (t + 1 == it.t1) {  // the item's Q is read
-            if (g1 > g0)
-              ptx::mma_commit(qempty);
-            else
-              ptx::mbar_arrive(qempty);
+        } else if (leader) {
+          ptx::mbar_arrive(kempty(st));
+        }
+        if (t + 1 == t1 && leader) {  // the item's Q is read
+          if (g1 > g0)
+            ptx::mma_commit(qempty);
+          else
+            ptx::mbar_arrive(qempty);
+        }
+        if (!wait_all(ffull(vf), (n / kVf) & 1) || (on && !wait_all(gbar(w, 1), live_tiles & 1)) ||
+            (on && t == g0 && live_items > 0 && !wait_all(gbar(w, 3), (live_items - 1) & 1))) {
+          ok = false;
+          break;
+        }
+        if (on) {
+          ptx::tc_fence_after();
+          const uint64_t vd = vdesc0 + static_cast<uint64_t>((vf * kVfTile) >> 4);
+          const uint32_t more = t > g0;
+          if (leader) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)  // 16 keys: 8 columns of P, 16 rows of V
+              mma_f16_ts(to, ts + 8 * kk, vd + 128 * kk, idesc_o, kk > 0 ? 1u : more);
           }
-          if (!wait(ffull(vf), (n / kVf) & 1) || (on && !wait(gbar(w, 1), live_tiles & 1)) ||
-              (on && t == g0 && live_items > 0 && !wait(gbar(w, 3), (live_items - 1) & 1))) {
+          __syncwarp();
+          if (!wait_all(phalf(w), live_tiles & 1)) {
             ok = false;
             break;
           }
-          if (on) {
-            ptx::tc_fence_after();
-            const uint64_t vd = vdesc0 + static_cast<uint64_t>((vf * kVfTile) >> 4);
+          ptx::tc_fence_after();
+          if (leader) {
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)  // 16 keys: 8 columns of P, 16 rows of V
-              mma_f16_ts(to, ts + 8 * kk, vd + 128 * kk, idesc_o, t > g0 || kk > 0);
+            for (int kk = 4; kk < 8; ++kk) mma_f16_ts(to, ts + 8 * kk, vd + 128 * kk, idesc_o, 1u);
             ptx::mma_commit(fempty(vf));
             if (t + 1 == g1) ptx::mma_commit(gbar(w, 2));
-            ++live_tiles;
-          } else {
-            ptx::mbar_arrive(fempty(vf));
           }
+          __syncwarp();
+          ++live_tiles;
+        } else if (leader) {
+          ptx::mbar_arrive(fempty(vf));
         }
-        if (g1 > g0) ++live_items;
       }
+      if (g1 > g0) ++live_items;
+    }
+    if (leader) {
       if (!ok) give_up(abort_flag, a.status);
       ptx::mma_commit(drain + 8u * w);
       volatile int never = 0;
       ptx::mbar_wait_bounded(drain + 8u * w, 0, &never, kWaitNs);
     }
+    __syncwarp();
   } else if (warp >= kConvWarp) {
     // ------------------------------------------------ Q and V conversion
     const int cw = warp - kConvWarp;
@@ -453,21 +480,28 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
     int live_tiles = 0, live_items = 0, items = 0;
     bool ok = true;
     for (int k = 0; ok && unit_at(k) < units; ++k) {
-      const int u = unit_at(k), g = u % a.h_k;
-      const PromptItem it = load_item(u);
-      const int row = it.row0 + w * kRows + r;
-      const int rows = it.n_tok * a.h_r;
-      const bool live = row < rows;
-      const int tok = live ? row / a.h_r : 0;
-      const int hr = live ? row - tok * a.h_r : 0;
-      int g0 = 0, g1 = 0;
-      group_tiles(it, w, &g0, &g1);
-      int lo = 0, lim = -1;  // the row sees keys lo .. lim
-      if (live) prompt_range(it.len, it.n_tok, tok, tok, a.causal, a.window, &lo, &lim);
-      const float raw_l0 = a.softmax_scale * a.qd[it.b * a.qd_seq + g * a.qd_head] * a.kd[it.b * a.kd_seq + g * a.kd_head];
-      const float vd = a.vd[it.b * a.vd_seq + g * a.vd_head];
-      float m_run = -INFINITY, l_run = 0.f;  // reference (units of the scores as read), sum of 2^kPBias p
-      float scale_l = 1.f, c2 = 1.f, head_c = kTau, cap_c1 = 0.f;
+      // the threads hold 128 scores: what only an item's ends need is looked up
+      // again there, so that it takes no register in between
+      auto unit = [&] {
+        int u = unit_at(k);
+        asm volatile("" : "+r"(u));
+        return u;
+      };
+      int g0 = 0, g1 = 0, lo = 0, lim = INT32_MAX;  // the group's tiles; the row sees keys lo .. lim
+      bool empty;
+      {
+        const PromptItem it = load_item(unit());
+        group_tiles(it, w, &g0, &g1);
+        empty = it.t1 <= it.t0;
+        const int row = it.row0 + w * kRows + r;  // (rows past the last compute what nobody reads)
+        if (row < it.n_tok * a.h_r) {
+          const int tok = row / a.h_r;
+          prompt_range(it.len, it.n_tok, tok, tok, a.causal, a.window, &lo, &lim);
+        }
+      }
+      // reference maximum (in units of the scores as read), sum of 2^kPBias p,
+      // score -> log2 units
+      float m_run = -INFINITY, l_run = 0.f, c2 = 1.f, cap_c1 = 0.f;
       for (int t = g0; t < g1; ++t) {
         const int key0 = t * kRows;
         if (!wait(gbar(w, 0), live_tiles & 1)) ok = false;
@@ -477,44 +511,34 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
         }
         ptx::tc_fence_after();
         if (t == g0) {  // the row's scale is there since its Q was laid out
-          float raw_l = raw_l0;
+          const int u = unit(), g = u % a.h_k, b = a.items[u / a.h_k].b;
+          float raw_l = a.softmax_scale * a.qd[b * a.qd_seq + g * a.qd_head] * a.kd[b * a.kd_seq + g * a.kd_head];
           if constexpr (!kQe4m3) raw_l *= __uint_as_float(static_cast<uint32_t>(127 - q_shift[(items & 1) * 256 + w * kRows + r]) << 23);
-          if constexpr (kCap) {  // scores become logits in log2 units as they are read
+          if constexpr (kCap)  // scores become logits in log2 units as they are read
             cap_c1 = raw_l / a.softcap;
-            scale_l = 1.f / kLog2e;
-          } else {
-            scale_l = raw_l;
+          else
             c2 = raw_l * kLog2e;
-            head_c = fminf(kTau / c2, 0x1p126f);  // finite: -inf + head_c stays -inf
-          }
         }
-        const bool unmasked = __all_sync(0xffffffffu, !live || (key0 >= lo && key0 + kRows - 1 <= lim));
-        auto visible = [&](int key) { return key >= lo && key <= lim; };
-        float mt = -INFINITY;
-#pragma unroll(kCap ? 1 : 2)
-        for (int h0 = 0; h0 < kRows; h0 += 64) {
-          uint32_t s[64];
+        const bool unmasked = __all_sync(0xffffffffu, key0 >= lo && key0 + kRows - 1 <= lim);
+        uint32_t s[kRows];
 #pragma unroll
-          for (int c = 0; c < 64; c += 16) MJ_TMEM_LD16(ts + h0 + c, (s + c));
-          ptx::tmem_ld_wait();
-          if constexpr (kCap) {
-            modify_scores<64>(s, cap_c1, a.softcap * kLog2e, false, 0.f, 0.f);
+        for (int c = 0; c < kRows; c += 16) MJ_TMEM_LD16(ts + c, (s + c));
+        ptx::tmem_ld_wait();
+        if constexpr (kCap) {
 #pragma unroll
-            for (int c = 0; c < 64; c += 16) MJ_TMEM_ST16(ts + h0 + c, (s + c));
-          }
-          if (unmasked) {
-#pragma unroll
-            for (int e = 0; e < 64; e += 2) mt = fmax3(mt, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
-          } else {
-#pragma unroll
-            for (int e = 0; e < 64; e += 2)
-              mt = fmax3(mt, visible(key0 + h0 + e) ? __uint_as_float(s[e]) : -INFINITY,
-                         visible(key0 + h0 + e + 1) ? __uint_as_float(s[e + 1]) : -INFINITY);
-          }
+          for (int h0 = 0; h0 < kRows; h0 += 32) modify_scores<32>(s + h0, cap_c1, a.softcap * kLog2e, false, 0.f, 0.f);
         }
-        if constexpr (kCap) ptx::tmem_st_wait();
-        if (!live) mt = -INFINITY;
-        const bool moved = mt > m_run + head_c;
+        if (!unmasked) {
+          const int e0 = lo - key0, e1 = lim - key0;
+#pragma unroll
+          for (int e = 0; e < kRows; ++e) s[e] = e >= e0 && e <= e1 ? s[e] : 0xFF800000u;  // -inf
+        }
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int e = 0; e < kRows; e += 2)
+          m4[(e >> 1) & 3] = fmax3(m4[(e >> 1) & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+        float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        const bool moved = (mt - m_run) * c2 > kTau;  // from -inf too; -inf after -inf is NaN: no
         const float m_new = moved ? mt : m_run;
         const float mu = m_new == -INFINITY ? 0.f : m_new;
         const float corr = moved ? fast_exp2((m_run - mu) * c2) : 1.f;  // 0 for a row that had seen no key
@@ -524,51 +548,45 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
         // of this tile's scores); a warp corrects it when any row moved
         if (t > g0 && __any_sync(0xffffffffu, moved)) {
 #pragma unroll 1
-          for (int h0 = 0; h0 < kRows; h0 += 32) {
-            uint32_t o[32];
+          for (int h0 = 0; h0 < kRows; h0 += 16) {
+            uint32_t o[16];
             MJ_TMEM_LD16(to + h0, o);
-            MJ_TMEM_LD16(to + h0 + 16, (o + 16));
             ptx::tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
             MJ_TMEM_ST16(to + h0, o);
-            MJ_TMEM_ST16(to + h0 + 16, (o + 16));
           }
         }
-        // P over the scores it was made of: columns h0 / 2 .. from columns h0 ..
+        // P over the scores, two a column, in halves: the first half's product
+        // runs while the second is made
         const float bias = fmaf(-mu, c2, kPBias);
         const float2 c22 = make_float2(c2, c2), bias2 = make_float2(bias, bias);
-        float2 sum2 = make_float2(0.f, 0.f);
+        float2 sum2[4] = {};
 #pragma unroll
-        for (int h0 = 0; h0 < kRows; h0 += 64) {
-          uint32_t s[64];
+        for (int h = 0; h < 2; ++h) {
 #pragma unroll
-          for (int c = 0; c < 64; c += 16) MJ_TMEM_LD16(ts + h0 + c, (s + c));
-          ptx::tmem_ld_wait();
-          uint32_t p[32];
+          for (int q = 0; q < 2; ++q) {
+            uint32_t p[16];
 #pragma unroll
-          for (int e = 0; e < 64; e += 2) {
-            float s0 = __uint_as_float(s[e]), s1 = __uint_as_float(s[e + 1]);
-            if (!unmasked) {
-              s0 = visible(key0 + h0 + e) ? s0 : -INFINITY;
-              s1 = visible(key0 + h0 + e + 1) ? s1 : -INFINITY;
+            for (int i = 0; i < 16; ++i) {
+              const int e = 64 * h + 32 * q + 2 * i;
+              const float2 y = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c22, bias2);
+              const float2 x = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+              sum2[i & 3] = add2(sum2[i & 3], x);
+              p[i] = f32x2_to_f16x2(x.x, x.y);
             }
-            const float2 y = fma2(make_float2(s0, s1), c22, bias2);
-            const float2 x = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-            sum2 = add2(sum2, x);
-            p[e / 2] = f32x2_to_f16x2(x.x, x.y);
+            MJ_TMEM_ST16(ts + 32 * h + 16 * q, p);
           }
-          MJ_TMEM_ST16(ts + h0 / 2, p);
-          MJ_TMEM_ST16(ts + h0 / 2 + 16, (p + 16));
+          ptx::tmem_st_wait();
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(h == 0 ? gbar(w, 1) : phalf(w));
         }
-        l_run += sum2.x + sum2.y;
-        ptx::tmem_st_wait();
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(gbar(w, 1));
+        const float2 all = add2(add2(sum2[0], sum2[1]), add2(sum2[2], sum2[3]));
+        l_run += all.x + all.y;
         ++live_tiles;
       }
-      if (it.t1 > it.t0) ++items;
+      if (!empty) ++items;
       if (!ok) break;
       // ---- epilogue: O, or its part, of this group's rows
       const bool any = g1 > g0;
@@ -578,10 +596,16 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
         break;
       }
       ptx::tc_fence_after();
+      const int u = unit(), g = u % a.h_k;
+      const PromptItem it = load_item(u);
+      const int row = it.row0 + w * kRows + r;
+      const bool live = row < it.n_tok * a.h_r;
+      const int tok = live ? row / a.h_r : 0;
+      const int hr = live ? row - tok * a.h_r : 0;
       const bool final_out = it.part < 0;
       const float l = l_run * (1.f / 128.f);  // 2^-kPBias
       const bool seen = m_run > -INFINITY;
-      const float f = vd * (1.f / 128.f) * (final_out ? a.scale_o / (seen ? l : 1.f) : 1.f);
+      const float f = a.vd[it.b * a.vd_seq + g * a.vd_head] * (1.f / 128.f) * (final_out ? a.scale_o / (seen ? l : 1.f) : 1.f);
       const int64_t part_row = (static_cast<int64_t>(it.part) * a.h_k + g) * kPromptRows + w * kRows + r;
       const int64_t orow = final_out ? prompt_at(a.o_rows, it.b, it.tok0 + tok, g, hr) : part_row * kHeadDimDev;
 #pragma unroll 1
@@ -620,7 +644,7 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
         ++live_items;
       }
       if (live) {
-        const float top = m_run * scale_l;
+        const float top = m_run * c2 * (1.f / kLog2e);
         if (!final_out) {
           a.m_part[part_row] = top;
           a.l_part[part_row] = l;

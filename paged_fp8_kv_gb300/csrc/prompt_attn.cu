@@ -45,6 +45,7 @@ namespace mj {
 namespace {
 
 constexpr int kRows = 128;               // rows of a group = MMA M; keys of a tile = MMA N
+constexpr int kStep = 64;                // keys of a softmax step: half a tile
 constexpr int kTile = 128 * 128;         // bytes of a K tile, a raw V tile, an e4m3 part of a group's Q
 constexpr int kVfTile = 2 * kTile;       // a V tile in half precision
 constexpr int kThreads = 512;
@@ -69,7 +70,7 @@ struct Cfg {
   static constexpr int kOffQ = kOffVf + kVf * kVfTile;           // [group][part]
   static constexpr int kOffShift = kOffQ + 2 * kParts * kTile;   // [2][256] s of each row
   static constexpr int kOffBar = kOffShift + 2 * 256;
-  static constexpr int kBars = 2 * (kSK + kSV + kVf) + 2 + 4 * 2 + 2 + 2;
+  static constexpr int kBars = 2 * (kSK + kSV + kVf) + 2 + 7 * 2 + 2;
   static constexpr int kOffMisc = kOffBar + kBars * 8;
   static constexpr int kBytes = kOffMisc + 16 + 1024;
   static_assert(kBytes <= 232448, "shared memory");
@@ -125,10 +126,11 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
   auto fempty = [&](int s) { return bar0 + 8u * (2 * SK + 2 * SV + kVf + s); };
   constexpr int kB = 2 * (SK + SV + kVf);
   const uint32_t qfull = bar0 + 8u * kB, qempty = qfull + 8u;
-  auto gbar = [&](int w, int k) { return bar0 + 8u * (kB + 2 + 4 * w + k); };
-  // of each group: 0 scores written, 1 P's first half written, 2 O final, 3 O read out
-  auto phalf = [&](int w) { return bar0 + 8u * (kB + 10 + w); };  // P's second half written
-  const uint32_t drain = bar0 + 8u * (kB + 12);  // [group]
+  // of each group: 0, 1 the halves' scores written, 2, 3 their P written, 4 O
+  // complete up to a step, 5 O read out, 6 the item's O final (two steps are in
+  // flight, so the end of the last one cannot be told from 4 by its parity)
+  auto gbar = [&](int w, int k) { return bar0 + 8u * (kB + 2 + 7 * w + k); };
+  const uint32_t drain = bar0 + 8u * (kB + 16);  // [group]
 
   if (tid == 0) {
     for (int s = 0; s < SK; ++s) {
@@ -146,11 +148,7 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
     ptx::mbar_init(qfull, 4);
     ptx::mbar_init(qempty, 2);
     for (int w = 0; w < 2; ++w) {
-      ptx::mbar_init(gbar(w, 0), 1);
-      ptx::mbar_init(gbar(w, 1), 4);
-      ptx::mbar_init(gbar(w, 2), 1);
-      ptx::mbar_init(gbar(w, 3), 4);
-      ptx::mbar_init(phalf(w), 4);
+      for (int k = 0; k < 7; ++k) ptx::mbar_init(gbar(w, k), k == 2 || k == 3 || k == 5 ? 4 : 1);
       ptx::mbar_init(drain + 8u * w, 1);
     }
     *abort_flag = 0;
@@ -176,22 +174,22 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
     reinterpret_cast<int4*>(&it)[1] = src[1];
     return it;
   };
-  // the tiles of the item that group w's rows see any key of
-  auto group_tiles = [&](const PromptItem& it, int w, int* g0, int* g1) {
-    prompt_tiles(it.len, it.n_tok, a.h_r, it.row0 + w * kRows, kRows, a.causal, a.window, g0, g1);
-    *g0 = *g0 > it.t0 ? *g0 : it.t0;
-    *g1 = *g1 < it.t1 ? *g1 : it.t1;
-    if (*g1 < *g0) *g1 = *g0;
+  // the steps (of 64 keys) of the item that group w's rows see any key of
+  auto group_steps = [&](const PromptItem& it, int w, int* s0, int* s1) {
+    prompt_steps(it.len, it.n_tok, a.h_r, it.row0 + w * kRows, kRows, a.causal, a.window, kStep, s0, s1);
+    *s0 = *s0 > 2 * it.t0 ? *s0 : 2 * it.t0;
+    *s1 = *s1 < 2 * it.t1 ? *s1 : 2 * it.t1;
+    if (*s1 < *s0) *s1 = *s0;
   };
 
-  // a warpgroup's share of the launch's 512 x 128 registers: 2 x 192 + 80 + 48
-  // = 4 x 128 (the softmax threads hold 128 scores)
+  // a warpgroup's share of the launch's 512 x 128 registers: 2 x 184 + 80 + 64
+  // = 4 x 128 (the softmax threads hold 64 scores and their P, with a cap its terms)
   if (warp >= kMmaWarp)
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
   else if (warp >= kConvWarp)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
   else
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
 
   if (warp >= kKWarp) {
     // ------------------------------------------------------------- TMA loads
@@ -254,7 +252,7 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
     // one lane each MMA took 118 cycles to issue.
     const int w = __shfl_sync(0xffffffffu, warp - kMmaWarp, 0);
     const bool leader = ptx::elect_one() != 0;
-    const uint32_t idesc_s = ptx::idesc_e4m3(kRows, kRows, false, false);
+    const uint32_t idesc_s = ptx::idesc_e4m3(kRows, kStep, false, false);
     const uint32_t idesc_o = ptx::idesc_e4m3(kRows, kRows, false, true);  // formats 0: half precision in kind::f16
     const uint64_t qdesc = ptx::smem_desc(sbase + C::kOffQ + w * C::kParts * kTile, 16, 1024, ptx::kSwizzle128B);
     const uint64_t kdesc0 = ptx::smem_desc(sbase + C::kOffK, 16, 1024, ptx::kSwizzle128B);
@@ -262,79 +260,77 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
     const uint64_t vdesc0 = ptx::smem_desc(sbase + C::kOffVf, kTile, 1024, ptx::kSwizzle128B);
     const uint32_t ts = __shfl_sync(0xffffffffu, tmem, 0) + w * 256, to = ts + 128;
     auto wait_all = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
-    int n = 0, live_tiles = 0, live_items = 0, items = 0;
+    int n = 0;  // tiles of the items before
+    uint32_t phase = 0;  // bits 0, 1: of the halves' P
+    int items = 0, live_items = 0;
     bool ok = true;
     for (int k = 0; ok && unit_at(k) < units; ++k) {
       const PromptItem it = load_item(unit_at(k));
       const int t0 = __shfl_sync(0xffffffffu, it.t0, 0), t1 = __shfl_sync(0xffffffffu, it.t1, 0);
       if (t1 <= t0) continue;
-      int g0, g1;
-      group_tiles(it, w, &g0, &g1);
-      g0 = __shfl_sync(0xffffffffu, g0, 0);
-      g1 = __shfl_sync(0xffffffffu, g1, 0);
+      int s0, s1;
+      group_steps(it, w, &s0, &s1);
+      s0 = __shfl_sync(0xffffffffu, s0, 0);
+      s1 = __shfl_sync(0xffffffffu, s1, 0);
       ok = wait_all(qfull, items & 1);
       ++items;
-      for (int t = t0; ok && t < t1; ++t, ++n) {
-        const int st = n % SK, vf = n % kVf;
-        const bool on = t >= g0 && t < g1;
-        if (!wait_all(kfull(st), (n / SK) & 1)) {
+      // tiles that only the other group's rows see
+      auto pass = [&](int t) {
+        const int i = n + t - t0;
+        if (!wait_all(kfull(i % SK), (i / SK) & 1) || !wait_all(ffull(i % kVf), (i / kVf) & 1)) return false;
+        if (leader) {
+          ptx::mbar_arrive(kempty(i % SK));
+          ptx::mbar_arrive(fempty(i % kVf));
+        }
+        return true;
+      };
+      auto scores = [&](int s) {  // S of step s
+        const int i = n + (s >> 1) - t0, st = i % SK, h = s & 1;
+        if ((h == 0 || s == s0) && !wait_all(kfull(st), (i / SK) & 1)) return false;
+        ptx::tc_fence_after();
+        const uint64_t kd = kdesc0 + static_cast<uint64_t>((st * kTile + h * (kStep * 128)) >> 4);
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+            for (int part = 0; part < C::kParts; ++part)
+              ptx::mma_e4m3(ts + kStep * h, qdesc + part * (kTile >> 4) + 2 * kk, kd + 2 * kk, idesc_s, kk > 0 || part > 0);
+          ptx::mma_commit(gbar(w, h));
+          if (h == 1 || s + 1 == s1) ptx::mma_commit(kempty(st));
+          if (s + 1 == s1) ptx::mma_commit(qempty);  // the item's Q is read
+        }
+        __syncwarp();
+        return true;
+      };
+      const int first = s1 > s0 ? s0 >> 1 : t1, last = s1 > s0 ? (s1 + 1) >> 1 : t1;  // the group's tiles
+      for (int t = t0; ok && t < first; ++t) ok = pass(t);
+      if (s1 <= s0 && leader) ptx::mbar_arrive(qempty);
+      for (int s = s0; ok && s < s1 && s < s0 + 2; ++s) ok = scores(s);
+      for (int s = s0; ok && s < s1; ++s) {
+        const int i = n + (s >> 1) - t0, vf = i % kVf, h = s & 1;
+        if (((h == 0 || s == s0) && !wait_all(ffull(vf), (i / kVf) & 1)) || !wait_all(gbar(w, 2 + h), (phase >> h) & 1) ||
+            (s == s0 && live_items > 0 && !wait_all(gbar(w, 5), (live_items - 1) & 1))) {
           ok = false;
           break;
         }
-        if (on) {
-          ptx::tc_fence_after();
-          const uint64_t kd = kdesc0 + static_cast<uint64_t>((st * kTile) >> 4);
-          if (leader) {
+        phase ^= 1u << h;
+        ptx::tc_fence_after();
+        const uint64_t vd = vdesc0 + static_cast<uint64_t>((vf * kVfTile + h * (kStep * 128)) >> 4);
+        const uint32_t more = s > s0;
+        if (leader) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-              for (int part = 0; part < C::kParts; ++part)
-                ptx::mma_e4m3(ts, qdesc + part * (kTile >> 4) + 2 * kk, kd + 2 * kk, idesc_s, kk > 0 || part > 0);
-            ptx::mma_commit(gbar(w, 0));
-            ptx::mma_commit(kempty(st));
-          }
-        } else if (leader) {
-          ptx::mbar_arrive(kempty(st));
+          for (int kk = 0; kk < 4; ++kk)  // 16 keys: 8 columns of P, 16 rows of V
+            mma_f16_ts(to, ts + kStep * h + 8 * kk, vd + 128 * kk, idesc_o, kk > 0 ? 1u : more);
+          ptx::mma_commit(gbar(w, 4));
+          if (h == 1 || s + 1 == s1) ptx::mma_commit(fempty(vf));
+          if (s + 1 == s1) ptx::mma_commit(gbar(w, 6));
         }
-        if (t + 1 == t1 && leader) {  // the item's Q is read
-          if (g1 > g0)
-            ptx::mma_commit(qempty);
-          else
-            ptx::mbar_arrive(qempty);
-        }
-        if (!wait_all(ffull(vf), (n / kVf) & 1) || (on && !wait_all(gbar(w, 1), live_tiles & 1)) ||
-            (on && t == g0 && live_items > 0 && !wait_all(gbar(w, 3), (live_items - 1) & 1))) {
-          ok = false;
-          break;
-        }
-        if (on) {
-          ptx::tc_fence_after();
-          const uint64_t vd = vdesc0 + static_cast<uint64_t>((vf * kVfTile) >> 4);
-          const uint32_t more = t > g0;
-          if (leader) {
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)  // 16 keys: 8 columns of P, 16 rows of V
-              mma_f16_ts(to, ts + 8 * kk, vd + 128 * kk, idesc_o, kk > 0 ? 1u : more);
-          }
-          __syncwarp();
-          if (!wait_all(phalf(w), live_tiles & 1)) {
-            ok = false;
-            break;
-          }
-          ptx::tc_fence_after();
-          if (leader) {
-#pragma unroll
-            for (int kk = 4; kk < 8; ++kk) mma_f16_ts(to, ts + 8 * kk, vd + 128 * kk, idesc_o, 1u);
-            ptx::mma_commit(fempty(vf));
-            if (t + 1 == g1) ptx::mma_commit(gbar(w, 2));
-          }
-          __syncwarp();
-          ++live_tiles;
-        } else if (leader) {
-          ptx::mbar_arrive(fempty(vf));
-        }
+        __syncwarp();
+        if (s + 2 < s1) ok = scores(s + 2);
       }
-      if (g1 > g0) ++live_items;
+      for (int t = last > first ? last : first; ok && t < t1; ++t) ok = pass(t);
+      n += t1 - t0;
+      if (s1 > s0) ++live_items;
     }
     if (leader) {
       if (!ok) give_up(abort_flag, a.status);
@@ -477,21 +473,22 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
     const int r = quarter * 32 + lane;  // row of the group = TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t ts = tmem + w * 256 + lane_off, to = ts + 128;
-    int live_tiles = 0, live_items = 0, items = 0;
+    uint32_t phase = 0;  // bits 0, 1: of the halves' scores
+    int steps = 0, items = 0, live_items = 0;
     bool ok = true;
     for (int k = 0; ok && unit_at(k) < units; ++k) {
-      // the threads hold 128 scores: what only an item's ends need is looked up
+      // the threads hold 64 scores: what only an item's ends need is looked up
       // again there, so that it takes no register in between
       auto unit = [&] {
         int u = unit_at(k);
         asm volatile("" : "+r"(u));
         return u;
       };
-      int g0 = 0, g1 = 0, lo = 0, lim = INT32_MAX;  // the group's tiles; the row sees keys lo .. lim
+      int s0 = 0, s1 = 0, lo = 0, lim = INT32_MAX;  // the group's steps; the row sees keys lo .. lim
       bool empty;
       {
         const PromptItem it = load_item(unit());
-        group_tiles(it, w, &g0, &g1);
+        group_steps(it, w, &s0, &s1);
         empty = it.t1 <= it.t0;
         const int row = it.row0 + w * kRows + r;  // (rows past the last compute what nobody reads)
         if (row < it.n_tok * a.h_r) {
@@ -502,15 +499,17 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
       // reference maximum (in units of the scores as read), sum of 2^kPBias p,
       // score -> log2 units
       float m_run = -INFINITY, l_run = 0.f, c2 = 1.f, cap_c1 = 0.f;
-      for (int t = g0; t < g1; ++t) {
-        const int key0 = t * kRows;
-        if (!wait(gbar(w, 0), live_tiles & 1)) ok = false;
+      for (int st = s0; st < s1; ++st, ++steps) {
+        const int h = st & 1, key0 = st * kStep;
+        const uint32_t tsh = ts + kStep * h;
+        if (!wait(gbar(w, h), (phase >> h) & 1)) ok = false;
         if (__any_sync(0xffffffffu, !ok)) {
           ok = false;
           break;
         }
+        phase ^= 1u << h;
         ptx::tc_fence_after();
-        if (t == g0) {  // the row's scale is there since its Q was laid out
+        if (st == s0) {  // the row's scale is there since its Q was laid out
           const int u = unit(), g = u % a.h_k, b = a.items[u / a.h_k].b;
           float raw_l = a.softmax_scale * a.qd[b * a.qd_seq + g * a.qd_head] * a.kd[b * a.kd_seq + g * a.kd_head];
           if constexpr (!kQe4m3) raw_l *= __uint_as_float(static_cast<uint32_t>(127 - q_shift[(items & 1) * 256 + w * kRows + r]) << 23);
@@ -519,78 +518,78 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
           else
             c2 = raw_l * kLog2e;
         }
-        const bool unmasked = __all_sync(0xffffffffu, key0 >= lo && key0 + kRows - 1 <= lim);
-        uint32_t s[kRows];
+        const bool unmasked = __all_sync(0xffffffffu, key0 >= lo && key0 + kStep - 1 <= lim);
+        uint32_t s[kStep];
 #pragma unroll
-        for (int c = 0; c < kRows; c += 16) MJ_TMEM_LD16(ts + c, (s + c));
+        for (int c = 0; c < kStep; c += 16) MJ_TMEM_LD16(tsh + c, (s + c));
         ptx::tmem_ld_wait();
-        if constexpr (kCap) {
-#pragma unroll
-          for (int h0 = 0; h0 < kRows; h0 += 32) modify_scores<32>(s + h0, cap_c1, a.softcap * kLog2e, false, 0.f, 0.f);
-        }
+        if constexpr (kCap) modify_scores<kStep>(s, cap_c1, a.softcap * kLog2e, false, 0.f, 0.f);
         if (!unmasked) {
           const int e0 = lo - key0, e1 = lim - key0;
 #pragma unroll
-          for (int e = 0; e < kRows; ++e) s[e] = e >= e0 && e <= e1 ? s[e] : 0xFF800000u;  // -inf
+          for (int e = 0; e < kStep; ++e) s[e] = e >= e0 && e <= e1 ? s[e] : 0xFF800000u;  // -inf
         }
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int e = 0; e < kRows; e += 2)
+        for (int e = 0; e < kStep; e += 2)
           m4[(e >> 1) & 3] = fmax3(m4[(e >> 1) & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
-        float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        const float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
         const bool moved = (mt - m_run) * c2 > kTau;  // from -inf too; -inf after -inf is NaN: no
-        const float m_new = moved ? mt : m_run;
-        const float mu = m_new == -INFINITY ? 0.f : m_new;
-        const float corr = moved ? fast_exp2((m_run - mu) * c2) : 1.f;  // 0 for a row that had seen no key
-        l_run *= corr;
-        m_run = m_new;
-        // O of the tiles before is complete (its products were issued ahead
-        // of this tile's scores); a warp corrects it when any row moved
-        if (t > g0 && __any_sync(0xffffffffu, moved)) {
+        if (__any_sync(0xffffffffu, moved)) {
+          const float m_new = moved ? mt : m_run;
+          const float corr = moved ? fast_exp2((m_run - m_new) * c2) : 1.f;  // 0 for a row that had seen no key
+          l_run *= corr;
+          m_run = m_new;
+          // a warp corrects O, complete up to the step before, when any row moved
+          if (st > s0) {
+            // (these scores were issued after the step before that one's O)
+            if (!wait(gbar(w, 4), (steps - 1) & 1)) ok = false;
+            if (__any_sync(0xffffffffu, !ok)) {
+              ok = false;
+              break;
+            }
+            ptx::tc_fence_after();
 #pragma unroll 1
-          for (int h0 = 0; h0 < kRows; h0 += 16) {
-            uint32_t o[16];
-            MJ_TMEM_LD16(to + h0, o);
-            ptx::tmem_ld_wait();
+            for (int h0 = 0; h0 < kRows; h0 += 16) {
+              uint32_t o[16];
+              MJ_TMEM_LD16(to + h0, o);
+              ptx::tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
-            MJ_TMEM_ST16(to + h0, o);
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+              MJ_TMEM_ST16(to + h0, o);
+            }
           }
         }
-        // P over the scores, two a column, in halves: the first half's product
-        // runs while the second is made
+        // P over the scores, two a column
+        const float mu = m_run == -INFINITY ? 0.f : m_run;
         const float bias = fmaf(-mu, c2, kPBias);
         const float2 c22 = make_float2(c2, c2), bias2 = make_float2(bias, bias);
         float2 sum2[4] = {};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int q = 0; q < 2; ++q) {
+          uint32_t p[16];
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            uint32_t p[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int e = 64 * h + 32 * q + 2 * i;
-              const float2 y = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c22, bias2);
-              const float2 x = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-              sum2[i & 3] = add2(sum2[i & 3], x);
-              p[i] = f32x2_to_f16x2(x.x, x.y);
-            }
-            MJ_TMEM_ST16(ts + 32 * h + 16 * q, p);
+          for (int i = 0; i < 16; ++i) {
+            const int e = 32 * q + 2 * i;
+            const float2 y = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c22, bias2);
+            const float2 x = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+            sum2[i & 3] = add2(sum2[i & 3], x);
+            p[i] = f32x2_to_f16x2(x.x, x.y);
           }
-          ptx::tmem_st_wait();
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(h == 0 ? gbar(w, 1) : phalf(w));
+          MJ_TMEM_ST16(tsh + 16 * q, p);
         }
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(gbar(w, 2 + h));
         const float2 all = add2(add2(sum2[0], sum2[1]), add2(sum2[2], sum2[3]));
         l_run += all.x + all.y;
-        ++live_tiles;
       }
       if (!empty) ++items;
       if (!ok) break;
       // ---- epilogue: O, or its part, of this group's rows
-      const bool any = g1 > g0;
-      if (any && !wait(gbar(w, 2), live_items & 1)) ok = false;
+      const bool any = s1 > s0;
+      if (any && !wait(gbar(w, 6), live_items & 1)) ok = false;
       if (__any_sync(0xffffffffu, !ok)) {
         ok = false;
         break;
@@ -640,7 +639,7 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
       if (any) {
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(gbar(w, 3));
+        if (lane == 0) ptx::mbar_arrive(gbar(w, 5));
         ++live_items;
       }
       if (live) {

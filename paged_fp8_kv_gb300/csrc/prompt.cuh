@@ -99,19 +99,19 @@ __host__ __device__ __forceinline__ void prompt_range(int len, int n_tok, int i0
   }
 }
 
-// The runs of `keys` keys that rows [row0, row0 + rows) see any key of (s1 ==
-// s0: none).
-__host__ __device__ __forceinline__ void prompt_steps(int len, int n_tok, int h_r, int row0, int rows, int causal,
-                                                      int window, int keys, int* s0, int* s1) {
+// The tiles of 128 keys that rows [row0, row0 + rows) see any key of (t1 == t0:
+// none).
+__host__ __device__ __forceinline__ void prompt_tiles(int len, int n_tok, int h_r, int row0, int rows, int causal,
+                                                      int window, int* t0, int* t1) {
   const int end = n_tok * h_r;  // checked to fit
-  *s0 = *s1 = 0;
+  *t0 = *t1 = 0;
   if (row0 >= end) return;
   const int last_row = (row0 + rows < end ? row0 + rows : end) - 1;
   int first, last;
   prompt_range(len, n_tok, row0 / h_r, last_row / h_r, causal, window, &first, &last);
   if (last < first) return;
-  *s0 = first / keys;
-  *s1 = last / keys + 1;
+  *t0 = first / 128;
+  *t1 = last / 128 + 1;
 }
 
 }  // namespace mj

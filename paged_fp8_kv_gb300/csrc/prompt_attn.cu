@@ -45,7 +45,6 @@ namespace mj {
 namespace {
 
 constexpr int kRows = 128;               // rows of a group = MMA M; keys of a tile = MMA N
-constexpr int kStep = 64;                // keys of a softmax step: half a tile
 constexpr int kTile = 128 * 128;         // bytes of a K tile, a raw V tile, an e4m3 part of a group's Q
 constexpr int kVfTile = 2 * kTile;       // a V tile in half precision
 constexpr int kThreads = 512;
@@ -70,7 +69,7 @@ struct Cfg {
   static constexpr int kOffQ = kOffVf + kVf * kVfTile;           // [group][part]
   static constexpr int kOffShift = kOffQ + 2 * kParts * kTile;   // [2][256] s of each row
   static constexpr int kOffBar = kOffShift + 2 * 256;
-  static constexpr int kBars = 2 * (kSK + kSV + kVf) + 2 + 7 * 2 + 2;
+  static constexpr int kBars = 2 * (kSK + kSV + kVf) + 3 + 4 * 2 + 1;
   static constexpr int kOffMisc = kOffBar + kBars * 8;
   static constexpr int kBytes = kOffMisc + 16 + 1024;
   static_assert(kBytes <= 232448, "shared memory");
@@ -125,17 +124,16 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
   auto ffull = [&](int s) { return bar0 + 8u * (2 * SK + 2 * SV + s); };   // converted V
   auto fempty = [&](int s) { return bar0 + 8u * (2 * SK + 2 * SV + kVf + s); };
   constexpr int kB = 2 * (SK + SV + kVf);
-  const uint32_t qfull = bar0 + 8u * kB, qempty = qfull + 8u;
-  // of each group: 0, 1 the halves' scores written, 2, 3 their P written, 4 O
-  // complete up to a step, 5 O read out, 6 the item's O final (two steps are in
-  // flight, so the end of the last one cannot be told from 4 by its parity)
-  auto gbar = [&](int w, int k) { return bar0 + 8u * (kB + 2 + 7 * w + k); };
-  const uint32_t drain = bar0 + 8u * (kB + 16);  // [group]
+  const uint32_t qfull = bar0 + 8u * kB, qempty = qfull + 8u, sread = qfull + 16u;
+  // of each group: 0 scores written, 1 P written, 2 a tile's product done, 3 O
+  // read out (sread: either group's scores read)
+  auto gbar = [&](int w, int k) { return bar0 + 8u * (kB + 3 + 4 * w + k); };
+  const uint32_t drain = bar0 + 8u * (kB + 11);
 
   if (tid == 0) {
     for (int s = 0; s < SK; ++s) {
       ptx::mbar_init(kfull(s), 1);
-      ptx::mbar_init(kempty(s), 2);
+      ptx::mbar_init(kempty(s), 1);
     }
     for (int s = 0; s < SV; ++s) {
       ptx::mbar_init(vfull(s), 1);
@@ -143,14 +141,15 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
     }
     for (int s = 0; s < kVf; ++s) {
       ptx::mbar_init(ffull(s), 4);
-      ptx::mbar_init(fempty(s), 2);
+      ptx::mbar_init(fempty(s), 1);
     }
     ptx::mbar_init(qfull, 4);
-    ptx::mbar_init(qempty, 2);
+    ptx::mbar_init(qempty, 1);
+    ptx::mbar_init(sread, 4);
     for (int w = 0; w < 2; ++w) {
-      for (int k = 0; k < 7; ++k) ptx::mbar_init(gbar(w, k), k == 2 || k == 3 || k == 5 ? 4 : 1);
-      ptx::mbar_init(drain + 8u * w, 1);
+      for (int k = 0; k < 4; ++k) ptx::mbar_init(gbar(w, k), k == 1 || k == 3 ? 4 : 1);
     }
+    ptx::mbar_init(drain, 1);
     *abort_flag = 0;
     ptx::fence_mbar_init();
   }
@@ -161,7 +160,10 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  const uint32_t tmem = *tmem_slot;  // group w: S at 256 w, O at 256 w + 128
+  // columns: the scores of either group (128), each group's P (64), each group's O (128)
+  const uint32_t tmem = *tmem_slot;
+  auto p_col = [&](int w) { return 128u + 64u * w; };
+  auto o_col = [&](int w) { return 256u + 128u * w; };
 
   auto wait = [&](uint32_t bar, uint32_t parity) { return ptx::mbar_wait_bounded(bar, parity, abort_flag, kWaitNs); };
   // the CTA's k-th unit: forth and back through the list (longest first)
@@ -174,25 +176,19 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
     reinterpret_cast<int4*>(&it)[1] = src[1];
     return it;
   };
-  // the steps (of 64 keys) of the item that group w's rows see any key of
-  auto group_steps = [&](const PromptItem& it, int w, int* s0, int* s1) {
-    prompt_steps(it.len, it.n_tok, a.h_r, it.row0 + w * kRows, kRows, a.causal, a.window, kStep, s0, s1);
-    *s0 = *s0 > 2 * it.t0 ? *s0 : 2 * it.t0;
-    *s1 = *s1 < 2 * it.t1 ? *s1 : 2 * it.t1;
-    if (*s1 < *s0) *s1 = *s0;
+  // the tiles of the item that group w's rows see any key of
+  auto group_tiles = [&](const PromptItem& it, int w, int* g0, int* g1) {
+    prompt_tiles(it.len, it.n_tok, a.h_r, it.row0 + w * kRows, kRows, a.causal, a.window, g0, g1);
+    *g0 = *g0 > it.t0 ? *g0 : it.t0;
+    *g1 = *g1 < it.t1 ? *g1 : it.t1;
+    if (*g1 < *g0) *g1 = *g0;
   };
 
-  // a warpgroup's share of the launch's 512 x 128 registers: 2 x 184 + 80 + 64
-  // = 4 x 128 (the softmax threads hold 64 scores and their P, with a cap its terms)
-  if (warp >= kMmaWarp)
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-  else if (warp >= kConvWarp)
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-  else
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
-
+  // A warpgroup's share of the launch's 512 x 128 registers: 2 x 192 + 80 + 48
+  // = 4 x 128 (the softmax threads hold 128 scores).
   if (warp >= kKWarp) {
     // ------------------------------------------------------------- TMA loads
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     const bool is_k = warp == kKWarp;
     const int NS = is_k ? SK : SV;
     const uint32_t ring = sbase + (is_k ? C::kOffK : C::kOffV);
@@ -245,102 +241,98 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
     }
   } else if (warp >= kMmaWarp) {
     // ------------------------------------------------------------------- MMA
-    // A group's S, its P and its next S share their columns: the products run
-    // in the order of issue, S of tile t + 1 after O of tile t.
-    // The whole warp goes through the loop and one lane issues, so that
-    // descriptors and addresses stay in uniform registers: inside a branch of
-    // one lane each MMA took 118 cycles to issue.
-    const int w = __shfl_sync(0xffffffffu, warp - kMmaWarp, 0);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    if (warp == kMmaWarp) {
+    // One warp issues everything, in the order S_0(t), O_0(t - 1), S_1(t),
+    // O_1(t - 1): a group's O product runs while its new scores are read, after
+    // which the other group's scores take their place.  The whole warp goes
+    // through the loop and one lane issues, so that descriptors and addresses
+    // stay in uniform registers: inside a branch of one lane each MMA took 118
+    // cycles to issue.
     const bool leader = ptx::elect_one() != 0;
-    const uint32_t idesc_s = ptx::idesc_e4m3(kRows, kStep, false, false);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    auto wait_all = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+    const uint32_t idesc_s = ptx::idesc_e4m3(kRows, kRows, false, false);
     const uint32_t idesc_o = ptx::idesc_e4m3(kRows, kRows, false, true);  // formats 0: half precision in kind::f16
-    const uint64_t qdesc = ptx::smem_desc(sbase + C::kOffQ + w * C::kParts * kTile, 16, 1024, ptx::kSwizzle128B);
+    const uint64_t qdesc0 = ptx::smem_desc(sbase + C::kOffQ, 16, 1024, ptx::kSwizzle128B);
     const uint64_t kdesc0 = ptx::smem_desc(sbase + C::kOffK, 16, 1024, ptx::kSwizzle128B);
     // V, d-major: 64 elements of d a 128-byte row, the other 64 a tile half further
     const uint64_t vdesc0 = ptx::smem_desc(sbase + C::kOffVf, kTile, 1024, ptx::kSwizzle128B);
-    const uint32_t ts = __shfl_sync(0xffffffffu, tmem, 0) + w * 256, to = ts + 128;
-    auto wait_all = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
-    int n = 0;  // tiles of the items before
-    uint32_t phase = 0;  // bits 0, 1: of the halves' P
-    int items = 0, live_items = 0;
+    int n = 0, items = 0;  // tiles of the items before, items
+    int scores = 0;        // tiles of scores, of both groups
+    int q[2] = {0, 0}, live_items[2] = {0, 0};  // tiles whose O was issued, and items, of each group
     bool ok = true;
     for (int k = 0; ok && unit_at(k) < units; ++k) {
       const PromptItem it = load_item(unit_at(k));
       const int t0 = __shfl_sync(0xffffffffu, it.t0, 0), t1 = __shfl_sync(0xffffffffu, it.t1, 0);
       if (t1 <= t0) continue;
-      int s0, s1;
-      group_steps(it, w, &s0, &s1);
-      s0 = __shfl_sync(0xffffffffu, s0, 0);
-      s1 = __shfl_sync(0xffffffffu, s1, 0);
+      int g0[2], g1[2];
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        group_tiles(it, w, &g0[w], &g1[w]);
+        g0[w] = __shfl_sync(0xffffffffu, g0[w], 0);
+        g1[w] = __shfl_sync(0xffffffffu, g1[w], 0);
+      }
       ok = wait_all(qfull, items & 1);
       ++items;
-      // tiles that only the other group's rows see
-      auto pass = [&](int t) {
-        const int i = n + t - t0;
-        if (!wait_all(kfull(i % SK), (i / SK) & 1) || !wait_all(ffull(i % kVf), (i / kVf) & 1)) return false;
-        if (leader) {
-          ptx::mbar_arrive(kempty(i % SK));
-          ptx::mbar_arrive(fempty(i % kVf));
+      for (int t = t0; ok && t <= t1; ++t) {  // scores of tile t, O of tile t - 1
+        const int st = (n + t - t0) % SK, vf = (n + t - 1 - t0) % kVf;
+        if (t < t1) ok = wait_all(kfull(st), ((n + t - t0) / SK) & 1);
+        if (ok && t > t0) ok = wait_all(ffull(vf), ((n + t - 1 - t0) / kVf) & 1);
+        const uint64_t kd = kdesc0 + static_cast<uint64_t>((st * kTile) >> 4);
+        const uint64_t vd = vdesc0 + static_cast<uint64_t>((vf * kVfTile) >> 4);
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          if (ok && t >= g0[w] && t < g1[w]) {
+            if (scores > 0) ok = wait_all(sread, (scores - 1) & 1);
+            ++scores;
+            ptx::tc_fence_after();
+            const uint64_t qd = qdesc0 + static_cast<uint64_t>((w * C::kParts * kTile) >> 4);
+            if (ok && leader) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+                for (int part = 0; part < C::kParts; ++part)
+                  ptx::mma_e4m3(tm, qd + part * (kTile >> 4) + 2 * kk, kd + 2 * kk, idesc_s, kk > 0 || part > 0);
+              ptx::mma_commit(gbar(w, 0));
+            }
+            __syncwarp();
+          }
+          if (ok && t > g0[w] && t <= g1[w]) {
+            ok = wait_all(gbar(w, 1), q[w] & 1);
+            if (ok && t == g0[w] + 1 && live_items[w]++ > 0) ok = wait_all(gbar(w, 3), live_items[w] & 1);  // O read out
+            ++q[w];
+            ptx::tc_fence_after();
+            const uint32_t more = t > g0[w] + 1;
+            if (ok && leader) {
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)  // 16 keys: 8 columns of P, 16 rows of V
+                mma_f16_ts(tm + o_col(w), tm + p_col(w) + 8 * kk, vd + 128 * kk, idesc_o, kk > 0 ? 1u : more);
+              ptx::mma_commit(gbar(w, 2));
+            }
+            __syncwarp();
+          }
         }
-        return true;
-      };
-      auto scores = [&](int s) {  // S of step s
-        const int i = n + (s >> 1) - t0, st = i % SK, h = s & 1;
-        if ((h == 0 || s == s0) && !wait_all(kfull(st), (i / SK) & 1)) return false;
-        ptx::tc_fence_after();
-        const uint64_t kd = kdesc0 + static_cast<uint64_t>((st * kTile + h * (kStep * 128)) >> 4);
-        if (leader) {
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-            for (int part = 0; part < C::kParts; ++part)
-              ptx::mma_e4m3(ts + kStep * h, qdesc + part * (kTile >> 4) + 2 * kk, kd + 2 * kk, idesc_s, kk > 0 || part > 0);
-          ptx::mma_commit(gbar(w, h));
-          if (h == 1 || s + 1 == s1) ptx::mma_commit(kempty(st));
-          if (s + 1 == s1) ptx::mma_commit(qempty);  // the item's Q is read
+        if (ok && leader) {
+          if (t < t1) ptx::mma_commit(kempty(st));
+          if (t + 1 == t1) ptx::mma_commit(qempty);  // the item's Q is read
+          if (t > t0) ptx::mma_commit(fempty(vf));
         }
         __syncwarp();
-        return true;
-      };
-      const int first = s1 > s0 ? s0 >> 1 : t1, last = s1 > s0 ? (s1 + 1) >> 1 : t1;  // the group's tiles
-      for (int t = t0; ok && t < first; ++t) ok = pass(t);
-      if (s1 <= s0 && leader) ptx::mbar_arrive(qempty);
-      for (int s = s0; ok && s < s1 && s < s0 + 2; ++s) ok = scores(s);
-      for (int s = s0; ok && s < s1; ++s) {
-        const int i = n + (s >> 1) - t0, vf = i % kVf, h = s & 1;
-        if (((h == 0 || s == s0) && !wait_all(ffull(vf), (i / kVf) & 1)) || !wait_all(gbar(w, 2 + h), (phase >> h) & 1) ||
-            (s == s0 && live_items > 0 && !wait_all(gbar(w, 5), (live_items - 1) & 1))) {
-          ok = false;
-          break;
-        }
-        phase ^= 1u << h;
-        ptx::tc_fence_after();
-        const uint64_t vd = vdesc0 + static_cast<uint64_t>((vf * kVfTile + h * (kStep * 128)) >> 4);
-        const uint32_t more = s > s0;
-        if (leader) {
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)  // 16 keys: 8 columns of P, 16 rows of V
-            mma_f16_ts(to, ts + kStep * h + 8 * kk, vd + 128 * kk, idesc_o, kk > 0 ? 1u : more);
-          ptx::mma_commit(gbar(w, 4));
-          if (h == 1 || s + 1 == s1) ptx::mma_commit(fempty(vf));
-          if (s + 1 == s1) ptx::mma_commit(gbar(w, 6));
-        }
-        __syncwarp();
-        if (s + 2 < s1) ok = scores(s + 2);
       }
-      for (int t = last > first ? last : first; ok && t < t1; ++t) ok = pass(t);
       n += t1 - t0;
-      if (s1 > s0) ++live_items;
     }
     if (leader) {
       if (!ok) give_up(abort_flag, a.status);
-      ptx::mma_commit(drain + 8u * w);
+      ptx::mma_commit(drain);
       volatile int never = 0;
-      ptx::mbar_wait_bounded(drain + 8u * w, 0, &never, kWaitNs);
+      ptx::mbar_wait_bounded(drain, 0, &never, kWaitNs);
     }
     __syncwarp();
+    }
   } else if (warp >= kConvWarp) {
     // ------------------------------------------------ Q and V conversion
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     const int cw = warp - kConvWarp;
     int n = 0, items = 0;
     bool ok = true;
@@ -468,27 +460,27 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
     if (!ok && lane == 0) give_up(abort_flag, a.status);
   } else {
     // --------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     const int w = warp >> 2;
     const int quarter = warp & 3;
     const int r = quarter * 32 + lane;  // row of the group = TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t ts = tmem + w * 256 + lane_off, to = ts + 128;
-    uint32_t phase = 0;  // bits 0, 1: of the halves' scores
-    int steps = 0, items = 0, live_items = 0;
+    const uint32_t ts = tmem + lane_off, tp = ts + p_col(w), to = ts + o_col(w);
+    int q = 0, items = 0;  // tiles, items
     bool ok = true;
     for (int k = 0; ok && unit_at(k) < units; ++k) {
-      // the threads hold 64 scores: what only an item's ends need is looked up
+      // the threads hold 128 scores: what only an item's ends need is looked up
       // again there, so that it takes no register in between
       auto unit = [&] {
         int u = unit_at(k);
         asm volatile("" : "+r"(u));
         return u;
       };
-      int s0 = 0, s1 = 0, lo = 0, lim = INT32_MAX;  // the group's steps; the row sees keys lo .. lim
+      int g0 = 0, g1 = 0, lo = 0, lim = INT32_MAX;  // the group's tiles; the row sees keys lo .. lim
       bool empty;
       {
         const PromptItem it = load_item(unit());
-        group_steps(it, w, &s0, &s1);
+        group_tiles(it, w, &g0, &g1);
         empty = it.t1 <= it.t0;
         const int row = it.row0 + w * kRows + r;  // (rows past the last compute what nobody reads)
         if (row < it.n_tok * a.h_r) {
@@ -499,17 +491,15 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
       // reference maximum (in units of the scores as read), sum of 2^kPBias p,
       // score -> log2 units
       float m_run = -INFINITY, l_run = 0.f, c2 = 1.f, cap_c1 = 0.f;
-      for (int st = s0; st < s1; ++st, ++steps) {
-        const int h = st & 1, key0 = st * kStep;
-        const uint32_t tsh = ts + kStep * h;
-        if (!wait(gbar(w, h), (phase >> h) & 1)) ok = false;
+      for (int t = g0; t < g1; ++t, ++q) {
+        const int key0 = t * kRows;
+        if (!wait(gbar(w, 0), q & 1)) ok = false;
         if (__any_sync(0xffffffffu, !ok)) {
           ok = false;
           break;
         }
-        phase ^= 1u << h;
         ptx::tc_fence_after();
-        if (st == s0) {  // the row's scale is there since its Q was laid out
+        if (t == g0) {  // the row's scale is there since its Q was laid out
           const int u = unit(), g = u % a.h_k, b = a.items[u / a.h_k].b;
           float raw_l = a.softmax_scale * a.qd[b * a.qd_seq + g * a.qd_head] * a.kd[b * a.kd_seq + g * a.kd_head];
           if constexpr (!kQe4m3) raw_l *= __uint_as_float(static_cast<uint32_t>(127 - q_shift[(items & 1) * 256 + w * kRows + r]) << 23);
@@ -518,37 +508,42 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
           else
             c2 = raw_l * kLog2e;
         }
-        const bool unmasked = __all_sync(0xffffffffu, key0 >= lo && key0 + kStep - 1 <= lim);
-        uint32_t s[kStep];
+        const bool unmasked = __all_sync(0xffffffffu, key0 >= lo && key0 + kRows - 1 <= lim);
+        uint32_t s[kRows];
 #pragma unroll
-        for (int c = 0; c < kStep; c += 16) MJ_TMEM_LD16(tsh + c, (s + c));
+        for (int c = 0; c < kRows; c += 16) MJ_TMEM_LD16(ts + c, (s + c));
         ptx::tmem_ld_wait();
-        if constexpr (kCap) modify_scores<kStep>(s, cap_c1, a.softcap * kLog2e, false, 0.f, 0.f);
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(sread);  // the other group's scores may come
+        if constexpr (kCap) {
+#pragma unroll
+          for (int h0 = 0; h0 < kRows; h0 += 32) modify_scores<32>(s + h0, cap_c1, a.softcap * kLog2e, false, 0.f, 0.f);
+        }
         if (!unmasked) {
           const int e0 = lo - key0, e1 = lim - key0;
 #pragma unroll
-          for (int e = 0; e < kStep; ++e) s[e] = e >= e0 && e <= e1 ? s[e] : 0xFF800000u;  // -inf
+          for (int e = 0; e < kRows; ++e) s[e] = e >= e0 && e <= e1 ? s[e] : 0xFF800000u;  // -inf
         }
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int e = 0; e < kStep; e += 2)
+        for (int e = 0; e < kRows; e += 2)
           m4[(e >> 1) & 3] = fmax3(m4[(e >> 1) & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
         const float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
         const bool moved = (mt - m_run) * c2 > kTau;  // from -inf too; -inf after -inf is NaN: no
+        // the tile before is added up: its P and O are free
+        if (q > 0 && !wait(gbar(w, 2), (q - 1) & 1)) ok = false;
+        if (__any_sync(0xffffffffu, !ok)) {
+          ok = false;
+          break;
+        }
+        ptx::tc_fence_after();
         if (__any_sync(0xffffffffu, moved)) {
           const float m_new = moved ? mt : m_run;
           const float corr = moved ? fast_exp2((m_run - m_new) * c2) : 1.f;  // 0 for a row that had seen no key
           l_run *= corr;
           m_run = m_new;
-          // a warp corrects O, complete up to the step before, when any row moved
-          if (st > s0) {
-            // (these scores were issued after the step before that one's O)
-            if (!wait(gbar(w, 4), (steps - 1) & 1)) ok = false;
-            if (__any_sync(0xffffffffu, !ok)) {
-              ok = false;
-              break;
-            }
-            ptx::tc_fence_after();
+          if (t > g0) {  // a warp corrects O when any of its rows moved
 #pragma unroll 1
             for (int h0 = 0; h0 < kRows; h0 += 16) {
               uint32_t o[16];
@@ -560,36 +555,36 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
             }
           }
         }
-        // P over the scores, two a column
+        // P, two keys a column
         const float mu = m_run == -INFINITY ? 0.f : m_run;
         const float bias = fmaf(-mu, c2, kPBias);
         const float2 c22 = make_float2(c2, c2), bias2 = make_float2(bias, bias);
         float2 sum2[4] = {};
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
+        for (int p0 = 0; p0 < 64; p0 += 16) {
           uint32_t p[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const int e = 32 * q + 2 * i;
+            const int e = 2 * (p0 + i);
             const float2 y = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c22, bias2);
             const float2 x = make_float2(fast_exp2(y.x), fast_exp2(y.y));
             sum2[i & 3] = add2(sum2[i & 3], x);
             p[i] = f32x2_to_f16x2(x.x, x.y);
           }
-          MJ_TMEM_ST16(tsh + 16 * q, p);
+          MJ_TMEM_ST16(tp + p0, p);
         }
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(gbar(w, 2 + h));
+        if (lane == 0) ptx::mbar_arrive(gbar(w, 1));
         const float2 all = add2(add2(sum2[0], sum2[1]), add2(sum2[2], sum2[3]));
         l_run += all.x + all.y;
       }
       if (!empty) ++items;
       if (!ok) break;
       // ---- epilogue: O, or its part, of this group's rows
-      const bool any = s1 > s0;
-      if (any && !wait(gbar(w, 6), live_items & 1)) ok = false;
+      const bool any = g1 > g0;
+      if (any && !wait(gbar(w, 2), (q - 1) & 1)) ok = false;
       if (__any_sync(0xffffffffu, !ok)) {
         ok = false;
         break;
@@ -639,8 +634,7 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
       if (any) {
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(gbar(w, 5));
-        ++live_items;
+        if (lane == 0) ptx::mbar_arrive(gbar(w, 3));
       }
       if (live) {
         const float top = m_run * c2 * (1.f / kLog2e);

@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kThreads) prompt_plan_kernel(const PromptPlanD
     shape(lo, &it.tok0, &it.n_tok, &it.len);
     it.row0 = (x - off[lo]) * kPromptRows;
     it.part = -1;
-    prompt_steps(it.len, it.n_tok, a.h_r, it.row0, kPromptRows, a.causal, a.window, 128, &it.t0, &it.t1);
+    prompt_tiles(it.len, it.n_tok, a.h_r, it.row0, kPromptRows, a.causal, a.window, &it.t0, &it.t1);
     return it;
   };
 

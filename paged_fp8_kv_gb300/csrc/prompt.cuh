@@ -17,9 +17,12 @@ constexpr int kPromptSortMax = 8192; // items ordered by length in shared memory
 // group) of one sequence, from row0 on, against the keys of tiles [t0, t1).
 // part < 0: the item holds all the keys its rows see and writes O and LSE;
 // else its partial results go to part `part`.
+// (g0, g1): of those tiles, the ones that the first and the second 128 rows see
+// any key of.
 struct __align__(16) PromptItem {
   int32_t b, row0, t0, t1;
   int32_t part, tok0, n_tok, len;  // tok0: the sequence's first token in Q and O
+  int32_t g0[2], g1[2];
 };
 // The row tile that parts part0 .. part0 + n_parts - 1 make up.
 struct __align__(16) PromptMerge {

@@ -50,7 +50,8 @@ constexpr int kVfTile = 2 * kTile;       // a V tile in half precision
 constexpr int kThreads = 512;
 constexpr int kConvWarp = 8, kMmaWarp = 12, kKWarp = 14;
 constexpr int kVf = 2;                   // converted V tiles held
-constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s: far above any legal wait
+constexpr int kTries = 1 << 22;          // of a wait: seconds, far above any legal one
+constexpr uint64_t kDrainNs = 500000000ull;
 constexpr int kStatusTimeout = 5;        // MJ_ERR_TIMEOUT
 constexpr int kStatusInvalid = 1;        // MJ_ERR_INVALID_ARG
 // P is 2^kPBias 2^(s - m): the reference m of a row moves only when a score
@@ -165,25 +166,17 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
   auto p_col = [&](int w) { return 128u + 64u * w; };
   auto o_col = [&](int w) { return 256u + 128u * w; };
 
-  auto wait = [&](uint32_t bar, uint32_t parity) { return ptx::mbar_wait_bounded(bar, parity, abort_flag, kWaitNs); };
+  auto wait = [&](uint32_t bar, uint32_t parity) { return ptx::mbar_wait_tries(bar, parity, abort_flag, kTries); };
   // the CTA's k-th unit: forth and back through the list (longest first)
   const int G = gridDim.x, me = blockIdx.x;
   auto unit_at = [&](int k) { return k * G + ((k & 1) ? G - 1 - me : me); };
   auto load_item = [&](int u) {
     PromptItem it;
     const int4* src = reinterpret_cast<const int4*>(a.items + u / a.h_k);
-    reinterpret_cast<int4*>(&it)[0] = src[0];
-    reinterpret_cast<int4*>(&it)[1] = src[1];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) reinterpret_cast<int4*>(&it)[i] = src[i];
     return it;
   };
-  // the tiles of the item that group w's rows see any key of
-  auto group_tiles = [&](const PromptItem& it, int w, int* g0, int* g1) {
-    prompt_tiles(it.len, it.n_tok, a.h_r, it.row0 + w * kRows, kRows, a.causal, a.window, g0, g1);
-    *g0 = *g0 > it.t0 ? *g0 : it.t0;
-    *g1 = *g1 < it.t1 ? *g1 : it.t1;
-    if (*g1 < *g0) *g1 = *g0;
-  };
-
   // A warpgroup's share of the launch's 512 x 128 registers: 2 x 192 + 80 + 48
   // = 4 x 128 (the softmax threads hold 128 scores).
   if (warp >= kKWarp) {
@@ -232,103 +225,107 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
         give_up(abort_flag, a.status);
         volatile int never = 0;
         for (int i = n > NS ? n - NS : 0; i < n; ++i)
-          ptx::mbar_wait_bounded(full(i % NS), (i / NS) & 1, &never, kWaitNs / 4);
+          ptx::mbar_wait_bounded(full(i % NS), (i / NS) & 1, &never, kDrainNs);
       }
     } else if (*abort_flag && lane == 0) {
       volatile int never = 0;
       for (int i = n > NS ? n - NS : 0; i < n; ++i)
-        ptx::mbar_wait_bounded(full(i % NS), (i / NS) & 1, &never, kWaitNs / 4);
+        ptx::mbar_wait_bounded(full(i % NS), (i / NS) & 1, &never, kDrainNs);
     }
   } else if (warp >= kMmaWarp) {
     // ------------------------------------------------------------------- MMA
     asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-    if (warp == kMmaWarp) {
     // One warp issues everything, in the order S_0(t), O_0(t - 1), S_1(t),
     // O_1(t - 1): a group's O product runs while its new scores are read, after
     // which the other group's scores take their place.  The whole warp goes
-    // through the loop and one lane issues, so that descriptors and addresses
-    // stay in uniform registers: inside a branch of one lane each MMA took 118
-    // cycles to issue.
-    const bool leader = ptx::elect_one() != 0;
-    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    auto wait_all = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
-    const uint32_t idesc_s = ptx::idesc_e4m3(kRows, kRows, false, false);
-    const uint32_t idesc_o = ptx::idesc_e4m3(kRows, kRows, false, true);  // formats 0: half precision in kind::f16
-    const uint64_t qdesc0 = ptx::smem_desc(sbase + C::kOffQ, 16, 1024, ptx::kSwizzle128B);
-    const uint64_t kdesc0 = ptx::smem_desc(sbase + C::kOffK, 16, 1024, ptx::kSwizzle128B);
-    // V, d-major: 64 elements of d a 128-byte row, the other 64 a tile half further
-    const uint64_t vdesc0 = ptx::smem_desc(sbase + C::kOffVf, kTile, 1024, ptx::kSwizzle128B);
-    int n = 0, items = 0;  // tiles of the items before, items
-    int scores = 0;        // tiles of scores, of both groups
-    int q[2] = {0, 0}, live_items[2] = {0, 0};  // tiles whose O was issued, and items, of each group
-    bool ok = true;
-    for (int k = 0; ok && unit_at(k) < units; ++k) {
-      const PromptItem it = load_item(unit_at(k));
-      const int t0 = __shfl_sync(0xffffffffu, it.t0, 0), t1 = __shfl_sync(0xffffffffu, it.t1, 0);
-      if (t1 <= t0) continue;
-      int g0[2], g1[2];
-#pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        group_tiles(it, w, &g0[w], &g1[w]);
-        g0[w] = __shfl_sync(0xffffffffu, g0[w], 0);
-        g1[w] = __shfl_sync(0xffffffffu, g1[w], 0);
-      }
-      ok = wait_all(qfull, items & 1);
-      ++items;
-      for (int t = t0; ok && t <= t1; ++t) {  // scores of tile t, O of tile t - 1
-        const int st = (n + t - t0) % SK, vf = (n + t - 1 - t0) % kVf;
-        if (t < t1) ok = wait_all(kfull(st), ((n + t - t0) / SK) & 1);
-        if (ok && t > t0) ok = wait_all(ffull(vf), ((n + t - 1 - t0) / kVf) & 1);
-        const uint64_t kd = kdesc0 + static_cast<uint64_t>((st * kTile) >> 4);
-        const uint64_t vd = vdesc0 + static_cast<uint64_t>((vf * kVfTile) >> 4);
+    // through the loop and computes descriptors, addresses and phases, so that
+    // they lie in uniform registers; one lane waits and issues (with the
+    // arithmetic in its branch each MMA took 118 cycles to issue, with all
+    // lanes waiting a wait took 200).
+    if (warp == kMmaWarp) {
+      const bool leader = ptx::elect_one() != 0;
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint32_t idesc_s = ptx::idesc_e4m3(kRows, kRows, false, false);
+      const uint32_t idesc_o = ptx::idesc_e4m3(kRows, kRows, false, true);  // formats 0: half precision in kind::f16
+      const uint64_t qdesc = ptx::smem_desc(sbase + C::kOffQ, 16, 1024, ptx::kSwizzle128B);
+      const uint64_t kdesc = ptx::smem_desc(sbase + C::kOffK, 16, 1024, ptx::kSwizzle128B);
+      // V, d-major: 64 elements of d a 128-byte row, the other 64 a tile half further
+      const uint64_t vdesc = ptx::smem_desc(sbase + C::kOffVf, kTile, 1024, ptx::kSwizzle128B);
+      uint32_t ks = 0, kph = 0, vs = 0, vph = 0;  // stage and phase of the next K and converted V tile
+      uint32_t qph = 0, sph = 1;                  // of Q, and of the scores read (none to wait for at first)
+      uint32_t pph = 0, oph = 3;                  // bit w: of group w's P, and of its O read out (likewise)
+      for (int k = 0; unit_at(k) < units; ++k) {
+        const PromptItem it = load_item(unit_at(k));
+        const int t0 = __shfl_sync(0xffffffffu, it.t0, 0), t1 = __shfl_sync(0xffffffffu, it.t1, 0);
+        if (t1 <= t0) continue;
+        int g0[2], g1[2];
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
-          if (ok && t >= g0[w] && t < g1[w]) {
-            if (scores > 0) ok = wait_all(sread, (scores - 1) & 1);
-            ++scores;
-            ptx::tc_fence_after();
-            const uint64_t qd = qdesc0 + static_cast<uint64_t>((w * C::kParts * kTile) >> 4);
-            if (ok && leader) {
+          g0[w] = __shfl_sync(0xffffffffu, it.g0[w], 0);
+          g1[w] = __shfl_sync(0xffffffffu, it.g1[w], 0);
+        }
+        bool ok = true;
+        if (leader) ok = wait(qfull, qph);
+        qph ^= 1;
+        for (int t = t0; t <= t1; ++t) {  // scores of tile t, O of tile t - 1
+          const uint64_t kd = kdesc + ks * (kTile >> 4), vd = vdesc + vs * (kVfTile >> 4);
+          const bool load_k = t < t1, load_v = t > t0;
+          if (load_k && leader) ok &= wait(kfull(ks), kph);
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
+          for (int w = 0; w < 2; ++w) {
+            if (t >= g0[w] && t < g1[w]) {
+              if (leader) {
+                ok &= wait(sread, sph);
+                ptx::tc_fence_after();
 #pragma unroll
-                for (int part = 0; part < C::kParts; ++part)
-                  ptx::mma_e4m3(tm, qd + part * (kTile >> 4) + 2 * kk, kd + 2 * kk, idesc_s, kk > 0 || part > 0);
-              ptx::mma_commit(gbar(w, 0));
+                for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+                  for (int part = 0; part < C::kParts; ++part)
+                    ptx::mma_e4m3(tm, qdesc + (w * C::kParts + part) * (kTile >> 4) + 2 * kk, kd + 2 * kk, idesc_s,
+                                  kk > 0 || part > 0);
+                ptx::mma_commit(gbar(w, 0));
+              }
+              sph ^= 1;
             }
-            __syncwarp();
+            if (w == 1 && load_k && leader) {
+              ptx::mma_commit(kempty(ks));
+              if (t + 1 == t1) ptx::mma_commit(qempty);  // the item's Q is read
+            }
+            if (t > g0[w] && t <= g1[w]) {
+              const uint32_t more = t > g0[w] + 1;
+              if (leader) {
+                ok &= wait(ffull(vs), vph);  // (the same phase for both groups)
+                ok &= wait(gbar(w, 1), (pph >> w) & 1);
+                if (!more) ok &= wait(gbar(w, 3), (oph >> w) & 1);  // O read out
+                ptx::tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)  // 16 keys: 8 columns of P, 16 rows of V
+                  mma_f16_ts(tm + o_col(w), tm + p_col(w) + 8 * kk, vd + 128 * kk, idesc_o, kk > 0 ? 1u : more);
+                ptx::mma_commit(gbar(w, 2));
+              }
+              pph ^= 1u << w;
+              if (!more) oph ^= 1u << w;
+            }
           }
-          if (ok && t > g0[w] && t <= g1[w]) {
-            ok = wait_all(gbar(w, 1), q[w] & 1);
-            if (ok && t == g0[w] + 1 && live_items[w]++ > 0) ok = wait_all(gbar(w, 3), live_items[w] & 1);  // O read out
-            ++q[w];
-            ptx::tc_fence_after();
-            const uint32_t more = t > g0[w] + 1;
-            if (ok && leader) {
-#pragma unroll
-              for (int kk = 0; kk < 8; ++kk)  // 16 keys: 8 columns of P, 16 rows of V
-                mma_f16_ts(tm + o_col(w), tm + p_col(w) + 8 * kk, vd + 128 * kk, idesc_o, kk > 0 ? 1u : more);
-              ptx::mma_commit(gbar(w, 2));
-            }
-            __syncwarp();
+          if (load_v && leader) ptx::mma_commit(fempty(vs));  // (tiles past a group's are the other's)
+          if (load_k && ++ks == SK) {
+            ks = 0;
+            kph ^= 1;
+          }
+          if (load_v && ++vs == kVf) {
+            vs = 0;
+            vph ^= 1;
           }
         }
-        if (ok && leader) {
-          if (t < t1) ptx::mma_commit(kempty(st));
-          if (t + 1 == t1) ptx::mma_commit(qempty);  // the item's Q is read
-          if (t > t0) ptx::mma_commit(fempty(vf));
-        }
-        __syncwarp();
+        if (leader && !ok) give_up(abort_flag, a.status);
+        if (__any_sync(0xffffffffu, !ok)) break;
       }
-      n += t1 - t0;
-    }
-    if (leader) {
-      if (!ok) give_up(abort_flag, a.status);
-      ptx::mma_commit(drain);
-      volatile int never = 0;
-      ptx::mbar_wait_bounded(drain, 0, &never, kWaitNs);
-    }
-    __syncwarp();
+      if (leader) {
+        ptx::mma_commit(drain);
+        volatile int never = 0;
+        ptx::mbar_wait_bounded(drain, 0, &never, kDrainNs);
+      }
+      __syncwarp();
     }
   } else if (warp >= kConvWarp) {
     // ------------------------------------------------ Q and V conversion
@@ -467,8 +464,9 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t ts = tmem + lane_off, tp = ts + p_col(w), to = ts + o_col(w);
     int q = 0, items = 0;  // tiles, items
-    bool ok = true;
-    for (int k = 0; ok && unit_at(k) < units; ++k) {
+    // a wait that gives up sets the abort flag and the loop runs on (later waits
+    // return at once), so that a warp's lanes stay together
+    for (int k = 0; unit_at(k) < units; ++k) {
       // the threads hold 128 scores: what only an item's ends need is looked up
       // again there, so that it takes no register in between
       auto unit = [&] {
@@ -480,7 +478,8 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
       bool empty;
       {
         const PromptItem it = load_item(unit());
-        group_tiles(it, w, &g0, &g1);
+        g0 = w ? it.g0[1] : it.g0[0];
+        g1 = w ? it.g1[1] : it.g1[0];
         empty = it.t1 <= it.t0;
         const int row = it.row0 + w * kRows + r;  // (rows past the last compute what nobody reads)
         if (row < it.n_tok * a.h_r) {
@@ -493,11 +492,7 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
       float m_run = -INFINITY, l_run = 0.f, c2 = 1.f, cap_c1 = 0.f;
       for (int t = g0; t < g1; ++t, ++q) {
         const int key0 = t * kRows;
-        if (!wait(gbar(w, 0), q & 1)) ok = false;
-        if (__any_sync(0xffffffffu, !ok)) {
-          ok = false;
-          break;
-        }
+        if (!wait(gbar(w, 0), q & 1)) give_up(abort_flag, a.status);
         ptx::tc_fence_after();
         if (t == g0) {  // the row's scale is there since its Q was laid out
           const int u = unit(), g = u % a.h_k, b = a.items[u / a.h_k].b;
@@ -532,11 +527,7 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
         const float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
         const bool moved = (mt - m_run) * c2 > kTau;  // from -inf too; -inf after -inf is NaN: no
         // the tile before is added up: its P and O are free
-        if (q > 0 && !wait(gbar(w, 2), (q - 1) & 1)) ok = false;
-        if (__any_sync(0xffffffffu, !ok)) {
-          ok = false;
-          break;
-        }
+        if (q > 0 && !wait(gbar(w, 2), (q - 1) & 1)) give_up(abort_flag, a.status);
         ptx::tc_fence_after();
         if (__any_sync(0xffffffffu, moved)) {
           const float m_new = moved ? mt : m_run;
@@ -581,14 +572,10 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
         l_run += all.x + all.y;
       }
       if (!empty) ++items;
-      if (!ok) break;
       // ---- epilogue: O, or its part, of this group's rows
       const bool any = g1 > g0;
-      if (any && !wait(gbar(w, 2), (q - 1) & 1)) ok = false;
-      if (__any_sync(0xffffffffu, !ok)) {
-        ok = false;
-        break;
-      }
+      if (any && !wait(gbar(w, 2), (q - 1) & 1)) give_up(abort_flag, a.status);
+      if (__any_sync(0xffffffffu, *abort_flag != 0)) break;  // nothing is written out after that
       ptx::tc_fence_after();
       const int u = unit(), g = u % a.h_k;
       const PromptItem it = load_item(u);
@@ -646,7 +633,6 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
         }
       }
     }
-    if (!ok && lane == 0) give_up(abort_flag, a.status);
   }
 
   ptx::tc_fence_before();

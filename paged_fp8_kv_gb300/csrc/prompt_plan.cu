@@ -165,6 +165,13 @@ __global__ void __launch_bounds__(kThreads) prompt_plan_kernel(const PromptPlanD
           it.t0 = t0 + static_cast<int>(static_cast<long long>(kt) * s / pieces);
           it.t1 = t0 + static_cast<int>(static_cast<long long>(kt) * (s + 1) / pieces);
           it.part = cut ? p0 + s : -1;
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            int g0, g1;
+            prompt_tiles(it.len, it.n_tok, a.h_r, it.row0 + w * kPromptRows / 2, kPromptRows / 2, a.causal, a.window, &g0, &g1);
+            it.g0[w] = max(g0, it.t0);
+            it.g1[w] = max(min(g1, it.t1), it.g0[w]);
+          }
           a.scratch[at + s] = it;
           if (at + s < kPromptSortMax)
             keys[at + s] = (static_cast<uint64_t>(0x7FFFFFFF - (it.t1 - it.t0)) << 32) | static_cast<uint32_t>(at + s);

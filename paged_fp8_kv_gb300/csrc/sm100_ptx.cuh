@@ -102,6 +102,19 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
   }
 }
 
+// The same bound by a number of tries, each of which the hardware may suspend
+// for about 2 us: less code around the case that the phase is complete already,
+// for kernels whose waits are many (14 cycles for 79 there).
+__device__ __forceinline__ bool mbar_wait_tries(uint32_t bar, uint32_t parity, volatile int* abort, int tries) {
+  if (mbar_try_wait(bar, parity)) return true;
+#pragma unroll 1
+  for (int i = 0; i < tries; ++i) {
+    if (mbar_try_wait_hint(bar, parity, 2000)) return true;
+    if (*abort) return false;
+  }
+  return false;
+}
+
 // ----------------------------------------------------------------------- TMA
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint32_t bar, int c0, int c1, int c2,

@@ -63,14 +63,15 @@ constexpr float kTau = 8.f;
 template <bool kQe4m3>
 struct Cfg {
   static constexpr int kParts = kQe4m3 ? 1 : 2;
-  static constexpr int kSK = kQe4m3 ? 4 : 3, kSV = kQe4m3 ? 4 : 3;  // K and raw V rings
+  static constexpr int kSK = kQe4m3 ? 4 : 3, kSV = kQe4m3 ? 3 : 2;  // K and raw V rings
   static constexpr int kOffK = 0;
   static constexpr int kOffV = kOffK + kSK * kTile;
   static constexpr int kOffVf = kOffV + kSV * kTile;
   static constexpr int kOffQ = kOffVf + kVf * kVfTile;           // [group][part]
-  static constexpr int kOffShift = kOffQ + 2 * kParts * kTile;   // [2][256] s of each row
+  static constexpr int kOffOut = kOffQ + 2 * kParts * kTile;     // [softmax warp] 32 rows x 64 bytes of O on their way out
+  static constexpr int kOffShift = kOffOut + 8 * 2048;           // [group][2][128] s of each row
   static constexpr int kOffBar = kOffShift + 2 * 256;
-  static constexpr int kBars = 2 * (kSK + kSV + kVf) + 3 + 4 * 2 + 1;
+  static constexpr int kBars = 2 * (kSK + kSV + kVf) + 1 + 6 * 2 + 1;
   static constexpr int kOffMisc = kOffBar + kBars * 8;
   static constexpr int kBytes = kOffMisc + 16 + 1024;
   static_assert(kBytes <= 232448, "shared memory");
@@ -125,11 +126,11 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
   auto ffull = [&](int s) { return bar0 + 8u * (2 * SK + 2 * SV + s); };   // converted V
   auto fempty = [&](int s) { return bar0 + 8u * (2 * SK + 2 * SV + kVf + s); };
   constexpr int kB = 2 * (SK + SV + kVf);
-  const uint32_t qfull = bar0 + 8u * kB, qempty = qfull + 8u, sread = qfull + 16u;
+  const uint32_t sread = bar0 + 8u * kB;  // either group's scores read
   // of each group: 0 scores written, 1 P written, 2 a tile's product done, 3 O
-  // read out (sread: either group's scores read)
-  auto gbar = [&](int w, int k) { return bar0 + 8u * (kB + 3 + 4 * w + k); };
-  const uint32_t drain = bar0 + 8u * (kB + 11);
+  // read out, 4 Q laid out, 5 Q read
+  auto gbar = [&](int w, int k) { return bar0 + 8u * (kB + 1 + 6 * w + k); };
+  const uint32_t drain = bar0 + 8u * (kB + 13);
 
   if (tid == 0) {
     for (int s = 0; s < SK; ++s) {
@@ -144,11 +145,9 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
       ptx::mbar_init(ffull(s), 4);
       ptx::mbar_init(fempty(s), 1);
     }
-    ptx::mbar_init(qfull, 4);
-    ptx::mbar_init(qempty, 1);
     ptx::mbar_init(sread, 4);
     for (int w = 0; w < 2; ++w) {
-      for (int k = 0; k < 4; ++k) ptx::mbar_init(gbar(w, k), k == 1 || k == 3 ? 4 : 1);
+      for (int k = 0; k < 6; ++k) ptx::mbar_init(gbar(w, k), k == 1 || k == 3 || k == 4 ? 4 : 1);
     }
     ptx::mbar_init(drain, 1);
     *abort_flag = 0;
@@ -178,10 +177,17 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
     return it;
   };
   // A warpgroup's share of the launch's 512 x 128 registers: 2 x 192 + 80 + 48
-  // = 4 x 128 (the softmax threads hold 128 scores).
+  // = 4 x 128 (the softmax threads hold 128 scores).  All four warps of a
+  // warpgroup execute the same instruction.
+  if (warp >= kMmaWarp)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+  else if (warp >= kConvWarp)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+  else
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+
   if (warp >= kKWarp) {
     // ------------------------------------------------------------- TMA loads
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     const bool is_k = warp == kKWarp;
     const int NS = is_k ? SK : SV;
     const uint32_t ring = sbase + (is_k ? C::kOffK : C::kOffV);
@@ -234,7 +240,6 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
     }
   } else if (warp >= kMmaWarp) {
     // ------------------------------------------------------------------- MMA
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     // One warp issues everything, in the order S_0(t), O_0(t - 1), S_1(t),
     // O_1(t - 1): a group's O product runs while its new scores are read, after
     // which the other group's scores take their place.  The whole warp goes
@@ -252,8 +257,8 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
       // V, d-major: 64 elements of d a 128-byte row, the other 64 a tile half further
       const uint64_t vdesc = ptx::smem_desc(sbase + C::kOffVf, kTile, 1024, ptx::kSwizzle128B);
       uint32_t ks = 0, kph = 0, vs = 0, vph = 0;  // stage and phase of the next K and converted V tile
-      uint32_t qph = 0, sph = 1;                  // of Q, and of the scores read (none to wait for at first)
-      uint32_t pph = 0, oph = 3;                  // bit w: of group w's P, and of its O read out (likewise)
+      uint32_t sph = 1;                           // of the scores read (none to wait for at first)
+      uint32_t qph = 0, pph = 0, oph = 3;         // bit w: of group w's Q, its P, and its O read out (likewise)
       for (int k = 0; unit_at(k) < units; ++k) {
         const PromptItem it = load_item(unit_at(k));
         const int t0 = __shfl_sync(0xffffffffu, it.t0, 0), t1 = __shfl_sync(0xffffffffu, it.t1, 0);
@@ -265,8 +270,6 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
           g1[w] = __shfl_sync(0xffffffffu, it.g1[w], 0);
         }
         bool ok = true;
-        if (leader) ok = wait(qfull, qph);
-        qph ^= 1;
         for (int t = t0; t <= t1; ++t) {  // scores of tile t, O of tile t - 1
           const uint64_t kd = kdesc + ks * (kTile >> 4), vd = vdesc + vs * (kVfTile >> 4);
           const bool load_k = t < t1, load_v = t > t0;
@@ -275,6 +278,7 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
           for (int w = 0; w < 2; ++w) {
             if (t >= g0[w] && t < g1[w]) {
               if (leader) {
+                if (t == g0[w]) ok &= wait(gbar(w, 4), (qph >> w) & 1);
                 ok &= wait(sread, sph);
                 ptx::tc_fence_after();
 #pragma unroll
@@ -284,13 +288,14 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
                     ptx::mma_e4m3(tm, qdesc + (w * C::kParts + part) * (kTile >> 4) + 2 * kk, kd + 2 * kk, idesc_s,
                                   kk > 0 || part > 0);
                 ptx::mma_commit(gbar(w, 0));
+                if (t + 1 == g1[w]) ptx::mma_commit(gbar(w, 5));  // the item's Q is read
               }
+              __syncwarp();
               sph ^= 1;
+              if (t == g0[w]) qph ^= 1u << w;
             }
-            if (w == 1 && load_k && leader) {
-              ptx::mma_commit(kempty(ks));
-              if (t + 1 == t1) ptx::mma_commit(qempty);  // the item's Q is read
-            }
+            if (w == 1 && load_k && leader) ptx::mma_commit(kempty(ks));
+            __syncwarp();
             if (t > g0[w] && t <= g1[w]) {
               const uint32_t more = t > g0[w] + 1;
               if (leader) {
@@ -303,11 +308,13 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
                   mma_f16_ts(tm + o_col(w), tm + p_col(w) + 8 * kk, vd + 128 * kk, idesc_o, kk > 0 ? 1u : more);
                 ptx::mma_commit(gbar(w, 2));
               }
+              __syncwarp();
               pph ^= 1u << w;
               if (!more) oph ^= 1u << w;
             }
           }
-          if (load_v && leader) ptx::mma_commit(fempty(vs));  // (tiles past a group's are the other's)
+          if (load_v && leader) ptx::mma_commit(fempty(vs));
+          __syncwarp();
           if (load_k && ++ks == SK) {
             ks = 0;
             kph ^= 1;
@@ -329,51 +336,59 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
     }
   } else if (warp >= kConvWarp) {
     // ------------------------------------------------ Q and V conversion
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     const int cw = warp - kConvWarp;
-    int n = 0, items = 0;
+    int n = 0;
+    uint32_t q_items[2] = {0, 0};  // items of each group
     bool ok = true;
     for (int k = 0; ok && unit_at(k) < units; ++k) {
       const int u = unit_at(k), g = u % a.h_k;
       const PromptItem it = load_item(u);
       if (it.t1 <= it.t0) continue;
-      // ---- Q: this warp lays out 64 of the 256 rows, the lanes of a load
+      // ---- Q: this warp lays out 32 of a group's 128 rows, the lanes of a load
       // side by side in a row (16, or 8 of e4m3)
-      {
-        constexpr int kLanes = kQe4m3 ? 8 : 16;
-        constexpr int kPer = 32 / kLanes;       // rows a load
-        constexpr int kLoads = 64 / kPer;
-        constexpr int kBatch = 8;               // loads in flight
-        const int piece = lane % kLanes;
+      constexpr int kLanes = kQe4m3 ? 8 : 16;
+      constexpr int kPer = 32 / kLanes;  // rows a load
+      constexpr int kLoads = 32 / kPer;
+      constexpr int kBatch = 8;          // loads in flight
+      const int piece = lane % kLanes;
+#pragma unroll 1
+      for (int w = 0; w < 2; ++w) {
+        if ((w ? it.g1[1] : it.g1[0]) <= (w ? it.g0[1] : it.g0[0])) continue;
+        const int r0 = cw * 32 + lane / kLanes;  // this lane's rows of the group: r0, r0 + kPer, ..
+        int row = it.row0 + w * kRows + r0;
         const int rows = it.n_tok * a.h_r;
-        uint4 raw[kBatch];
-        auto load = [&](int l0) {
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i) {
-            const int row = it.row0 + cw * 64 + (l0 + i) * kPer + lane / kLanes;
-            raw[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (row < rows) {
-              const int tok = row / a.h_r;
-              const int64_t at = prompt_at(a.q_rows, it.b, it.tok0 + tok, g, row - tok * a.h_r);
-              raw[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.q) + at * (kQe4m3 ? 1 : 2)) + piece);
-            }
-          }
-        };
-        load(0);
-        if (items > 0 && !wait(qempty, (items - 1) & 1)) ok = false;
-        if (__any_sync(0xffffffffu, !ok)) {
-          ok = false;
-          break;
-        }
-        int8_t* const shifts = q_shift + (items & 1) * 256;
+        int tok = row / a.h_r, hr = row - tok * a.h_r;
+        const uint8_t* const base = static_cast<const uint8_t*>(a.q) + piece * 16;
+        const uint32_t turn = w ? q_items[1]++ : q_items[0]++;
+        int8_t* const shifts = q_shift + (2 * w + (turn & 1)) * 128;
+        uint8_t* const part = sm + C::kOffQ + w * C::kParts * kTile;
 #pragma unroll 1
         for (int l0 = 0; l0 < kLoads; l0 += kBatch) {
-          if (l0 > 0) load(l0);
+          uint4 raw[kBatch];
 #pragma unroll
           for (int i = 0; i < kBatch; ++i) {
-            const int r256 = cw * 64 + (l0 + i) * kPer + lane / kLanes;
-            uint8_t* const part = sm + C::kOffQ + (r256 >> 7) * C::kParts * kTile;
-            const int r = r256 & 127;
+            raw[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (row < rows) {
+              const int64_t at = prompt_at(a.q_rows, it.b, it.tok0 + tok, g, hr);
+              raw[i] = __ldg(reinterpret_cast<const uint4*>(base + at * (kQe4m3 ? 1 : 2)));
+            }
+            row += kPer;
+            hr += kPer;
+            while (hr >= a.h_r) {
+              hr -= a.h_r;
+              ++tok;
+            }
+          }
+          if (l0 == 0) {
+            if (turn > 0 && !wait(gbar(w, 5), (turn - 1) & 1)) ok = false;
+            if (__any_sync(0xffffffffu, !ok)) {
+              ok = false;
+              break;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const int r = r0 + (l0 + i) * kPer;
             if constexpr (kQe4m3) {
               *reinterpret_cast<uint4*>(part + swz(r, piece)) = raw[i];
             } else {
@@ -405,14 +420,30 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
               const uint32_t at = swz(r, piece >> 1) + (piece & 1) * 8;
               *reinterpret_cast<uint2*>(part + at) = make_uint2(hw[0], hw[1]);
               *reinterpret_cast<uint2*>(part + kTile + at) = make_uint2(lw[0], lw[1]);
-              if (piece == 0) shifts[r256] = static_cast<int8_t>(shift);
+              if (piece == 0) shifts[r] = static_cast<int8_t>(shift);
             }
           }
         }
+        if (!ok) break;
         ptx::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(qfull);
-        ++items;
+        if (lane == 0) ptx::mbar_arrive(gbar(w, 4));
+      }
+      if (!ok) break;
+      // the next item's Q is on its way to L2 meanwhile
+      if (unit_at(k + 1) < units) {
+        const int u2 = unit_at(k + 1);
+        const PromptItem nx = load_item(u2);
+        constexpr int kLines = kQe4m3 ? 1 : 2;  // of 128 bytes a row
+#pragma unroll 1
+        for (int i = cw * 32 + lane; i < kPromptRows * kLines; i += 128) {
+          const int row = nx.row0 + i / kLines, tok = row / a.h_r;
+          if (row < nx.n_tok * a.h_r) {
+            const int64_t at = prompt_at(a.q_rows, nx.b, nx.tok0 + tok, u2 % a.h_k, row - tok * a.h_r);
+            const uint8_t* const line = static_cast<const uint8_t*>(a.q) + at * (kQe4m3 ? 1 : 2) + (i % kLines) * 128;
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(line));
+          }
+        }
       }
       // ---- V tiles: this warp turns 32 keys, four rows a load, 16 codes a lane
       for (int t = it.t0; t < it.t1; ++t, ++n) {
@@ -457,13 +488,12 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
     if (!ok && lane == 0) give_up(abort_flag, a.status);
   } else {
     // --------------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     const int w = warp >> 2;
     const int quarter = warp & 3;
     const int r = quarter * 32 + lane;  // row of the group = TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t ts = tmem + lane_off, tp = ts + p_col(w), to = ts + o_col(w);
-    int q = 0, items = 0;  // tiles, items
+    int q = 0, items = 0;  // the group's tiles and items
     // a wait that gives up sets the abort flag and the loop runs on (later waits
     // return at once), so that a warp's lanes stay together
     for (int k = 0; unit_at(k) < units; ++k) {
@@ -475,12 +505,10 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
         return u;
       };
       int g0 = 0, g1 = 0, lo = 0, lim = INT32_MAX;  // the group's tiles; the row sees keys lo .. lim
-      bool empty;
       {
         const PromptItem it = load_item(unit());
         g0 = w ? it.g0[1] : it.g0[0];
         g1 = w ? it.g1[1] : it.g1[0];
-        empty = it.t1 <= it.t0;
         const int row = it.row0 + w * kRows + r;  // (rows past the last compute what nobody reads)
         if (row < it.n_tok * a.h_r) {
           const int tok = row / a.h_r;
@@ -497,7 +525,7 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
         if (t == g0) {  // the row's scale is there since its Q was laid out
           const int u = unit(), g = u % a.h_k, b = a.items[u / a.h_k].b;
           float raw_l = a.softmax_scale * a.qd[b * a.qd_seq + g * a.qd_head] * a.kd[b * a.kd_seq + g * a.kd_head];
-          if constexpr (!kQe4m3) raw_l *= __uint_as_float(static_cast<uint32_t>(127 - q_shift[(items & 1) * 256 + w * kRows + r]) << 23);
+          if constexpr (!kQe4m3) raw_l *= __uint_as_float(static_cast<uint32_t>(127 - q_shift[(2 * w + (items & 1)) * 128 + r]) << 23);
           if constexpr (kCap)  // scores become logits in log2 units as they are read
             cap_c1 = raw_l / a.softcap;
           else
@@ -571,7 +599,7 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
         const float2 all = add2(add2(sum2[0], sum2[1]), add2(sum2[2], sum2[3]));
         l_run += all.x + all.y;
       }
-      if (!empty) ++items;
+      if (g1 > g0) ++items;
       // ---- epilogue: O, or its part, of this group's rows
       const bool any = g1 > g0;
       if (any && !wait(gbar(w, 2), (q - 1) & 1)) give_up(abort_flag, a.status);
@@ -589,34 +617,59 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
       const float f = a.vd[it.b * a.vd_seq + g * a.vd_head] * (1.f / 128.f) * (final_out ? a.scale_o / (seen ? l : 1.f) : 1.f);
       const int64_t part_row = (static_cast<int64_t>(it.part) * a.h_k + g) * kPromptRows + w * kRows + r;
       const int64_t orow = final_out ? prompt_at(a.o_rows, it.b, it.tok0 + tok, g, hr) : part_row * kHeadDimDev;
+      // A lane holds a row; the rows leave through shared memory, 64 bytes of each
+      // at a time, as pieces of four lanes (16 bytes a lane and row would be 32
+      // half-used sectors an instruction): 16-byte chunk c of row i at chunk
+      // c ^ (i / 2 % 4) of its 64 bytes
+      uint8_t* const out = sm + C::kOffOut + warp * 2048;
+      uint8_t* const mine = out + lane * 64;
+      uint8_t* dst[4];
+      bool on[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = 8 * j + (lane >> 2);
+        const int64_t at = __shfl_sync(0xffffffffu, orow, i);
+        on[j] = __shfl_sync(0xffffffffu, static_cast<int>(live), i) != 0;
+        dst[j] = (final_out ? reinterpret_cast<uint8_t*>(a.o + at) : reinterpret_cast<uint8_t*>(a.o_part + at)) + (lane & 3) * 16;
+      }
+      const int cols = final_out ? 32 : 16;  // of 64 bytes
 #pragma unroll 1
-      for (int h0 = 0; h0 < kRows; h0 += 32) {
-        uint32_t o[32];
-        if (any) {
-          MJ_TMEM_LD16(to + h0, o);
-          MJ_TMEM_LD16(to + h0 + 16, (o + 16));
-          ptx::tmem_ld_wait();
-        }
-        if (!live) continue;
+      for (int h0 = 0; h0 < kRows; h0 += cols) {
         float x[32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) x[e] = any && seen ? __uint_as_float(o[e]) * f : 0.f;
-        if (final_out) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            uint32_t b4[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const __nv_bfloat162 v = __floats2bfloat162_rn(x[e + 2 * i], x[e + 2 * i + 1]);
-              b4[i] = *reinterpret_cast<const uint32_t*>(&v);
+        for (int c = 0; c < 32; c += 16) {
+          if (c < cols) {
+            uint32_t o[16];
+            if (any) {
+              MJ_TMEM_LD16(to + h0 + c, o);
+              ptx::tmem_ld_wait();
             }
-            *reinterpret_cast<uint4*>(a.o + orow + h0 + e) = make_uint4(b4[0], b4[1], b4[2], b4[3]);
-          }
-        } else {
 #pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<float4*>(a.o_part + orow + h0 + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+            for (int e = 0; e < 16; ++e) x[c + e] = any && seen ? __uint_as_float(o[e]) * f : 0.f;
+          }
         }
+        uint4 v[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t b4[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 y = __floats2bfloat162_rn(x[8 * c + 2 * i], x[8 * c + 2 * i + 1]);
+            b4[i] = final_out ? *reinterpret_cast<const uint32_t*>(&y) : __float_as_uint(x[4 * c + i]);
+          }
+          v[c] = make_uint4(b4[0], b4[1], b4[2], b4[3]);
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4*>(mine + ((c ^ ((lane >> 1) & 3)) << 4)) = v[c];
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int i = 8 * j + (lane >> 2);
+          const uint4 y = *reinterpret_cast<const uint4*>(out + i * 64 + (((lane & 3) ^ ((i >> 1) & 3)) << 4));
+          if (on[j]) *reinterpret_cast<uint4*>(dst[j]) = y;
+          dst[j] += 64;
+        }
+        __syncwarp();
       }
       if (any) {
         ptx::tc_fence_before();

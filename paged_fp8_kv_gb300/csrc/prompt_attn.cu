@@ -176,15 +176,15 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
     for (int i = 0; i < 3; ++i) reinterpret_cast<int4*>(&it)[i] = src[i];
     return it;
   };
-  // A warpgroup's share of the launch's 512 x 128 registers: 2 x 192 + 80 + 48
+  // A warpgroup's share of the launch's 512 x 128 registers: 2 x 184 + 88 + 56
   // = 4 x 128 (the softmax threads hold 128 scores).  All four warps of a
   // warpgroup execute the same instruction.
   if (warp >= kMmaWarp)
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
   else if (warp >= kConvWarp)
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   else
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
 
   if (warp >= kKWarp) {
     // ------------------------------------------------------------- TMA loads
@@ -256,6 +256,18 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
       const uint64_t kdesc = ptx::smem_desc(sbase + C::kOffK, 16, 1024, ptx::kSwizzle128B);
       // V, d-major: 64 elements of d a 128-byte row, the other 64 a tile half further
       const uint64_t vdesc = ptx::smem_desc(sbase + C::kOffVf, kTile, 1024, ptx::kSwizzle128B);
+      auto scores = [&](int w, uint64_t kd) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+          for (int part = 0; part < C::kParts; ++part)
+            ptx::mma_e4m3(tm, qdesc + (w * C::kParts + part) * (kTile >> 4) + 2 * kk, kd + 2 * kk, idesc_s, kk > 0 || part > 0);
+      };
+      auto output = [&](int w, uint64_t vd, uint32_t more) {
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)  // 16 keys: 8 columns of P, 16 rows of V
+          mma_f16_ts(tm + o_col(w), tm + p_col(w) + 8 * kk, vd + 128 * kk, idesc_o, kk > 0 ? 1u : more);
+      };
       uint32_t ks = 0, kph = 0, vs = 0, vph = 0;  // stage and phase of the next K and converted V tile
       uint32_t sph = 1;                           // of the scores read (none to wait for at first)
       uint32_t qph = 0, pph = 0, oph = 3;         // bit w: of group w's Q, its P, and its O read out (likewise)
@@ -270,10 +282,46 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
           g1[w] = __shfl_sync(0xffffffffu, it.g1[w], 0);
         }
         bool ok = true;
+        const int t_all = (g0[0] > g0[1] ? g0[0] : g0[1]) + 1, t_end = (g1[0] < g1[1] ? g1[0] : g1[1]) - 1;
         for (int t = t0; t <= t1; ++t) {  // scores of tile t, O of tile t - 1
           const uint64_t kd = kdesc + ks * (kTile >> 4), vd = vdesc + vs * (kVfTile >> 4);
+          // Most tiles: all four products, none of them an item's first or last.
+          // (The instructions between two products are on the critical path.)
+          if (t > t_all && t < t_end) {
+            const uint32_t kf = kfull(ks), ke = kempty(ks), vf = ffull(vs), ve = fempty(vs);
+            const uint32_t p0 = pph & 1, p1 = pph >> 1;
+            const uint32_t ks_next = ks + 1 == SK ? 0 : ks + 1, vs_next = vs + 1 == kVf ? 0 : vs + 1;
+            if (leader) {
+              ok &= wait(kf, kph) & wait(sread, sph);
+              ptx::tc_fence_after();
+              scores(0, kd);
+              ptx::mma_commit(gbar(0, 0));
+              ok &= wait(vf, vph) & wait(gbar(0, 1), p0);
+              ptx::tc_fence_after();
+              output(0, vd, 1u);
+              ptx::mma_commit(gbar(0, 2));
+              ok &= wait(sread, sph ^ 1);
+              ptx::tc_fence_after();
+              scores(1, kd);
+              ptx::mma_commit(gbar(1, 0));
+              ptx::mma_commit(ke);
+              ok &= wait(gbar(1, 1), p1);
+              ptx::tc_fence_after();
+              output(1, vd, 1u);
+              ptx::mma_commit(gbar(1, 2));
+              ptx::mma_commit(ve);
+            }
+            __syncwarp();
+            pph ^= 3;
+            kph ^= ks_next == 0;
+            vph ^= vs_next == 0;
+            ks = ks_next;
+            vs = vs_next;
+            continue;
+          }
           const bool load_k = t < t1, load_v = t > t0;
           if (load_k && leader) ok &= wait(kfull(ks), kph);
+          __syncwarp();
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
             if (t >= g0[w] && t < g1[w]) {
@@ -281,12 +329,7 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
                 if (t == g0[w]) ok &= wait(gbar(w, 4), (qph >> w) & 1);
                 ok &= wait(sread, sph);
                 ptx::tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-                  for (int part = 0; part < C::kParts; ++part)
-                    ptx::mma_e4m3(tm, qdesc + (w * C::kParts + part) * (kTile >> 4) + 2 * kk, kd + 2 * kk, idesc_s,
-                                  kk > 0 || part > 0);
+                scores(w, kd);
                 ptx::mma_commit(gbar(w, 0));
                 if (t + 1 == g1[w]) ptx::mma_commit(gbar(w, 5));  // the item's Q is read
               }
@@ -303,9 +346,7 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
                 ok &= wait(gbar(w, 1), (pph >> w) & 1);
                 if (!more) ok &= wait(gbar(w, 3), (oph >> w) & 1);  // O read out
                 ptx::tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk)  // 16 keys: 8 columns of P, 16 rows of V
-                  mma_f16_ts(tm + o_col(w), tm + p_col(w) + 8 * kk, vd + 128 * kk, idesc_o, kk > 0 ? 1u : more);
+                output(w, vd, more);
                 ptx::mma_commit(gbar(w, 2));
               }
               __syncwarp();

@@ -385,115 +385,11 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
       const int u = unit_at(k), g = u % a.h_k;
       const PromptItem it = load_item(u);
       if (it.t1 <= it.t0) continue;
-      // ---- Q: this warp lays out 32 of a group's 128 rows, the lanes of a load
-      // side by side in a row (16, or 8 of e4m3)
-      constexpr int kLanes = kQe4m3 ? 8 : 16;
-      constexpr int kPer = 32 / kLanes;  // rows a load
-      constexpr int kLoads = 32 / kPer;
-      constexpr int kBatch = 8;          // loads in flight
-      const int piece = lane % kLanes;
-#pragma unroll 1
-      for (int w = 0; w < 2; ++w) {
-        if ((w ? it.g1[1] : it.g1[0]) <= (w ? it.g0[1] : it.g0[0])) continue;
-        const int r0 = cw * 32 + lane / kLanes;  // this lane's rows of the group: r0, r0 + kPer, ..
-        int row = it.row0 + w * kRows + r0;
-        const int rows = it.n_tok * a.h_r;
-        int tok = row / a.h_r, hr = row - tok * a.h_r;
-        const uint8_t* const base = static_cast<const uint8_t*>(a.q) + piece * 16;
-        const uint32_t turn = w ? q_items[1]++ : q_items[0]++;
-        int8_t* const shifts = q_shift + (2 * w + (turn & 1)) * 128;
-        uint8_t* const part = sm + C::kOffQ + w * C::kParts * kTile;
-#pragma unroll 1
-        for (int l0 = 0; l0 < kLoads; l0 += kBatch) {
-          uint4 raw[kBatch];
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i) {
-            raw[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (row < rows) {
-              const int64_t at = prompt_at(a.q_rows, it.b, it.tok0 + tok, g, hr);
-              raw[i] = __ldg(reinterpret_cast<const uint4*>(base + at * (kQe4m3 ? 1 : 2)));
-            }
-            row += kPer;
-            hr += kPer;
-            while (hr >= a.h_r) {
-              hr -= a.h_r;
-              ++tok;
-            }
-          }
-          if (l0 == 0) {
-            if (turn > 0 && !wait(gbar(w, 5), (turn - 1) & 1)) ok = false;
-            if (__any_sync(0xffffffffu, !ok)) {
-              ok = false;
-              break;
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i) {
-            const int r = r0 + (l0 + i) * kPer;
-            if constexpr (kQe4m3) {
-              *reinterpret_cast<uint4*>(part + swz(r, piece)) = raw[i];
-            } else {
-              // the row's largest |q| goes to [128, 256): hi + lo then hold
-              // every bit of an element down to 2^-9 of it, and 2^-18 of it below
-              const uint32_t v4[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-              uint32_t top = 0;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) top = max(top, max(v4[e] & 0x7FFFu, (v4[e] >> 16) & 0x7FFFu));
-#pragma unroll
-              for (int o = 8; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-              int shift = 134 - static_cast<int>(top >> 7);  // 7 - exponent
-              shift = top == 0 ? 0 : (shift > 126 ? 126 : (shift < -126 ? -126 : shift));
-              const float qs = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
-              uint32_t hw[2], lw[2];
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                float x[4], f[4];
-                x[0] = __uint_as_float(v4[2 * h] << 16) * qs;
-                x[1] = __uint_as_float(v4[2 * h] & 0xFFFF0000u) * qs;
-                x[2] = __uint_as_float(v4[2 * h + 1] << 16) * qs;
-                x[3] = __uint_as_float(v4[2 * h + 1] & 0xFFFF0000u) * qs;
-                hw[h] = static_cast<uint32_t>(ptx::f32x2_to_e4m3x2(x[0], x[1])) |
-                        (static_cast<uint32_t>(ptx::f32x2_to_e4m3x2(x[2], x[3])) << 16);
-                e4m3x4_to_f32(hw[h], f);
-                lw[h] = static_cast<uint32_t>(ptx::f32x2_to_e4m3x2(x[0] - f[0], x[1] - f[1])) |
-                        (static_cast<uint32_t>(ptx::f32x2_to_e4m3x2(x[2] - f[2], x[3] - f[3])) << 16);
-              }
-              const uint32_t at = swz(r, piece >> 1) + (piece & 1) * 8;
-              *reinterpret_cast<uint2*>(part + at) = make_uint2(hw[0], hw[1]);
-              *reinterpret_cast<uint2*>(part + kTile + at) = make_uint2(lw[0], lw[1]);
-              if (piece == 0) shifts[r] = static_cast<int8_t>(shift);
-            }
-          }
-        }
-        if (!ok) break;
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(gbar(w, 4));
-      }
-      if (!ok) break;
-      // the next item's Q is on its way to L2 meanwhile
-      if (unit_at(k + 1) < units) {
-        const int u2 = unit_at(k + 1);
-        const PromptItem nx = load_item(u2);
-        constexpr int kLines = kQe4m3 ? 1 : 2;  // of 128 bytes a row
-#pragma unroll 1
-        for (int i = cw * 32 + lane; i < kPromptRows * kLines; i += 128) {
-          const int row = nx.row0 + i / kLines, tok = row / a.h_r;
-          if (row < nx.n_tok * a.h_r) {
-            const int64_t at = prompt_at(a.q_rows, nx.b, nx.tok0 + tok, u2 % a.h_k, row - tok * a.h_r);
-            const uint8_t* const line = static_cast<const uint8_t*>(a.q) + at * (kQe4m3 ? 1 : 2) + (i % kLines) * 128;
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(line));
-          }
-        }
-      }
-      // ---- V tiles: this warp turns 32 keys, four rows a load, 16 codes a lane
-      for (int t = it.t0; t < it.t1; ++t, ++n) {
+      // ---- a V tile: this warp turns 32 keys, four rows a load, 16 codes a lane
+      auto convert = [&](int t) {
         const int st = n % SV, vf = n % kVf;
         if (!wait(vfull(st), (n / SV) & 1) || (n >= kVf && !wait(fempty(vf), ((n / kVf) - 1) & 1))) ok = false;
-        if (__any_sync(0xffffffffu, !ok)) {
-          ok = false;
-          break;
-        }
+        if (__any_sync(0xffffffffu, !ok)) return false;
         const uint8_t* const src = sm + C::kOffV + st * kTile;
         uint8_t* const dst = sm + C::kOffVf + vf * kVfTile;
         const int cc = lane & 7;
@@ -524,7 +420,125 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
           ptx::mbar_arrive(ffull(vf));
           ptx::mbar_arrive(vempty(st));
         }
+        ++n;
+        return true;
+      };
+      // The first tile's buffer is free before the last item's Q is read; the
+      // others' V after this item's Q.
+      ok = convert(it.t0);
+      if (!ok) break;
+      // ---- Q: this warp lays out 32 of a group's 128 rows, eight lanes a row
+      // (a lane 16 elements: one 16-byte chunk of each part), four rows a turn
+      constexpr int kVecs = kQe4m3 ? 1 : 2;  // 16-byte loads a lane and row
+      constexpr int kBatch = 4;              // turns in flight
+      const int piece = lane & 7;
+#pragma unroll 1
+      for (int w = 0; w < 2; ++w) {
+        if ((w ? it.g1[1] : it.g1[0]) <= (w ? it.g0[1] : it.g0[0])) continue;
+        const int r0 = cw * 32 + (lane >> 3);  // this lane's rows of the group: r0, r0 + 4, ..
+        const int first = it.row0 + w * kRows + r0;
+        int left = it.n_tok * a.h_r - first;  // rows there are from this one on
+        const int tok = first / a.h_r;
+        int hr = first - tok * a.h_r;
+        constexpr int kEl = kQe4m3 ? 1 : 2;
+        // (a lane without a row of its own reads the item's first one)
+        const uint8_t* const valid = static_cast<const uint8_t*>(a.q) + piece * 16 * kEl +
+                                     prompt_at(a.q_rows, it.b, it.tok0 + it.row0 / a.h_r, g, it.row0 % a.h_r) * kEl;
+        const uint8_t* at = static_cast<const uint8_t*>(a.q) + piece * 16 * kEl + prompt_at(a.q_rows, it.b, it.tok0 + tok, g, hr) * kEl;
+        const int64_t step_h = 4 * a.q_rows.s_h * kEl, step_t = (a.q_rows.s_tok - a.h_r * a.q_rows.s_h) * kEl;
+        const uint32_t turn = w ? q_items[1]++ : q_items[0]++;
+        int8_t* const shifts = q_shift + (2 * w + (turn & 1)) * 128;
+        uint8_t* const part = sm + C::kOffQ + w * C::kParts * kTile;
+#pragma unroll 1
+        for (int l0 = 0; l0 < 8; l0 += kBatch) {
+          uint4 raw[kBatch][kVecs];
+          uint32_t there = 0;
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const uint4* const src = reinterpret_cast<const uint4*>(left > 0 ? at : valid);
+#pragma unroll
+            for (int v = 0; v < kVecs; ++v) raw[i][v] = __ldg(src + v);
+            there |= (left > 0 ? 1u : 0u) << i;
+            left -= 4;
+            at += step_h;
+            for (hr += 4; hr >= a.h_r; hr -= a.h_r) at += step_t;
+          }
+          if (l0 == 0) {
+            if (turn > 0 && !wait(gbar(w, 5), (turn - 1) & 1)) ok = false;
+            if (__any_sync(0xffffffffu, !ok)) {
+              ok = false;
+              break;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const int r = r0 + (l0 + i) * 4;
+            const uint32_t keep = (there >> i) & 1u ? 0xFFFFFFFFu : 0u;
+#pragma unroll
+            for (int v = 0; v < kVecs; ++v)
+              raw[i][v] = make_uint4(raw[i][v].x & keep, raw[i][v].y & keep, raw[i][v].z & keep, raw[i][v].w & keep);
+            if constexpr (kQe4m3) {
+              *reinterpret_cast<uint4*>(part + swz(r, piece)) = raw[i][0];
+            } else {
+              // the row's largest |q| goes to [128, 256).  Half precision then
+              // holds every element's 8 bits down to 2^-22 of it; hi = e4m3(x),
+              // lo = e4m3(x - hi), the difference exact: hi + lo is within 2^-10
+              const uint32_t v8[8] = {raw[i][0].x, raw[i][0].y, raw[i][0].z, raw[i][0].w,
+                                      raw[i][kVecs - 1].x, raw[i][kVecs - 1].y, raw[i][kVecs - 1].z, raw[i][kVecs - 1].w};
+              uint32_t top = 0;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) top = max(top, max(v8[e] & 0x7FFFu, (v8[e] >> 16) & 0x7FFFu));
+#pragma unroll
+              for (int o = 4; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+              int shift = 134 - static_cast<int>(top >> 7);  // 7 - exponent
+              shift = top == 0 ? 0 : (shift > 126 ? 126 : (shift < -126 ? -126 : shift));
+              const float qs = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
+              uint32_t hw[4], lw[4];
+#pragma unroll
+              for (int h = 0; h < 4; ++h) {
+                uint32_t e2[2], l2[2];
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                  const uint32_t z = v8[2 * h + y];
+                  const float2 x = mul2(make_float2(__uint_as_float(z << 16), __uint_as_float(z & 0xFFFF0000u)), make_float2(qs, qs));
+                  const uint32_t x2 = f32x2_to_f16x2(x.x, x.y);
+                  const uint16_t hi = f16x2_to_e4m3x2(x2);
+                  e2[y] = hi;
+                  l2[y] = f16x2_to_e4m3x2(sub_f16x2(x2, e4m3x2_to_f16x2(hi)));
+                }
+                hw[h] = e2[0] | (e2[1] << 16);
+                lw[h] = l2[0] | (l2[1] << 16);
+              }
+              *reinterpret_cast<uint4*>(part + swz(r, piece)) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+              *reinterpret_cast<uint4*>(part + kTile + swz(r, piece)) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+              if (piece == 0) shifts[r] = static_cast<int8_t>(shift);
+            }
+          }
+        }
+        if (!ok) break;
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(gbar(w, 4));
       }
+      if (!ok) break;
+      if (it.t0 + 1 < it.t1) ok = convert(it.t0 + 1);
+      if (!ok) break;
+      // the next item's Q is on its way to L2 meanwhile
+      if (unit_at(k + 1) < units) {
+        const int u2 = unit_at(k + 1);
+        const PromptItem nx = load_item(u2);
+        constexpr int kLines = kQe4m3 ? 1 : 2;  // of 128 bytes a row
+#pragma unroll 1
+        for (int i = cw * 32 + lane; i < kPromptRows * kLines; i += 128) {
+          const int row = nx.row0 + i / kLines, tok = row / a.h_r;
+          if (row < nx.n_tok * a.h_r) {
+            const int64_t at = prompt_at(a.q_rows, nx.b, nx.tok0 + tok, u2 % a.h_k, row - tok * a.h_r);
+            const uint8_t* const line = static_cast<const uint8_t*>(a.q) + at * (kQe4m3 ? 1 : 2) + (i % kLines) * 128;
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(line));
+          }
+        }
+      }
+      for (int t = it.t0 + 2; ok && t < it.t1; ++t) ok = convert(t);
     }
     if (!ok && lane == 0) give_up(abort_flag, a.status);
   } else {
@@ -673,33 +687,7 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
         on[j] = __shfl_sync(0xffffffffu, static_cast<int>(live), i) != 0;
         dst[j] = (final_out ? reinterpret_cast<uint8_t*>(a.o + at) : reinterpret_cast<uint8_t*>(a.o_part + at)) + (lane & 3) * 16;
       }
-      const int cols = final_out ? 32 : 16;  // of 64 bytes
-#pragma unroll 1
-      for (int h0 = 0; h0 < kRows; h0 += cols) {
-        float x[32];
-#pragma unroll
-        for (int c = 0; c < 32; c += 16) {
-          if (c < cols) {
-            uint32_t o[16];
-            if (any) {
-              MJ_TMEM_LD16(to + h0 + c, o);
-              ptx::tmem_ld_wait();
-            }
-#pragma unroll
-            for (int e = 0; e < 16; ++e) x[c + e] = any && seen ? __uint_as_float(o[e]) * f : 0.f;
-          }
-        }
-        uint4 v[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t b4[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 y = __floats2bfloat162_rn(x[8 * c + 2 * i], x[8 * c + 2 * i + 1]);
-            b4[i] = final_out ? *reinterpret_cast<const uint32_t*>(&y) : __float_as_uint(x[4 * c + i]);
-          }
-          v[c] = make_uint4(b4[0], b4[1], b4[2], b4[3]);
-        }
+      auto emit = [&](const uint4 (&v)[4]) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4*>(mine + ((c ^ ((lane >> 1) & 3)) << 4)) = v[c];
         __syncwarp();
@@ -711,6 +699,46 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
           dst[j] += 64;
         }
         __syncwarp();
+      };
+      // (a row that saw no key of the group's tiles has O = 0 there; a group
+      // without tiles has nothing in its columns)
+#pragma unroll 1
+      for (int h0 = 0; h0 < kRows; h0 += 32) {
+        uint32_t o[32];
+        if (any) {
+          MJ_TMEM_LD16(to + h0, o);
+          MJ_TMEM_LD16(to + h0 + 16, (o + 16));
+          ptx::tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0u;
+        }
+        uint4 v[4];
+        if (final_out) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t b4[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const __nv_bfloat162 y = __floats2bfloat162_rn(__uint_as_float(o[8 * c + 2 * i]) * f, __uint_as_float(o[8 * c + 2 * i + 1]) * f);
+              b4[i] = *reinterpret_cast<const uint32_t*>(&y);
+            }
+            v[c] = make_uint4(b4[0], b4[1], b4[2], b4[3]);
+          }
+          emit(v);
+        } else {
+#pragma unroll
+          for (int c0 = 0; c0 < 32; c0 += 16) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t b4[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) b4[i] = __float_as_uint(__uint_as_float(o[c0 + 4 * c + i]) * f);
+              v[c] = make_uint4(b4[0], b4[1], b4[2], b4[3]);
+            }
+            emit(v);
+          }
+        }
       }
       if (any) {
         ptx::tc_fence_before();

@@ -89,6 +89,15 @@ __device__ __forceinline__ bool prompt_plan_fits(const PromptDev& a) {
          h.h_r == a.h_r && h.causal == a.causal && h.window == a.window && h.max_splits == a.max_splits;
 }
 
+// The same kernel over a decode plan's work items (mj_decode_attn_tree above 128
+// rows): packed rows, context keys by ranges, the last keys a drafted tree's.
+// Q, O and LSE rows as above (b, token of q_len, kv head, head of the group);
+// parts as the decode merge reads them.
+struct PromptTreeDev : PromptDev {
+  DecodeTreeDev t;
+  int32_t n_q_tiles;  // of 256 rows
+};
+
 // Keys [first, last] that tokens [i0, i1] of a sequence (n_tok new ones at the
 // end of len keys) see between them; last < first: none.
 __host__ __device__ __forceinline__ void prompt_range(int len, int n_tok, int i0, int i1, int causal, int window,

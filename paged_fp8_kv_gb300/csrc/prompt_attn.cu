@@ -36,6 +36,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "mj_kernels.h"
 #include "prompt.cuh"
 #include "score_mod.cuh"
@@ -95,19 +97,41 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b_de
       : "memory");
 }
 
-template <bool kQe4m3, bool kCap>
+// An item with, for a tree, the keys its sequence's rows see (score_mod.cuh):
+// tile v of the plan's list is the sequence's tile v below the span's prefix
+// tiles, then v + jump.
+struct TreeItem : PromptItem {
+  int4 span;
+  int prefix_tiles, jump;
+};
+
+template <bool kTree>
+__device__ __forceinline__ int tile_key(const std::conditional_t<kTree, TreeItem, PromptItem>& it, int t) {
+  if constexpr (kTree)
+    return (t < it.prefix_tiles ? t : t + it.jump) * kRows;
+  else
+    return t * kRows;
+}
+
+template <bool kQe4m3, bool kCap, bool kTree>
 __global__ void __launch_bounds__(kThreads, 1)
-prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k,
+prompt_attn_kernel(const std::conditional_t<kTree, PromptTreeDev, PromptDev> a, const __grid_constant__ CUtensorMap tmap_k,
                    const __grid_constant__ CUtensorMap tmap_v) {
   using C = Cfg<kQe4m3>;
   constexpr int SK = C::kSK, SV = C::kSV;
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
-  if (!prompt_plan_fits(a)) {
-    if (threadIdx.x == 0 && blockIdx.x == 0 && a.status) atomicExch(a.status, kStatusInvalid);
-    return;
+  using Item = std::conditional_t<kTree, TreeItem, PromptItem>;
+  int units;
+  if constexpr (kTree) {
+    units = a.t.num_work * a.n_q_tiles * a.h_k;
+  } else {
+    if (!prompt_plan_fits(a)) {
+      if (threadIdx.x == 0 && blockIdx.x == 0 && a.status) atomicExch(a.status, kStatusInvalid);
+      return;
+    }
+    units = a.head->n_items * a.h_k;
   }
-  const int units = a.head->n_items * a.h_k;
   if (static_cast<int>(blockIdx.x) >= units) return;
 
   extern __shared__ uint8_t smem_raw[];
@@ -170,10 +194,36 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
   const int G = gridDim.x, me = blockIdx.x;
   auto unit_at = [&](int k) { return k * G + ((k & 1) ? G - 1 - me : me); };
   auto load_item = [&](int u) {
-    PromptItem it;
-    const int4* src = reinterpret_cast<const int4*>(a.items + u / a.h_k);
+    Item it;
+    if constexpr (kTree) {
+      const int rest = u / a.h_k;
+      const int4 w = reinterpret_cast<const int4*>(a.t.work)[rest / a.n_q_tiles];
+      it.b = w.x;
+      it.t0 = w.y;
+      it.t1 = w.z;
+      it.row0 = rest % a.n_q_tiles * kPromptRows;
+      it.len = a.t.seq_lens[w.x];
+      it.part = a.t.n_splits[w.x] > 1 ? w.w : -1;
+      it.tok0 = 0;
+      it.n_tok = a.t.q_len;
 #pragma unroll
-    for (int i = 0; i < 3; ++i) reinterpret_cast<int4*>(&it)[i] = src[i];
+      for (int w2 = 0; w2 < 2; ++w2) {
+        it.g0[w2] = it.t0;
+        it.g1[w2] = it.row0 + w2 * kRows < a.t.n_q ? it.t1 : it.t0;
+      }
+      it.span = make_int4(it.len, 0, it.len, 0);
+      it.prefix_tiles = it.jump = 0;
+      if (a.t.mod.spans) {
+        it.span = a.t.mod.spans[w.x];
+        it.span.z = min(it.span.z, it.len);
+        it.prefix_tiles = (it.span.x + kRows - 1) / kRows;
+        it.jump = max(it.span.y / kRows - it.prefix_tiles, 0);
+      }
+    } else {
+      const int4* src = reinterpret_cast<const int4*>(a.items + u / a.h_k);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) reinterpret_cast<int4*>(&it)[i] = src[i];
+    }
     return it;
   };
   // A warpgroup's share of the launch's 512 x 128 registers: 2 x 184 + 88 + 56
@@ -203,11 +253,11 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
     bool ok = true;
     for (int k = 0; ok && unit_at(k) < units; ++k) {
       const int u = unit_at(k), g = u % a.h_k;
-      const PromptItem it = load_item(u);
+      const Item it = load_item(u);
       const int64_t table = static_cast<int64_t>(it.b) * a.max_blocks;
       // lane l loads the tile's l-th page; its table entry comes a tile ahead
       auto page_of = [&](int t) {
-        const int key = t * kRows + lane * PS;
+        const int key = tile_key<kTree>(it, t) + lane * PS;
         return t < it.t1 && lane < nbox && key < it.len ? a.block_table[table + key / PS] : a.num_pages;
       };
       int page = page_of(it.t0);
@@ -272,7 +322,7 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
       uint32_t sph = 1;                           // of the scores read (none to wait for at first)
       uint32_t qph = 0, pph = 0, oph = 3;         // bit w: of group w's Q, its P, and its O read out (likewise)
       for (int k = 0; unit_at(k) < units; ++k) {
-        const PromptItem it = load_item(unit_at(k));
+        const Item it = load_item(unit_at(k));
         const int t0 = __shfl_sync(0xffffffffu, it.t0, 0), t1 = __shfl_sync(0xffffffffu, it.t1, 0);
         if (t1 <= t0) continue;
         int g0[2], g1[2];
@@ -383,7 +433,7 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
     bool ok = true;
     for (int k = 0; ok && unit_at(k) < units; ++k) {
       const int u = unit_at(k), g = u % a.h_k;
-      const PromptItem it = load_item(u);
+      const Item it = load_item(u);
       if (it.t1 <= it.t0) continue;
       // ---- a V tile: this warp turns 32 keys, four rows a load, 16 codes a lane
       auto convert = [&](int t) {
@@ -391,13 +441,17 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
         if (!wait(vfull(st), (n / SV) & 1) || (n >= kVf && !wait(fempty(vf), ((n / kVf) - 1) & 1))) ok = false;
         if (__any_sync(0xffffffffu, !ok)) return false;
         const uint8_t* const src = sm + C::kOffV + st * kTile;
+        const int key0 = tile_key<kTree>(it, t);
         uint8_t* const dst = sm + C::kOffVf + vf * kVfTile;
         const int cc = lane & 7;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int r = cw * 32 + i * 4 + (lane >> 3);
           uint4 x = *reinterpret_cast<const uint4*>(src + swz(r, cc));
-          if (t * kRows + r >= it.len) x = make_uint4(0u, 0u, 0u, 0u);  // 0 x what lies there must not reach O
+          const int key = key0 + r;
+          bool dead = key >= it.len;
+          if constexpr (kTree) dead = key >= it.span.z || (key >= it.span.x && key < it.span.y);
+          if (dead) x = make_uint4(0u, 0u, 0u, 0u);  // 0 x what lies there must not reach O
           const uint32_t v4[4] = {x.x, x.y, x.z, x.w};
           uint32_t h[8];
 #pragma unroll
@@ -526,7 +580,7 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
       // the next item's Q is on its way to L2 meanwhile
       if (unit_at(k + 1) < units) {
         const int u2 = unit_at(k + 1);
-        const PromptItem nx = load_item(u2);
+        const Item nx = load_item(u2);
         constexpr int kLines = kQe4m3 ? 1 : 2;  // of 128 bytes a row
 #pragma unroll 1
         for (int i = cw * 32 + lane; i < kPromptRows * kLines; i += 128) {
@@ -560,25 +614,41 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
         return u;
       };
       int g0 = 0, g1 = 0, lo = 0, lim = INT32_MAX;  // the group's tiles; the row sees keys lo .. lim
+      int pfx = 0, prefix_tiles = 0, jump = 0;      // kTree: and those below pfx, and nodes by its mask
       {
-        const PromptItem it = load_item(unit());
+        const Item it = load_item(unit());
         g0 = w ? it.g0[1] : it.g0[0];
         g1 = w ? it.g1[1] : it.g1[0];
+        if constexpr (kTree) {
+          if (it.t1 <= it.t0) continue;  // padding of the work list
+          prefix_tiles = it.prefix_tiles;
+          jump = it.jump;
+        }
         const int row = it.row0 + w * kRows + r;  // (rows past the last compute what nobody reads)
         if (row < it.n_tok * a.h_r) {
           const int tok = row / a.h_r;
-          prompt_range(it.len, it.n_tok, tok, tok, a.causal, a.window, &lo, &lim);
+          if constexpr (kTree) {
+            const TreeShape tree = tree_shape(a.t, it.b, it.len);
+            if (tok < tree.nodes) {  // (rows without a node compute too, and are written as rows without a key)
+              const RowRange rr = tree_range(a.t, it.b, tok, tree.ctx);
+              lim = min(rr.hi, it.span.z - 1);
+              lo = max(rr.lo, it.span.y);
+              pfx = min(rr.pfx, it.span.x);
+            }
+          } else {
+            prompt_range(it.len, it.n_tok, tok, tok, a.causal, a.window, &lo, &lim);
+          }
         }
       }
       // reference maximum (in units of the scores as read), sum of 2^kPBias p,
       // score -> log2 units
       float m_run = -INFINITY, l_run = 0.f, c2 = 1.f, cap_c1 = 0.f;
       for (int t = g0; t < g1; ++t, ++q) {
-        const int key0 = t * kRows;
+        const int key0 = kTree ? (t < prefix_tiles ? t : t + jump) * kRows : t * kRows;
         if (!wait(gbar(w, 0), q & 1)) give_up(abort_flag, a.status);
         ptx::tc_fence_after();
         if (t == g0) {  // the row's scale is there since its Q was laid out
-          const int u = unit(), g = u % a.h_k, b = a.items[u / a.h_k].b;
+          const int u = unit(), g = u % a.h_k, b = load_item(u).b;
           float raw_l = a.softmax_scale * a.qd[b * a.qd_seq + g * a.qd_head] * a.kd[b * a.kd_seq + g * a.kd_head];
           if constexpr (!kQe4m3) raw_l *= __uint_as_float(static_cast<uint32_t>(127 - q_shift[(2 * w + (items & 1)) * 128 + r]) << 23);
           if constexpr (kCap)  // scores become logits in log2 units as they are read
@@ -586,7 +656,7 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
           else
             c2 = raw_l * kLog2e;
         }
-        const bool unmasked = __all_sync(0xffffffffu, key0 >= lo && key0 + kRows - 1 <= lim);
+        const bool unmasked = __all_sync(0xffffffffu, (key0 >= lo && key0 + kRows - 1 <= lim) || (kTree && key0 + kRows <= pfx));
         uint32_t s[kRows];
 #pragma unroll
         for (int c = 0; c < kRows; c += 16) MJ_TMEM_LD16(ts + c, (s + c));
@@ -600,8 +670,27 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
         }
         if (!unmasked) {
           const int e0 = lo - key0, e1 = lim - key0;
+          if constexpr (kTree) {  // (few tiles: the row's node is looked up again)
+            uint32_t bits[4] = {};
+            const Item it = load_item(unit());
+            const int row = it.row0 + w * kRows + r;
+            if (row < it.n_tok * a.h_r) {
+              const int tok = row / a.h_r;
+              const TreeShape tree = tree_shape(a.t, it.b, it.len);
+              if (tok < tree.nodes) {
+                const uint32_t* const mask = a.t.mask + (static_cast<int64_t>(it.b) * a.t.q_len + tok) * a.t.mask_words;
 #pragma unroll
-          for (int e = 0; e < kRows; ++e) s[e] = e >= e0 && e <= e1 ? s[e] : 0xFF800000u;  // -inf
+                for (int i = 0; i < 4; ++i) bits[i] = tree_bits(mask, tree.nodes, key0 + 32 * i - tree.ctx);
+              }
+            }
+            const int e2 = pfx - key0;
+#pragma unroll
+            for (int e = 0; e < kRows; ++e)
+              s[e] = (e >= e0 && e <= e1) || e < e2 || ((bits[e >> 5] >> (e & 31)) & 1u) != 0 ? s[e] : 0xFF800000u;
+          } else {
+#pragma unroll
+            for (int e = 0; e < kRows; ++e) s[e] = e >= e0 && e <= e1 ? s[e] : 0xFF800000u;  // -inf
+          }
         }
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -661,16 +750,22 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
       if (__any_sync(0xffffffffu, *abort_flag != 0)) break;  // nothing is written out after that
       ptx::tc_fence_after();
       const int u = unit(), g = u % a.h_k;
-      const PromptItem it = load_item(u);
+      const Item it = load_item(u);
       const int row = it.row0 + w * kRows + r;
       const bool live = row < it.n_tok * a.h_r;
       const int tok = live ? row / a.h_r : 0;
       const int hr = live ? row - tok * a.h_r : 0;
       const bool final_out = it.part < 0;
-      const float l = l_run * (1.f / 128.f);  // 2^-kPBias
-      const bool seen = m_run > -INFINITY;
-      const float f = a.vd[it.b * a.vd_seq + g * a.vd_head] * (1.f / 128.f) * (final_out ? a.scale_o / (seen ? l : 1.f) : 1.f);
-      const int64_t part_row = (static_cast<int64_t>(it.part) * a.h_k + g) * kPromptRows + w * kRows + r;
+      float l = l_run * (1.f / 128.f);  // 2^-kPBias
+      bool seen = m_run > -INFINITY;
+      if constexpr (kTree) seen = seen && tok < tree_shape(a.t, it.b, it.len).nodes;
+      float f = a.vd[it.b * a.vd_seq + g * a.vd_head] * (1.f / 128.f) * (final_out ? a.scale_o / (seen ? l : 1.f) : 1.f);
+      if (kTree && !seen) l = f = 0.f;
+      int64_t part_row;
+      if constexpr (kTree)
+        part_row = mj::part_row(a.t, it.b, g, it.part, live ? row : 0);
+      else
+        part_row = (static_cast<int64_t>(it.part) * a.h_k + g) * kPromptRows + w * kRows + r;
       const int64_t orow = final_out ? prompt_at(a.o_rows, it.b, it.tok0 + tok, g, hr) : part_row * kHeadDimDev;
       // A lane holds a row; the rows leave through shared memory, 64 bytes of each
       // at a time, as pieces of four lanes (16 bytes a lane and row would be 32
@@ -713,6 +808,10 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0u;
         }
+        if constexpr (kTree) {  // a row without a node may have added up anything
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = seen ? o[e] : 0u;
+        }
         uint4 v[4];
         if (final_out) {
 #pragma unroll
@@ -746,7 +845,7 @@ prompt_attn_kernel(const PromptDev a, const __grid_constant__ CUtensorMap tmap_k
         if (lane == 0) ptx::mbar_arrive(gbar(w, 3));
       }
       if (live) {
-        const float top = m_run * c2 * (1.f / kLog2e);
+        const float top = kTree && !seen ? -INFINITY : m_run * c2 * (1.f / kLog2e);
         if (!final_out) {
           a.m_part[part_row] = top;
           a.l_part[part_row] = l;
@@ -843,31 +942,82 @@ __global__ void __launch_bounds__(kMergeWarps * 32) prompt_merge_kernel(const Pr
   }
 }
 
-template <bool kQe4m3, bool kCap>
-cudaError_t launch(const PromptDev& a, int sm_count, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t stream) {
+template <bool kQe4m3, bool kCap, bool kTree>
+cudaError_t launch(const std::conditional_t<kTree, PromptTreeDev, PromptDev>& a, int sm_count, const CUtensorMap& mk,
+                   const CUtensorMap& mv, cudaStream_t stream) {
   constexpr int smem = Cfg<kQe4m3>::kBytes;
-  auto kern = prompt_attn_kernel<kQe4m3, kCap>;
+  auto kern = prompt_attn_kernel<kQe4m3, kCap, kTree>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(static_cast<unsigned>(sm_count), 1, 1), dim3(kThreads, 1, 1), smem, stream, a, mk, mv);
 }
 
-}  // namespace
-
-cudaError_t launch_prompt_attn(const PromptDev& a, bool q_e4m3, int sm_count, cudaStream_t stream) {
+template <bool kTree>
+cudaError_t launch_maps(const std::conditional_t<kTree, PromptTreeDev, PromptDev>& a, bool q_e4m3, int sm_count,
+                        cudaStream_t stream) {
   CUtensorMap mk, mv;
   if (!make_kv_map(&mk, a.k, a.page_size, a.h_k, a.num_pages, a.k_row, a.k_head, a.k_page, a.page_size, 1, 0) ||
       !make_kv_map(&mv, a.v, a.page_size, a.h_k, a.num_pages, a.v_row, a.v_head, a.v_page, a.page_size, 1, 0))
     return cudaErrorInvalidValue;
-  const bool cap = a.softcap > 0.f;
-  cudaError_t e;
-  if (q_e4m3)
-    e = cap ? launch<true, true>(a, sm_count, mk, mv, stream) : launch<true, false>(a, sm_count, mk, mv, stream);
-  else
-    e = cap ? launch<false, true>(a, sm_count, mk, mv, stream) : launch<false, false>(a, sm_count, mk, mv, stream);
+  if (a.softcap > 0.f)
+    return q_e4m3 ? launch<true, true, kTree>(a, sm_count, mk, mv, stream) : launch<false, true, kTree>(a, sm_count, mk, mv, stream);
+  return q_e4m3 ? launch<true, false, kTree>(a, sm_count, mk, mv, stream) : launch<false, false, kTree>(a, sm_count, mk, mv, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_prompt_attn(const PromptDev& a, bool q_e4m3, int sm_count, cudaStream_t stream) {
+  const cudaError_t e = launch_maps<false>(a, q_e4m3, sm_count, stream);
   if (e != cudaSuccess || a.max_splits == 1) return e;
   return launch_pdl(prompt_merge_kernel, dim3(static_cast<unsigned>(4 * sm_count), 1, 1), dim3(kMergeWarps * 32, 1, 1), 0,
                     stream, a);
+}
+
+cudaError_t launch_prompt_tree(const DecodeTreeDev& a, int n_q_tiles, bool q_e4m3, int sm_count, cudaStream_t stream) {
+  PromptTreeDev d{};
+  d.t = a;
+  d.n_q_tiles = n_q_tiles;
+  d.q = a.q;
+  d.q_rows = {a.q_seq, static_cast<int64_t>(a.h_r) * kHeadDimDev, static_cast<int64_t>(a.n_q) * kHeadDimDev, kHeadDimDev};
+  d.o = a.o;
+  d.o_rows = {a.o_seq, static_cast<int64_t>(a.h_r) * kHeadDimDev, static_cast<int64_t>(a.n_q) * kHeadDimDev, kHeadDimDev};
+  d.lse = a.lse;
+  d.lse_rows = {static_cast<int64_t>(a.h_k) * a.n_q, a.h_r, a.n_q, 1};
+  d.k = a.k;
+  d.v = a.v;
+  d.k_page = a.k_page;
+  d.k_row = a.k_row;
+  d.k_head = a.k_head;
+  d.v_page = a.v_page;
+  d.v_row = a.v_row;
+  d.v_head = a.v_head;
+  d.block_table = a.block_table;
+  d.qd = a.qd;
+  d.kd = a.kd;
+  d.vd = a.vd;
+  d.qd_seq = a.qd_seq;
+  d.qd_head = a.qd_head;
+  d.kd_seq = a.kd_seq;
+  d.kd_head = a.kd_head;
+  d.vd_seq = a.vd_seq;
+  d.vd_head = a.vd_head;
+  d.softmax_scale = a.softmax_scale;
+  d.scale_o = a.scale_o;
+  d.softcap = a.mod.softcap;
+  d.o_part = a.o_part;
+  d.m_part = a.m_part;
+  d.l_part = a.l_part;
+  d.status = a.status;
+  d.num_seqs = a.num_seqs;
+  d.h_k = a.h_k;
+  d.h_r = a.h_r;
+  d.page_size = a.page_size;
+  d.max_blocks = a.max_blocks;
+  d.num_pages = a.num_pages;
+  d.kv_evict_first = a.kv_evict_first && n_q_tiles == 1;  // several q tiles share the pages
+  d.max_splits = a.max_splits;
+  const int64_t units = static_cast<int64_t>(a.num_work) * n_q_tiles * a.h_k;
+  return launch_maps<true>(d, q_e4m3, static_cast<int>(units < sm_count ? units : sm_count), stream);
 }
 
 }  // namespace mj

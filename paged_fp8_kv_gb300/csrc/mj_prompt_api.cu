@@ -197,9 +197,9 @@ extern "C" mj_status mj_prompt_attn(const mj_decode_params* params, const mj_pro
   d.window = std::min(a.window, 1 << 30);
   d.kv_evict_first = p.kv_evict_first == 1;
   d.max_splits = p.max_splits;
-  const int sms = device_sm_count();
-  if (sms < 1) return MJ_ERR_CUDA;
+  // keys are cut only into parts of kPromptMinChunk tiles or more
+  const bool merge = p.max_splits > 1 && static_cast<int64_t>(p.max_blocks) * p.page_size > kPromptMinChunk * 128;
   const NvtxRange range("mj_prompt_attn");
-  const cudaError_t e = launch_prompt_attn(d, p.q_dtype == MJ_E4M3, sms, reinterpret_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_prompt_attn(d, p.q_dtype == MJ_E4M3, merge, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MJ_OK : MJ_ERR_CUDA;
 }

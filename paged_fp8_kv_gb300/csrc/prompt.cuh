@@ -11,14 +11,15 @@ namespace mj {
 constexpr int kPromptRows = 256;  // packed query rows of a work item
 constexpr int kPromptSlots = 152; // CTAs the plan cuts for (a GB300's SMs)
 constexpr int kPromptMinChunk = 4;   // tiles of the shortest piece a row tile is cut into
-constexpr int kPromptSortMax = 8192; // items ordered by length in shared memory
+constexpr int kPromptSortMax = 8192; // items ordered by cost in shared memory
 
 // 256 packed rows (row n of a sequence: token n / h_r, head n % h_r of the
 // group) of one sequence, from row0 on, against the keys of tiles [t0, t1).
 // part < 0: the item holds all the keys its rows see and writes O and LSE;
 // else its partial results go to part `part`.
 // (g0, g1): of those tiles, the ones that the first and the second 128 rows see
-// any key of.
+// any key of; g1[1] < 0: there are 128 rows at most and two tiles at least, and
+// both row groups hold those rows and take the tiles in turn.
 struct __align__(16) PromptItem {
   int32_t b, row0, t0, t1;
   int32_t part, tok0, n_tok, len;  // tok0: the sequence's first token in Q and O

@@ -73,7 +73,7 @@ struct Cfg {
   static constexpr int kOffOut = kOffQ + 2 * kParts * kTile;     // [softmax warp] 32 rows x 64 bytes of O on their way out
   static constexpr int kOffShift = kOffOut + 8 * 2048;           // [group][2][128] s of each row
   static constexpr int kOffBar = kOffShift + 2 * 256;
-  static constexpr int kBars = 2 * (kSK + kSV + kVf) + 1 + 6 * 2 + 1;
+  static constexpr int kBars = 2 * (kSK + kSV + kVf) + 1 + 6 * 2 + 2;
   static constexpr int kOffMisc = kOffBar + kBars * 8;
   static constexpr int kBytes = kOffMisc + 16 + 1024;
   static_assert(kBytes <= 232448, "shared memory");
@@ -154,7 +154,7 @@ prompt_attn_kernel(const std::conditional_t<kTree, PromptTreeDev, PromptDev> a, 
   // of each group: 0 scores written, 1 P written, 2 a tile's product done, 3 O
   // read out, 4 Q laid out, 5 Q read
   auto gbar = [&](int w, int k) { return bar0 + 8u * (kB + 1 + 6 * w + k); };
-  const uint32_t drain = bar0 + 8u * (kB + 13);
+  const uint32_t drain = bar0 + 8u * (kB + 13), stats = drain + 8u;  // stats: the second group's row statistics written
 
   if (tid == 0) {
     for (int s = 0; s < SK; ++s) {
@@ -174,6 +174,7 @@ prompt_attn_kernel(const std::conditional_t<kTree, PromptTreeDev, PromptDev> a, 
       for (int k = 0; k < 6; ++k) ptx::mbar_init(gbar(w, k), k == 1 || k == 3 || k == 4 ? 4 : 1);
     }
     ptx::mbar_init(drain, 1);
+    ptx::mbar_init(stats, 4);
     *abort_flag = 0;
     ptx::fence_mbar_init();
   }
@@ -211,6 +212,7 @@ prompt_attn_kernel(const std::conditional_t<kTree, PromptTreeDev, PromptDev> a, 
         it.g0[w2] = it.t0;
         it.g1[w2] = it.row0 + w2 * kRows < a.t.n_q ? it.t1 : it.t0;
       }
+      if (it.row0 + kRows >= a.t.n_q && it.t1 - it.t0 >= 2) it.g1[1] = -1;
       it.span = make_int4(it.len, 0, it.len, 0);
       it.prefix_tiles = it.jump = 0;
       if (a.t.mod.spans) {
@@ -311,7 +313,8 @@ prompt_attn_kernel(const std::conditional_t<kTree, PromptTreeDev, PromptDev> a, 
         for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
           for (int part = 0; part < C::kParts; ++part)
-            ptx::mma_e4m3(tm, qdesc + (w * C::kParts + part) * (kTile >> 4) + 2 * kk, kd + 2 * kk, idesc_s, kk > 0 || part > 0);
+            ptx::mma_e4m3(tm, qdesc + static_cast<uint32_t>((w * C::kParts + part) * (kTile >> 4) + 2 * kk), kd + 2 * kk, idesc_s,
+                          kk > 0 || part > 0);
       };
       auto output = [&](int w, uint64_t vd, uint32_t more) {
 #pragma unroll
@@ -332,6 +335,57 @@ prompt_attn_kernel(const std::conditional_t<kTree, PromptTreeDev, PromptDev> a, 
           g1[w] = __shfl_sync(0xffffffffu, it.g1[w], 0);
         }
         bool ok = true;
+        if (g1[1] < 0) {
+          // both groups hold the same rows and take the tiles in turn: scores of
+          // tile t, O of tile t - 2 (of the same group, whose next scores these are)
+          for (int t = t0; t < t1 + 2; ++t) {
+            const int w = (t - t0) & 1;
+            const uint32_t sc = gbar(w, 0), pf = gbar(w, 1), pd = gbar(w, 2);
+            if (t < t1) {
+              const uint64_t kd = kdesc + ks * (kTile >> 4);
+              if (leader) {
+                ok &= wait(kfull(ks), kph);
+                if (t < t0 + 2) ok &= wait(gbar(w, 4), (qph >> w) & 1);
+                ok &= wait(sread, sph);
+                ptx::tc_fence_after();
+                scores(w, kd);
+                ptx::mma_commit(sc);
+                ptx::mma_commit(kempty(ks));
+                if (t + 2 >= t1) ptx::mma_commit(gbar(w, 5));
+              }
+              __syncwarp();
+              sph ^= 1;
+              if (t < t0 + 2) qph ^= 1u << w;
+              if (++ks == SK) {
+                ks = 0;
+                kph ^= 1;
+              }
+            }
+            if (t >= t0 + 2) {
+              const uint64_t vd = vdesc + vs * (kVfTile >> 4);
+              const uint32_t more = t >= t0 + 4;
+              if (leader) {
+                ok &= wait(ffull(vs), vph);
+                ok &= wait(pf, (pph >> w) & 1);
+                if (!more) ok &= wait(gbar(w, 3), (oph >> w) & 1);
+                ptx::tc_fence_after();
+                output(w, vd, more);
+                ptx::mma_commit(pd);
+                ptx::mma_commit(fempty(vs));
+              }
+              __syncwarp();
+              pph ^= 1u << w;
+              if (!more) oph ^= 1u << w;
+              if (++vs == kVf) {
+                vs = 0;
+                vph ^= 1;
+              }
+            }
+          }
+          if (leader && !ok) give_up(abort_flag, a.status);
+          if (__any_sync(0xffffffffu, !ok)) break;
+          continue;
+        }
         const int t_all = (g0[0] > g0[1] ? g0[0] : g0[1]) + 1, t_end = (g1[0] < g1[1] ? g1[0] : g1[1]) - 1;
         for (int t = t0; t <= t1; ++t) {  // scores of tile t, O of tile t - 1
           const uint64_t kd = kdesc + ks * (kTile >> 4), vd = vdesc + vs * (kVfTile >> 4);
@@ -488,9 +542,10 @@ prompt_attn_kernel(const std::conditional_t<kTree, PromptTreeDev, PromptDev> a, 
       const int piece = lane & 7;
 #pragma unroll 1
       for (int w = 0; w < 2; ++w) {
-        if ((w ? it.g1[1] : it.g1[0]) <= (w ? it.g0[1] : it.g0[0])) continue;
+        const bool dual = it.g1[1] < 0;
+        if (!dual && (w ? it.g1[1] : it.g1[0]) <= (w ? it.g0[1] : it.g0[0])) continue;
         const int r0 = cw * 32 + (lane >> 3);  // this lane's rows of the group: r0, r0 + 4, ..
-        const int first = it.row0 + w * kRows + r0;
+        const int first = it.row0 + (dual ? 0 : w * kRows) + r0;
         int left = it.n_tok * a.h_r - first;  // rows there are from this one on
         const int tok = first / a.h_r;
         int hr = first - tok * a.h_r;
@@ -602,7 +657,7 @@ prompt_attn_kernel(const std::conditional_t<kTree, PromptTreeDev, PromptDev> a, 
     const int r = quarter * 32 + lane;  // row of the group = TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t ts = tmem + lane_off, tp = ts + p_col(w), to = ts + o_col(w);
-    int q = 0, items = 0;  // the group's tiles and items
+    int q = 0, items = 0, duals = 0;  // the group's tiles and items, and those it shares
     // a wait that gives up sets the abort flag and the loop runs on (later waits
     // return at once), so that a warp's lanes stay together
     for (int k = 0; unit_at(k) < units; ++k) {
@@ -614,17 +669,19 @@ prompt_attn_kernel(const std::conditional_t<kTree, PromptTreeDev, PromptDev> a, 
         return u;
       };
       int g0 = 0, g1 = 0, lo = 0, lim = INT32_MAX;  // the group's tiles; the row sees keys lo .. lim
+      bool dual;                                    // both groups hold these rows and take turns
       int pfx = 0, prefix_tiles = 0, jump = 0;      // kTree: and those below pfx, and nodes by its mask
       {
         const Item it = load_item(unit());
-        g0 = w ? it.g0[1] : it.g0[0];
-        g1 = w ? it.g1[1] : it.g1[0];
+        dual = it.g1[1] < 0;
+        g0 = dual ? it.t0 + w : (w ? it.g0[1] : it.g0[0]);
+        g1 = dual ? it.t1 : (w ? it.g1[1] : it.g1[0]);
         if constexpr (kTree) {
           if (it.t1 <= it.t0) continue;  // padding of the work list
           prefix_tiles = it.prefix_tiles;
           jump = it.jump;
         }
-        const int row = it.row0 + w * kRows + r;  // (rows past the last compute what nobody reads)
+        const int row = it.row0 + (dual ? 0 : w * kRows) + r;  // (rows past the last compute what nobody reads)
         if (row < it.n_tok * a.h_r) {
           const int tok = row / a.h_r;
           if constexpr (kTree) {
@@ -643,7 +700,7 @@ prompt_attn_kernel(const std::conditional_t<kTree, PromptTreeDev, PromptDev> a, 
       // reference maximum (in units of the scores as read), sum of 2^kPBias p,
       // score -> log2 units
       float m_run = -INFINITY, l_run = 0.f, c2 = 1.f, cap_c1 = 0.f;
-      for (int t = g0; t < g1; ++t, ++q) {
+      for (int t = g0; t < g1; t += dual ? 2 : 1, ++q) {
         const int key0 = kTree ? (t < prefix_tiles ? t : t + jump) * kRows : t * kRows;
         if (!wait(gbar(w, 0), q & 1)) give_up(abort_flag, a.status);
         ptx::tc_fence_after();
@@ -673,7 +730,7 @@ prompt_attn_kernel(const std::conditional_t<kTree, PromptTreeDev, PromptDev> a, 
           if constexpr (kTree) {  // (few tiles: the row's node is looked up again)
             uint32_t bits[4] = {};
             const Item it = load_item(unit());
-            const int row = it.row0 + w * kRows + r;
+            const int row = it.row0 + (dual ? 0 : w * kRows) + r;
             if (row < it.n_tok * a.h_r) {
               const int tok = row / a.h_r;
               const TreeShape tree = tree_shape(a.t, it.b, it.len);
@@ -748,19 +805,41 @@ prompt_attn_kernel(const std::conditional_t<kTree, PromptTreeDev, PromptDev> a, 
       const bool any = g1 > g0;
       if (any && !wait(gbar(w, 2), (q - 1) & 1)) give_up(abort_flag, a.status);
       if (__any_sync(0xffffffffu, *abort_flag != 0)) break;  // nothing is written out after that
+      // the second group's row statistics go to the first one, which reads both O
+      float* const stat = reinterpret_cast<float*>(sm + C::kOffOut + 4 * 2048) + 2 * r;
+      float m1 = -INFINITY, l1 = 0.f;
+      if (dual) {
+        if (w == 1) {
+          *reinterpret_cast<float2*>(stat) = make_float2(m_run, l_run);
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(stats);
+          continue;
+        }
+        if (!wait(stats, duals & 1)) give_up(abort_flag, a.status);
+        if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+        ++duals;
+        const float2 x = *reinterpret_cast<const float2*>(stat);
+        m1 = x.x;
+        l1 = x.y;
+      }
       ptx::tc_fence_after();
       const int u = unit(), g = u % a.h_k;
       const Item it = load_item(u);
-      const int row = it.row0 + w * kRows + r;
+      const int row = it.row0 + (dual ? 0 : w * kRows) + r;
       const bool live = row < it.n_tok * a.h_r;
       const int tok = live ? row / a.h_r : 0;
       const int hr = live ? row - tok * a.h_r : 0;
       const bool final_out = it.part < 0;
-      float l = l_run * (1.f / 128.f);  // 2^-kPBias
+      const float mx = fmaxf(m_run, m1);
+      const float f0 = m_run == -INFINITY ? 0.f : fast_exp2((m_run - mx) * c2), f1 = m1 == -INFINITY ? 0.f : fast_exp2((m1 - mx) * c2);
+      m_run = mx;
+      float l = (l_run * f0 + l1 * f1) * (1.f / 128.f);  // 2^-kPBias
       bool seen = m_run > -INFINITY;
       if constexpr (kTree) seen = seen && tok < tree_shape(a.t, it.b, it.len).nodes;
       float f = a.vd[it.b * a.vd_seq + g * a.vd_head] * (1.f / 128.f) * (final_out ? a.scale_o / (seen ? l : 1.f) : 1.f);
       if (kTree && !seen) l = f = 0.f;
+      const float fa = f * f0, fb = f * f1;  // of this group's O and, where rows are shared, of the other's
       int64_t part_row;
       if constexpr (kTree)
         part_row = mj::part_row(a.t, it.b, g, it.part, live ? row : 0);
@@ -808,6 +887,16 @@ prompt_attn_kernel(const std::conditional_t<kTree, PromptTreeDev, PromptDev> a, 
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0u;
         }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fa);
+        if (dual) {
+          uint32_t o1[32];
+          MJ_TMEM_LD16(ts + o_col(1) + h0, o1);
+          MJ_TMEM_LD16(ts + o_col(1) + h0 + 16, (o1 + 16));
+          ptx::tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), fb, __uint_as_float(o[e])));
+        }
         if constexpr (kTree) {  // a row without a node may have added up anything
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = seen ? o[e] : 0u;
@@ -819,7 +908,7 @@ prompt_attn_kernel(const std::conditional_t<kTree, PromptTreeDev, PromptDev> a, 
             uint32_t b4[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const __nv_bfloat162 y = __floats2bfloat162_rn(__uint_as_float(o[8 * c + 2 * i]) * f, __uint_as_float(o[8 * c + 2 * i + 1]) * f);
+              const __nv_bfloat162 y = __floats2bfloat162_rn(__uint_as_float(o[8 * c + 2 * i]), __uint_as_float(o[8 * c + 2 * i + 1]));
               b4[i] = *reinterpret_cast<const uint32_t*>(&y);
             }
             v[c] = make_uint4(b4[0], b4[1], b4[2], b4[3]);
@@ -832,7 +921,7 @@ prompt_attn_kernel(const std::conditional_t<kTree, PromptTreeDev, PromptDev> a, 
             for (int c = 0; c < 4; ++c) {
               uint32_t b4[4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) b4[i] = __float_as_uint(__uint_as_float(o[c0 + 4 * c + i]) * f);
+              for (int i = 0; i < 4; ++i) b4[i] = o[c0 + 4 * c + i];
               v[c] = make_uint4(b4[0], b4[1], b4[2], b4[3]);
             }
             emit(v);
@@ -842,7 +931,10 @@ prompt_attn_kernel(const std::conditional_t<kTree, PromptTreeDev, PromptDev> a, 
       if (any) {
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(gbar(w, 3));
+        if (lane == 0) {
+          ptx::mbar_arrive(gbar(w, 3));
+          if (dual) ptx::mbar_arrive(gbar(1, 3));
+        }
       }
       if (live) {
         const float top = kTree && !seen ? -INFINITY : m_run * c2 * (1.f / kLog2e);
@@ -966,10 +1058,10 @@ cudaError_t launch_maps(const std::conditional_t<kTree, PromptTreeDev, PromptDev
 
 }  // namespace
 
-cudaError_t launch_prompt_attn(const PromptDev& a, bool q_e4m3, int sm_count, cudaStream_t stream) {
-  const cudaError_t e = launch_maps<false>(a, q_e4m3, sm_count, stream);
-  if (e != cudaSuccess || a.max_splits == 1) return e;
-  return launch_pdl(prompt_merge_kernel, dim3(static_cast<unsigned>(4 * sm_count), 1, 1), dim3(kMergeWarps * 32, 1, 1), 0,
+cudaError_t launch_prompt_attn(const PromptDev& a, bool q_e4m3, bool merge, cudaStream_t stream) {
+  const cudaError_t e = launch_maps<false>(a, q_e4m3, kPromptSlots, stream);
+  if (e != cudaSuccess || !merge) return e;
+  return launch_pdl(prompt_merge_kernel, dim3(4 * kPromptSlots, 1, 1), dim3(kMergeWarps * 32, 1, 1), 0,
                     stream, a);
 }
 

@@ -8,8 +8,10 @@
 // tiles are longer than T / S, and their pieces are at most T / chunk plus one
 // each, so 2 S parts hold all partial results whatever the lengths.
 //
-// Items are ordered by length, longest first (up to 8192; beyond that order
-// hardly matters): the attention's CTAs take them in turns, forth and back.
+// Items are ordered by their cost in tiles, longest first (up to 8192; beyond that order
+// hardly matters): the attention's CTAs take them in turns, forth and back.  (A
+// list that gives each unit to the CTA with the least so far ended a step of a
+// long chunk among decode tokens 1 % sooner and took 130 us to make.)
 //
 // One CTA of 1024 threads, latency-bound: a prefix sum over the sequences, one
 // pass over the row tiles for T, one with prefix sums over batches of 1024 row
@@ -172,9 +174,16 @@ __global__ void __launch_bounds__(kThreads) prompt_plan_kernel(const PromptPlanD
             it.g0[w] = max(g0, it.t0);
             it.g1[w] = max(min(g1, it.t1), it.g0[w]);
           }
+          if (it.n_tok * a.h_r - it.row0 <= kPromptRows / 2 && it.t1 - it.t0 >= 2) {
+            it.g0[0] = it.g0[1] = it.t0;
+            it.g1[0] = it.t1;
+            it.g1[1] = -1;
+          }
           a.scratch[at + s] = it;
+          // (a tile that the row groups take in turn costs about 5/8 of one they share)
+          const int cost = (it.t1 - it.t0) * (it.g1[1] < 0 ? 5 : 8);
           if (at + s < kPromptSortMax)
-            keys[at + s] = (static_cast<uint64_t>(0x7FFFFFFF - (it.t1 - it.t0)) << 32) | static_cast<uint32_t>(at + s);
+            keys[at + s] = (static_cast<uint64_t>(0x7FFFFFFF - cost) << 32) | static_cast<uint32_t>(at + s);
         }
       }
       n_items += t_items;

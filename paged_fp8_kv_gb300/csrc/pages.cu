@@ -148,27 +148,40 @@ __global__ void __launch_bounds__(kThreads, 1) reserve_kernel(const PagesDev a) 
     else if (wrong)
       report(a.status, kStatusCapacity);
   }
-  auto free_page = [&](int x) { return a.free_pages[n_free - 1 - x]; };
+  auto free_page = [&](int x) { return __ldg(a.free_pages + n_free - 1 - x); };
   // the new tokens' positions and slots
   if (a.positions || a.slots) {
-    for (int t = rank * kThreads + tid; t < a.num_tokens; t += ctas * kThreads) {
-      int pos = 0;
-      int64_t slot = -1;
-      if (t < tokens) {
-        const int b = find(tok, a.num_seqs, t);
-        const int old = held[b];
-        if (old >= 0) {
-          pos = old + t - tok[b];
-          const int blk = pos >> shift, have = (old + row_mask) >> shift;
-          if (a.slots) {
-            const int page = blk < have ? a.block_table[static_cast<int64_t>(b) * a.max_blocks + blk]
-                                        : free_page(need[b] + blk - have);
-            slot = (static_cast<int64_t>(page) << shift) + (pos & row_mask);
+    // four a thread at a time, so that their loads are in flight together
+    constexpr int kBatch = 4;
+    const int step = ctas * kThreads;
+    for (int t0 = rank * kThreads + tid; t0 < a.num_tokens; t0 += kBatch * step) {
+      int pos[kBatch];
+      int64_t slot[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int t = t0 + i * step;
+        pos[i] = 0;
+        slot[i] = -1;
+        if (t < a.num_tokens && t < tokens) {
+          const int b = find(tok, a.num_seqs, t);
+          const int old = held[b];
+          if (old >= 0) {
+            pos[i] = old + t - tok[b];
+            const int blk = pos[i] >> shift, have = (old + row_mask) >> shift;
+            // (the old pages' entries are not written here, the new ones' not read)
+            if (a.slots)
+              slot[i] = blk < have ? __ldg(a.block_table + static_cast<int64_t>(b) * a.max_blocks + blk)
+                                   : free_page(need[b] + blk - have);
           }
         }
       }
-      if (a.positions) a.positions[t] = pos;
-      if (a.slots) a.slots[t] = slot;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int t = t0 + i * step;
+        if (t >= a.num_tokens) continue;
+        if (a.positions) a.positions[t] = pos[i];
+        if (a.slots) a.slots[t] = slot[i] < 0 ? -1 : (slot[i] << shift) + (pos[i] & row_mask);
+      }
     }
   }
   // the new pages' entries

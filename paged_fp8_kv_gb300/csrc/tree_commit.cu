@@ -29,17 +29,20 @@ __global__ void __launch_bounds__(kMaxThreads) tree_commit_kernel(const CommitDe
   __shared__ int4 moves[kChunk];
   const int b = blockIdx.x, tid = threadIdx.x;
   const int shift = a.page_shift, row_mask = (1 << shift) - 1;
-  const int L = a.seq_lens[b];
+  const int32_t* const path = a.accepted + static_cast<int64_t>(b) * a.max_accept;
+  // one round of loads: the branch beside the numbers that say how much of it counts
+  const int mine = tid < a.max_accept ? path[tid] : 0;
+  const int ahead = tid > 0 && tid < a.max_accept ? path[tid - 1] : -1;
+  const int L = a.seq_lens[b], count = a.num_accepted[b];
   int nodes = a.tree_lens ? a.tree_lens[b] : a.q_len;
   nodes = nodes < 0 ? 0 : (nodes > a.q_len ? a.q_len : nodes);
-  const int count = a.num_accepted[b];
-  const int32_t* const path = a.accepted + static_cast<int64_t>(b) * a.max_accept;
   int bad = L < 0 || L > a.max_len || count < 0 || count > a.max_accept;
   if (!bad) {
     nodes = nodes > L ? L : nodes;
-    for (int i = tid; i < count; i += blockDim.x) {
+    if (tid < count) bad |= mine < 0 || mine >= nodes || mine <= ahead;
+    for (int i = tid + blockDim.x; i < count; i += blockDim.x) {
       const int m = path[i];
-      bad |= m < 0 || m >= nodes || (i > 0 && m <= path[i - 1]);
+      bad |= m < 0 || m >= nodes || m <= path[i - 1];
     }
   }
   bad = __syncthreads_or(bad);  // also: every thread has read the length
@@ -63,7 +66,7 @@ __global__ void __launch_bounds__(kMaxThreads) tree_commit_kernel(const CommitDe
   for (int c0 = 0; c0 < count; c0 += kChunk) {
     const int n = count - c0 < kChunk ? count - c0 : kChunk;
     if (tid < n) {
-      const int to = ctx + c0 + tid, of = ctx + path[c0 + tid];
+      const int to = ctx + c0 + tid, of = ctx + (c0 == 0 ? mine : path[c0 + tid]);
       int pt = -1, pf = -1;
       if (to != of) {
         const int64_t row = static_cast<int64_t>(b) * a.max_blocks;

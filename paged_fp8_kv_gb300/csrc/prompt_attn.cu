@@ -6,32 +6,54 @@
 //
 // A work item is 256 packed rows (token, head of the group) of one sequence
 // and one kv head against its keys, 128 at a time: one read of a K and V tile
-// serves both groups of 128 rows, one MMA warp and one softmax warpgroup each,
-// which go through their tiles half a period apart.  Operands:
+// serves two groups of 128 rows, a softmax warpgroup each.  Operands:
 //   S   Q as hi + lo e4m3 parts (q 2^s = hi + lo, s by row) against the K codes
 //       as they lie in the cache, kind::f8f6f4: K is never converted, and the
 //       two parts cost what one bf16 product would
-//   O   P in half precision from TMEM, where it overwrites its scores, against
-//       V in half precision (every e4m3 value is one), kind::f16.  A converter
-//       warpgroup turns each V tile once for both groups.  Splitting P into
-//       e4m3 parts instead would cost the softmax threads four conversions a
-//       pair of scores for one, and keeps 8 bits of P for 11.
+//   O   P in half precision from TMEM against V in half precision (every e4m3
+//       value is one), kind::f16.  A converter warpgroup turns each V tile once
+//       for both groups.  Splitting P into e4m3 parts instead would cost the
+//       softmax threads four conversions a pair of scores for one, and keep 8
+//       bits of P for 11 (trees of 244 rows by the query-rows kernel, which does
+//       that: 598 us for 449 here).
 //
-// Bound: per pair of row groups and key tile the tensor core runs 4 x 512
-// cycles; the softmax threads 2 x (128 exponentials, a maximum, a fused
-// multiply-add, a sum and half a conversion each) on the other pipes.
+// TMEM has room for both O (2 x 128 columns), both P (2 x 64) and one S of 128
+// keys, which the groups use in turn: the softmax threads read a row of scores
+// whole (128 registers of 184), after which the other group's scores take its
+// place, while their exponentials run and the last tile's O product fills the
+// gap.  Measured on a prompt of 20001 tokens, 32 heads: S, P and the next S of
+// a group in the same 128 columns 3123 us (every product waits for the one
+// before); two S of 64 keys a group 2611 (a product of 64 keys reads its Q
+// operand from shared memory for half the work: 48 cycles for 32); this 2180
+// to 2290, 1.43 to 1.50 PFLOP/s, 0.75 to 0.79 of what cuBLAS reaches.
+//
+// Up to 128 rows (decode tokens, a prompt's end) both groups hold the same rows
+// and take the tiles in turn, each with a maximum, sum and O of its own, joined
+// at the end: 1.05 us a tile for 1.65 of both groups' rows, 4.7 TB/s over 19
+// tokens of 32769 keys, 8 heads.
+//
+// Bound, 256 rows: the tensor core needs 2048 cycles a tile, a tile takes about
+// 2900.  The rest is the chain score product -> read -> maximum -> exponentials
+// -> P -> O product, each step of it near 200 cycles of waits and arrivals
+// (without the exponentials, the maximum or the conversions: 3 to 4 % less
+// each).  Between items Q's conversion (about 5000 cycles a group) and O's way
+// out are not hidden: 12 to 15 thousand cycles an item, 40 % of a prompt of
+// 3000 tokens (405 to 440 us for five such, floor 218).
 //
 // Roles (512 threads, one CTA an SM): warps 0-3 and 4-7 softmax of the two row
-// groups (thread = row = TMEM lane; S and O 128 columns each, a group's S, P
-// and next S in the same columns); 8-11 Q and V conversion; 12 and 13 issue a
-// group's MMAs (one warp alone issues an MMA every 70 to 100 cycles); 14 and
-// 15 load K and V tiles by TMA, one box a page.  The CTA takes items in turns,
-// forth and back through a list ordered by length; the loads, conversions and
-// first products of an item run under the end of the one before it.
+// groups (thread = row = TMEM lane) and O's way out; 8-11 Q and V conversion; 12
+// issues the MMAs; 14 and 15 load K and V tiles by TMA, one box a page (13 idles).
+// The CTA takes items in turns, forth and back through a list ordered by cost;
+// the loads and conversions of an item run under the end of the one before it.
 //
 // Every wait is bounded: a role that gives up sets the abort flag and the
 // status word, the others stop at their next wait, copies and MMAs in flight
 // are drained and TMEM is freed.
+//
+// kTree: the same over a decode plan's work items (mj_decode_attn_tree): packed
+// rows, context keys by a range and a prefix, the last keys a tree's nodes by
+// the row's bits of the mask, spans.  Rows without a node compute too and are
+// written as rows without a key.
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -458,7 +480,10 @@ prompt_attn_kernel(const std::conditional_t<kTree, PromptTreeDev, PromptDev> a, 
               if (!more) oph ^= 1u << w;
             }
           }
-          if (load_v && leader) ptx::mma_commit(fempty(vs));
+          if (load_v && leader) {
+            ok &= wait(ffull(vs), vph);  // (also where no group's rows see the tile)
+            ptx::mma_commit(fempty(vs));
+          }
           __syncwarp();
           if (load_k && ++ks == SK) {
             ks = 0;

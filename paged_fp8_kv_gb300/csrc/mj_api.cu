@@ -338,7 +338,8 @@ mj_status decode_step(const mj_decode_params& p, const mj_decode_args& a, const 
   if (tree && kc.kind == KernelKind::kTensorCoreQRows && kc.rows_per_cta == 256 && p.kv_format == MJ_KV_E4M3) {
     // The prompts' kernel holds P in half precision and converts V once for 256
     // rows (32 trees of up to 61 tokens x 4 heads before 2048 to 32768 keys:
-    // 598 us by the query-rows kernel's pairs, whose P goes in two e4m3 parts).
+    // 419 to 445 us; 598 by the query-rows kernel's pairs, whose P goes in two
+    // e4m3 parts).
     // It takes one q tile of 256 rows a CTA, so few rows stay where they are.
     const int sms = device_sm_count();
     if (sms < 1) return MJ_ERR_CUDA;

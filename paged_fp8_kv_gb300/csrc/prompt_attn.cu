@@ -15,7 +15,7 @@
 //       for both groups.  Splitting P into e4m3 parts instead would cost the
 //       softmax threads four conversions a pair of scores for one, and keep 8
 //       bits of P for 11 (trees of 244 rows by the query-rows kernel, which does
-//       that: 598 us for 449 here).
+//       that: 598 us for 419 to 445 here).
 //
 // TMEM has room for both O (2 x 128 columns), both P (2 x 64) and one S of 128
 // keys, which the groups use in turn: the softmax threads read a row of scores
@@ -38,7 +38,8 @@
 // (without the exponentials, the maximum or the conversions: 3 to 4 % less
 // each).  Between items Q's conversion (about 5000 cycles a group) and O's way
 // out are not hidden: 12 to 15 thousand cycles an item, 40 % of a prompt of
-// 3000 tokens (405 to 440 us for five such, floor 218).
+// 3000 tokens (405 to 413 us for five such, floor 218).  Half of the next item's
+// first Q laid out before the last V tile: 442 us, that tile's product waits.
 //
 // Roles (512 threads, one CTA an SM): warps 0-3 and 4-7 softmax of the two row
 // groups (thread = row = TMEM lane) and O's way out; 8-11 Q and V conversion; 12

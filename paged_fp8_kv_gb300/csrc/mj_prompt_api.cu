@@ -89,6 +89,8 @@ extern "C" mj_status mj_prompt_plan(const mj_decode_params* params, const int32_
   d.causal = p.causal;
   d.window = std::min(window, 1 << 30);  // no length is longer
   d.max_splits = p.max_splits;
+  d.page_size = p.page_size;
+  d.max_blocks = p.max_blocks;
   d.max_len = static_cast<int64_t>(p.max_blocks) * p.page_size;
   d.head = reinterpret_cast<PromptHeader*>(base);
   d.items = reinterpret_cast<PromptItem*>(base + l.items);

@@ -34,13 +34,14 @@ struct __align__(16) PromptHeader {
   int32_t n_items, n_merges, n_parts, chunk;
   // what it was made for: another shape's attention refuses it
   int32_t num_seqs, num_tokens, h_k, h_r, causal, window, max_splits, magic;
+  int32_t page_size, max_blocks;  // (items' lengths are within these tables)
 };
-constexpr int32_t kPromptMagic = 0x6d6a7070;
+constexpr int32_t kPromptMagic = 0x6d6a7071;
 
 struct PromptPlanDev {
   const int32_t* cu_tokens;
   const int32_t* seq_lens;
-  int32_t num_seqs, num_tokens, h_k, h_r, causal, window, max_splits;
+  int32_t num_seqs, num_tokens, h_k, h_r, causal, window, max_splits, page_size, max_blocks;
   int64_t max_len;
   PromptHeader* head;
   PromptItem* items;    // [items_cap]
@@ -87,7 +88,8 @@ struct PromptDev {
 __device__ __forceinline__ bool prompt_plan_fits(const PromptDev& a) {
   const PromptHeader& h = *a.head;
   return h.magic == kPromptMagic && h.num_seqs == a.num_seqs && h.num_tokens == a.num_tokens && h.h_k == a.h_k &&
-         h.h_r == a.h_r && h.causal == a.causal && h.window == a.window && h.max_splits == a.max_splits;
+         h.h_r == a.h_r && h.causal == a.causal && h.window == a.window && h.max_splits == a.max_splits && h.page_size == a.page_size &&
+         h.max_blocks == a.max_blocks;
 }
 
 // The same kernel over a decode plan's work items (mj_decode_attn_tree above 128

@@ -227,6 +227,8 @@ __global__ void __launch_bounds__(kThreads) prompt_plan_kernel(const PromptPlanD
     a.head->causal = a.causal;
     a.head->window = a.window;
     a.head->max_splits = a.max_splits;
+    a.head->page_size = a.page_size;
+    a.head->max_blocks = a.max_blocks;
     a.head->magic = kPromptMagic;
     if (a.status && (bad || bad_cu)) atomicExch(a.status, kStatusInvalid);
     else if (a.status && !fits) atomicExch(a.status, kStatusCapacity);

@@ -271,3 +271,22 @@ def test_bad_tensors_refused():
         mj.prompt_attn(p.params, **{**good, "plan": p.plan[:64]})
     with pytest.raises(mj.MjError):
         mj.prompt_attn(p.params, **{**good, "workspace": None})
+
+
+@pytest.mark.parametrize("page,fewer", [(16, 1), (32, 0)])
+def test_plan_of_other_tables_refused(page, fewer):
+    """A plan for longer tables or other pages names keys that this call's table does not list."""
+    p = Prompt([90, 33], [40, 33], 1, 4, 16, extra_blocks=2)
+    c = p.c
+    blocks = c.max_blocks - fewer if page == 16 else c.max_blocks
+    params = mj.make_params(2, 1, 1, 4, page, blocks, c.num_pages, max_splits=256)
+    assert mj.prompt_plan_bytes(params, 73) == p.plan.numel()
+    p.make_plan()
+    k, v = (x if page == 16 else x[: c.num_pages // 2 * 2].view(-1, page, 1, D) for x in (c.k, c.v))
+    if page != 16:
+        params.num_pages = k.shape[0]
+    mj.prompt_attn(params, q=p.q, k_cache=k, v_cache=v, block_table=c.table[:, :blocks].contiguous(), plan=p.plan, q_descale=p.qd,
+                   k_descale=c.kd, v_descale=c.vd, o=p.o, lse=p.lse, workspace=p.ws, softmax_scale=D**-0.5, status=p.status)
+    torch.cuda.synchronize()
+    assert int(p.status.item()) == mj.MJ_ERR_INVALID_ARG
+    assert torch.isnan(p.o).all() and torch.isnan(p.lse).all()

@@ -716,7 +716,8 @@ typedef struct {
  *                 written, the others left as they are
  *   seq_lens_out  int32[num_seqs] (may be seq_lens)
  *   cu_tokens     optional out int32[num_seqs + 1]: tokens of the sequences
- *                 before (as mj_rope_append and mj_prompt_plan take it)
+ *                 before (as mj_rope_append and mj_prompt_plan take it), at
+ *                 most 2^31 - 1
  *   positions     optional out int32[num_tokens]: each new token's position
  *   slots         optional out int64[num_tokens]: page * page_size + row of
  *                 each new token

@@ -198,7 +198,8 @@ __global__ void __launch_bounds__(kThreads, 1) reserve_kernel(const PagesDev a) 
   if (ctas > 1) cluster_sync();
   for (int b = rank * kThreads + tid; b < a.num_seqs; b += ctas * kThreads) {
     const int old = held[b];
-    a.seq_lens_out[b] = old >= 0 ? old + tok[b + 1] - tok[b] : a.seq_lens[b];
+    // (the sums of tokens may have been clamped)
+    a.seq_lens_out[b] = old >= 0 ? old + (a.new_tokens ? a.new_tokens[b] : a.q_len) : a.seq_lens[b];
   }
   if (a.cu_tokens)
     for (int b = rank * kThreads + tid; b <= a.num_seqs; b += ctas * kThreads) a.cu_tokens[b] = tok[b];

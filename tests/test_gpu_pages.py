@@ -155,3 +155,19 @@ def test_reserve_then_release_gives_every_page_back():
         used = [d["block_table"][b, : -(-int(n) // page)].tolist() for b, n in enumerate(lens)]
         free = d["free_pages"][: int(d["num_free"].item())].tolist()
         assert sorted(sum(used, []) + free) == list(range(pages)) and int(status.item()) == 0
+
+
+def test_reserve_behind_impossible_demands():
+    """More tokens in all than an int32 counts, of sequences left out: those behind them get theirs."""
+    most = 2**31 - 1
+    d = dict(seq_lens=_dev(np.array([0, 7, 3, 16], np.int32)), free_pages=_dev(np.arange(4, dtype=np.int32)),
+             num_free=_dev(np.array([2], np.int32)), block_table=torch.full((4, 3), -1, dtype=torch.int32, device="cuda"),
+             seq_lens_out=torch.zeros(4, dtype=torch.int32, device="cuda"), cu_tokens=torch.zeros(5, dtype=torch.int32, device="cuda"))
+    d["block_table"][2, 0] = 3
+    d["block_table"][3, 0] = 2
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    mj.pages_reserve(mj.make_page_params(4, 16, 3, 4), new_tokens=_dev(np.array([most, most, 14, 1], np.int32)), status=status, **d)
+    assert d["seq_lens_out"].tolist() == [0, 7, 17, 17]
+    assert d["block_table"].tolist() == [[-1] * 3, [-1] * 3, [3, 1, -1], [2, 0, -1]]
+    assert d["cu_tokens"].tolist() == [0, most, most, most, most] and d["num_free"].item() == 0
+    assert int(status.item()) == mj.MJ_ERR_INVALID_ARG

@@ -754,7 +754,7 @@ typedef struct {
  * (taken as 0).  A step whose status is not 0 must not append its tokens.
  * Deterministic.
  * Errors: MJ_ERR_INVALID_ARG, MJ_ERR_UNSUPPORTED (page_size, num_seqs, over
- * 2^30 slots a sequence), MJ_ERR_CUDA. */
+ * 2^30 slots a sequence, pages or num_tokens), MJ_ERR_CUDA. */
 mj_status mj_pages_reserve(const mj_page_params* params, const mj_reserve_args* args, mj_stream_t stream);
 
 /* Arguments of mj_pages_release, device memory.

@@ -13,11 +13,15 @@
 namespace mj {
 namespace {
 
+// entries of the free list, and tokens of a call: the kernels' threads count past
+// them in int32 by a few thousand
+constexpr int32_t kMaxEntries = 1 << 30;
+
 mj_status check_pages(const mj_page_params* p) {
   if (!p) return MJ_ERR_INVALID_ARG;
   if (p->num_seqs < 1 || p->max_blocks < 1 || p->num_pages < 1) return MJ_ERR_INVALID_ARG;
   if (!page_size_ok(p->page_size) || p->num_seqs > kMaxDevicePlanSeqs) return MJ_ERR_UNSUPPORTED;
-  if (static_cast<int64_t>(p->max_blocks) * p->page_size > (int64_t{1} << 30)) return MJ_ERR_UNSUPPORTED;
+  if (p->num_pages > kMaxEntries || static_cast<int64_t>(p->max_blocks) * p->page_size > (int64_t{1} << 30)) return MJ_ERR_UNSUPPORTED;
   return MJ_OK;
 }
 
@@ -51,6 +55,7 @@ extern "C" mj_status mj_pages_reserve(const mj_page_params* params, const mj_res
   if (!a.seq_lens || !a.free_pages || !a.num_free || !a.num_free_out || !a.block_table || !a.seq_lens_out)
     return MJ_ERR_INVALID_ARG;
   if ((!a.new_tokens && a.q_len < 1) || a.num_tokens < 0) return MJ_ERR_INVALID_ARG;
+  if (a.num_tokens > kMaxEntries) return MJ_ERR_UNSUPPORTED;
   for (const void* x :
        {static_cast<const void*>(a.seq_lens), static_cast<const void*>(a.new_tokens),
         static_cast<const void*>(a.free_pages), static_cast<const void*>(a.num_free),

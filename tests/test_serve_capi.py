@@ -53,7 +53,8 @@ def _release():
 def test_page_params_refused(make):
     p, a, call = make()
     for field, value, want in [("num_seqs", 0, BAD), ("max_blocks", 0, BAD), ("num_pages", 0, BAD), ("page_size", 24, UNSUP),
-                               ("page_size", 256, UNSUP), ("num_seqs", 16385, UNSUP), ("max_blocks", (1 << 26) + 1, UNSUP)]:
+                               ("page_size", 256, UNSUP), ("num_seqs", 16385, UNSUP), ("max_blocks", (1 << 26) + 1, UNSUP),
+                               ("num_pages", (1 << 30) + 1, UNSUP)]:
         _refused(call, p, field, value, want)
 
 
@@ -77,6 +78,7 @@ def test_reserve_counts_and_overlaps_refused():
         _refused(call, a, "q_len", q_len, BAD)
     a.q_len = 1
     _refused(call, a, "num_tokens", -1, BAD)
+    _refused(call, a, "num_tokens", (1 << 30) + 1, UNSUP)
     _refused(call, a, "slots", a.slots + 4, BAD)  # 64-bit entries
     for out in ("seq_lens_out", "block_table", "positions", "cu_tokens"):
         _refused(call, a, out, a.free_pages + 4, BAD)

@@ -95,7 +95,8 @@ struct Cfg {
   static constexpr int kOffQ = kOffVf + kVf * kVfTile;           // [group][part]
   static constexpr int kOffOut = kOffQ + 2 * kParts * kTile;     // [softmax warp] 32 rows x 64 bytes of O on their way out
   static constexpr int kOffShift = kOffOut + 8 * 2048;           // [group][2][128] s of each row
-  static constexpr int kOffBar = kOffShift + 2 * 256;
+  static constexpr int kOffStat = kOffShift + 2 * 256;           // maximum and sum of the second group's rows
+  static constexpr int kOffBar = kOffStat + 128 * 8;
   static constexpr int kBars = 2 * (kSK + kSV + kVf) + 1 + 6 * 2 + 2;
   static constexpr int kOffMisc = kOffBar + kBars * 8;
   static constexpr int kBytes = kOffMisc + 16 + 1024;
@@ -831,8 +832,10 @@ prompt_attn_kernel(const std::conditional_t<kTree, PromptTreeDev, PromptDev> a, 
       const bool any = g1 > g0;
       if (any && !wait(gbar(w, 2), (q - 1) & 1)) give_up(abort_flag, a.status);
       if (__any_sync(0xffffffffu, *abort_flag != 0)) break;  // nothing is written out after that
-      // the second group's row statistics go to the first one, which reads both O
-      float* const stat = reinterpret_cast<float*>(sm + C::kOffOut + 4 * 2048) + 2 * r;
+      // The second group's row statistics go to the first one, which reads both O
+      // (and gives them free with O, without which no later item's are written;
+      // the second group may be writing out an item without keys by then).
+      float* const stat = reinterpret_cast<float*>(sm + C::kOffStat) + 2 * r;
       float m1 = -INFINITY, l1 = 0.f;
       if (dual) {
         if (w == 1) {

@@ -36,16 +36,19 @@ I32 = dict(dtype=torch.int32, device="cuda")
 
 class Cache:
     """Pools with sequences of `lens` keys on random pages; rows past each
-    sequence's end and pages of no sequence hold NaN codes."""
+    sequence's end and pages of no sequence hold NaN codes.  The first `ahead`
+    pages are nobody's."""
+
+    ahead = 0
 
     def __init__(self, lens, h_k, page, seed=0, extra_blocks=0, spread=1.0):
         rng = np.random.default_rng(seed)
         gen = torch.Generator("cuda").manual_seed(seed)
         self.lens, self.h_k, self.page = list(lens), h_k, page
         need = [-(-n // page) for n in lens]
-        self.num_pages = sum(need) + 3
+        self.num_pages = self.ahead + sum(need) + 3
         self.max_blocks = max(1, max(need)) + extra_blocks
-        perm = rng.permutation(self.num_pages)
+        perm = self.ahead + rng.permutation(self.num_pages - self.ahead)
         table = rng.integers(-(2**31), 2**31 - 1, (len(lens), self.max_blocks)).astype(np.int32)  # never read past the end
         at = 0
         self.k, self.v = (torch.full((self.num_pages, page, h_k, 128), 0x7F, dtype=torch.uint8, device="cuda") for _ in range(2))

@@ -290,3 +290,14 @@ def test_plan_of_other_tables_refused(page, fewer):
     torch.cuda.synchronize()
     assert int(p.status.item()) == mj.MJ_ERR_INVALID_ARG
     assert torch.isnan(p.o).all() and torch.isnan(p.lse).all()
+
+
+@pytest.mark.parametrize("h_k,h_r", [(1, 4), (2, 8)])
+def test_shared_rows_before_short_items(h_k, h_r):
+    """Items whose rows both row groups hold, an odd number of tiles, and behind them on the same CTA items in which the
+    second group has no tile: its rows' statistics of the first kind must outlive the second."""
+    lens = [300] * 200 + [60] * 200 + [0, 5]
+    news = [1] * 400 + [0, 1]
+    Prompt(lens, news, h_k, h_r, 64).run().check()
+    p = Prompt([300] * 200 + [20] * 20, [1] * 200 + [129 // h_r + 31] * 20, h_k, h_r, 64, seed=1)  # tokens ahead of any key
+    p.run().check()

@@ -599,10 +599,6 @@ prompt_attn_kernel(const std::conditional_t<kTree, PromptTreeDev, PromptDev> a, 
         ++n;
         return true;
       };
-      // The first tile's buffer is free before the last item's Q is read; the
-      // others' V after this item's Q.
-      ok = convert(it.t0);
-      if (!ok) break;
       // ---- Q: this warp lays out 32 of a group's 128 rows, eight lanes a row
       // (a lane 16 elements: one 16-byte chunk of each part), four rows a turn
       constexpr int kVecs = kQe4m3 ? 1 : 2;  // 16-byte loads a lane and row
@@ -662,11 +658,16 @@ prompt_attn_kernel(const std::conditional_t<kTree, PromptTreeDev, PromptDev> a, 
               // lo = e4m3(x - hi), the difference exact: hi + lo is within 2^-10
               const uint32_t v8[8] = {raw[i][0].x, raw[i][0].y, raw[i][0].z, raw[i][0].w,
                                       raw[i][kVecs - 1].x, raw[i][kVecs - 1].y, raw[i][kVecs - 1].z, raw[i][kVecs - 1].w};
-              uint32_t top = 0;
+              uint32_t m2[8];  // pairs of magnitudes
 #pragma unroll
-              for (int e = 0; e < 8; ++e) top = max(top, max(v8[e] & 0x7FFFu, (v8[e] >> 16) & 0x7FFFu));
+              for (int e = 0; e < 8; ++e) m2[e] = v8[e] & 0x7FFF7FFFu;
 #pragma unroll
-              for (int o = 4; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+              for (int o = 4; o >= 1; o >>= 1)
+#pragma unroll
+                for (int e = 0; e < o; ++e) m2[e] = __vmaxu2(m2[e], m2[e + o]);
+#pragma unroll
+              for (int o = 4; o >= 1; o >>= 1) m2[0] = __vmaxu2(m2[0], __shfl_xor_sync(0xffffffffu, m2[0], o));
+              const uint32_t top = max(m2[0] & 0xFFFFu, m2[0] >> 16);
               int shift = 134 - static_cast<int>(top >> 7);  // 7 - exponent
               shift = top == 0 ? 0 : (shift > 126 ? 126 : (shift < -126 ? -126 : shift));
               const float qs = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
@@ -698,7 +699,7 @@ prompt_attn_kernel(const std::conditional_t<kTree, PromptTreeDev, PromptDev> a, 
         if (lane == 0) ptx::mbar_arrive(gbar(w, 4));
       }
       if (!ok) break;
-      if (it.t0 + 1 < it.t1) ok = convert(it.t0 + 1);
+      ok = convert(it.t0);
       if (!ok) break;
       // the next item's Q is on its way to L2 meanwhile
       if (unit_at(k + 1) < units) {
@@ -715,7 +716,7 @@ prompt_attn_kernel(const std::conditional_t<kTree, PromptTreeDev, PromptDev> a, 
           }
         }
       }
-      for (int t = it.t0 + 2; ok && t < it.t1; ++t) ok = convert(t);
+      for (int t = it.t0 + 1; ok && t < it.t1; ++t) ok = convert(t);
     }
     if (!ok && lane == 0) give_up(abort_flag, a.status);
   } else {
@@ -739,8 +740,18 @@ prompt_attn_kernel(const std::conditional_t<kTree, PromptTreeDev, PromptDev> a, 
       int g0 = 0, g1 = 0, lo = 0, lim = INT32_MAX;  // the group's tiles; the row sees keys lo .. lim
       bool dual;                                    // both groups hold these rows and take turns
       int pfx = 0, prefix_tiles = 0, jump = 0;      // kTree: and those below pfx, and nodes by its mask
+      // reference maximum (in units of the scores as read), sum of 2^kPBias p,
+      // score -> log2 units, or over the cap (less the shift of the row's Q, which
+      // is not known yet)
+      float m_run = -INFINITY, l_run = 0.f, c2 = 1.f, cap_c1 = 0.f;
       {
-        const Item it = load_item(unit());
+        const int u = unit(), g = u % a.h_k;
+        const Item it = load_item(u);
+        const float raw_l = a.softmax_scale * a.qd[it.b * a.qd_seq + g * a.qd_head] * a.kd[it.b * a.kd_seq + g * a.kd_head];
+        if constexpr (kCap)  // scores become logits in log2 units as they are read
+          cap_c1 = raw_l / a.softcap;
+        else
+          c2 = raw_l * kLog2e;
         dual = it.g1[1] < 0;
         g0 = dual ? it.t0 + w : (w ? it.g0[1] : it.g0[0]);
         g1 = dual ? it.t1 : (w ? it.g1[1] : it.g1[0]);
@@ -765,21 +776,16 @@ prompt_attn_kernel(const std::conditional_t<kTree, PromptTreeDev, PromptDev> a, 
           }
         }
       }
-      // reference maximum (in units of the scores as read), sum of 2^kPBias p,
-      // score -> log2 units
-      float m_run = -INFINITY, l_run = 0.f, c2 = 1.f, cap_c1 = 0.f;
       for (int t = g0; t < g1; t += dual ? 2 : 1, ++q) {
         const int key0 = kTree ? (t < prefix_tiles ? t : t + jump) * kRows : t * kRows;
         if (!wait(gbar(w, 0), q & 1)) give_up(abort_flag, a.status);
         ptx::tc_fence_after();
-        if (t == g0) {  // the row's scale is there since its Q was laid out
-          const int u = unit(), g = u % a.h_k, b = load_item(u).b;
-          float raw_l = a.softmax_scale * a.qd[b * a.qd_seq + g * a.qd_head] * a.kd[b * a.kd_seq + g * a.kd_head];
-          if constexpr (!kQe4m3) raw_l *= __uint_as_float(static_cast<uint32_t>(127 - q_shift[(2 * w + (items & 1)) * 128 + r]) << 23);
-          if constexpr (kCap)  // scores become logits in log2 units as they are read
-            cap_c1 = raw_l / a.softcap;
+        if (!kQe4m3 && t == g0) {  // the row's shift is there since its Q was laid out
+          const float f = __uint_as_float(static_cast<uint32_t>(127 - q_shift[(2 * w + (items & 1)) * 128 + r]) << 23);
+          if constexpr (kCap)
+            cap_c1 *= f;
           else
-            c2 = raw_l * kLog2e;
+            c2 *= f;
         }
         const bool unmasked = __all_sync(0xffffffffu, (key0 >= lo && key0 + kRows - 1 <= lim) || (kTree && key0 + kRows <= pfx));
         uint32_t s[kRows];
@@ -868,6 +874,30 @@ prompt_attn_kernel(const std::conditional_t<kTree, PromptTreeDev, PromptDev> a, 
       if (g1 > g0) ++items;
       // ---- epilogue: O, or its part, of this group's rows
       const bool any = g1 > g0;
+      // (what does not depend on O is looked up while the last product runs)
+      const int u = unit(), g = u % a.h_k;
+      const Item it = load_item(u);
+      const int row = it.row0 + (dual ? 0 : w * kRows) + r;
+      const bool live = row < it.n_tok * a.h_r;
+      const int tok = live ? row / a.h_r : 0;
+      const int hr = live ? row - tok * a.h_r : 0;
+      const bool final_out = it.part < 0;
+      const float vd = a.vd[it.b * a.vd_seq + g * a.vd_head];
+      int64_t part_row;
+      if constexpr (kTree)
+        part_row = mj::part_row(a.t, it.b, g, it.part, live ? row : 0);
+      else
+        part_row = (static_cast<int64_t>(it.part) * a.h_k + g) * kPromptRows + w * kRows + r;
+      const int64_t orow = final_out ? prompt_at(a.o_rows, it.b, it.tok0 + tok, g, hr) : part_row * kHeadDimDev;
+      uint8_t* dst[4];
+      bool on[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = 8 * j + (lane >> 2);
+        const int64_t at = __shfl_sync(0xffffffffu, orow, i);
+        on[j] = __shfl_sync(0xffffffffu, static_cast<int>(live), i) != 0;
+        dst[j] = (final_out ? reinterpret_cast<uint8_t*>(a.o + at) : reinterpret_cast<uint8_t*>(a.o_part + at)) + (lane & 3) * 16;
+      }
       if (any && !wait(gbar(w, 2), (q - 1) & 1)) give_up(abort_flag, a.status);
       if (__any_sync(0xffffffffu, *abort_flag != 0)) break;  // nothing is written out after that
       // The second group's row statistics go to the first one, which reads both O
@@ -891,43 +921,21 @@ prompt_attn_kernel(const std::conditional_t<kTree, PromptTreeDev, PromptDev> a, 
         l1 = x.y;
       }
       ptx::tc_fence_after();
-      const int u = unit(), g = u % a.h_k;
-      const Item it = load_item(u);
-      const int row = it.row0 + (dual ? 0 : w * kRows) + r;
-      const bool live = row < it.n_tok * a.h_r;
-      const int tok = live ? row / a.h_r : 0;
-      const int hr = live ? row - tok * a.h_r : 0;
-      const bool final_out = it.part < 0;
       const float mx = fmaxf(m_run, m1);
       const float f0 = m_run == -INFINITY ? 0.f : fast_exp2((m_run - mx) * c2), f1 = m1 == -INFINITY ? 0.f : fast_exp2((m1 - mx) * c2);
       m_run = mx;
       float l = (l_run * f0 + l1 * f1) * (1.f / 128.f);  // 2^-kPBias
       bool seen = m_run > -INFINITY;
       if constexpr (kTree) seen = seen && tok < tree_shape(a.t, it.b, it.len).nodes;
-      float f = a.vd[it.b * a.vd_seq + g * a.vd_head] * (1.f / 128.f) * (final_out ? a.scale_o / (seen ? l : 1.f) : 1.f);
+      float f = vd * (1.f / 128.f) * (final_out ? a.scale_o / (seen ? l : 1.f) : 1.f);
       if (kTree && !seen) l = f = 0.f;
       const float fa = f * f0, fb = f * f1;  // of this group's O and, where rows are shared, of the other's
-      int64_t part_row;
-      if constexpr (kTree)
-        part_row = mj::part_row(a.t, it.b, g, it.part, live ? row : 0);
-      else
-        part_row = (static_cast<int64_t>(it.part) * a.h_k + g) * kPromptRows + w * kRows + r;
-      const int64_t orow = final_out ? prompt_at(a.o_rows, it.b, it.tok0 + tok, g, hr) : part_row * kHeadDimDev;
       // A lane holds a row; the rows leave through shared memory, 64 bytes of each
       // at a time, as pieces of four lanes (16 bytes a lane and row would be 32
       // half-used sectors an instruction): 16-byte chunk c of row i at chunk
       // c ^ (i / 2 % 4) of its 64 bytes
       uint8_t* const out = sm + C::kOffOut + warp * 2048;
       uint8_t* const mine = out + lane * 64;
-      uint8_t* dst[4];
-      bool on[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int i = 8 * j + (lane >> 2);
-        const int64_t at = __shfl_sync(0xffffffffu, orow, i);
-        on[j] = __shfl_sync(0xffffffffu, static_cast<int>(live), i) != 0;
-        dst[j] = (final_out ? reinterpret_cast<uint8_t*>(a.o + at) : reinterpret_cast<uint8_t*>(a.o_part + at)) + (lane & 3) * 16;
-      }
       auto emit = [&](const uint4 (&v)[4]) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4*>(mine + ((c ^ ((lane >> 1) & 3)) << 4)) = v[c];

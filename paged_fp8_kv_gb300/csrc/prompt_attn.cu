@@ -36,10 +36,13 @@
 // 2900.  The rest is the chain score product -> read -> maximum -> exponentials
 // -> P -> O product, each step of it near 200 cycles of waits and arrivals
 // (without the exponentials, the maximum or the conversions: 3 to 4 % less
-// each).  Between items Q's conversion (about 5000 cycles a group) and O's way
-// out are not hidden: 12 to 15 thousand cycles an item, 40 % of a prompt of
-// 3000 tokens (405 to 413 us for five such, floor 218).  Half of the next item's
-// first Q laid out before the last V tile: 442 us, that tile's product waits.
+// each).  Between items Q's conversion (about 5500 cycles a group, from its last
+// score product on) and O's way out (5500) are hidden in part: about 12 thousand
+// cycles an item of a prompt of 3000 tokens (384 to 400 us for five such, floor
+// 218).  Measured and not kept: the first V tile ahead of Q 407 us; half of the
+// next Q ahead of the last V tile 442; all of O read before any of it is written
+// 412.  Changes of a few hundred instructions anywhere move each case by 3 % one
+// way or the other: the loops are as large as the instruction caches.
 //
 // Roles (512 threads, one CTA an SM): warps 0-3 and 4-7 softmax of the two row
 // groups (thread = row = TMEM lane) and O's way out; 8-11 Q and V conversion; 12
@@ -566,7 +569,9 @@ prompt_attn_kernel(const std::conditional_t<kTree, PromptTreeDev, PromptDev> a, 
         const int key0 = tile_key<kTree>(it, t);
         uint8_t* const dst = sm + C::kOffVf + vf * kVfTile;
         const int cc = lane & 7;
-#pragma unroll
+        // (the roles' code contends for the instruction caches: unrolled whole, five
+        // prompts take 397 us, so 384)
+#pragma unroll 2
         for (int i = 0; i < 8; ++i) {
           const int r = cw * 32 + i * 4 + (lane >> 3);
           uint4 x = *reinterpret_cast<const uint4*>(src + swz(r, cc));

@@ -301,3 +301,25 @@ def test_shared_rows_before_short_items(h_k, h_r):
     Prompt(lens, news, h_k, h_r, 64).run().check()
     p = Prompt([300] * 200 + [20] * 20, [1] * 200 + [129 // h_r + 31] * 20, h_k, h_r, 64, seed=1)  # tokens ahead of any key
     p.run().check()
+
+
+def test_more_items_than_are_ordered():
+    """Over 8192 work items: the list stays in the sequences' order; sequences without tokens between."""
+    rng = np.random.default_rng(0)
+    news = rng.integers(0, 3, 12500)
+    lens = news + rng.integers(0, 40, 12500)
+    p = Prompt(lens.tolist(), news.tolist(), 1, 2, 16)
+    p.run()
+    assert p.plan_head()[0] > 8192
+    keep = rng.choice(np.nonzero(news)[0], 400, replace=False)
+    at = np.concatenate([[0], np.cumsum(news)])
+    c, sel = p.c, sorted(keep.tolist())
+    for b in sel:
+        n, L, t0 = int(news[b]), c.lens[b], int(at[b])
+        k, v = c.rows(c.k, b), c.rows(c.v, b)
+        seen = torch.arange(L, device="cuda")[None] <= torch.arange(L - n, L, device="cuda")[:, None]
+        for h in range(2):
+            scale = float(c.kd[b, 0].double()) * D**-0.5
+            ref = attend(value_of(p.q[t0 : t0 + n, h]), k[0], v[0] * c.vd[b, 0].double() * 0.75, scale, seen, 0.0, HALF_P)
+            check_rows(p.o[t0 : t0 + n, h], p.lse[t0 : t0 + n, h], ref, f"sequence {b}, head {h}")
+    assert not torch.isnan(p.o).any()

@@ -6,7 +6,8 @@ import pytest
 import torch
 
 import paged_fp8_kv_gb300 as mj
-from oracle import serve_ref
+from oracle import e4m3_table, serve_ref
+from oracle.narrow_ref import pack_bits, to_e4m3_codes
 from tests.serving_helpers import I32, SPLIT_P, Cache, attend, check_rows, value_of
 
 pytestmark = pytest.mark.gpu
@@ -223,3 +224,25 @@ def test_commit_reports(path, count, length, bad_page):
     assert int(status.item()) == mj.MJ_ERR_INVALID_ARG
     assert all(torch.equal(x, y) for x, y in zip(pools, before))
     assert new.item() == (34 if bad_page else length)
+
+
+@pytest.mark.parametrize("kv", ["e2m1", "e2m3", "e3m2"])
+@pytest.mark.parametrize("q_len,h_r", [(4, 2), (4, 4), (8, 4), (13, 4), (31, 4), (61, 4)])
+def test_tree_over_narrow_pools(q_len, h_r, kv):
+    """Codes of a narrow format, by every row count's kernel, against the e4m3 codes of equal value."""
+    nodes = [q_len, max(1, q_len // 2), 1]
+    t = Tree([400, 128 + q_len, 61], nodes, q_len, 2, h_r, 32, seed=q_len)
+    c, bits = t.c, 4 if kv == "e2m1" else 6
+    codes = [c.rng.integers(0, 2**bits, (c.num_pages, c.page, 2, D)).astype(np.uint8) for _ in range(2)]
+    for pool, x in zip((c.k, c.v), codes):
+        pool.copy_(torch.from_numpy(to_e4m3_codes(x, kv, e4m3_table())))
+    k, v = (torch.from_numpy(pack_bits(x, bits)).cuda() for x in codes)
+    p = mj.make_params(3, q_len, 2, h_r, 32, c.max_blocks, c.num_pages, max_splits=16, kv_format=mj.KV_FORMATS[kv])
+    plan = mj.decode_plan(p, c.lens)
+    mj.decode_attn_tree(p, tree_mask=t.mask, tree_lens=t.tree_lens, q=t.q, k_cache=k, v_cache=v, block_table=c.table,
+                        seq_lens=c.seq_lens, work=torch.from_numpy(plan.work).cuda(), n_splits=torch.from_numpy(plan.n_splits).cuda(),
+                        q_descale=t.qd, k_descale=c.kd, v_descale=c.vd, o=t.o, lse=t.lse, softmax_scale=D**-0.5, scale_o=0.75,
+                        workspace=torch.empty(mj.workspace_bytes(p), dtype=torch.uint8, device="cuda"), status=t.status,
+                        max_n_splits=plan.max_n_splits)
+    assert int(t.status.item()) == 0
+    t.check()

@@ -882,14 +882,30 @@ typedef struct {
   const int32_t* tree_lens;
 } mj_tree;
 
+/* mj_score_spans for trees: spans[4 b] = (n_prefix, first, L_b, 0), where the
+ * nodes' key_begin and the prefix leave out context keys that no node sees; key_begin
+ * of rows without a node is not looked at, nor params->causal.  A sequence
+ * without a node has the span (0, 0, 0, 0).
+ *   tree         tree_lens (HOST memory in mj_tree_spans, device memory in
+ *                mj_tree_spans_device) or NULL there; the mask is not looked at
+ *   mod          as in mj_decode_attn_tree; pointers HOST or device alike
+ * The rest, and the errors, as there; MJ_ERR_UNSUPPORTED for a mod that
+ * mj_decode_attn_tree refuses. */
+mj_status mj_tree_spans(const mj_decode_params* params, const mj_tree* tree, const mj_score_mod* mod,
+                        const int32_t* seq_lens_host, int32_t* spans_host, int32_t* plan_lens_host);
+mj_status mj_tree_spans_device(const mj_decode_params* params, const mj_tree* tree, const mj_score_mod* mod,
+                               const int32_t* seq_lens, int32_t* spans, int32_t* plan_lens, mj_stream_t stream);
+
 /* mj_decode_attn_mod for trees.  The same arguments and results; params->causal
  * is not looked at.  mod (NULL: none) may hold a softcap, key_begin (node i sees
  * context keys from key_begin[b*q_len + i] on: the window of a token whose
  * position is its depth) and prefix (context keys seen ahead of that); a
  * window, slopes or key_end, which take positions for slots, are refused
- * (MJ_ERR_UNSUPPORTED).  spans as there, of mj_score_spans with the same mod
- * and params, for which every key_begin entry, also of rows without a node, is
- * at most ctx. */
+ * (MJ_ERR_UNSUPPORTED).  spans as there, of mj_tree_spans or
+ * mj_tree_spans_device with the same tree, mod and params (mj_score_spans ends
+ * a row's keys by its place among q_len rows, which is not a node's context):
+ * spans that leave out a key which a node may see become MJ_ERR_INVALID_ARG in
+ * the status word, and that sequence's rows lack those keys. */
 mj_status mj_decode_attn_tree(const mj_decode_params* params, const mj_tree* tree, const mj_score_mod* mod,
                               const int32_t* spans, const mj_decode_args* args, mj_stream_t stream);
 

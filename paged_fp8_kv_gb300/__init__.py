@@ -409,6 +409,10 @@ def lib() -> ctypes.CDLL:
         L.mj_prompt_attn.argtypes = [P(DecodeParams), P(PromptArgs), _vp]
         L.mj_decode_attn_tree.restype = ctypes.c_int
         L.mj_decode_attn_tree.argtypes = [P(DecodeParams), P(TreeArgs), P(ScoreModArgs), _vp, P(DecodeArgs), _vp]
+        L.mj_tree_spans.restype = ctypes.c_int
+        L.mj_tree_spans.argtypes = [P(DecodeParams), P(TreeArgs), P(ScoreModArgs), _vp, _vp, _vp]
+        L.mj_tree_spans_device.restype = ctypes.c_int
+        L.mj_tree_spans_device.argtypes = [P(DecodeParams), P(TreeArgs), P(ScoreModArgs), _vp, _vp, _vp, _vp]
         L.mj_tree_commit.restype = ctypes.c_int
         L.mj_tree_commit.argtypes = [P(DecodeParams), P(CommitArgs), _vp]
         L.mj_kernel_name.restype = ctypes.c_int
@@ -1045,26 +1049,37 @@ class ScoreMod:
 def score_spans(params: DecodeParams, mod: ScoreMod, seq_lens: Sequence[int]) -> Tuple[np.ndarray, np.ndarray]:
     """mj_score_spans on host seq_lens: (spans (num_seqs, 4), plan_lens
     (num_seqs,)), int32.  The modifiers' tensors are read back to the host."""
+    return _spans_host(params, mod, seq_lens, None)
+
+
+def _host_i32(name, t, shape):
+    """A device tensor or host sequence as a host int32 array, or None."""
+    if t is None:
+        return None
+    x = np.ascontiguousarray(t.cpu().numpy() if hasattr(t, "cpu") else np.asarray(t), dtype=np.int32)
+    if x.shape != shape:
+        raise ValueError(f"{name}: shape {x.shape}, expected {shape}")
+    return x
+
+
+def _spans_host(params, mod, seq_lens, tree):
+    """mj_score_spans, or mj_tree_spans with ``tree`` = (tree_lens or None,)."""
     nb, ql = int(params.num_seqs), int(params.q_len)
     sl = np.ascontiguousarray(np.asarray(seq_lens, dtype=np.int32))
     if sl.shape != (nb,):
         raise ValueError(f"seq_lens shape {sl.shape}, expected {(nb,)}")
-
-    def host(name, shape):
-        t = getattr(mod, name)
-        if t is None:
-            return None
-        x = np.ascontiguousarray(t.cpu().numpy() if hasattr(t, "cpu") else np.asarray(t), dtype=np.int32)
-        if x.shape != shape:
-            raise ValueError(f"{name}: shape {x.shape}, expected {shape}")
-        return x
-
-    begin, end, prefix = host("key_begin", (nb, ql)), host("key_end", (nb, ql)), host("prefix", (nb,))
-    m = ScoreModArgs(float(mod.softcap), int(mod.window), None, *(None if x is None else x.ctypes.data for x in (begin, end, prefix)))
+    x = [_host_i32(name, getattr(mod, name), shape) for name, shape in (("key_begin", (nb, ql)), ("key_end", (nb, ql)), ("prefix", (nb,)))]
+    slopes = None if tree is None else _ptr(mod.alibi_slopes)  # (refused for trees, not looked at else)
+    m = ScoreModArgs(float(mod.softcap), int(mod.window), slopes, *(None if y is None else y.ctypes.data for y in x))
     spans = np.zeros((nb, 4), dtype=np.int32)
     plan_lens = np.zeros(nb, dtype=np.int32)
-    st = lib().mj_score_spans(ctypes.byref(params), ctypes.byref(m), sl.ctypes.data, spans.ctypes.data, plan_lens.ctypes.data)
-    _check(st, "mj_score_spans")
+    out = (sl.ctypes.data, spans.ctypes.data, plan_lens.ctypes.data)
+    if tree is None:
+        _check(lib().mj_score_spans(ctypes.byref(params), ctypes.byref(m), *out), "mj_score_spans")
+    else:
+        nodes = _host_i32("tree_lens", tree[0], (nb,))
+        t = TreeArgs(None, 0, None if nodes is None else nodes.ctypes.data)
+        _check(lib().mj_tree_spans(ctypes.byref(params), ctypes.byref(t), ctypes.byref(m), *out), "mj_tree_spans")
     return spans, plan_lens
 
 
@@ -1079,6 +1094,27 @@ def score_spans_device(params: DecodeParams, mod: ScoreMod, seq_lens, spans, pla
     st = lib().mj_score_spans_device(ctypes.byref(params), ctypes.byref(m), _ptr(seq_lens), _ptr(spans), _ptr(plan_lens),
                                      _stream_handle(stream))
     _check(st, "mj_score_spans_device")
+
+
+def tree_spans(params: DecodeParams, mod: Optional[ScoreMod], seq_lens: Sequence[int], tree_lens=None) -> Tuple[np.ndarray, np.ndarray]:
+    """mj_tree_spans on host seq_lens: score_spans for DecodeAttnTree, with
+    its mod and tree_lens (read back to the host)."""
+    return _spans_host(params, ScoreMod() if mod is None else mod, seq_lens, (tree_lens,))
+
+
+def tree_spans_device(params: DecodeParams, mod: Optional[ScoreMod], seq_lens, spans, plan_lens, tree_lens=None, stream=None) -> None:
+    """mj_tree_spans_device: spans (num_seqs, 4) and plan_lens (num_seqs,)
+    int32 from device seq_lens and DecodeAttnTree's mod and tree_lens."""
+    i32, nb = _dtypes()[2], int(params.num_seqs)
+    for name, t, shape in (("seq_lens", seq_lens, (nb,)), ("spans", spans, (nb, 4)), ("plan_lens", plan_lens, (nb,)),
+                           ("tree_lens", tree_lens, (nb,))):
+        if t is not None:
+            _tensor(name, t, (i32,), shape)
+    m = (ScoreMod() if mod is None else mod)._marshal(params)
+    t = TreeArgs(None, 0, _ptr(tree_lens))
+    st = lib().mj_tree_spans_device(ctypes.byref(params), ctypes.byref(t), ctypes.byref(m), _ptr(seq_lens), _ptr(spans),
+                                    _ptr(plan_lens), _stream_handle(stream))
+    _check(st, "mj_tree_spans_device")
 
 
 def _check_queries(params, q):
@@ -1153,7 +1189,8 @@ class DecodeAttnTree(DecodeAttnMod):
     """mj_decode_attn_tree on device tensors: DecodeAttnMod's (mod None, or
     with softcap, key_begin and prefix alone), tree_mask (num_seqs, q_len,
     words) int32, bit m of a token's words set if it sees node m, and tree_lens
-    (num_seqs,) int32 (None: q_len nodes each)."""
+    (num_seqs,) int32 (None: q_len nodes each).  spans and the plan's lengths
+    are of tree_spans."""
 
     _name = "mj_decode_attn_tree"
 

@@ -71,6 +71,7 @@ constexpr int kTileBytes = kRows * 128;      // one K or V tile (128 keys x d): 
 constexpr int kPartBytes = kRows * 128;      // one e4m3 operand of 128 rows x 128 bytes
 constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s: far above any legal wait
 constexpr int kStatusTimeout = 5;            // MJ_ERR_TIMEOUT
+constexpr int kStatusInvalid = 1;            // MJ_ERR_INVALID_ARG
 // P is produced as x = 448 p 2^-kTau: a row's reference maximum m moves only
 // when the tile's maximum passes m + kTau (log2 units), so x stays within
 // e4m3's range and most tiles need no O correction; the result does not
@@ -550,6 +551,7 @@ decode_qm_kernel(const QmArgs<kMod, kTree> a, const __grid_constant__ CUtensorMa
       live = in_range && qi < tree.nodes;
       if (live) {
         const RowRange rr = tree_range(a, b, qi, tree.ctx);
+        if (!tree_span_holds(span, rr, tree) && a.status) atomicExch(a.status, kStatusInvalid);
         lim = rr.hi < span.z - 1 ? rr.hi : span.z - 1;
         lo = rr.lo > span.y ? rr.lo : span.y;
         pfx = rr.pfx < span.x ? rr.pfx : span.x;

@@ -133,6 +133,7 @@ constexpr int kTileKV = 128;                 // KV rows per tile (MMA M)
 constexpr int kKVTileBytes = kTileKV * 128;  // one K or V tile: 16 KB
 constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s: far above any legal wait
 constexpr int kStatusTimeout = 5;            // MJ_ERR_TIMEOUT
+constexpr int kStatusInvalid = 1;            // MJ_ERR_INVALID_ARG
 constexpr uint32_t kNode = 1u << 31;         // kTree: the row is a node of its sequence's tree
 // P is produced as x = 448 p 2^-kTau: a column's reference maximum m moves
 // only when a score passes m + kTau (log2 units), so x stays within e4m3's
@@ -683,6 +684,7 @@ decode_tc_kernel(const TcArgs<kMod, kTree> a, const __grid_constant__ CUtensorMa
           uint32_t bits = 0;
           if (n < a.n_q && qi < tree.nodes) {
             const RowRange rr = tree_range(a, b, qi, tree.ctx);
+            if (!tree_span_holds(span, rr, tree) && a.status) atomicExch(a.status, kStatusInvalid);
             hi = rr.hi < span.z - 1 ? rr.hi : span.z - 1;
             lo = rr.lo > span.y ? rr.lo : span.y;
             bits = tree_bits(a.mask + (static_cast<int64_t>(b) * a.q_len + qi) * a.mask_words, tree.nodes, 0) | kNode;

@@ -413,11 +413,8 @@ extern "C" mj_status mj_decode_attn_tree(const mj_decode_params* params, const m
   if (params->kv_format == MJ_KV_NVFP4 ||
       !(kc.kind == KernelKind::kTensorCoreQRows || (kc.kind == KernelKind::kTensorCore && kc.rows_per_cta <= 16)))
     return MJ_ERR_UNSUPPORTED;
-  // these take positions for slots, which a tree's are not
-  if (mod && (mod->window != 0 || mod->alibi_slopes || mod->key_end)) return MJ_ERR_UNSUPPORTED;
   ScoreModDev m{};
-  const mj_score_mod none{};
-  st = score_mod_dev(*params, mod ? *mod : none, spans, &m);
+  st = tree_mod_dev(*params, mod, spans, &m);
   if (st != MJ_OK) return st;
   return decode_step(*params, *args, &m, tree, stream);
 }

@@ -31,6 +31,13 @@ mj_status score_mod_dev(const mj_decode_params& p, const mj_score_mod& mod, cons
   return MJ_OK;
 }
 
+mj_status tree_mod_dev(const mj_decode_params& p, const mj_score_mod* mod, const int32_t* spans, ScoreModDev* out) {
+  // these take positions for slots, which a tree's are not
+  if (mod && (mod->window != 0 || mod->alibi_slopes || mod->key_end)) return MJ_ERR_UNSUPPORTED;
+  const mj_score_mod none{};
+  return score_mod_dev(p, mod ? *mod : none, spans, out);
+}
+
 }  // namespace mj
 
 using namespace mj;
@@ -204,6 +211,47 @@ extern "C" mj_status mj_score_spans_device(const mj_decode_params* params, const
   const cudaError_t e = launch_score_spans(m, seq_lens, params->num_seqs, params->q_len, params->causal, max_len,
                                            reinterpret_cast<int4*>(spans), plan_lens,
                                            reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MJ_OK : MJ_ERR_CUDA;
+}
+
+extern "C" mj_status mj_tree_spans(const mj_decode_params* params, const mj_tree* tree, const mj_score_mod* mod,
+                                   const int32_t* seq_lens_host, int32_t* spans_host, int32_t* plan_lens_host) {
+  mj_status st = check_params(params);
+  if (st != MJ_OK) return st;
+  if (!tree || !seq_lens_host || !spans_host || !plan_lens_host || !aligned4(tree->tree_lens)) return MJ_ERR_INVALID_ARG;
+  const mj_decode_params& p = *params;
+  ScoreModDev m{};
+  st = tree_mod_dev(p, mod, nullptr, &m);
+  if (st != MJ_OK) return st;
+  for (int b = 0; b < p.num_seqs; ++b) {
+    const int L = seq_lens_host[b];
+    if (L < 0 || L > static_cast<int64_t>(p.max_blocks) * p.page_size) return MJ_ERR_INVALID_ARG;
+    const TreeShape t = tree_shape(tree->tree_lens, p.q_len, b, L);
+    int first = INT32_MAX, pfx = 0;
+    for (int qi = 0; qi < t.nodes; ++qi) {
+      const RowRange r = tree_range(m, p.q_len, b, qi, t.ctx);
+      pfx = r.pfx;
+      first = std::min(first, r.lo);
+    }
+    const int4 s = make_tree_span(t, first, pfx, &plan_lens_host[b]);
+    const int32_t four[4] = {s.x, s.y, s.z, s.w};
+    std::memcpy(spans_host + 4 * static_cast<int64_t>(b), four, sizeof(four));
+  }
+  return MJ_OK;
+}
+
+extern "C" mj_status mj_tree_spans_device(const mj_decode_params* params, const mj_tree* tree, const mj_score_mod* mod,
+                                          const int32_t* seq_lens, int32_t* spans, int32_t* plan_lens, mj_stream_t stream) {
+  mj_status st = check_params(params);
+  if (st != MJ_OK) return st;
+  if (!tree || !seq_lens || !spans || !plan_lens || !aligned4(tree->tree_lens) || !aligned4(seq_lens) || !aligned4(plan_lens))
+    return MJ_ERR_INVALID_ARG;
+  ScoreModDev m{};
+  st = tree_mod_dev(*params, mod, spans, &m);
+  if (st != MJ_OK) return st;
+  const int64_t max_len = static_cast<int64_t>(params->max_blocks) * params->page_size;
+  const cudaError_t e = launch_tree_spans(m, tree->tree_lens, seq_lens, params->num_seqs, params->q_len, max_len,
+                                          reinterpret_cast<int4*>(spans), plan_lens, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MJ_OK : MJ_ERR_CUDA;
 }
 

@@ -47,6 +47,8 @@ int kv_evict_first(const mj_decode_params& p);
 // Checked score modifiers as the kernels take them.
 struct ScoreModDev;
 mj_status score_mod_dev(const mj_decode_params& p, const mj_score_mod& mod, const int32_t* spans, ScoreModDev* out);
+// The same of a drafted tree's scores (null: none).
+mj_status tree_mod_dev(const mj_decode_params& p, const mj_score_mod* mod, const int32_t* spans, ScoreModDev* out);
 
 // Kernel choice for valid params.
 KernelChoice choose_kernel(const mj_decode_params& p);

@@ -79,6 +79,9 @@ cudaError_t launch_decode_qm_tree(const DecodeTreeDev& a, int rows_per_cta, int 
 // Spans of the keys any row sees and the lengths to plan with.
 cudaError_t launch_score_spans(const ScoreModDev& m, const int32_t* seq_lens, int num_seqs, int q_len, int causal,
                                int64_t max_len, int4* spans, int32_t* plan_lens, cudaStream_t stream);
+// The same of drafted trees.
+cudaError_t launch_tree_spans(const ScoreModDev& m, const int32_t* tree_lens, const int32_t* seq_lens, int num_seqs, int q_len,
+                              int64_t max_len, int4* spans, int32_t* plan_lens, cudaStream_t stream);
 
 // Accumulated attention weights of packed rows n0 .. n0 + n_rows - 1 (at
 // most 256, or 128 of bf16 Q): acc[b][g][j] of a.work's tiles.

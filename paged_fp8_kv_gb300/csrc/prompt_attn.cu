@@ -772,6 +772,7 @@ prompt_attn_kernel(const std::conditional_t<kTree, PromptTreeDev, PromptDev> a, 
             const TreeShape tree = tree_shape(a.t, it.b, it.len);
             if (tok < tree.nodes) {  // (rows without a node compute too, and are written as rows without a key)
               const RowRange rr = tree_range(a.t, it.b, tok, tree.ctx);
+              if (!tree_span_holds(it.span, rr, tree) && a.status) atomicExch(a.status, kStatusInvalid);
               lim = min(rr.hi, it.span.z - 1);
               lo = max(rr.lo, it.span.y);
               pfx = min(rr.pfx, it.span.x);

@@ -58,14 +58,17 @@ __host__ __device__ __forceinline__ RowRange row_range(const ScoreModDev& m, int
 struct TreeShape {
   int nodes, ctx;
 };
-__device__ __forceinline__ TreeShape tree_shape(const DecodeTreeDev& a, int b, int L) {
+__host__ __device__ __forceinline__ TreeShape tree_shape(const int32_t* tree_lens, int q_len, int b, int L) {
   TreeShape t;
-  t.nodes = a.tree_lens ? a.tree_lens[b] : a.q_len;
-  t.nodes = t.nodes > a.q_len ? a.q_len : t.nodes;
+  t.nodes = tree_lens ? tree_lens[b] : q_len;
+  t.nodes = t.nodes > q_len ? q_len : t.nodes;
   t.nodes = t.nodes > L ? L : t.nodes;
   t.nodes = t.nodes < 0 ? 0 : t.nodes;
   t.ctx = L - t.nodes;
   return t;
+}
+__device__ __forceinline__ TreeShape tree_shape(const DecodeTreeDev& a, int b, int L) {
+  return tree_shape(a.tree_lens, a.q_len, b, L);
 }
 
 // Nodes m .. m + 31 of a row of the tree's mask (m may be negative), those that
@@ -80,20 +83,23 @@ __device__ __forceinline__ uint32_t tree_bits(const uint32_t* row, int nodes, in
 }
 
 // The context keys a node sees: those from its first one on, and the prefix.
-__device__ __forceinline__ RowRange tree_range(const DecodeTreeDev& a, int b, int qi, int ctx) {
+__host__ __device__ __forceinline__ RowRange tree_range(const ScoreModDev& m, int q_len, int b, int qi, int ctx) {
   RowRange r;
   r.hi = ctx - 1;
   r.lo = 0;
-  if (a.mod.key_begin) {
-    const int k = a.mod.key_begin[static_cast<int64_t>(b) * a.q_len + qi];
+  if (m.key_begin) {
+    const int k = m.key_begin[static_cast<int64_t>(b) * q_len + qi];
     r.lo = k > 0 ? k : 0;
   }
   r.pfx = 0;
-  if (a.mod.prefix) {
-    const int p = a.mod.prefix[b];
+  if (m.prefix) {
+    const int p = m.prefix[b];
     r.pfx = p < 0 ? 0 : (p > ctx ? ctx : p);
   }
   return r;
+}
+__device__ __forceinline__ RowRange tree_range(const DecodeTreeDev& a, int b, int qi, int ctx) {
+  return tree_range(a.mod, a.q_len, b, qi, ctx);
 }
 
 // The span of a sequence whose rows see keys [first, last] between them
@@ -109,6 +115,22 @@ __host__ __device__ __forceinline__ int4 make_span(int first, int last, int pfx,
   const int jump = begin / 128 - (pfx + 127) / 128;  // tiles between them
   *plan_len = jump > 0 ? end - 128 * jump : end;
   return make_int4(pfx, begin, end, 0);
+}
+
+// The same of a tree: its nodes, the prefix and the context from the first key
+// that any node sees on (a node's range ends with the context, wherever the
+// node stands among q_len rows; without a node nothing is seen).
+__host__ __device__ __forceinline__ int4 make_tree_span(TreeShape t, int first, int pfx, int32_t* plan_len) {
+  if (t.nodes == 0) return make_span(0, -1, 0, plan_len);
+  return make_span(first < t.ctx ? first : t.ctx, t.ctx + t.nodes - 1, pfx, plan_len);
+}
+
+// Whether a span (its end clamped to the length; (L, 0, L) where there is none)
+// holds all that a node with context keys rr may see, the whole tree among it.
+__device__ __forceinline__ bool tree_span_holds(int4 span, RowRange rr, TreeShape t) {
+  const int first = rr.lo < t.ctx ? rr.lo : t.ctx;
+  const bool gap = span.x < span.y && (rr.pfx > span.x || (first > span.x ? first : span.x) < span.y);
+  return !gap && span.z >= t.ctx + t.nodes;
 }
 
 // tanh(t) to about fp32 precision.  Below 0.6 an odd polynomial (degree 11,

@@ -64,7 +64,7 @@ extern "C" mj_status mj_pages_reserve(const mj_page_params* params, const mj_res
         static_cast<const void*>(a.positions), static_cast<const void*>(a.status)})
     if (!aligned4(x)) return MJ_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(a.slots) & 7) != 0) return MJ_ERR_INVALID_ARG;
-  // an output over an input is refused, but for the lengths and the list's size
+  // an output over an input is refused, but for the lengths and the list's size (the first two outputs) in place
   const int64_t lens = static_cast<int64_t>(p.num_seqs) * 4, list = static_cast<int64_t>(p.num_pages) * 4;
   const int64_t table = static_cast<int64_t>(p.num_seqs) * p.max_blocks * 4, tokens = a.num_tokens;
   const struct {
@@ -76,7 +76,7 @@ extern "C" mj_status mj_pages_reserve(const mj_page_params* params, const mj_res
   for (const auto& o : outs) {
     if (!o.at) continue;
     for (const auto& i : ins) {
-      const bool same = o.at == i.at && (i.at == a.seq_lens || i.at == a.num_free) && o.bytes == i.bytes;
+      const bool same = o.at == i.at && ((&o == &outs[0] && &i == &ins[0]) || (&o == &outs[1] && &i == &ins[3]));
       if (i.at && !same && overlap(o.at, o.bytes, i.at, i.bytes)) return MJ_ERR_INVALID_ARG;
     }
     for (const auto& q : outs)

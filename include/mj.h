@@ -481,7 +481,12 @@ typedef struct {
  *   status       optional int32, caller-zeroed: MJ_ERR_INVALID_ARG when a
  *                position is outside [0, max_pos) (that token is left out
  *                whole), or a slot past max_blocks*page_size or its page
- *                outside [0, num_pages) (no K / V is written) */
+ *                outside [0, num_pages) (no K / V is written)
+ *   granted      optional int32[num_seqs] (mj_pages_reserve's): a sequence's
+ *                n tokens get K / V only if its entry is n; 0 is a sequence
+ *                without pages for them, whose Q alone is written, and another
+ *                number MJ_ERR_INVALID_ARG in the status word as well.  NULL:
+ *                every sequence has its pages */
 typedef struct {
   const void* q;
   const void* k;
@@ -507,6 +512,7 @@ typedef struct {
   int32_t* key_pos;
   int64_t kp_seq, kp_head;
   int32_t* status;
+  const int32_t* granted;
 } mj_rope_args;
 
 /* Rotary positions with one to four axes, and the new tokens' rows:
@@ -723,7 +729,9 @@ typedef struct {
  *                 each new token
  *   num_tokens    entries of positions and slots; those behind the last
  *                 sequence's tokens get position 0 and slot -1
- *   status        optional int32, caller-zeroed */
+ *   status        optional int32, caller-zeroed
+ *   granted       optional out int32[num_seqs]: the tokens a sequence got, its
+ *                 n_b, or 0 where it was left out */
 typedef struct {
   const int32_t* seq_lens;
   const int32_t* new_tokens;
@@ -738,6 +746,7 @@ typedef struct {
   int64_t* slots;
   int32_t num_tokens;
   int32_t* status;
+  int32_t* granted;
 } mj_reserve_args;
 
 /* Pages for new tokens, in one launch: with need_b = ceil((L_b + n_b) /
@@ -751,8 +760,14 @@ typedef struct {
  * then count as none) or whose tokens do not fit max_blocks: MJ_ERR_INVALID_ARG,
  * as for more than num_tokens tokens in all where positions or slots are given
  * (the first num_tokens are written), and for num_free outside [0, num_pages]
- * (taken as 0).  A step whose status is not 0 must not append its tokens.
- * Deterministic.
+ * (taken as 0).  Deterministic.
+ * The tokens of a sequence that was left out must not be appended: its length
+ * does not count them, so their slots would be its last keys'.  A step that
+ * nobody looks at in between (a captured one) passes `granted` on: to
+ * mj_rope_append, which then leaves those tokens out, and as the tree_lens of
+ * mj_decode_attn_tree and mj_tree_commit, for which the sequence then has no
+ * node (its rows are 0, and nothing of it moves).  Without granted, a step whose
+ * status is not 0 must not append.
  * Errors: MJ_ERR_INVALID_ARG, MJ_ERR_UNSUPPORTED (page_size, num_seqs, over
  * 2^30 slots a sequence, pages or num_tokens), MJ_ERR_CUDA. */
 mj_status mj_pages_reserve(const mj_page_params* params, const mj_reserve_args* args, mj_stream_t stream);

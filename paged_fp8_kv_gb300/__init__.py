@@ -83,6 +83,7 @@ class PlanOpts(ctypes.Structure):
 
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
+_pi32 = ctypes.POINTER(ctypes.c_int32)
 
 
 class DecodeArgs(ctypes.Structure):
@@ -190,6 +191,7 @@ class RopeArgs(ctypes.Structure):
         ("kp_seq", _i64),
         ("kp_head", _i64),
         ("status", _vp),
+        ("granted", _pi32),
     ]
 
 
@@ -258,6 +260,7 @@ class ReserveArgs(ctypes.Structure):
         ("slots", _vp),
         ("num_tokens", ctypes.c_int32),
         ("status", _vp),
+        ("granted", _pi32),
     ]
 
 
@@ -529,6 +532,11 @@ def kernel_name(params: DecodeParams) -> str:
 
 def _ptr(t) -> Optional[int]:
     return None if t is None else int(t.data_ptr())
+
+
+def _i32_ptr(t):
+    """_ptr for a field of type _pi32."""
+    return None if t is None else ctypes.cast(_ptr(t), _pi32)
 
 
 def _stream_handle(stream) -> Optional[int]:
@@ -945,12 +953,14 @@ class RopeAppend(_Call):
     rot_dim/2 axes (None: axis 0).  q_out is the packed (num_seqs, h_k,
     q_len*h_r, 128) or the token layout (tokens, h_k*h_r, 128), which may be q.
     cu_tokens (num_seqs + 1,) int32 gives the sequences their tokens where
-    they differ in number.  key_pos (num_seqs, h_k, slots) int32 is optional."""
+    they differ in number.  key_pos (num_seqs, h_k, slots) int32 is optional;
+    granted (num_seqs,) int32 of pages_reserve keeps the tokens of sequences
+    that it left out from the cache."""
 
     _name = "mj_rope_append"
 
     def __init__(self, params: RopeParams, *, q, k, v, positions, cos_sin, q_out, k_cache, v_cache, block_table, seq_lens,
-                 k_descale, v_descale, freq_axis=None, cu_tokens=None, key_pos=None, status=None):
+                 k_descale, v_descale, freq_axis=None, cu_tokens=None, key_pos=None, status=None, granted=None):
         params = self._own(params)
         bf16, f32, i32, _ = _dtypes()
         nb, hk, hq = int(params.num_seqs), int(params.h_k), int(params.h_k) * int(params.h_r)
@@ -978,6 +988,8 @@ class RopeAppend(_Call):
         _check_descale("v_descale", v_descale, nb, hk)
         if cu_tokens is not None:
             _tensor("cu_tokens", cu_tokens, (i32,), (nb + 1,))
+        if granted is not None:
+            _tensor("granted", granted, (i32,), (nb,))
         axes = None
         if freq_axis is not None:
             axes = np.ascontiguousarray(np.asarray(freq_axis), dtype=np.uint8)
@@ -1005,10 +1017,10 @@ class RopeAppend(_Call):
         if key_pos is not None:
             a.kp_seq, a.kp_head = _per_slot("key_pos", key_pos, i32, params)
             a.key_pos = _ptr(key_pos)
-        a.status = _ptr(status)
+        a.status, a.granted = _ptr(status), _i32_ptr(granted)
         self._bind(lib().mj_rope_append, (ctypes.byref(params), ctypes.byref(a)),
                    (params, a, axes, q, k, v, positions, cos_sin, q_out, k_cache, v_cache, block_table, seq_lens, k_descale,
-                    v_descale, cu_tokens, key_pos, status))
+                    v_descale, cu_tokens, key_pos, status, granted))
 
 
 def rope_append(params: RopeParams, *, stream=None, **tensors) -> None:
@@ -1351,12 +1363,13 @@ class PagesReserve(_Call):
     for new_tokens (num_seqs,) int32 (None: q_len each) behind seq_lens.
     seq_lens_out and num_free_out may be (and are, if None) seq_lens and
     num_free themselves; cu_tokens (num_seqs + 1,) int32, positions (tokens,)
-    int32 and slots (tokens,) int64 are optional outputs."""
+    int32, slots (tokens,) int64 and granted (num_seqs,) int32, the tokens each
+    sequence got (0: left out), are optional outputs."""
 
     _name = "mj_pages_reserve"
 
     def __init__(self, params: PageParams, *, seq_lens, free_pages, num_free, block_table, new_tokens=None, q_len: int = 1,
-                 num_free_out=None, seq_lens_out=None, cu_tokens=None, positions=None, slots=None, status=None):
+                 num_free_out=None, seq_lens_out=None, cu_tokens=None, positions=None, slots=None, status=None, granted=None):
         import torch
 
         params = self._own(params)
@@ -1369,6 +1382,8 @@ class PagesReserve(_Call):
             _tensor("new_tokens", new_tokens, (i32,), (nb,))
         if cu_tokens is not None:
             _tensor("cu_tokens", cu_tokens, (i32,), (nb + 1,))
+        if granted is not None:
+            _tensor("granted", granted, (i32,), (nb,))
         n = 0
         for name, t, dtype in (("positions", positions, i32), ("slots", slots, torch.int64)):
             if t is not None:
@@ -1377,10 +1392,10 @@ class PagesReserve(_Call):
         if positions is not None and slots is not None and positions.shape != slots.shape:
             raise ValueError(f"slots: {slots.shape[0]} entries, positions has {positions.shape[0]}")
         a = ReserveArgs(_ptr(seq_lens), _ptr(new_tokens), int(q_len), _ptr(free_pages), _ptr(num_free), _ptr(num_free_out),
-                        _ptr(block_table), _ptr(seq_lens_out), _ptr(cu_tokens), _ptr(positions), _ptr(slots), n, _ptr(status))
+                        _ptr(block_table), _ptr(seq_lens_out), _ptr(cu_tokens), _ptr(positions), _ptr(slots), n, _ptr(status), _i32_ptr(granted))
         self._bind(lib().mj_pages_reserve, (ctypes.byref(params), ctypes.byref(a)),
                    (params, a, seq_lens, new_tokens, free_pages, num_free, num_free_out, block_table, seq_lens_out, cu_tokens,
-                    positions, slots, status))
+                    positions, slots, status, granted))
 
 
 def pages_reserve(params: PageParams, *, stream=None, **tensors) -> None:

@@ -69,7 +69,7 @@ extern "C" mj_status mj_rope_append(const mj_rope_params* params, const mj_rope_
        {static_cast<const void*>(a.positions), static_cast<const void*>(a.cu_tokens),
         static_cast<const void*>(a.block_table), static_cast<const void*>(a.seq_lens),
         static_cast<const void*>(a.k_descale), static_cast<const void*>(a.v_descale),
-        static_cast<const void*>(a.key_pos), static_cast<const void*>(a.status)})
+        static_cast<const void*>(a.key_pos), static_cast<const void*>(a.status), static_cast<const void*>(a.granted)})
     if (!aligned4(x)) return MJ_ERR_INVALID_ARG;
   const int64_t in_strides[6] = {a.q_tok, a.q_head, a.k_tok, a.k_head_in, a.v_tok, a.v_head_in};
   for (int64_t s : in_strides)
@@ -154,6 +154,7 @@ extern "C" mj_status mj_rope_append(const mj_rope_params* params, const mj_rope_
   d.kp_seq = a.kp_seq;
   d.kp_head = a.kp_head;
   d.status = a.status;
+  d.granted = a.granted;
   d.num_tokens = a.num_tokens;
   d.num_seqs = p.num_seqs;
   d.q_len = p.q_len;

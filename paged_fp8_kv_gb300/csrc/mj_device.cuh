@@ -86,6 +86,7 @@ struct RopeDev {
   int32_t* key_pos;
   int64_t kp_seq, kp_head;
   int32_t* status;
+  const int32_t* granted;  // or null
   int32_t num_tokens, num_seqs, q_len, h_k, h_r, page_size, max_blocks, num_pages;
   int32_t rot_dim, max_pos, q_packed, interleaved;
   uint8_t axis_of[64];  // the axis of each frequency
@@ -133,6 +134,7 @@ struct PagesDev {
   int32_t* cu_tokens;
   int32_t* positions;
   int64_t* slots;
+  int32_t* granted;
   int32_t* status;
   int64_t max_len;
   int32_t num_seqs, q_len, page_shift, max_blocks, num_pages, num_tokens;

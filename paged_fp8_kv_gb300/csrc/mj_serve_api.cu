@@ -61,7 +61,7 @@ extern "C" mj_status mj_pages_reserve(const mj_page_params* params, const mj_res
         static_cast<const void*>(a.free_pages), static_cast<const void*>(a.num_free),
         static_cast<const void*>(a.num_free_out), static_cast<const void*>(a.block_table),
         static_cast<const void*>(a.seq_lens_out), static_cast<const void*>(a.cu_tokens),
-        static_cast<const void*>(a.positions), static_cast<const void*>(a.status)})
+        static_cast<const void*>(a.positions), static_cast<const void*>(a.status), static_cast<const void*>(a.granted)})
     if (!aligned4(x)) return MJ_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(a.slots) & 7) != 0) return MJ_ERR_INVALID_ARG;
   // an output over an input is refused, but for the lengths and the list's size (the first two outputs) in place
@@ -72,7 +72,7 @@ extern "C" mj_status mj_pages_reserve(const mj_page_params* params, const mj_res
     int64_t bytes;
   } ins[] = {{a.seq_lens, lens}, {a.new_tokens, lens}, {a.free_pages, list}, {a.num_free, 4}},
     outs[] = {{a.seq_lens_out, lens}, {a.num_free_out, 4},           {a.block_table, table},
-              {a.cu_tokens, lens + 4}, {a.positions, tokens * 4}, {a.slots, tokens * 8}};
+              {a.cu_tokens, lens + 4}, {a.positions, tokens * 4}, {a.slots, tokens * 8}, {a.granted, lens}};
   for (const auto& o : outs) {
     if (!o.at) continue;
     for (const auto& i : ins) {
@@ -95,6 +95,7 @@ extern "C" mj_status mj_pages_reserve(const mj_page_params* params, const mj_res
   d.cu_tokens = a.cu_tokens;
   d.positions = a.positions;
   d.slots = a.slots;
+  d.granted = a.granted;
   d.num_tokens = a.num_tokens;
   d.status = a.status;
   const NvtxRange range("mj_pages_reserve");

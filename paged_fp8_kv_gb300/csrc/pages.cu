@@ -199,7 +199,9 @@ __global__ void __launch_bounds__(kThreads, 1) reserve_kernel(const PagesDev a) 
   for (int b = rank * kThreads + tid; b < a.num_seqs; b += ctas * kThreads) {
     const int old = held[b];
     // (the sums of tokens may have been clamped)
-    a.seq_lens_out[b] = old >= 0 ? old + (a.new_tokens ? a.new_tokens[b] : a.q_len) : a.seq_lens[b];
+    const int n = old < 0 ? 0 : (a.new_tokens ? a.new_tokens[b] : a.q_len);
+    a.seq_lens_out[b] = old >= 0 ? old + n : a.seq_lens[b];
+    if (a.granted) a.granted[b] = n;
   }
   if (a.cu_tokens)
     for (int b = rank * kThreads + tid; b <= a.num_seqs; b += ctas * kThreads) a.cu_tokens[b] = tok[b];

@@ -185,8 +185,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeDev
     }
     if (f.seq >= 0) {
       const int64_t slot = static_cast<int64_t>(a.seq_lens[f.seq]) - n + f.qi;
-      if (slot >= 0) {
-        bool ok = slot < a.max_blocks * a.page_size;
+      // (a sequence left out by the reservation: these slots are its last keys')
+      const int granted = a.granted ? a.granted[f.seq] : n;
+      if (slot >= 0 && granted != 0) {
+        bool ok = granted == n && slot < a.max_blocks * a.page_size;
         if (ok) {
           f.page = a.block_table[static_cast<int64_t>(f.seq) * a.max_blocks + slot / a.page_size];
           ok = f.page >= 0 && f.page < a.num_pages;

@@ -325,10 +325,13 @@ prompt_attn_kernel(const std::conditional_t<kTree, PromptTreeDev, PromptDev> a, 
       const int u = unit_at(k), g = u % a.h_k;
       const Item it = load_item(u);
       const int64_t table = static_cast<int64_t>(it.b) * a.max_blocks;
-      // lane l loads the tile's l-th page; its table entry comes a tile ahead
+      // lane l loads the tile's l-th page; its table entry comes a tile ahead (a
+      // tree's length is the device's, which may pass its table: the plan reports that)
       auto page_of = [&](int t) {
         const int key = tile_key<kTree>(it, t) + lane * PS;
-        return t < it.t1 && lane < nbox && key < it.len ? a.block_table[table + key / PS] : a.num_pages;
+        bool there = t < it.t1 && lane < nbox && key < it.len;
+        if constexpr (kTree) there = there && key / PS < a.max_blocks;
+        return there ? a.block_table[table + key / PS] : a.num_pages;
       };
       int page = page_of(it.t0);
       for (int t = it.t0; t < it.t1; ++t, ++n) {

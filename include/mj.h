@@ -760,7 +760,11 @@ typedef struct {
  * then count as none) or whose tokens do not fit max_blocks: MJ_ERR_INVALID_ARG,
  * as for more than num_tokens tokens in all where positions or slots are given
  * (the first num_tokens are written), and for num_free outside [0, num_pages]
- * (taken as 0).  Deterministic.
+ * (taken as 0).  A free page to be given that is outside [0, num_pages) ends the
+ * list (MJ_ERR_INVALID_ARG): it and the entries below it stay where they are, and
+ * the sequence it would go to and those behind that need pages are left out.
+ * Tokens in a page that their sequence holds already and that is outside that range
+ * get slot -1 (MJ_ERR_INVALID_ARG).  Deterministic.
  * The tokens of a sequence that was left out must not be appended: its length
  * does not count them, so their slots would be its last keys'.  A step that
  * nobody looks at in between (a captured one) passes `granted` on: to
@@ -794,8 +798,10 @@ typedef struct {
  * table keeps their entries, which nothing reads any more.  A sequence whose
  * lengths are not 0 <= keep_b <= L_b <= max_blocks*page_size releases nothing
  * (MJ_ERR_INVALID_ARG in the status); pages past the list's num_pages entries
- * (a page given back twice, somewhere) are dropped, MJ_ERR_CAPACITY.  Pages
- * must not be shared between sequences.  Deterministic.
+ * (a page given back twice, somewhere) are dropped, MJ_ERR_CAPACITY; a page
+ * outside [0, num_pages) is dropped, MJ_ERR_INVALID_ARG (entries of the list at
+ * or past num_free_out may then hold anything).  Pages must not be shared
+ * between sequences.  Deterministic.
  * Errors: as mj_pages_reserve. */
 mj_status mj_pages_release(const mj_page_params* params, const mj_release_args* args, mj_stream_t stream);
 

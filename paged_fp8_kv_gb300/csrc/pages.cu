@@ -8,7 +8,11 @@
 // for itself (a thousand threads, one sequence each in a decode batch) and then
 // takes its share of the tokens and pages, finding each one's sequence by a
 // binary search in shared memory.  The lengths and the list's size may be
-// written where they were read: the cluster's barrier is between.
+// written where they were read: the cluster's barrier is between.  Numbers that
+// are no page of the pool are neither given nor taken back: every CTA looks at
+// all pages to be given (a round of loads that the stores repeat from L1); what
+// comes back is written as it is read, and once more by one CTA if a number
+// among it was none.
 //
 // Measured: one token for each of 256 sequences 4.2 us a call (4.3 in a graph),
 // 33 prompts of 65000 tokens in all 10.3 (10.1; two tokens a thread in flight for
@@ -28,8 +32,17 @@ constexpr int kCluster = 8;  // CTAs of a call with many tokens or pages
 constexpr int kStatusInvalid = 1;   // MJ_ERR_INVALID_ARG
 constexpr int kStatusCapacity = 3;  // MJ_ERR_CAPACITY
 
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  cluster_arrive();
+  cluster_wait();
+}
+// *flag = 1 in the cluster's first CTA
+__device__ __forceinline__ void set_in_first(int* flag) {
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"(ptx::smem_u32(flag)));
+  asm volatile("st.shared::cluster.u32 [%0], 1;" ::"r"(at) : "memory");
 }
 
 __device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {
@@ -95,56 +108,76 @@ __global__ void __launch_bounds__(kThreads, 1) reserve_kernel(const PagesDev a) 
   int32_t* const need = tok + a.num_seqs + 1;      // [num_seqs + 1] pages before b
   int32_t* const held = need + a.num_seqs + 1;     // [num_seqs] tokens held; -1: gets no slots
   __shared__ Pair red[kWarps];
-  __shared__ int wrong, taken;  // bit 0: an invalid length, bit 1: too few pages
+  __shared__ int wrong, taken;  // bit 0: an invalid length or page, bit 1: too few pages
+  __shared__ int bad_page;      // the first of the list's pages, from its end, that is none
   const int tid = threadIdx.x, rank = blockIdx.x, ctas = gridDim.x;
   const int shift = a.page_shift, row_mask = (1 << shift) - 1;
   if (tid == 0) {
     wrong = taken = 0;
     tok[0] = need[0] = 0;
+    bad_page = INT32_MAX;
   }
   int n_free = a.num_free[0];
   if (n_free < 0 || n_free > a.num_pages) {
     n_free = 0;
     if (tid == 0) wrong = 1;
   }
+  auto free_page = [&](int x) { return __ldg(a.free_pages + n_free - 1 - x); };
+  auto is_page = [&](int64_t page) { return page >= 0 && page < a.num_pages; };
   __syncthreads();
-  Pair base{0, 0};
-  for (int b0 = 0; b0 < a.num_seqs; b0 += kThreads) {
-    const int b = b0 + tid;
-    Pair v{0, 0};
-    int old = -1;
-    if (b < a.num_seqs) {
-      const int L = a.seq_lens[b], n = a.new_tokens ? a.new_tokens[b] : a.q_len;
-      if (L < 0 || n < 0) {
-        atomicOr(&wrong, 1);
-      } else {
-        v.a = n;
-        if (static_cast<int64_t>(L) + n > a.max_len) {
+  for (int avail = n_free;;) {  // pages that may be given
+    Pair base{0, 0};
+    for (int b0 = 0; b0 < a.num_seqs; b0 += kThreads) {
+      const int b = b0 + tid;
+      Pair v{0, 0};
+      int old = -1;
+      if (b < a.num_seqs) {
+        const int L = a.seq_lens[b], n = a.new_tokens ? a.new_tokens[b] : a.q_len;
+        if (L < 0 || n < 0) {
           atomicOr(&wrong, 1);
         } else {
-          old = L;
-          v.b = ((static_cast<int64_t>(L) + n + row_mask) >> shift) - ((static_cast<int64_t>(L) + row_mask) >> shift);
+          v.a = n;
+          if (static_cast<int64_t>(L) + n > a.max_len) {
+            atomicOr(&wrong, 1);
+          } else {
+            old = L;
+            v.b = ((static_cast<int64_t>(L) + n + row_mask) >> shift) - ((static_cast<int64_t>(L) + row_mask) >> shift);
+          }
         }
       }
-    }
-    Pair total;
-    const Pair inc = block_scan(v, red, &total);
-    if (b < a.num_seqs) {
-      const int64_t end = base.b + inc.b;
-      if (v.b > 0 && end > n_free) {  // its pages are no longer in the list
-        old = -1;
-        atomicOr(&wrong, 2);
-      } else if (v.b > 0) {
-        atomicMax(&taken, static_cast<int>(end));
+      Pair total;
+      const Pair inc = block_scan(v, red, &total);
+      if (b < a.num_seqs) {
+        const int64_t end = base.b + inc.b;
+        if (v.b > 0 && end > avail) {  // its pages are no longer in the list
+          old = -1;
+          atomicOr(&wrong, 2);
+        } else if (v.b > 0) {
+          atomicMax(&taken, static_cast<int>(end));
+        }
+        tok[b + 1] = clamp32(base.a + inc.a);
+        need[b + 1] = clamp32(end);
+        held[b] = old;
       }
-      tok[b + 1] = clamp32(base.a + inc.a);
-      need[b + 1] = clamp32(end);
-      held[b] = old;
+      base.a += total.a;
+      base.b += total.b;
     }
-    base.a += total.a;
-    base.b += total.b;
+    __syncthreads();
+    // The pages to give, all of them by every CTA (they are read again below): the
+    // list ends at one that is no page of the pool, and what its sequence and those
+    // behind it wanted is left out.
+    for (int x = tid; x < taken; x += kThreads)
+      if (!is_page(free_page(x))) atomicMin(&bad_page, x);
+    __syncthreads();
+    if (bad_page >= taken) break;  // (the second time at the latest: no more than bad_page are taken then)
+    avail = bad_page;
+    __syncthreads();  // both are read
+    if (tid == 0) {
+      wrong |= 1;
+      taken = 0;
+    }
+    __syncthreads();
   }
-  __syncthreads();
   const int tokens = tok[a.num_seqs];
   if (tid == 0 && rank == 0) {
     if ((wrong & 1) || ((a.positions || a.slots) && tokens > a.num_tokens))
@@ -152,8 +185,8 @@ __global__ void __launch_bounds__(kThreads, 1) reserve_kernel(const PagesDev a) 
     else if (wrong)
       report(a.status, kStatusCapacity);
   }
-  auto free_page = [&](int x) { return __ldg(a.free_pages + n_free - 1 - x); };
   // the new tokens' positions and slots
+  bool bad_held = false;
   if (a.positions || a.slots) {
     // four a thread at a time, so that their loads are in flight together
     constexpr int kBatch = 4;
@@ -173,9 +206,14 @@ __global__ void __launch_bounds__(kThreads, 1) reserve_kernel(const PagesDev a) 
             pos[i] = old + t - tok[b];
             const int blk = pos[i] >> shift, have = (old + row_mask) >> shift;
             // (the old pages' entries are not written here, the new ones' not read)
-            if (a.slots)
+            if (a.slots) {
               slot[i] = blk < have ? __ldg(a.block_table + static_cast<int64_t>(b) * a.max_blocks + blk)
                                    : free_page(need[b] + blk - have);
+              if (!is_page(slot[i])) {  // (one the sequence holds)
+                slot[i] = -1;
+                bad_held = true;
+              }
+            }
           }
         }
       }
@@ -195,7 +233,11 @@ __global__ void __launch_bounds__(kThreads, 1) reserve_kernel(const PagesDev a) 
     a.block_table_out[static_cast<int64_t>(b) * a.max_blocks + blk] = free_page(x);
   }
   // every CTA of the cluster has read the lengths and the list's size
-  if (ctas > 1) cluster_sync();
+  if (ctas > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  if (bad_held) report(a.status, kStatusInvalid);  // (behind a report of too few pages)
   for (int b = rank * kThreads + tid; b < a.num_seqs; b += ctas * kThreads) {
     const int old = held[b];
     // (the sums of tokens may have been clamped)
@@ -215,13 +257,14 @@ __global__ void __launch_bounds__(kThreads, 1) release_kernel(const PagesDev a) 
   int32_t* const gone = smem;                   // [num_seqs + 1] pages before b
   int32_t* const kept = gone + a.num_seqs + 1;  // [num_seqs] pages that stay
   __shared__ Pair red[kWarps];
-  __shared__ int wrong;
+  __shared__ int wrong, bad_page;  // bad_page: of the first CTA, one that is no page is among those given back
   const int tid = threadIdx.x, rank = blockIdx.x, ctas = gridDim.x;
   const int shift = a.page_shift, row_mask = (1 << shift) - 1;
   if (tid == 0) {
-    wrong = 0;
+    wrong = bad_page = 0;
     gone[0] = 0;
   }
+  if (ctas > 1) cluster_arrive();  // bad_page may be set from here on
   int n_free = a.num_free[0];
   if (n_free < 0 || n_free > a.num_pages) {
     n_free = 0;
@@ -254,12 +297,43 @@ __global__ void __launch_bounds__(kThreads, 1) release_kernel(const PagesDev a) 
   } else if (wrong && tid == 0 && rank == 0) {
     report(a.status, wrong);
   }
+  if (ctas > 1) cluster_wait();
+  auto is_page = [&](int page) { return page >= 0 && page < a.num_pages; };
   for (int x = rank * kThreads + tid; x < pages; x += ctas * kThreads) {
     const int b = find(gone, a.num_seqs, x);
-    a.free_pages_out[n_free + x] = a.block_table[static_cast<int64_t>(b) * a.max_blocks + kept[b] + x - gone[b]];
+    const int page = a.block_table[static_cast<int64_t>(b) * a.max_blocks + kept[b] + x - gone[b]];
+    a.free_pages_out[n_free + x] = page;
+    if (!is_page(page)) set_in_first(&bad_page);
   }
-  if (ctas > 1) cluster_sync();  // every CTA has read the list's size
-  if (rank == 0 && tid == 0) a.num_free_out[0] = n_free + pages;
+  if (ctas > 1)  // every CTA has read the list's size
+    cluster_sync();
+  else
+    __syncthreads();
+  if (rank != 0) return;
+  if (bad_page) {
+    // An entry is no page of the pool: the first CTA writes the others' once more
+    // without it, a thread a sequence.
+    int at = n_free, full = 0;
+    for (int b0 = 0; b0 < a.num_seqs; b0 += kThreads) {
+      const int b = b0 + tid;
+      const int64_t row = static_cast<int64_t>(b) * a.max_blocks;
+      const int first = b < a.num_seqs ? kept[b] : 0, n = b < a.num_seqs ? gone[b + 1] - gone[b] : 0;
+      Pair v{0, 0};
+      for (int i = 0; i < n; ++i) v.a += is_page(a.block_table[row + first + i]);
+      Pair total;
+      const Pair inc = block_scan(v, red, &total);
+      int64_t to = at + inc.a - v.a;
+      for (int i = 0; i < n; ++i) {
+        const int page = a.block_table[row + first + i];
+        if (is_page(page) && to++ < a.num_pages) a.free_pages_out[to - 1] = page;
+      }
+      if (at + total.a > a.num_pages) full = 1;
+      at = full ? a.num_pages : static_cast<int>(at + total.a);
+    }
+    pages = at - n_free;
+    if (tid == 0) report(a.status, full ? kStatusCapacity : kStatusInvalid);
+  }
+  if (tid == 0) a.num_free_out[0] = n_free + pages;
 }
 
 cudaError_t launch(void (*kern)(PagesDev), const PagesDev& a, size_t smem, int64_t elements, cudaStream_t stream) {

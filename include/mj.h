@@ -918,7 +918,9 @@ mj_status mj_tree_spans_device(const mj_decode_params* params, const mj_tree* tr
                                const int32_t* seq_lens, int32_t* spans, int32_t* plan_lens, mj_stream_t stream);
 
 /* mj_decode_attn_mod for trees.  The same arguments and results; params->causal
- * is not looked at.  mod (NULL: none) may hold a softcap, key_begin (node i sees
+ * is not looked at.  Above 128 packed rows MJ_KERNEL_AUTO takes the prompts' kernel
+ * over e4m3 pools (planned as the query-rows kernel, which mj_kernel_name names
+ * for these params), MJ_KERNEL_TENSOR_CORE_QROWS the query-rows kernel.  mod (NULL: none) may hold a softcap, key_begin (node i sees
  * context keys from key_begin[b*q_len + i] on: the window of a token whose
  * position is its depth) and prefix (context keys seen ahead of that); a
  * window, slopes or key_end, which take positions for slots, are refused

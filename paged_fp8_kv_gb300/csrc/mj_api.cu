@@ -182,6 +182,21 @@ KernelChoice choose_kernel(const mj_decode_params& p) {
   return k;
 }
 
+KernelChoice choose_tree_kernel(const mj_decode_params& p) {
+  KernelChoice k = choose_kernel(p);
+  // The prompts' kernel holds P in half precision and converts V once for 256
+  // rows (32 trees of up to 61 tokens x 4 heads before 2048 to 32768 keys:
+  // 419 to 445 us; 598 by the query-rows kernel's pairs, whose P goes in two
+  // e4m3 parts).  It takes one q tile of 256 rows a CTA, so few rows stay where
+  // they are; it reads e4m3 pools alone.  Planned as the query-rows kernel.
+  if (p.kernel == MJ_KERNEL_AUTO && k.kind == KernelKind::kTensorCoreQRows && k.rows_per_cta == 256 &&
+      p.kv_format == MJ_KV_E4M3) {
+    k.kind = KernelKind::kPrompt;
+    k.name = p.q_dtype == MJ_E4M3 ? "prompt_e4m3" : "prompt_bf16";
+  }
+  return k;
+}
+
 }  // namespace mj
 
 using namespace mj;
@@ -316,7 +331,7 @@ mj_status decode_step(const mj_decode_params& p, const mj_decode_args& a, const 
   if (a.timing_events)
     for (int i = 0; i < 3; ++i) ev[i] = static_cast<cudaEvent_t>(a.timing_events[i]);
 
-  const KernelChoice kc = choose_kernel(p);
+  const KernelChoice kc = tree ? choose_tree_kernel(p) : choose_kernel(p);
   const int merge_splits = a.max_n_splits == 0 ? p.max_splits : a.max_n_splits;
   const bool merge = p.max_splits > 1 && merge_splits > 1;
   if (verbose())
@@ -335,12 +350,7 @@ mj_status decode_step(const mj_decode_params& p, const mj_decode_args& a, const 
   } range_end;
   cudaError_t e = cudaSuccess;
   if (ev[0] && (e = cudaEventRecord(ev[0], stream)) != cudaSuccess) return MJ_ERR_CUDA;
-  if (tree && kc.kind == KernelKind::kTensorCoreQRows && kc.rows_per_cta == 256 && p.kv_format == MJ_KV_E4M3) {
-    // The prompts' kernel holds P in half precision and converts V once for 256
-    // rows (32 trees of up to 61 tokens x 4 heads before 2048 to 32768 keys:
-    // 419 to 445 us; 598 by the query-rows kernel's pairs, whose P goes in two
-    // e4m3 parts).
-    // It takes one q tile of 256 rows a CTA, so few rows stay where they are.
+  if (kc.kind == KernelKind::kPrompt) {
     const int sms = device_sm_count();
     if (sms < 1) return MJ_ERR_CUDA;
     e = launch_prompt_tree(d, kc.n_q_tiles, p.q_dtype == MJ_E4M3, sms, stream);
@@ -409,9 +419,10 @@ extern "C" mj_status mj_decode_attn_tree(const mj_decode_params* params, const m
   if ((reinterpret_cast<uintptr_t>(tree->mask) & 3) != 0 || (reinterpret_cast<uintptr_t>(tree->tree_lens) & 3) != 0)
     return MJ_ERR_INVALID_ARG;
   if (tree->mask_words < (params->q_len + 31) / 32) return MJ_ERR_INVALID_ARG;
-  const KernelChoice kc = choose_kernel(*params);
+  const KernelChoice kc = choose_tree_kernel(*params);
   if (params->kv_format == MJ_KV_NVFP4 ||
-      !(kc.kind == KernelKind::kTensorCoreQRows || (kc.kind == KernelKind::kTensorCore && kc.rows_per_cta <= 16)))
+      !(kc.kind == KernelKind::kTensorCoreQRows || kc.kind == KernelKind::kPrompt ||
+        (kc.kind == KernelKind::kTensorCore && kc.rows_per_cta <= 16)))
     return MJ_ERR_UNSUPPORTED;
   ScoreModDev m{};
   st = tree_mod_dev(*params, mod, spans, &m);

@@ -13,7 +13,7 @@ constexpr int kMaxSplits = 256;
 constexpr int kDefaultSmCount = 152;  // GB300
 constexpr int kMaxDevicePlanSeqs = 16384;  // device plan: one CTA, keys and tiles in shared memory
 
-enum class KernelKind { kCudaCore = 0, kTensorCore = 1, kTensorCoreGrouped = 2, kTensorCoreQRows = 3 };
+enum class KernelKind { kCudaCore = 0, kTensorCore = 1, kTensorCoreGrouped = 2, kTensorCoreQRows = 3, kPrompt = 4 };
 
 // The decode kernel mj_decode_attn launches for a problem, and the
 // occupancy facts the plan needs about it.
@@ -52,6 +52,8 @@ mj_status tree_mod_dev(const mj_decode_params& p, const mj_score_mod* mod, const
 
 // Kernel choice for valid params.
 KernelChoice choose_kernel(const mj_decode_params& p);
+// The same of mj_decode_attn_tree.
+KernelChoice choose_tree_kernel(const mj_decode_params& p);
 
 // MJ_VERBOSE set to a non-empty value other than "0" in the environment
 // (read once per process): the entry points print what they chose to stderr.

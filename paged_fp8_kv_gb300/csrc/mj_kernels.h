@@ -94,7 +94,7 @@ cudaError_t launch_key_weights(const DecodeModDev& a, bool q_e4m3, bool has_mod,
 struct PromptPlanDev;
 struct PromptDev;
 cudaError_t launch_prompt_plan(const PromptPlanDev& a, cudaStream_t stream);
-cudaError_t launch_prompt_attn(const PromptDev& a, bool q_e4m3, bool merge, cudaStream_t stream);
+cudaError_t launch_prompt_attn(const PromptDev& a, bool q_e4m3, bool merge, int sm_count, cudaStream_t stream);
 // Trees above 128 packed rows by the same kernel (e4m3 pools; the decode merge follows).
 cudaError_t launch_prompt_tree(const DecodeTreeDev& a, int n_q_tiles, bool q_e4m3, int sm_count, cudaStream_t stream);
 

@@ -201,7 +201,9 @@ extern "C" mj_status mj_prompt_attn(const mj_decode_params* params, const mj_pro
   d.max_splits = p.max_splits;
   // keys are cut only into parts of kPromptMinChunk tiles or more
   const bool merge = p.max_splits > 1 && static_cast<int64_t>(p.max_blocks) * p.page_size > kPromptMinChunk * 128;
+  const int sms = device_sm_count();  // a CTA each: they share the items out among themselves
+  if (sms < 1) return MJ_ERR_CUDA;
   const NvtxRange range("mj_prompt_attn");
-  const cudaError_t e = launch_prompt_attn(d, p.q_dtype == MJ_E4M3, merge, reinterpret_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_prompt_attn(d, p.q_dtype == MJ_E4M3, merge, sms, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MJ_OK : MJ_ERR_CUDA;
 }

@@ -9,7 +9,7 @@
 namespace mj {
 
 constexpr int kPromptRows = 256;  // packed query rows of a work item
-constexpr int kPromptSlots = 152; // CTAs the plan cuts for (a GB300's SMs)
+constexpr int kPromptSlots = 152; // CTAs the plan cuts for (a GB300's SMs; sizes of plans and workspaces follow from it)
 constexpr int kPromptMinChunk = 4;   // tiles of the shortest piece a row tile is cut into
 constexpr int kPromptSortMax = 8192; // items ordered by cost in shared memory
 

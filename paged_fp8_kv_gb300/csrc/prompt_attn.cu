@@ -1142,10 +1142,10 @@ cudaError_t launch_maps(const std::conditional_t<kTree, PromptTreeDev, PromptDev
 
 }  // namespace
 
-cudaError_t launch_prompt_attn(const PromptDev& a, bool q_e4m3, bool merge, cudaStream_t stream) {
-  const cudaError_t e = launch_maps<false>(a, q_e4m3, kPromptSlots, stream);
+cudaError_t launch_prompt_attn(const PromptDev& a, bool q_e4m3, bool merge, int sm_count, cudaStream_t stream) {
+  const cudaError_t e = launch_maps<false>(a, q_e4m3, sm_count, stream);
   if (e != cudaSuccess || !merge) return e;
-  return launch_pdl(prompt_merge_kernel, dim3(4 * kPromptSlots, 1, 1), dim3(kMergeWarps * 32, 1, 1), 0,
+  return launch_pdl(prompt_merge_kernel, dim3(static_cast<unsigned>(4 * sm_count), 1, 1), dim3(kMergeWarps * 32, 1, 1), 0,
                     stream, a);
 }
 

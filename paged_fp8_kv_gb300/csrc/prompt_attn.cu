@@ -87,6 +87,10 @@ constexpr int kStatusInvalid = 1;        // MJ_ERR_INVALID_ARG
 // half precision's 11 bits down to 2^-21 of the reference.
 constexpr float kPBias = 7.f;
 constexpr float kTau = 8.f;
+// The least factor from scores to log2 units: one that had become 0 would turn a
+// masked key's -inf into NaN.  A score of at most 2^25 is below 2^-100 by it, which
+// adds nothing to a sum of exponentials.
+constexpr float kLeastScale = 0x1p-126f;
 
 template <bool kQe4m3>
 struct Cfg {
@@ -759,7 +763,7 @@ prompt_attn_kernel(const std::conditional_t<kTree, PromptTreeDev, PromptDev> a, 
         if constexpr (kCap)  // scores become logits in log2 units as they are read
           cap_c1 = raw_l / a.softcap;
         else
-          c2 = raw_l * kLog2e;
+          c2 = fmaxf(raw_l * kLog2e, kLeastScale);
         dual = it.g1[1] < 0;
         g0 = dual ? it.t0 + w : (w ? it.g0[1] : it.g0[0]);
         g1 = dual ? it.t1 : (w ? it.g1[1] : it.g1[0]);
@@ -794,7 +798,7 @@ prompt_attn_kernel(const std::conditional_t<kTree, PromptTreeDev, PromptDev> a, 
           if constexpr (kCap)
             cap_c1 *= f;
           else
-            c2 *= f;
+            c2 = fmaxf(c2 * f, kLeastScale);
         }
         const bool unmasked = __all_sync(0xffffffffu, (key0 >= lo && key0 + kRows - 1 <= lim) || (kTree && key0 + kRows <= pfx));
         uint32_t s[kRows];

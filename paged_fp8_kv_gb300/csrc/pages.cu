@@ -10,13 +10,14 @@
 // binary search in shared memory.  The lengths and the list's size may be
 // written where they were read: the cluster's barrier is between.  Numbers that
 // are no page of the pool are neither given nor taken back: every CTA looks at
-// all pages to be given (a round of loads that the stores repeat from L1); what
-// comes back is written as it is read, and once more by one CTA if a number
-// among it was none.
+// all pages to be given (a round of loads that the stores repeat from L1: 0.2 us
+// of the smallest call; looked at when the sums are done 0.1 more, loaded ahead
+// of the sums no less); what comes back is written as it is read, and once more
+// by one CTA if a number among it was none.
 //
-// Measured: one token for each of 256 sequences 4.2 us a call (4.3 in a graph),
-// 33 prompts of 65000 tokens in all 10.3 (10.1; two tokens a thread in flight for
-// four made no difference beyond the noise), a trim 4.6 (3.9).
+// Measured: one token for each of 256 sequences 4.9 us a call (4.6 in a graph),
+// 33 prompts of 65000 tokens in all 11.5 (10.4; two tokens a thread in flight for
+// four made no difference beyond the noise), a trim 4.4 (4.0).
 
 #include <cuda_runtime.h>
 
@@ -162,13 +163,16 @@ __global__ void __launch_bounds__(kThreads, 1) reserve_kernel(const PagesDev a) 
       base.a += total.a;
       base.b += total.b;
     }
+    // The pages to give, all of them looked at by every CTA, a thousand before the
+    // sums are done: the list ends at one that is no page of the pool, and what its
+    // sequence and those behind it wanted is left out.
+    if (tid < n_free && !is_page(free_page(tid))) atomicMin(&bad_page, tid);
     __syncthreads();
-    // The pages to give, all of them by every CTA (they are read again below): the
-    // list ends at one that is no page of the pool, and what its sequence and those
-    // behind it wanted is left out.
-    for (int x = tid; x < taken; x += kThreads)
-      if (!is_page(free_page(x))) atomicMin(&bad_page, x);
-    __syncthreads();
+    if (taken > kThreads) {
+      for (int x = kThreads + tid; x < taken; x += kThreads)
+        if (!is_page(free_page(x))) atomicMin(&bad_page, x);
+      __syncthreads();
+    }
     if (bad_page >= taken) break;  // (the second time at the latest: no more than bad_page are taken then)
     avail = bad_page;
     __syncthreads();  // both are read
@@ -182,14 +186,15 @@ __global__ void __launch_bounds__(kThreads, 1) reserve_kernel(const PagesDev a) 
   if (tid == 0 && rank == 0) {
     if ((wrong & 1) || ((a.positions || a.slots) && tokens > a.num_tokens))
       report(a.status, kStatusInvalid);
-    else if (wrong)
-      report(a.status, kStatusCapacity);
+    else if (wrong && a.status)
+      atomicCAS(a.status, 0, kStatusCapacity);  // (what is wrong may be reported meanwhile)
   }
   // the new tokens' positions and slots
-  bool bad_held = false;
+  bool bad_held = false;  // a page that a sequence holds is none
   if (a.positions || a.slots) {
     // four a thread at a time, so that their loads are in flight together
     constexpr int kBatch = 4;
+    constexpr int64_t kNone = INT64_MIN;
     const int step = ctas * kThreads;
     for (int t0 = rank * kThreads + tid; t0 < a.num_tokens; t0 += kBatch * step) {
       int pos[kBatch];
@@ -198,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1) reserve_kernel(const PagesDev a) 
       for (int i = 0; i < kBatch; ++i) {
         const int t = t0 + i * step;
         pos[i] = 0;
-        slot[i] = -1;
+        slot[i] = kNone;
         if (t < a.num_tokens && t < tokens) {
           const int b = find(tok, a.num_seqs, t);
           const int old = held[b];
@@ -206,14 +211,9 @@ __global__ void __launch_bounds__(kThreads, 1) reserve_kernel(const PagesDev a) 
             pos[i] = old + t - tok[b];
             const int blk = pos[i] >> shift, have = (old + row_mask) >> shift;
             // (the old pages' entries are not written here, the new ones' not read)
-            if (a.slots) {
+            if (a.slots)
               slot[i] = blk < have ? __ldg(a.block_table + static_cast<int64_t>(b) * a.max_blocks + blk)
                                    : free_page(need[b] + blk - have);
-              if (!is_page(slot[i])) {  // (one the sequence holds)
-                slot[i] = -1;
-                bad_held = true;
-              }
-            }
           }
         }
       }
@@ -222,10 +222,12 @@ __global__ void __launch_bounds__(kThreads, 1) reserve_kernel(const PagesDev a) 
         const int t = t0 + i * step;
         if (t >= a.num_tokens) continue;
         if (a.positions) a.positions[t] = pos[i];
-        if (a.slots) a.slots[t] = slot[i] < 0 ? -1 : (slot[i] << shift) + (pos[i] & row_mask);
+        if (a.slots) a.slots[t] = is_page(slot[i]) ? (slot[i] << shift) + (pos[i] & row_mask) : -1;
+        bad_held |= slot[i] != kNone && !is_page(slot[i]);
       }
     }
   }
+  if (bad_held) report(a.status, kStatusInvalid);
   // the new pages' entries
   for (int x = rank * kThreads + tid; x < taken; x += ctas * kThreads) {
     const int b = find(need, a.num_seqs, x);
@@ -233,11 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1) reserve_kernel(const PagesDev a) 
     a.block_table_out[static_cast<int64_t>(b) * a.max_blocks + blk] = free_page(x);
   }
   // every CTA of the cluster has read the lengths and the list's size
-  if (ctas > 1)
-    cluster_sync();
-  else
-    __syncthreads();
-  if (bad_held) report(a.status, kStatusInvalid);  // (behind a report of too few pages)
+  if (ctas > 1) cluster_sync();
   for (int b = rank * kThreads + tid; b < a.num_seqs; b += ctas * kThreads) {
     const int old = held[b];
     // (the sums of tokens may have been clamped)

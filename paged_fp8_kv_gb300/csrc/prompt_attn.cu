@@ -763,7 +763,7 @@ prompt_attn_kernel(const std::conditional_t<kTree, PromptTreeDev, PromptDev> a, 
         if constexpr (kCap)  // scores become logits in log2 units as they are read
           cap_c1 = raw_l / a.softcap;
         else
-          c2 = fmaxf(raw_l * kLog2e, kLeastScale);
+          c2 = kQe4m3 ? fmaxf(raw_l * kLog2e, kLeastScale) : raw_l * kLog2e;
         dual = it.g1[1] < 0;
         g0 = dual ? it.t0 + w : (w ? it.g0[1] : it.g0[0]);
         g1 = dual ? it.t1 : (w ? it.g1[1] : it.g1[0]);

@@ -75,6 +75,25 @@ def test_spans_without_a_nodes_keys_are_reported(q_len, h_r):
     assert t.attend(*mj.tree_spans(t.params, t.mod, t.c.lens, t.tree_lens)) == 0
 
 
+@pytest.mark.parametrize("q_len,h_r", ROWS)
+def test_keys_outside_the_spans_may_hold_anything(q_len, h_r):
+    """NaN codes of K and V between the prefix and the first key, and pages of the table that no key of the spans lies in."""
+    nodes = [max(1, q_len // 8), q_len, 0]
+    t = Windowed([1500, 517, 300], nodes, q_len, h_r, 20, None, prefix=True)
+    spans, plan_lens = mj.tree_spans(t.params, t.mod, t.c.lens, t.tree_lens)
+    assert t.attend(spans, plan_lens) == 0
+    want = t.o.clone(), t.lse.clone()
+    t.check()
+    for b in range(3):
+        for j in range(int(spans[b][0]), int(spans[b][1])):
+            at = t.c.table_host[b, j // 16], j % 16
+            t.c.k[at], t.c.v[at] = 0x7F, 0x7F
+        for blk in range(-(-int(spans[b][0]) // 16), int(spans[b][1]) // 16):
+            t.c.table[b, blk] = (-1, 2**31 - 1, t.c.num_pages)[blk % 3]
+    assert t.attend(spans, plan_lens) == 0
+    assert torch.equal(t.o, want[0]) and torch.equal(t.lse, want[1])
+
+
 def test_spans_follow_the_lengths_in_a_graph():
     """Spans, plan and attention captured together; lengths, trees and first keys change in their buffers."""
     q_len, h_r = 16, 4

@@ -770,8 +770,9 @@ typedef struct {
  * nobody looks at in between (a captured one) passes `granted` on: to
  * mj_rope_append, which then leaves those tokens out, and as the tree_lens of
  * mj_decode_attn_tree and mj_tree_commit, for which the sequence then has no
- * node (its rows are 0, and nothing of it moves).  Without granted, a step whose
- * status is not 0 must not append.
+ * node (its rows are 0, and nothing of it moves).  The rows of such tokens in
+ * other attentions mean nothing.  Without granted, a step whose status is not 0
+ * must not append.
  * Errors: MJ_ERR_INVALID_ARG, MJ_ERR_UNSUPPORTED (page_size, num_seqs, over
  * 2^30 slots a sequence, pages or num_tokens), MJ_ERR_CUDA. */
 mj_status mj_pages_reserve(const mj_page_params* params, const mj_reserve_args* args, mj_stream_t stream);

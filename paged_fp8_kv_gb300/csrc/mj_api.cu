@@ -185,9 +185,9 @@ KernelChoice choose_kernel(const mj_decode_params& p) {
 KernelChoice choose_tree_kernel(const mj_decode_params& p) {
   KernelChoice k = choose_kernel(p);
   // The prompts' kernel holds P in half precision and converts V once for 256
-  // rows (32 trees of up to 61 tokens x 4 heads before 2048 to 32768 keys:
-  // 419 to 445 us; 598 by the query-rows kernel's pairs, whose P goes in two
-  // e4m3 parts).  It takes one q tile of 256 rows a CTA, so few rows stay where
+  // rows (32 trees of up to 61 tokens x 4 heads before 2048 to 32768 keys: 424 to
+  // 437 us; 593 by the query-rows kernel's pairs, whose P goes in two e4m3
+  // parts).  It takes one q tile of 256 rows a CTA, so few rows stay where
   // they are; it reads e4m3 pools alone.  Planned as the query-rows kernel.
   if (p.kernel == MJ_KERNEL_AUTO && k.kind == KernelKind::kTensorCoreQRows && k.rows_per_cta == 256 &&
       p.kv_format == MJ_KV_E4M3) {

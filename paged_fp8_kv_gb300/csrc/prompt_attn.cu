@@ -15,7 +15,7 @@
 //       for both groups.  Splitting P into e4m3 parts instead would cost the
 //       softmax threads four conversions a pair of scores for one, and keep 8
 //       bits of P for 11 (trees of 244 rows by the query-rows kernel, which does
-//       that: 598 us for 419 to 445 here).
+//       that: 593 us for 424 to 437 here).
 //
 // TMEM has room for both O (2 x 128 columns), both P (2 x 64) and one S of 128
 // keys, which the groups use in turn: the softmax threads read a row of scores

@@ -1391,6 +1391,8 @@ class PagesReserve(_Call):
                 n = int(t.shape[0])
         if positions is not None and slots is not None and positions.shape != slots.shape:
             raise ValueError(f"slots: {slots.shape[0]} entries, positions has {positions.shape[0]}")
+        # (an empty tensor's pointer is NULL, which would say that none was given)
+        positions, slots = (t.new_empty(1) if t is not None and n == 0 else t for t in (positions, slots))
         a = ReserveArgs(_ptr(seq_lens), _ptr(new_tokens), int(q_len), _ptr(free_pages), _ptr(num_free), _ptr(num_free_out),
                         _ptr(block_table), _ptr(seq_lens_out), _ptr(cu_tokens), _ptr(positions), _ptr(slots), n, _ptr(status), _i32_ptr(granted))
         self._bind(lib().mj_pages_reserve, (ctypes.byref(params), ctypes.byref(a)),

@@ -121,3 +121,15 @@ def test_bad_pages_and_a_full_list():
     for n_free, want, status in ((1, [0, 0, 1, 2, 3, 5, 6, 8, 1], INVALID), (2, [0, 1, 0, 1, 2, 3, 5, 6, 8, 1], INVALID),
                                  (3, [0, 1, 2, 0, 1, 2, 3, 5, 6, 8], CAPACITY), (6, [0, 1, 2, 3, 4, 5, 0, 1, 2, 3], CAPACITY)):
         assert _release(lens, keep, 16, table, free, n_free, False) == (want, status)
+
+
+@pytest.mark.parametrize("outputs", [("positions",), ("slots",), ("positions", "slots"), ()])
+@pytest.mark.parametrize("new", [0, 3])
+def test_no_entries_for_new_tokens(outputs, new):
+    """Outputs of no entries are given all the same: tokens that they do not hold are reported."""
+    d = {name: torch.zeros(0, dtype=torch.int64 if name == "slots" else torch.int32, device="cuda") for name in outputs}
+    status, lens = torch.zeros(1, **I32), torch.zeros(2, **I32)
+    mj.pages_reserve(mj.make_page_params(2, 16, 4, 9), seq_lens=lens, new_tokens=torch.tensor([0, new], **I32),
+                     free_pages=torch.arange(9, **I32), num_free=torch.tensor([9], **I32), block_table=torch.zeros(2, 4, **I32),
+                     status=status, **d)
+    assert int(status.item()) == (INVALID if outputs and new else 0) and lens.tolist() == [0, new]
